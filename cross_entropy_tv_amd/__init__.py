@@ -98,6 +98,10 @@ def _load() -> ctypes.CDLL:
     L.lx_ce_tvd_linear_forward_backward.argtypes = [p, p, i64, p, p, i64, p, i64, i64, i64, p, p, p, p, p, p, p,
                                                     f32, f32, p, i64, p, sz, p]
     L.lx_ce_tvd_linear_forward_backward.restype = i32
+    L.lx_draft_verify_workspace_bytes.argtypes = [i64, i64, i64]
+    L.lx_draft_verify_workspace_bytes.restype = sz
+    L.lx_draft_verify.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, i64, p, p, p, p, p, p, i32, p, sz, p]
+    L.lx_draft_verify.restype = i32
     return L
 
 
@@ -140,6 +144,47 @@ def _rows2d(t, name):
         raise ValueError(f"{name} must be a 2-D (BT, V) device tensor with contiguous rows")
     BT, V = t.shape
     return BT, V, (t.stride(0) if BT > 1 else V)
+
+
+def _arg(t, name, dtype, shape, device):
+    """A contiguous device tensor of this dtype and shape on this device."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+class _Launch:
+    """The device, stream and workspace of one call: the device of its tensors is made
+    current (a stream belongs to a device), the stream is the given one or that device's
+    current one, and a workspace allocated here comes from the memory of the stream that
+    uses it."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device, self.stream = device, stream
+        self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        self.guard.__enter__()
+        self.ptr = _stream(self.stream)
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+    def workspace(self, given, need):
+        import torch
+        if given is not None:
+            if given.device != self.device:
+                raise ValueError(f"workspace must be on {self.device}")
+        elif need:
+            if self.stream is None:
+                given = torch.empty(need, dtype=torch.uint8, device=self.device)
+            else:
+                s = self.stream if hasattr(self.stream, "cuda_stream") else torch.cuda.ExternalStream(self.ptr)
+                with torch.cuda.stream(s):
+                    given = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return given, 0 if given is None else given.numel() * given.element_size()
 
 
 def _check(status: int, where: str) -> None:
@@ -415,6 +460,48 @@ def lx_ce_tvd_linear_forward_backward(x_s, w_s, x_t, w_t, target, ignore_index, 
                                                  wbytes, _stream(stream)), "lx_ce_tvd_linear_forward_backward")
 
 
+def lx_draft_verify_workspace_bytes(S: int, max_draft: int, V: int) -> int:
+    return lib.lx_draft_verify_workspace_bytes(S, max_draft, V)
+
+
+def lx_draft_verify(target, draft, draft_tokens, draft_start, max_draft: int, temperature, u_accept, u_sample,
+                    n_accepted, tokens, logprobs=None, workspace=None, stream=None) -> None:
+    """Verification of S sequences' drafted tokens: ``target`` (N + S, V) and ``draft`` (N, V)
+    or None, 2-D with contiguous rows; ``draft_tokens`` int64 [N], ``draft_start`` int64
+    [S + 1]; ``temperature`` float32 [S] or None, ``u_accept`` float32 [N], ``u_sample``
+    float32 [S]; into ``n_accepted`` int64 [S], ``tokens`` int64 [S, max_draft + 1] and
+    ``logprobs`` float32 [S, max_draft + 1] or None.  The workspace (uint8 device tensor) is
+    allocated here with torch when not given."""
+    import torch
+    rows, V, ldt = _rows2d(target, "target")
+    dt, dev, max_draft = _dtype_code(target), target.device, int(max_draft)
+    N, S = draft_tokens.shape[0], u_sample.shape[0]
+    if rows != N + S:
+        raise ValueError(f"target must have a row per draft and one per sequence, {N} + {S}, got {rows}")
+    ldd = V
+    if draft is not None:
+        if tuple(draft.shape) != (N, V) or draft.dtype != target.dtype or draft.device != dev:
+            raise ValueError(f"draft must be ({N}, {V}), of target's dtype and on its device")
+        ldd = _rows2d(draft, "draft")[2]
+    f32, i64 = torch.float32, torch.int64
+    _arg(draft_tokens, "draft_tokens", i64, (N,), dev)
+    _arg(draft_start, "draft_start", i64, (S + 1,), dev)
+    if temperature is not None:
+        _arg(temperature, "temperature", f32, (S,), dev)
+    _arg(u_accept, "u_accept", f32, (N,), dev)
+    _arg(u_sample, "u_sample", f32, (S,), dev)
+    _arg(n_accepted, "n_accepted", i64, (S,), dev)
+    _arg(tokens, "tokens", i64, (S, max_draft + 1), dev)
+    if logprobs is not None:
+        _arg(logprobs, "logprobs", f32, (S, max_draft + 1), dev)
+    with _Launch(dev, stream) as at:
+        ws, wbytes = at.workspace(workspace, lx_draft_verify_workspace_bytes(S, max_draft, V))
+        _check(lib.lx_draft_verify(_ptr(target), ldt, _ptr(draft), ldd, _ptr(draft_tokens), _ptr(draft_start), S, N,
+                                   max_draft, V, _ptr(temperature), _ptr(u_accept), _ptr(u_sample),
+                                   _ptr(n_accepted), _ptr(tokens), _ptr(logprobs), dt, _ptr(ws), wbytes, at.ptr),
+               "lx_draft_verify")
+
+
 __all__ = [
     "LxError", "lib", "LIB_PATH", "LX_OK", "LX_ERR_INVALID_ARG", "LX_ERR_UNSUPPORTED_DTYPE", "LX_ERR_ALIAS",
     "LX_ERR_WORKSPACE", "LX_ERR_HIP", "LX_F32", "LX_BF16", "LX_F16", "lx_status_string", "lx_abi_version",
@@ -423,6 +510,7 @@ __all__ = [
     "lx_vp_stats_floats", "lx_ce_tvd_vp_stats", "lx_ce_tvd_vp_merge_stats", "lx_ce_tvd_vp_tv", "lx_ce_tvd_vp_merge_tv",
     "lx_ce_tvd_backward_shard", "lx_ce_tvd_forward_ex", "lx_ce_tvd_backward_ex", "lx_ce_tvd_forward_backward_ex",
     "lx_gemm_bf16", "lx_ce_tvd_linear_workspace_bytes", "lx_ce_tvd_linear_forward_backward",
+    "lx_draft_verify_workspace_bytes", "lx_draft_verify",
 ]
 
 

@@ -8,6 +8,7 @@
 #include "launch.hpp"
 #include "linear.hpp"
 #include "lx_ce_tvd.h"
+#include "verify.hpp"
 
 namespace {
 
@@ -81,6 +82,13 @@ struct Tensor {
   const void* p;
   int64_t ld;
 };
+
+// Sizes that lx_draft_verify takes: grids of one workgroup per (position, sequence, at
+// least 2048 logits) and tables of S * (max_draft + 1) entries stay within int32.
+bool verify_shape_ok(int64_t S, int64_t max_draft, int64_t V) {
+  if (S < 0 || max_draft < 0 || V < 1 || V > (int64_t)INT_MAX || S > (1 << 24) || max_draft > (1 << 20)) return false;
+  return S * (max_draft + 1) <= (1 << 24) && S * (max_draft + 1) <= (int64_t)INT_MAX / ((V + 2047) / 2048);
+}
 
 lx_status forward_impl(Tensor zs, Tensor us, const int64_t* target, int64_t BT, int64_t V, int64_t ignore_index,
                        float* ce, float* tvd, float* lse_s, float* lse_t, float* sigma, lx_dtype dt,
@@ -621,6 +629,64 @@ lx_status lx_ce_tvd_linear_forward_backward(const void* x_s, const void* w_s, in
   a.chunk_rows = chunk_rows;
   a.workspace = workspace;
   return from_hip(lx::run_linear(a, static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ drafted tokens
+
+size_t lx_draft_verify_workspace_bytes(int64_t S, int64_t max_draft, int64_t V) {
+  if (!verify_shape_ok(S, max_draft, V) || S == 0) return 0;
+  return lx::verify_workspace_bytes(S, max_draft, V);
+}
+
+lx_status lx_draft_verify(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft,
+                          const int64_t* draft_tokens, const int64_t* draft_start, int64_t S, int64_t N,
+                          int64_t max_draft, int64_t V, const float* temperature, const float* u_accept,
+                          const float* u_sample, int64_t* n_accepted, int64_t* tokens, float* logprobs, lx_dtype dt,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  const int es = esize_of(dt);
+  if (!es) return LX_ERR_UNSUPPORTED_DTYPE;
+  if (!verify_shape_ok(S, max_draft, V) || N < 0) return LX_ERR_INVALID_ARG;
+  if (S == 0) return LX_OK;
+  if (N > S * max_draft || (N > 0 && N > INT64_MAX / 2 / V / es)) return LX_ERR_INVALID_ARG;
+  const bool has_d = draft != nullptr && N > 0;
+  if (!stride_ok(N + S, V, ld_target, es) || (has_d && !stride_ok(N, V, ld_draft, es))) return LX_ERR_INVALID_ARG;
+  if (!target || !draft_start || !u_sample || !n_accepted || !tokens || (N > 0 && (!draft_tokens || !u_accept)))
+    return LX_ERR_INVALID_ARG;
+  if (!aligned(target, es) || (has_d && !aligned(draft, es)) || !aligned(draft_tokens, 8) ||
+      !aligned(draft_start, 8) || !aligned(temperature, 4) || !aligned(u_accept, 4) || !aligned(u_sample, 4) ||
+      !aligned(n_accepted, 8) || !aligned(tokens, 8) || !aligned(logprobs, 4))
+    return LX_ERR_INVALID_ARG;
+  const size_t need = lx::verify_workspace_bytes(S, max_draft, V);
+  // 0..6 inputs (may overlap each other), 7..10 outputs and the workspace
+  const Span sp[11] = {span(target, strided_bytes(N + S, V, ld_target, es)),
+                       span(has_d ? draft : nullptr, has_d ? strided_bytes(N, V, ld_draft, es) : 0),
+                       span(draft_tokens, N * 8), span(draft_start, (S + 1) * 8), span(temperature, S * 4),
+                       span(u_accept, N * 4), span(u_sample, S * 4), span(n_accepted, S * 8),
+                       span(tokens, S * (max_draft + 1) * 8), span(logprobs, S * (max_draft + 1) * 4),
+                       span(workspace, (int64_t)need)};
+  for (int o = 7; o < 11; ++o)
+    for (int i = 0; i < 11; ++i)
+      if (i != o && overlaps(sp[o], sp[i])) return LX_ERR_ALIAS;
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
+  lx::VerifyArgs a{};
+  a.target = target;
+  a.draft = has_d ? draft : nullptr;
+  a.ldt = ld_target;
+  a.ldd = ld_draft;
+  a.tokens = draft_tokens;
+  a.start = draft_start;
+  a.S = S;
+  a.N = N;
+  a.L = max_draft;
+  a.V = V;
+  a.temperature = temperature;
+  a.u_accept = u_accept;
+  a.u_sample = u_sample;
+  a.n_accepted = n_accepted;
+  a.out = tokens;
+  a.logprobs = logprobs;
+  a.workspace = workspace;
+  return from_hip(lx::launch_verify(a, dt_of(dt), static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,1004 @@
+// Verification of drafted tokens against the target's probabilities.
+//
+// Sequence i has n_i drafted tokens x_0 .. x_{n_i - 1}, a row of target logits
+// for each of them and one more for the token behind the last, and a row of
+// draft logits for each.  With p = softmax(z / T), q = softmax(u / T) of a
+// position and its random number r in [0, 1):
+//
+//   x is accepted when r q(x) < p(x)                  (probability min(1, p / q));
+//   the first rejection at position a ends the sequence, and its token is drawn
+//   from max(p - q, 0) / sum max(p - q, 0)             (1 / sum = 1 / tvd);
+//   with every draft accepted (a = n_i) the token is drawn from p.
+//
+// The emitted tokens are then distributed as the target's own (the total
+// variation distance that the loss trains down is the rejection probability).
+// A token is drawn by inversion: the smallest v whose running sum of masses
+// exceeds w * total, w in [0, 1) given.  Without draft logits q is 1 at the
+// drafted token: accepted when r < p(x), and x is left out of the draw.  T = 0
+// takes the first largest logit throughout.
+//
+// What bounds it: reading the logits, once for every position that is reached.
+// Three steps:
+//
+//   1. verify_accept_kernel, one workgroup per (position, sequence, chunk of the
+//      row), position by position: partial (max, sum-exp) of target and draft in
+//      fp32; the last workgroup of a position merges them and decides.  Workgroups
+//      of positions behind a rejection already decided read nothing: they look,
+//      and never wait (the results do not depend on what they see).
+//   2. verify_sums_kernel, one workgroup per (sequence, chunk) of the one row that
+//      the token is drawn from: fp64 sums of the masses.  Where they need no draft
+//      the last workgroup draws.
+//   3. verify_residual_kernel (draft logits): the fp64 sums of max(p - q, 0), and
+//      the draw by the last workgroup.
+//
+// Precision.  An answer here is a whole number that a comparison decides, so the
+// values compared are held tighter than the rounding of the logits would ask
+// for.  The acceptance compares r q(x) with p(x) from fp32 sums (good to a few
+// 2^-21) and, where the two lie within 2^-15 of each other, again from fp64 sums
+// over both rows.  The draw's running sums are fp64 throughout: with 150 000
+// tokens the borders between them lie too close for fp32 sums to tell which side
+// w * total falls on.
+#include "common.hpp"
+#include "verify.hpp"
+
+namespace lx {
+
+namespace {
+
+constexpr int kVThreads = 256;
+constexpr int kVWaves = kVThreads / 64;
+constexpr int kVUnit = kVThreads * 8;  // elements that one load of every thread covers
+constexpr int kVHold = 4;              // groups of 8 elements that a thread holds at once
+constexpr int kVMaxChunks = 1024;      // chunks of a row at most (the draw keeps their sums in LDS)
+constexpr float kBorder = 0x1p-15f;
+// max(p - q, 0) sums to the total variation distance.  Below 2^-40 it is the rounding of equal rows
+// (a rejection there has a probability of less than that).
+constexpr double kNothing = 0x1p-40;
+constexpr double kLog2e64 = 1.4426950408889634074;
+constexpr double kLn2 = 0.69314718055994530942;
+
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------------ rows
+
+// 8 consecutive logits as they lie in memory.  Rows may start on any element
+// (odd vocabularies, views), so the loads carry the element's alignment only;
+// gfx950 runs 16-byte loads at any address.
+template <typename T>
+struct Group;
+template <>
+struct Group<uint16_t> {
+  u32x4_t w;
+  __device__ __forceinline__ void load(const uint16_t* p) { __builtin_memcpy(&w, p, 16); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const unsigned w0 = w.x, w1 = w.y, w2 = w.z, w3 = w.w;
+    x[0] = __uint_as_float(w0 << 16); x[1] = __uint_as_float(w0 & 0xffff0000u);
+    x[2] = __uint_as_float(w1 << 16); x[3] = __uint_as_float(w1 & 0xffff0000u);
+    x[4] = __uint_as_float(w2 << 16); x[5] = __uint_as_float(w2 & 0xffff0000u);
+    x[6] = __uint_as_float(w3 << 16); x[7] = __uint_as_float(w3 & 0xffff0000u);
+  }
+};
+template <>
+struct Group<_Float16> {
+  u32x4_t w;
+  __device__ __forceinline__ void load(const _Float16* p) { __builtin_memcpy(&w, p, 16); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const unsigned w0 = w.x, w1 = w.y, w2 = w.z, w3 = w.w;
+    unpack_f16x2(w0, x[0], x[1]); unpack_f16x2(w1, x[2], x[3]);
+    unpack_f16x2(w2, x[4], x[5]); unpack_f16x2(w3, x[6], x[7]);
+  }
+};
+template <>
+struct Group<float> {
+  u32x4_t w, v;
+  __device__ __forceinline__ void load(const float* p) {
+    __builtin_memcpy(&w, p, 16);
+    __builtin_memcpy(&v, p + 4, 16);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const unsigned a[8] = {w.x, w.y, w.z, w.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(a[k]);
+  }
+};
+
+__device__ __forceinline__ float ninf() { return -__builtin_inff(); }
+
+// The 8 logits of elements v .. v + 7 of a row, -inf (mass 0) from `end` on.
+template <typename T>
+__device__ __forceinline__ void load_edge(const T* row, int64_t v, int64_t end, float (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = v + k < end ? load1(row + v + k) : ninf();
+}
+
+// Elements [lo, hi) of a row, lo a multiple of kVUnit from the row's start: f(v, x) for
+// every group of 8 of this thread, with up to kVHold groups loaded at once.
+template <typename T, typename F>
+__device__ __forceinline__ void for_groups(const T* row, int64_t lo, int64_t hi, F f) {
+  const int tid = tid_x();
+  const int64_t whole = lo + (hi - lo) / 8 * 8;
+  for (int64_t b = lo; b < hi; b += kVUnit * kVHold) {
+    Group<T> g[kVHold];
+#pragma unroll
+    for (int k = 0; k < kVHold; ++k) {
+      const int64_t v = b + k * kVUnit + tid * 8;
+      if (v < whole) g[k].load(row + v);
+    }
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < kVHold; ++k) {
+      const int64_t v = b + k * kVUnit + tid * 8;
+      if (v < whole) {
+        g[k].get(x);
+        f(v, x);
+      } else if (v < hi) {
+        load_edge(row, v, hi, x);
+        f(v, x);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ arithmetic
+
+// 2^t for t <= 0 in fp64 to a few 1e-15: t = n + f with |f| <= 1/2, and the Taylor
+// series of e^(f ln 2) to the 12th power (|f ln 2| <= 0.347: the rest is below 2e-16).
+__device__ __forceinline__ double exp2_64(double t) {
+  t = t > -1100.0 ? t : -1100.0;  // 2^-1100 is 0 in fp64, and -inf would make n - n below NaN
+  const double n = __builtin_rint(t);
+  const double g = (t - n) * kLn2;
+  double s = 1.0 / 479001600.0;
+  s = __builtin_fma(s, g, 1.0 / 39916800.0);
+  s = __builtin_fma(s, g, 1.0 / 3628800.0);
+  s = __builtin_fma(s, g, 1.0 / 362880.0);
+  s = __builtin_fma(s, g, 1.0 / 40320.0);
+  s = __builtin_fma(s, g, 1.0 / 5040.0);
+  s = __builtin_fma(s, g, 1.0 / 720.0);
+  s = __builtin_fma(s, g, 1.0 / 120.0);
+  s = __builtin_fma(s, g, 1.0 / 24.0);
+  s = __builtin_fma(s, g, 1.0 / 6.0);
+  s = __builtin_fma(s, g, 0.5);
+  s = __builtin_fma(s, g, 1.0);
+  s = __builtin_fma(s, g, 1.0);
+  return __builtin_ldexp(s, (int)n);
+}
+
+// log s for 0 < s < inf: s = 2^k m with m in [1/sqrt 2, sqrt 2), and log m = 2 atanh(y),
+// y = (m - 1) / (m + 1), |y| <= 0.1716, by its series to y^19 (the rest is below 1e-17).
+__device__ __forceinline__ double log_64(double s) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, s);
+  int k = (int)(b >> 52) - 1023;
+  double m = __builtin_bit_cast(double, (b & 0xfffffffffffffull) | 0x3ff0000000000000ull);
+  if (m > 1.4142135623730951) {
+    m *= 0.5;
+    k += 1;
+  }
+  const double y = (m - 1.0) / (m + 1.0), y2 = y * y;
+  double t = 1.0 / 19.0;
+#pragma unroll
+  for (int d = 17; d >= 1; d -= 2) t = __builtin_fma(t, y2, 1.0 / (double)d);
+  return __builtin_fma((double)k, kLn2, 2.0 * y * t);
+}
+
+// The scale of a sequence's exponents: e^((z - m) / T) = 2^((z - m) scale).
+struct Temp {
+  bool greedy;
+  float c;
+  double c64, inv;
+};
+__device__ __forceinline__ Temp temp_of(const float* temperature, int i) {
+  const float t = temperature ? temperature[i] : 1.0f;
+  Temp r;
+  r.greedy = !(t > 0.0f);
+  const double d = r.greedy ? 1.0 : (double)t;
+  r.inv = 1.0 / d;
+  r.c64 = kLog2e64 / d;
+  // (finite also for the smallest temperatures: 0 * c must stay 0 at the largest logit)
+  r.c = r.c64 < 3.0e38 ? (float)r.c64 : 3.0e38f;
+  return r;
+}
+
+// A reference for exponents: the maximum, or 0 for a row without any mass (-inf - 0 = -inf: all masses 0).
+__device__ __forceinline__ float ref_of(float m) { return m == ninf() ? 0.0f : m; }
+
+struct Sum32 {
+  float m, s;  // sum of 2^((x - m) c) over what was added; m = -inf: nothing with mass
+};
+struct Sum64 {
+  float m;
+  double s;
+};
+struct Best {
+  float v;
+  unsigned at;
+};
+constexpr unsigned kNone = 0xffffffffu;
+
+__device__ __forceinline__ void add8(Sum32& a, const float (&x)[8], float c) {
+  const float mn = fmaxf(a.m, max8(x));
+  const float ref = ref_of(mn);
+  float s0 = a.s * exp2_hw((a.m - ref) * c), s1 = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    s0 += exp2_hw((x[k] - ref) * c);
+    s1 += exp2_hw((x[k + 1] - ref) * c);
+  }
+  a.m = mn;
+  a.s = s0 + s1;
+}
+// (the maximum rises a few times in a thread's elements at most, so the rescale is a branch)
+__device__ __forceinline__ void add8(Sum64& a, const float (&x)[8], double c) {
+  const float mn = fmaxf(a.m, max8(x));
+  const double ref = (double)ref_of(mn);
+  if (mn != a.m) {
+    a.s *= exp2_64(((double)a.m - ref) * c);
+    a.m = mn;
+  }
+  double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    s0 += exp2_64(((double)x[k] - ref) * c);
+    s1 += exp2_64(((double)x[k + 1] - ref) * c);
+  }
+  a.s += s0 + s1;
+}
+__device__ __forceinline__ void add8(Best& a, int64_t v, const float (&x)[8]) {
+  const float m = max8(x);
+  if (m > a.v) {
+    a.v = m;
+#pragma unroll
+    for (int k = 7; k >= 0; --k) {
+      if (x[k] == m) a.at = (unsigned)(v + k);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ reductions over a workgroup
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  return v;
+}
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+__device__ __forceinline__ unsigned wave_min_u(unsigned v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const unsigned o = __shfl_xor(v, off, 64);
+    v = o < v ? o : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ Sum32 wave_merge(Sum32 a, float c) {
+  const float m = wave_max(a.m);
+  return Sum32{m, wave_sum(a.s * exp2_hw((a.m - ref_of(m)) * c))};
+}
+__device__ __forceinline__ Sum64 wave_merge(Sum64 a, double c) {
+  const float m = wave_max(a.m);
+  return Sum64{m, wave_sum64(a.s * exp2_64(((double)a.m - (double)ref_of(m)) * c))};
+}
+// the first of the largest
+__device__ __forceinline__ Best wave_merge(Best a) {
+  const float m = wave_max(a.v);
+  return Best{m, wave_min_u(a.v == m ? a.at : kNone)};
+}
+
+// ------------------------------------------------------------------ exchange between workgroups
+
+// What one workgroup hands to another inside a launch goes through device-coherent
+// atomics, which pass the caches of the chip's dies by.  A workgroup publishes,
+// waits until its stores have been acknowledged, and counts itself; the one that
+// counts last reads.  Nobody waits for anybody.
+__device__ __forceinline__ void publish(uint64_t* p, uint64_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t fetch(const uint64_t* p) {
+  return __hip_atomic_load(const_cast<uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish(uint64_t* p, double v) { publish(p, __builtin_bit_cast(uint64_t, v)); }
+__device__ __forceinline__ double fetch64(const uint64_t* p) { return __builtin_bit_cast(double, fetch(p)); }
+__device__ __forceinline__ uint64_t pack(float lo, unsigned hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)hi << 32);
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((unsigned)v); }
+__device__ __forceinline__ unsigned hi_of(uint64_t v) { return (unsigned)(v >> 32); }
+
+// Called by thread 0 after its publish(): whether this workgroup is the last of `of`.
+__device__ __forceinline__ bool count_last(int* counter, int of) {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0);  // the published values have reached memory
+  asm volatile("" ::: "memory");
+  const bool last = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == of - 1;
+  asm volatile("" ::: "memory");
+  return last;
+}
+
+// ------------------------------------------------------------------ workspace
+
+constexpr int kP1 = 2;  // 64-bit words of a chunk's partials in step 1: (m, s) of target and of draft
+constexpr int kP2 = 3;  // in step 2: (m_t, m_d), s_t, s_d
+constexpr int kSt = 3;  // a sequence's merged sums for step 3: (m_t, m_d), s_t, s_d
+
+struct Ws {
+  int* first;      // [S] the first rejected position, or INT_MAX
+  int* count1;     // [L][S] arrivals of step 1
+  int* count2;     // [S]
+  int* count3;     // [S]
+  int* best;       // [L][S] greedy: the target's token
+  float* logp;     // [L][S] log p of the drafted token
+  uint64_t *part1, *part2, *part3, *state;
+  int K1, K2;
+  int64_t chunk1, chunk2;
+  int64_t n_zero;  // ints from count1 on that start at 0
+  size_t bytes;
+};
+
+// Chunks of a row: whole kVUnits, `per` of them each, so that `rows` rows make enough
+// workgroups for the chip (1024) before chunks grow, and at most 8 of them (16384
+// elements): a longer chunk would only delay the decision that spares later positions.
+void chunking(int64_t rows, int64_t V, int64_t& chunk, int& K) {
+  const int64_t units = (V + kVUnit - 1) / kVUnit;
+  int64_t per = rows * units / 1024;
+  per = per < 1 ? 1 : per > 8 ? 8 : per;
+  const int64_t least = (units + kVMaxChunks - 1) / kVMaxChunks;
+  if (per < least) per = least;
+  chunk = per * kVUnit;
+  K = (int)((units + per - 1) / per);
+}
+
+Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
+  Ws w{};
+  chunking(S * L, V, w.chunk1, w.K1);
+  chunking(S, V, w.chunk2, w.K2);
+  size_t off = 0;
+  char* p = static_cast<char*>(base);
+  auto take = [&](size_t bytes) {
+    char* q = p ? p + off : nullptr;
+    off += (bytes + 255) & ~(size_t)255;
+    return q;
+  };
+  w.first = reinterpret_cast<int*>(take((size_t)S * 4));
+  w.n_zero = S * L + 2 * S;
+  w.count1 = reinterpret_cast<int*>(take((size_t)w.n_zero * 4));
+  w.count2 = w.count1 ? w.count1 + S * L : nullptr;
+  w.count3 = w.count1 ? w.count2 + S : nullptr;
+  w.best = reinterpret_cast<int*>(take((size_t)S * L * 4));
+  w.logp = reinterpret_cast<float*>(take((size_t)S * L * 4));
+  w.part1 = reinterpret_cast<uint64_t*>(take((size_t)S * L * w.K1 * kP1 * 8));
+  w.part2 = reinterpret_cast<uint64_t*>(take((size_t)S * w.K2 * kP2 * 8));
+  w.part3 = reinterpret_cast<uint64_t*>(take((size_t)S * w.K2 * 8));
+  w.state = reinterpret_cast<uint64_t*>(take((size_t)S * kSt * 8));
+  w.bytes = off;
+  return w;
+}
+
+struct Args {
+  VerifyArgs a;
+  Ws w;
+};
+
+__global__ __launch_bounds__(kVThreads) void verify_init_kernel(int* __restrict__ first, int S, int* __restrict__ zero,
+                                                                int64_t n_zero) {
+  const int64_t i = (int64_t)bid_x() * kVThreads + tid_x();
+  if (i < S) first[i] = 0x7fffffff;
+  if (i < n_zero) zero[i] = 0;
+}
+
+// A sequence's place in the arrays; ok: its rows lie inside them.
+struct Seq {
+  int64_t first;  // its first draft
+  int n;
+  bool ok;
+};
+__device__ __forceinline__ Seq seq_of(const VerifyArgs& a, int i) {
+  const int64_t s = a.start[i], e = a.start[i + 1];
+  Seq q;
+  q.ok = s >= 0 && e >= s && e <= a.N && e - s <= a.L;
+  q.first = q.ok ? s : 0;
+  q.n = q.ok ? (int)(e - s) : 0;
+  return q;
+}
+
+// ------------------------------------------------------------------ step 1: accept
+
+// The fp64 sum of a whole row against its maximum, by the workgroup (valid in every thread).
+template <typename T>
+__device__ double row_sum64(const T* row, int64_t V, float m, double c, double* red) {
+  const double ref = (double)ref_of(m);
+  double s = 0.0;
+  for_groups(row, 0, V, [&](int64_t, const float (&x)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += exp2_64(((double)x[k] - ref) * c);
+  });
+  s = wave_sum64(s);
+  __syncthreads();
+  if ((tid_x() & 63) == 0) red[tid_x() >> 6] = s;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int w = 0; w < kVWaves; ++w) t += red[w];
+  return t;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
+  const VerifyArgs& a = g.a;
+  const Ws& w = g.w;
+  __shared__ uint64_t red[2][kVWaves];
+  __shared__ double red64[kVWaves];
+  __shared__ float sh_m[2];
+  __shared__ double sh_s[2];
+  __shared__ int sh_flag;
+  const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
+  const int K = w.K1;
+  const int c = (int)(bid_x() % (unsigned)K);
+  const unsigned slot = bid_x() / (unsigned)K;  // position-major: all first positions, then all second ones, ...
+  const int i = (int)(slot % (unsigned)a.S), j = (int)(slot / (unsigned)a.S);
+  const Seq q = seq_of(a, i);
+  if (j >= q.n) return;
+  // a rejection before this position: nothing here is asked for (one load per
+  // workgroup, so that all its threads go the same way)
+  if (tid == 0)
+    sh_flag = __hip_atomic_load(w.first + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < j;
+  __syncthreads();
+  if (sh_flag) return;
+  const Temp t = temp_of(a.temperature, i);
+  const T* zr = static_cast<const T*>(a.target) + (q.first + i + j) * a.ldt;
+  const bool has_d = a.draft != nullptr && !t.greedy;
+  const T* ur = has_d ? static_cast<const T*>(a.draft) + (q.first + j) * a.ldd : nullptr;
+  const int64_t lo = c * w.chunk1, hi = lo + w.chunk1 < a.V ? lo + w.chunk1 : a.V;
+
+  if (t.greedy) {
+    Best b{ninf(), kNone};
+    for_groups(zr, lo, hi, [&](int64_t v, const float (&x)[8]) { add8(b, v, x); });
+    b = wave_merge(b);
+    if (lane == 0) red[0][wave] = pack(b.v, b.at);
+  } else {
+    Sum32 st{ninf(), 0.0f}, sd{ninf(), 0.0f};
+    for_groups(zr, lo, hi, [&](int64_t, const float (&x)[8]) { add8(st, x, t.c); });
+    if (has_d) for_groups(ur, lo, hi, [&](int64_t, const float (&x)[8]) { add8(sd, x, t.c); });
+    st = wave_merge(st, t.c);
+    if (has_d) sd = wave_merge(sd, t.c);
+    if (lane == 0) {
+      red[0][wave] = pack(st.m, __float_as_uint(st.s));
+      red[1][wave] = pack(sd.m, __float_as_uint(sd.s));
+    }
+  }
+  __syncthreads();
+  uint64_t* part = w.part1 + ((int64_t)slot * K + c) * kP1;
+  if (tid == 0) {
+    if (t.greedy) {
+      Best b{ninf(), kNone};
+#pragma unroll
+      for (int k = 0; k < kVWaves; ++k) {  // waves hold ascending runs only inside a pass: compare places too
+        const float v = lo_of(red[0][k]);
+        const unsigned at = hi_of(red[0][k]);
+        if (v > b.v || (v == b.v && at < b.at)) b = Best{v, at};
+      }
+      publish(part, pack(b.v, b.at));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float m = ninf();
+#pragma unroll
+        for (int k = 0; k < kVWaves; ++k) m = fmaxf(m, lo_of(red[h][k]));
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kVWaves; ++k)
+          s += __uint_as_float(hi_of(red[h][k])) * exp2_hw((lo_of(red[h][k]) - ref_of(m)) * t.c);
+        if (h == 0 || has_d) publish(part + h, pack(m, __float_as_uint(s)));
+      }
+    }
+    sh_flag = count_last(w.count1 + slot, K);
+  }
+  __syncthreads();
+  if (!sh_flag) return;
+
+  // the position's last workgroup: merge the chunks and decide
+  const uint64_t* parts = w.part1 + (int64_t)slot * K * kP1;
+  const int64_t x = a.tokens[q.first + j];
+  const bool x_ok = x >= 0 && x < a.V;
+  if (t.greedy) {
+    if (wave == 0) {
+      Best b{ninf(), kNone};
+      for (int k = lane; k < K; k += 64) {
+        const uint64_t v = fetch(parts + k * kP1);
+        if (lo_of(v) > b.v || (lo_of(v) == b.v && hi_of(v) < b.at)) b = Best{lo_of(v), hi_of(v)};
+      }
+      b = wave_merge(b);
+      if (lane == 0) {
+        // a row with no mass has no largest logit: nothing is accepted, no token drawn
+        const int at = b.v == ninf() ? -1 : (int)b.at;
+        w.best[slot] = at;
+        w.logp[slot] = 0.0f;
+        if (!x_ok || x != at) __hip_atomic_fetch_min(w.first + i, j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    return;
+  }
+  if (wave == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && !has_d) break;
+      Sum64 s{ninf(), 0.0};
+      for (int k = lane; k < K; k += 64) {
+        const uint64_t v = fetch(parts + k * kP1 + h);
+        const float mn = fmaxf(s.m, lo_of(v)), ref = ref_of(mn);
+        s.s = s.s * exp2_64(((double)s.m - ref) * t.c64) +
+              (double)__uint_as_float(hi_of(v)) * exp2_64(((double)lo_of(v) - ref) * t.c64);
+        s.m = mn;
+      }
+      s = wave_merge(s, t.c64);
+      if (lane == 0) {
+        sh_m[h] = s.m;
+        sh_s[h] = s.s;
+      }
+    }
+  }
+  __syncthreads();
+  const double r = (double)a.u_accept[q.first + j];
+  const float zx = x_ok ? load1(zr + x) : ninf();
+  const float ux = x_ok && has_d ? load1(ur + x) : ninf();
+  const double ez = exp2_64(((double)zx - (double)ref_of(sh_m[0])) * t.c64);
+  const double eu = has_d ? exp2_64(((double)ux - (double)ref_of(sh_m[1])) * t.c64) : 1.0;
+  double St = sh_s[0], Sd = has_d ? sh_s[1] : 1.0;
+  // r q < p with p = ez / St and q = eu / Sd (q = 1 without draft logits), multiplied out;
+  // a row without mass has p = 0 or q = 0
+  double left = r * eu * St, right = ez * Sd;
+  bool pz = ez > 0.0 && St > 0.0, qz = eu > 0.0 && Sd > 0.0;
+  if (pz && qz && __builtin_fabs(left - right) <= (double)kBorder * right) {
+    St = row_sum64(zr, a.V, sh_m[0], t.c64, red64);
+    if (has_d) Sd = row_sum64(ur, a.V, sh_m[1], t.c64, red64);
+    left = r * eu * St;
+    right = ez * Sd;
+  }
+  if (tid == 0) {
+    const bool accept = pz && (!qz || left < right);
+    w.logp[slot] = pz ? (float)(((double)zx - (double)sh_m[0]) * t.inv - log_64(St)) : ninf();
+    if (!accept) __hip_atomic_fetch_min(w.first + i, j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+
+// ------------------------------------------------------------------ steps 2 and 3: the token behind the accepted ones
+
+// The masses that the token is drawn from, relative to what the callers hold.
+template <typename T>
+struct Masses {
+  const T *zr, *ur;  // ur: the residual's draft row, or nullptr
+  int64_t V, skip;   // skip: a token left out, or -1
+  double c, mt, md;  // references
+  double it, id;     // residual: 1 / S_t, 1 / S_d
+
+  // masses of elements v .. v + 7 (v a multiple of 8 from the row's start)
+  __device__ __forceinline__ void get(int64_t v, double (&e)[8]) const {
+    float x[8];
+    fill(zr, v, x);
+    if (ur) {
+      float y[8];
+      fill(ur, v, y);
+      of(v, x, y, e);
+    } else {
+      of(v, x, e);
+    }
+  }
+  __device__ __forceinline__ void of(int64_t v, const float (&x)[8], double (&e)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = v + k == skip ? 0.0 : exp2_64(((double)x[k] - mt) * c);
+  }
+  __device__ __forceinline__ void of(int64_t, const float (&x)[8], const float (&y)[8], double (&e)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const double d = exp2_64(((double)x[k] - mt) * c) * it - exp2_64(((double)y[k] - md) * c) * id;
+      e[k] = d > 0.0 ? d : 0.0;
+    }
+  }
+  __device__ __forceinline__ void fill(const T* row, int64_t v, float (&x)[8]) const {
+    if (v + 8 <= V) {
+      Group<T> g;
+      g.load(row + v);
+      g.get(x);
+    } else {
+      load_edge(row, v, V, x);
+    }
+  }
+};
+
+// Wave-wide inclusive prefix sum.
+__device__ __forceinline__ double wave_scan64(double v, int lane) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const double o = __shfl_up(v, off, 64);
+    if (lane >= off) v += o;
+  }
+  return v;
+}
+
+struct PickShared {
+  double sums[kVMaxChunks];
+  double wave[kVWaves];
+  double before;  // the sum in front of the chosen chunk
+  int chunk;
+  int found;  // token + 1 of the border's element, 0: not found
+  int last;   // token + 1 of the last element with mass
+};
+
+// The token at w of the total, by the workgroup: the chunk whose running sum first
+// exceeds w * total (sums[0..K) filled by the caller, scaled like the masses), then
+// the element.  The running sums are in vocabulary order.  Should rounding leave no
+// element above the goal, the last one with mass is the token; -1: no mass at all.
+template <typename T>
+__device__ int64_t pick(const Masses<T>& m, PickShared& sh, int K, int64_t chunk, double w) {
+  const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
+  if (wave == 0) {
+    // each lane a run of consecutive chunks
+    const int per = (K + 63) / 64, k0 = lane * per, k1 = k0 + per < K ? k0 + per : K;
+    double own = 0.0;
+    for (int k = k0; k < k1; ++k) own += sh.sums[k];
+    const double upto = wave_scan64(own, lane);
+    const double total = __shfl(upto, 63, 64);
+    const double goal = w * total;
+    double run = upto - own;
+    int at = 0x7fffffff, last = -1;
+    double before = 0.0;
+    for (int k = k0; k < k1; ++k) {
+      if (sh.sums[k] > 0.0) {
+        if (at == 0x7fffffff && run + sh.sums[k] > goal) {
+          at = k;
+          before = run;
+        }
+        last = k;
+      }
+      run += sh.sums[k];
+    }
+    // the lowest lane's find; else the last chunk with mass
+    const unsigned long long hit = __ballot(at != 0x7fffffff), some = __ballot(last >= 0);
+    const int hl = hit ? __builtin_ctzll(hit) : 0, ll = some ? 63 - __builtin_clzll(some) : 0;
+    const int at_h = __shfl(at, hl, 64), last_l = __shfl(last, ll, 64);
+    const double before_h = __shfl(before, hl, 64);
+    if (lane == 0) {
+      sh.chunk = hit ? at_h : some ? last_l : -1;
+      // (no running sum above the goal: a goal no sum of the chunk exceeds, so that its last element is taken)
+      sh.before = hit ? goal - before_h : __builtin_inf();
+      sh.found = 0;
+      sh.last = 0;
+    }
+  }
+  __syncthreads();
+  if (sh.chunk < 0) return -1;
+  const double goal = sh.before;
+  const int64_t lo = sh.chunk * chunk, hi = lo + chunk < m.V ? lo + chunk : m.V;
+  double base = 0.0;
+  for (int64_t b = lo; b < hi; b += kVUnit) {
+    const int64_t v = b + tid * 8;
+    double e[8], own = 0.0;
+    int last = 0;
+    if (v < hi) {
+      m.get(v, e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        own += e[k];
+        if (e[k] > 0.0) last = (int)(v + k) + 1;
+      }
+    }
+    const double incl = wave_scan64(own, lane);
+    if (lane == 63) sh.wave[wave] = incl;
+    if (last) atomicMax(&sh.last, last);
+    __syncthreads();
+    double run = base + incl - own, all = base;
+#pragma unroll
+    for (int k = 0; k < kVWaves; ++k) {
+      if (k < wave) run += sh.wave[k];
+      all += sh.wave[k];
+    }
+    if (all > goal) {
+      // the first element whose running sum exceeds the goal: the lowest token among the finds
+      if (v < hi && run + own > goal) {
+        int at = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          run += e[k];
+          if (!at && e[k] > 0.0 && run > goal) at = (int)(v + k) + 1;
+        }
+        // (positive, so that atomicMax of the negative keeps the lowest)
+        if (at) atomicMax(&sh.found, 0x7fffffff - at);
+      }
+      __syncthreads();
+      if (sh.found) return 0x7fffffff - sh.found - 1;
+    }
+    base = all;
+    __syncthreads();  // sh.wave is written again
+  }
+  return sh.last - 1;
+}
+
+// The outputs of sequence i: the accepted tokens, the drawn one, -1 behind it.
+__device__ __forceinline__ void write_out(const VerifyArgs& a, const Ws& w, int i, const Seq& q, int acc, int64_t tok,
+                                          float lp) {
+  for (int64_t k = tid_x(); k <= a.L; k += kVThreads) {
+    const int64_t o = i * (a.L + 1) + k;
+    a.out[o] = k < acc ? a.tokens[q.first + k] : k == acc ? tok : -1;
+    if (a.logprobs) a.logprobs[o] = k < acc ? w.logp[k * a.S + i] : k == acc && tok >= 0 ? lp : 0.0f;
+  }
+  if (tid_x() == 0) a.n_accepted[i] = q.ok ? acc : -1;
+}
+
+// log p of a token from its logit and the row's sum.
+template <typename T>
+__device__ __forceinline__ float logp_of(const T* zr, int64_t tok, float m, double s, const Temp& t) {
+  return tok < 0 ? 0.0f : (float)(((double)load1(zr + tok) - (double)m) * t.inv - log_64(s));
+}
+
+template <typename T>
+__global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
+  const VerifyArgs& a = g.a;
+  const Ws& w = g.w;
+  __shared__ uint64_t red[kVWaves];
+  __shared__ double red64[2][kVWaves];
+  __shared__ float red_m[2][kVWaves];
+  __shared__ PickShared sh;
+  __shared__ float sh_m[2];
+  __shared__ double sh_s[2];
+  __shared__ int sh_flag;
+  const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
+  const int K = w.K2;
+  const int c = (int)(bid_x() % (unsigned)K), i = (int)(bid_x() / (unsigned)K);
+  const Seq q = seq_of(a, i);
+  const Temp t = temp_of(a.temperature, i);
+  const int acc = min(w.first[i], q.n);
+  if (!q.ok || (t.greedy && acc < q.n)) {
+    if (c == 0) write_out(a, w, i, q, acc, q.ok ? w.best[(int64_t)acc * a.S + i] : -1, 0.0f);
+    return;
+  }
+  const T* zr = static_cast<const T*>(a.target) + (q.first + i + acc) * a.ldt;
+  const bool residual = a.draft != nullptr && acc < q.n;  // (not greedy: returned above)
+  const T* ur = residual ? static_cast<const T*>(a.draft) + (q.first + acc) * a.ldd : nullptr;
+  // a rejected draft without a distribution is left out of the draw
+  const int64_t skip = !residual && acc < q.n ? a.tokens[q.first + acc] : -1;
+  const int64_t lo = c * w.chunk2, hi = lo + w.chunk2 < a.V ? lo + w.chunk2 : a.V;
+  uint64_t* part = w.part2 + ((int64_t)i * K + c) * kP2;
+  if (t.greedy) {
+    Best b{ninf(), kNone};
+    for_groups(zr, lo, hi, [&](int64_t v, const float (&x)[8]) { add8(b, v, x); });
+    b = wave_merge(b);
+    if (lane == 0) red[wave] = pack(b.v, b.at);
+    __syncthreads();
+    if (tid == 0) {
+      b = Best{ninf(), kNone};
+#pragma unroll
+      for (int k = 0; k < kVWaves; ++k)
+        if (lo_of(red[k]) > b.v || (lo_of(red[k]) == b.v && hi_of(red[k]) < b.at)) b = Best{lo_of(red[k]), hi_of(red[k])};
+      publish(part, pack(b.v, b.at));
+      sh_flag = count_last(w.count2 + i, K);
+    }
+    __syncthreads();
+    if (!sh_flag) return;
+    if (wave == 0) {
+      b = Best{ninf(), kNone};
+      for (int k = lane; k < K; k += 64) {
+        const uint64_t v = fetch(w.part2 + ((int64_t)i * K + k) * kP2);
+        if (lo_of(v) > b.v || (lo_of(v) == b.v && hi_of(v) < b.at)) b = Best{lo_of(v), hi_of(v)};
+      }
+      b = wave_merge(b);
+      if (lane == 0) sh.chunk = b.v == ninf() ? -1 : (int)b.at;  // (not sh_flag: other waves may still be reading it)
+    }
+    __syncthreads();
+    write_out(a, w, i, q, acc, sh.chunk, 0.0f);
+    return;
+  }
+
+  // fp64 sums of the chunk, each against its own maximum; the token left out is summed on its own
+  Sum64 st{ninf(), 0.0}, sd{ninf(), 0.0};
+  for_groups(zr, lo, hi, [&](int64_t v, const float (&x)[8]) {
+    if (skip >= v && skip < v + 8) {
+      float y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        y[k] = v + k == skip ? ninf() : x[k];
+        if (v + k == skip) sd = Sum64{x[k], x[k] == ninf() ? 0.0 : 1.0};
+      }
+      add8(st, y, t.c64);
+    } else {
+      add8(st, x, t.c64);
+    }
+  });
+  if (residual) for_groups(ur, lo, hi, [&](int64_t, const float (&x)[8]) { add8(sd, x, t.c64); });
+  st = wave_merge(st, t.c64);
+  sd = wave_merge(sd, t.c64);
+  if (lane == 0) {
+    red_m[0][wave] = st.m;
+    red64[0][wave] = st.s;
+    red_m[1][wave] = sd.m;
+    red64[1][wave] = sd.s;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    float m[2];
+    double s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      m[h] = ninf();
+#pragma unroll
+      for (int k = 0; k < kVWaves; ++k) m[h] = fmaxf(m[h], red_m[h][k]);
+      s[h] = 0.0;
+#pragma unroll
+      for (int k = 0; k < kVWaves; ++k)
+        s[h] += red64[h][k] * exp2_64(((double)red_m[h][k] - (double)ref_of(m[h])) * t.c64);
+    }
+    publish(part, pack(m[0], __float_as_uint(m[1])));
+    publish(part + 1, s[0]);
+    publish(part + 2, s[1]);
+    sh_flag = count_last(w.count2 + i, K);
+  }
+  __syncthreads();
+  if (!sh_flag) return;
+
+  // the sequence's last workgroup: the row's sums
+  const uint64_t* parts = w.part2 + (int64_t)i * K * kP2;
+  if (wave == 0) {
+    float m0 = ninf(), m1 = ninf();
+    for (int k = lane; k < K; k += 64) {
+      const uint64_t v = fetch(parts + k * kP2);
+      m0 = fmaxf(m0, lo_of(v));
+      m1 = fmaxf(m1, __uint_as_float(hi_of(v)));
+    }
+    m0 = wave_max(m0);
+    m1 = wave_max(m1);
+    double s0 = 0.0, s1 = 0.0;
+    for (int k = lane; k < K; k += 64) {
+      const uint64_t v = fetch(parts + k * kP2);
+      const double e = fetch64(parts + k * kP2 + 1) * exp2_64(((double)lo_of(v) - (double)ref_of(m0)) * t.c64);
+      sh.sums[k] = e;
+      s0 += e;
+      s1 += fetch64(parts + k * kP2 + 2) *
+            exp2_64(((double)__uint_as_float(hi_of(v)) - (double)ref_of(m1)) * t.c64);
+    }
+    s0 = wave_sum64(s0);
+    s1 = wave_sum64(s1);
+    if (lane == 0) {
+      sh_m[0] = m0;
+      sh_m[1] = m1;
+      sh_s[0] = s0;
+      sh_s[1] = s1;
+    }
+  }
+  __syncthreads();
+  if (residual) {
+    if (tid == 0) {
+      uint64_t* st_out = w.state + (int64_t)i * kSt;
+      st_out[0] = pack(sh_m[0], __float_as_uint(sh_m[1]));
+      st_out[1] = __builtin_bit_cast(uint64_t, sh_s[0]);
+      st_out[2] = __builtin_bit_cast(uint64_t, sh_s[1]);
+    }
+    return;
+  }
+  float m = sh_m[0];
+  double s = sh_s[0];
+  int64_t left_out = skip;
+  if (skip >= 0) {
+    // with no mass beside the token left out it is drawn after all (p is 1 there)
+    if (!(s > 0.0)) left_out = -1;
+    const float mn = fmaxf(m, sh_m[1]);
+    const double full = s * exp2_64(((double)m - (double)ref_of(mn)) * t.c64) +
+                        sh_s[1] * exp2_64(((double)sh_m[1] - (double)ref_of(mn)) * t.c64);
+    if (left_out < 0) {
+      if (tid == 0 && skip < a.V) sh.sums[skip / w.chunk2] = sh_s[1];
+      __syncthreads();
+      m = mn;
+    }
+    const Masses<T> ms{zr, nullptr, a.V, left_out, t.c64, (double)ref_of(m), 0.0, 0.0, 0.0};
+    const int64_t tok = pick(ms, sh, K, w.chunk2, (double)a.u_sample[i]);
+    write_out(a, w, i, q, acc, tok, logp_of(zr, tok, mn, full, t));
+    return;
+  }
+  const Masses<T> ms{zr, nullptr, a.V, -1, t.c64, (double)ref_of(m), 0.0, 0.0, 0.0};
+  const int64_t tok = pick(ms, sh, K, w.chunk2, (double)a.u_sample[i]);
+  write_out(a, w, i, q, acc, tok, logp_of(zr, tok, m, s, t));
+}
+
+template <typename T>
+__global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
+  const VerifyArgs& a = g.a;
+  const Ws& w = g.w;
+  __shared__ double red64[kVWaves];
+  __shared__ PickShared sh;
+  __shared__ int sh_flag;
+  const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
+  const int K = w.K2;
+  const int c = (int)(bid_x() % (unsigned)K), i = (int)(bid_x() / (unsigned)K);
+  const Seq q = seq_of(a, i);
+  const int acc = min(w.first[i], q.n);
+  if (!q.ok || acc >= q.n) return;  // drawn from p in step 2
+  const Temp t = temp_of(a.temperature, i);
+  if (t.greedy) return;
+  const uint64_t* state = w.state + (int64_t)i * kSt;
+  const float mt = lo_of(state[0]), md = __uint_as_float(hi_of(state[0]));
+  const double St = __builtin_bit_cast(double, state[1]), Sd = __builtin_bit_cast(double, state[2]);
+  const T* zr = static_cast<const T*>(a.target) + (q.first + i + acc) * a.ldt;
+  const T* ur = static_cast<const T*>(a.draft) + (q.first + acc) * a.ldd;
+  const int64_t lo = c * w.chunk2, hi = lo + w.chunk2 < a.V ? lo + w.chunk2 : a.V;
+  Masses<T> ms{zr, ur, a.V, -1, t.c64, (double)ref_of(mt), (double)ref_of(md), St > 0.0 ? 1.0 / St : 0.0,
+               Sd > 0.0 ? 1.0 / Sd : 0.0};
+  double s = 0.0;
+  for (int64_t v = lo + tid * 8; v < hi; v += kVUnit) {
+    double e[8];
+    ms.get(v, e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += e[k];
+  }
+  s = wave_sum64(s);
+  if (lane == 0) red64[wave] = s;
+  __syncthreads();
+  if (tid == 0) {
+    double r = 0.0;
+#pragma unroll
+    for (int k = 0; k < kVWaves; ++k) r += red64[k];
+    publish(w.part3 + (int64_t)i * K + c, r);
+    sh_flag = count_last(w.count3 + i, K);
+  }
+  __syncthreads();
+  if (!sh_flag) return;
+  double any = 0.0;
+  for (int k = tid; k < K; k += kVThreads) {
+    sh.sums[k] = fetch64(w.part3 + (int64_t)i * K + k);
+    any += sh.sums[k];
+  }
+  __syncthreads();
+  any = wave_sum64(any);
+  if (lane == 0) red64[wave] = any;
+  __syncthreads();
+  any = 0.0;
+#pragma unroll
+  for (int k = 0; k < kVWaves; ++k) any += red64[k];
+  if (!(any > kNothing)) {
+    // nothing in p beyond q (a draft that neither row could have produced): drawn from p
+    for (int k = tid; k < K; k += kVThreads) {
+      const uint64_t* part = w.part2 + ((int64_t)i * K + k) * kP2;
+      sh.sums[k] = __builtin_bit_cast(double, part[1]) * exp2_64(((double)lo_of(part[0]) - ms.mt) * t.c64);
+    }
+    __syncthreads();
+    ms.ur = nullptr;
+  }
+  const int64_t tok = pick(ms, sh, K, w.chunk2, (double)a.u_sample[i]);
+  write_out(a, w, i, q, acc, tok, logp_of(zr, tok, mt, St, t));
+}
+
+template <typename T>
+hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
+  (void)hipGetLastError();
+  Args g{a, verify_ws(a.workspace, a.S, a.L, a.V)};
+  const Ws& w = g.w;
+  const int64_t n = w.n_zero > a.S ? w.n_zero : a.S;
+  hipLaunchKernelGGL(verify_init_kernel, dim3((unsigned)((n + kVThreads - 1) / kVThreads)), dim3(kVThreads), 0, st,
+                     w.first, (int)a.S, w.count1, w.n_zero);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (a.L > 0) {
+    hipLaunchKernelGGL((verify_accept_kernel<T>), dim3((unsigned)(a.S * a.L * w.K1)), dim3(kVThreads), 0, st, g);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  hipLaunchKernelGGL((verify_sums_kernel<T>), dim3((unsigned)(a.S * w.K2)), dim3(kVThreads), 0, st, g);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (a.L > 0 && a.draft) {
+    hipLaunchKernelGGL((verify_residual_kernel<T>), dim3((unsigned)(a.S * w.K2)), dim3(kVThreads), 0, st, g);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t verify_workspace_bytes(int64_t S, int64_t L, int64_t V) { return verify_ws(nullptr, S, L, V).bytes; }
+
+hipError_t launch_verify(const VerifyArgs& a, Dt dt, hipStream_t st) {
+  switch (dt) {
+    case Dt::BF16: return launch_verify_t<uint16_t>(a, st);
+    case Dt::F16: return launch_verify_t<_Float16>(a, st);
+    default: return launch_verify_t<float>(a, st);
+  }
+}
+
+}  // namespace lx

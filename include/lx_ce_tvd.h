@@ -477,6 +477,67 @@ lx_status lx_ce_tvd_linear_forward_backward(const void* x_s, const void* w_s, in
 
 /*
  * ---------------------------------------------------------------------------
+ * Verification of drafted tokens.  A draft model trained with the loss above
+ * proposes tokens that the target model checks in one pass: the total variation
+ * distance of the two is the probability that a proposal is rejected.
+ *
+ * Sequence i of S has n_i = draft_start[i + 1] - draft_start[i] drafted tokens
+ * (0 <= n_i <= max_draft), x_j = draft_tokens[draft_start[i] + j].  For position
+ * j, with p = softmax(target row / T), q = softmax(draft row / T) and
+ * r = u_accept[draft_start[i] + j],
+ *
+ *   x_j is accepted when r * q(x_j) < p(x_j)           (probability min(1, p / q))
+ *
+ * and a, the first position that is not (n_i if all are), ends the sequence:
+ * its token is drawn from max(p - q, 0), normalised, when a < n_i, and from p of
+ * the row behind the last draft when a = n_i, as the smallest v whose running sum
+ * of masses over 0..v exceeds u_sample[i] times their total.  The accepted
+ * tokens and this one are distributed as tokens of the target.
+ *
+ * - target (N + S, V), row stride ld_target: position j of sequence i is row
+ *   draft_start[i] + i + j, j = 0..n_i (one row more than drafts per sequence).
+ * - draft (N, V), row stride ld_draft, the same type: position j of sequence i is
+ *   row draft_start[i] + j.  NULL: drafts without a distribution (looked up, or
+ *   the draft's most likely tokens): x_j is accepted when r < p(x_j), and a
+ *   rejected x_j is left out of the draw.
+ * - draft_tokens int64[N], draft_start int64[S + 1] (from 0 to N, not decreasing).
+ * - temperature float[S] or NULL (1 for all): T of each sequence.  Where it is 0 (or
+ *   below) the sequence is greedy: x_j is accepted when it is the first largest
+ *   logit of its row, and the token that ends it is that of its own row; draft,
+ *   u_accept and u_sample are not used.
+ * - u_accept float[N], u_sample float[S]: random numbers in [0, 1).
+ * Outputs: n_accepted int64[S] = a; tokens int64[S][max_draft + 1]: the accepted
+ *   tokens, the drawn one, then -1; logprobs float[S][max_draft + 1] or NULL: log p
+ *   of each of them (0 for greedy sequences), then 0.
+ * - Masked tokens: -inf (or the type's lowest value beside others) has mass 0.  A
+ *   target row without any finite logit accepts nothing and gives token -1,
+ *   logprob 0; a draft row without any counts as q = 0.  A drafted token outside
+ *   [0, V) is not accepted.  Where a rejection leaves nothing in max(p - q, 0)
+ *   (less than 2^-40 in sum: p and q equal, and both 0 at x_j) the token is drawn from p.  NaN or
+ *   +inf logits give an unspecified token in [-1, V) for their sequence.
+ * - A sequence whose draft_start entries decrease, leave [0, N] or span more than
+ *   max_draft gives n_accepted = -1 and tokens -1.
+ * - Rows behind a sequence's first rejection need not be read; whether they are
+ *   does not change a result.  Comparisons that fp32 sums cannot decide are made
+ *   again from fp64 sums, and the draw's running sums are fp64.
+ * Workspace: at least lx_draft_verify_workspace_bytes(S, max_draft, V) bytes,
+ *   256-byte aligned, contents ignored and clobbered.
+ * Requirements: S * (max_draft + 1) <= 2^24 and, times ceil(V / 2048), below 2^31;
+ *   N <= S * max_draft; logits pointers element aligned, any row stride >= V.
+ *   S == 0 is a no-op.
+ * Errors : LX_ERR_INVALID_ARG, LX_ERR_UNSUPPORTED_DTYPE, LX_ERR_ALIAS (an output or
+ *   the workspace overlapping anything else), LX_ERR_WORKSPACE, LX_ERR_HIP.
+ */
+size_t lx_draft_verify_workspace_bytes(int64_t S, int64_t max_draft, int64_t V);
+
+lx_status lx_draft_verify(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft,
+                          const int64_t* draft_tokens, const int64_t* draft_start, int64_t S, int64_t N,
+                          int64_t max_draft, int64_t V, const float* temperature, const float* u_accept,
+                          const float* u_sample, int64_t* n_accepted, int64_t* tokens, float* logprobs,
+                          lx_dtype dt, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Reference streams: the practical HBM ceilings the loss kernels are measured
  * against (not part of the loss).  They move bytes the way the loss kernels
  * do: 16-byte buffer loads and stores with the streamed-once cache policy.
