@@ -102,6 +102,16 @@ def _load() -> ctypes.CDLL:
     L.lx_draft_verify_workspace_bytes.restype = sz
     L.lx_draft_verify.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, i64, p, p, p, p, p, p, i32, p, sz, p]
     L.lx_draft_verify.restype = i32
+    L.lx_lora_forward_workspace_bytes.argtypes = [i64] * 5
+    L.lx_lora_forward_workspace_bytes.restype = sz
+    L.lx_lora_forward.argtypes = [p, i64, p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, p, i64, i32, p, i64, i32, p, sz,
+                                  p]
+    L.lx_lora_forward.restype = i32
+    L.lx_lora_backward_workspace_bytes.argtypes = [i64] * 6
+    L.lx_lora_backward_workspace_bytes.restype = sz
+    L.lx_lora_backward.argtypes = [p, i64, p, i64, p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, p, i64, p, i64, p, p, p,
+                                   sz, p]
+    L.lx_lora_backward.restype = i32
     return L
 
 
@@ -502,6 +512,88 @@ def lx_draft_verify(target, draft, draft_tokens, draft_start, max_draft: int, te
                "lx_draft_verify")
 
 
+def lx_lora_forward_workspace_bytes(T: int, R: int, H: int, N: int, r: int) -> int:
+    return lib.lx_lora_forward_workspace_bytes(T, R, H, N, r)
+
+
+def lx_lora_backward_workspace_bytes(T: int, R: int, n_adapters: int, H: int, N: int, r: int) -> int:
+    return lib.lx_lora_backward_workspace_bytes(T, R, n_adapters, H, N, r)
+
+
+def _lora_set(x, A, B, adapter, req_start, scale, rank):
+    """(T, R, n_adapters, H, N, r, device) of the arguments that both directions take, checked."""
+    import torch
+    dev, bf16, i64 = x.device, torch.bfloat16, torch.int64
+    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+        raise ValueError("A must be (n_adapters, r, H) and B (n_adapters, N, r)")
+    (n, r, H), N, R = A.shape, B.shape[1], adapter.shape[0]
+    T = x.shape[0]
+    _bf16_rows(x, "x", T, H, dev)
+    _arg(A, "A", bf16, (n, r, H), dev)
+    _arg(B, "B", bf16, (n, N, r), dev)
+    _arg(adapter, "adapter", i64, (R,), dev)
+    _arg(req_start, "req_start", i64, (R + 1,), dev)
+    _arg(scale, "scale", torch.float32, (n,), dev)
+    if rank is not None:
+        _arg(rank, "rank", i64, (n,), dev)
+    return T, R, n, H, N, r, dev
+
+
+def _rows_of(t, name, dtypes, rows, cols, dev):
+    """The row stride of a 2-D (rows, cols) device tensor with contiguous rows, of one of these dtypes."""
+    if t.dtype not in dtypes or tuple(t.shape) != (rows, cols) or t.device != dev:
+        raise ValueError(f"{name} must be ({rows}, {cols}) on {dev}, {' or '.join(map(str, dtypes))}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return _rows2d(t, name)[2]
+
+
+def _bf16_rows(t, name, rows, cols, dev):
+    import torch
+    return _rows_of(t, name, (torch.bfloat16,), rows, cols, dev)
+
+
+def lx_lora_forward(x, A, B, adapter, req_start, scale, rank, base, y, workspace=None, stream=None) -> None:
+    """y = base + scale (x A^T) B^T with each request's adapter: ``x`` (T, H) bfloat16; ``A``
+    (n_adapters, r, H) and ``B`` (n_adapters, N, r) bfloat16; ``adapter`` int64 [R],
+    ``req_start`` int64 [R + 1]; ``scale`` float32 [n_adapters], ``rank`` int64 [n_adapters]
+    or None; ``base`` (T, N) or None and ``y`` (T, N), float32 or bfloat16 each (``y`` may be
+    ``base``).  The workspace is allocated here with torch when not given."""
+    import torch
+    T, R, n, H, N, r, dev = _lora_set(x, A, B, adapter, req_start, scale, rank)
+    kinds = (torch.float32, torch.bfloat16)
+    ldb = N if base is None else _rows_of(base, "base", kinds, T, N, dev)
+    ldy = _rows_of(y, "y", kinds, T, N, dev)
+    with _Launch(dev, stream) as at:
+        ws, wbytes = at.workspace(workspace, lx_lora_forward_workspace_bytes(T, R, H, N, r))
+        _check(lib.lx_lora_forward(_ptr(x), _rows2d(x, "x")[2], _ptr(A), _ptr(B), _ptr(adapter), _ptr(req_start),
+                                   _ptr(scale), _ptr(rank), T, R, n, H, N, r, _ptr(base), ldb,
+                                   LX_F32 if base is None else _dtype_code(base), _ptr(y), ldy, _dtype_code(y),
+                                   _ptr(ws), wbytes, at.ptr), "lx_lora_forward")
+
+
+def lx_lora_backward(grad_y, x, A, B, adapter, req_start, scale, rank, base, grad_x, grad_A, grad_B, workspace=None,
+                     stream=None) -> None:
+    """The gradients of lx_lora_forward: ``grad_y`` (T, N) bfloat16 and its inputs, into
+    ``grad_x`` (T, H) (``base`` or 0 added; may be ``base``), ``grad_A`` and ``grad_B`` (as A
+    and B), float32, each or None; grad_A and grad_B are overwritten."""
+    import torch
+    T, R, n, H, N, r, dev = _lora_set(x, A, B, adapter, req_start, scale, rank)
+    f32 = (torch.float32,)
+    lddy = _bf16_rows(grad_y, "grad_y", T, N, dev)
+    ldb = H if base is None else _rows_of(base, "base", f32, T, H, dev)
+    ldgx = H if grad_x is None else _rows_of(grad_x, "grad_x", f32, T, H, dev)
+    if grad_A is not None:
+        _arg(grad_A, "grad_A", torch.float32, (n, r, H), dev)
+    if grad_B is not None:
+        _arg(grad_B, "grad_B", torch.float32, (n, N, r), dev)
+    with _Launch(dev, stream) as at:
+        ws, wbytes = at.workspace(workspace, lx_lora_backward_workspace_bytes(T, R, n, H, N, r))
+        _check(lib.lx_lora_backward(_ptr(grad_y), lddy, _ptr(x), _rows2d(x, "x")[2], _ptr(A), _ptr(B), _ptr(adapter),
+                                    _ptr(req_start), _ptr(scale), _ptr(rank), T, R, n, H, N, r, _ptr(base), ldb,
+                                    _ptr(grad_x), ldgx, _ptr(grad_A), _ptr(grad_B), _ptr(ws), wbytes, at.ptr),
+               "lx_lora_backward")
+
+
 __all__ = [
     "LxError", "lib", "LIB_PATH", "LX_OK", "LX_ERR_INVALID_ARG", "LX_ERR_UNSUPPORTED_DTYPE", "LX_ERR_ALIAS",
     "LX_ERR_WORKSPACE", "LX_ERR_HIP", "LX_F32", "LX_BF16", "LX_F16", "lx_status_string", "lx_abi_version",
@@ -510,7 +602,8 @@ __all__ = [
     "lx_vp_stats_floats", "lx_ce_tvd_vp_stats", "lx_ce_tvd_vp_merge_stats", "lx_ce_tvd_vp_tv", "lx_ce_tvd_vp_merge_tv",
     "lx_ce_tvd_backward_shard", "lx_ce_tvd_forward_ex", "lx_ce_tvd_backward_ex", "lx_ce_tvd_forward_backward_ex",
     "lx_gemm_bf16", "lx_ce_tvd_linear_workspace_bytes", "lx_ce_tvd_linear_forward_backward",
-    "lx_draft_verify_workspace_bytes", "lx_draft_verify",
+    "lx_draft_verify_workspace_bytes", "lx_draft_verify", "lx_lora_forward_workspace_bytes", "lx_lora_forward",
+    "lx_lora_backward_workspace_bytes", "lx_lora_backward",
 ]
 
 

@@ -7,6 +7,7 @@
 #include "gemm.hpp"
 #include "launch.hpp"
 #include "linear.hpp"
+#include "lora.hpp"
 #include "lx_ce_tvd.h"
 #include "verify.hpp"
 
@@ -300,6 +301,22 @@ lx_status forward_backward_impl(Tensor zs, Tensor us, const int64_t* target, int
   b.vec = (same_mod16(grad, ldg, zs.p, zs.ld, BT, es) && (!has_t || same_mod16(us.p, us.ld, zs.p, zs.ld, BT, es)))
               ? 1 : 0;
   return from_hip(lx::launch_backward(b, dt_of(dt), st));
+}
+
+// Sizes that the low-rank adapters take: operand rows of whole 16 bytes, grids and
+// tables within int32.
+bool lora_shape_ok(int64_t T, int64_t R, int64_t n, int64_t H, int64_t N, int64_t r) {
+  if (T < 0 || T > (1 << 22) || R < 0 || R > (1 << 24) || n < 1 || n > (1 << 20)) return false;
+  if (H < 8 || H % 8 || H > lx::kGemmMaxLd || N < 8 || N % 8 || N > lx::kGemmMaxLd) return false;
+  if (r < 8 || r % 8 || r > lx::kLoraMaxRank) return false;
+  return n * (r / 8) * ((H + N) / 8) <= (int64_t)INT_MAX;
+}
+bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld % 8 == 0 && ld <= lx::kGemmMaxLd; }
+
+// The pointers of the adapters and requests that both directions read.
+bool lora_set_ok(const lx::LoraSet& s) {
+  return s.A && s.B && s.adapter && s.start && s.scale && aligned(s.A, 16) && aligned(s.B, 16) && aligned(s.adapter, 8) &&
+         aligned(s.start, 8) && aligned(s.scale, 4) && aligned(s.rank, 8);
 }
 
 }  // namespace
@@ -687,6 +704,92 @@ lx_status lx_draft_verify(const void* target, int64_t ld_target, const void* dra
   a.logprobs = logprobs;
   a.workspace = workspace;
   return from_hip(lx::launch_verify(a, dt_of(dt), static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ low-rank adapters
+
+size_t lx_lora_forward_workspace_bytes(int64_t T, int64_t R, int64_t H, int64_t N, int64_t r) {
+  if (!lora_shape_ok(T, R, 1, H, N, r) || T == 0 || R == 0) return 0;
+  return lx::lora_forward_workspace_bytes(T, R, H, N, r);
+}
+
+lx_status lx_lora_forward(const void* x, int64_t ldx, const void* A, const void* B, const int64_t* adapter,
+                          const int64_t* req_start, const float* scale, const int64_t* rank, int64_t T, int64_t R,
+                          int64_t n_adapters, int64_t H, int64_t N, int64_t r, const void* base, int64_t ld_base,
+                          lx_dtype base_dt, void* y, int64_t ldy, lx_dtype y_dt, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if ((y_dt != LX_F32 && y_dt != LX_BF16) || (base && base_dt != LX_F32 && base_dt != LX_BF16))
+    return LX_ERR_UNSUPPORTED_DTYPE;
+  if (!lora_shape_ok(T, R, n_adapters, H, N, r)) return LX_ERR_INVALID_ARG;
+  if (T == 0 || R == 0) return LX_OK;
+  const lx::LoraSet s{static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scale, rank, adapter,
+                      req_start, T, R, n_adapters, H, N, r};
+  if (!ld_ok(ldx, H) || !ld_ok(ldy, N) || (base && !ld_ok(ld_base, N))) return LX_ERR_INVALID_ARG;
+  if (!x || !y || !lora_set_ok(s) || !aligned(x, 16) || !aligned(y, 16) || !aligned(base, 16)) return LX_ERR_INVALID_ARG;
+  const size_t need = lx::lora_forward_workspace_bytes(T, R, H, N, r);
+  const int ys = esize_of(y_dt), bs = base ? esize_of(base_dt) : 0;
+  const Span out[2] = {span(y, strided_bytes(T, N, ldy, ys)), span(workspace, (int64_t)need)};
+  const Span ins[7] = {span(x, strided_bytes(T, H, ldx, 2)), span(A, n_adapters * r * H * 2),
+                       span(B, n_adapters * r * N * 2), span(adapter, R * 8), span(req_start, (R + 1) * 8),
+                       span(scale, n_adapters * 4), span(rank, n_adapters * 8)};
+  const Span sb = span(base, base ? strided_bytes(T, N, ld_base, bs) : 0);
+  for (int o = 0; o < 2; ++o)
+    for (int i = 0; i < 7; ++i)
+      if (overlaps(out[o], ins[i])) return LX_ERR_ALIAS;
+  // y may be base itself (every element is read before it is written)
+  const bool in_place = base == y && base_dt == y_dt && ld_base == ldy;
+  if ((!in_place && overlaps(out[0], sb)) || overlaps(out[1], sb) || overlaps(out[0], out[1])) return LX_ERR_ALIAS;
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
+  const lx::LoraForwardArgs a{s, static_cast<const uint16_t*>(x), ldx, base, ld_base, dt_of(base_dt), y, ldy,
+                              dt_of(y_dt), workspace};
+  return from_hip(lx::launch_lora_forward(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t lx_lora_backward_workspace_bytes(int64_t T, int64_t R, int64_t n_adapters, int64_t H, int64_t N, int64_t r) {
+  if (!lora_shape_ok(T, R, n_adapters, H, N, r) || T == 0 || R == 0) return 0;
+  return lx::lora_backward_workspace_bytes(T, R, n_adapters, H, N, r);
+}
+
+lx_status lx_lora_backward(const void* grad_y, int64_t ld_grad_y, const void* x, int64_t ldx, const void* A,
+                           const void* B, const int64_t* adapter, const int64_t* req_start, const float* scale,
+                           const int64_t* rank, int64_t T, int64_t R, int64_t n_adapters, int64_t H, int64_t N,
+                           int64_t r, const float* base, int64_t ld_base, float* grad_x, int64_t ld_grad_x,
+                           float* grad_A, float* grad_B, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!lora_shape_ok(T, R, n_adapters, H, N, r) || (!grad_x && !grad_A && !grad_B)) return LX_ERR_INVALID_ARG;
+  if (!grad_x) base = nullptr;
+  if (!aligned(grad_x, 16) || !aligned(grad_A, 16) || !aligned(grad_B, 16) || !aligned(base, 16))
+    return LX_ERR_INVALID_ARG;
+  const lx::LoraSet s{static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scale, rank, adapter,
+                      req_start, T, R, n_adapters, H, N, r};
+  const bool any = T > 0 && R > 0;
+  size_t need = 0;
+  if (any) {
+    if (!ld_ok(ld_grad_y, N) || !ld_ok(ldx, H) || (grad_x && !ld_ok(ld_grad_x, H)) || (base && !ld_ok(ld_base, H)))
+      return LX_ERR_INVALID_ARG;
+    if (!grad_y || !x || !lora_set_ok(s) || !aligned(grad_y, 16) || !aligned(x, 16)) return LX_ERR_INVALID_ARG;
+    need = lx::lora_backward_workspace_bytes(T, R, n_adapters, H, N, r);
+    const Span out[4] = {span(grad_x, grad_x ? strided_bytes(T, H, ld_grad_x, 4) : 0),
+                         span(grad_A, n_adapters * r * H * 4), span(grad_B, n_adapters * r * N * 4),
+                         span(workspace, (int64_t)need)};
+    const Span ins[8] = {span(grad_y, strided_bytes(T, N, ld_grad_y, 2)), span(x, strided_bytes(T, H, ldx, 2)),
+                         span(A, n_adapters * r * H * 2), span(B, n_adapters * r * N * 2), span(adapter, R * 8),
+                         span(req_start, (R + 1) * 8), span(scale, n_adapters * 4), span(rank, n_adapters * 8)};
+    const Span sb = span(base, base ? strided_bytes(T, H, ld_base, 4) : 0);
+    // grad_x may be base itself
+    const bool in_place = base == grad_x && ld_base == ld_grad_x;
+    for (int o = 0; o < 4; ++o) {
+      for (int i = 0; i < 8; ++i)
+        if (overlaps(out[o], ins[i])) return LX_ERR_ALIAS;
+      if (!(o == 0 && in_place) && overlaps(out[o], sb)) return LX_ERR_ALIAS;
+    }
+    if (any_overlap(out, 4)) return LX_ERR_ALIAS;
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
+  } else if (overlaps(span(grad_A, n_adapters * r * H * 4), span(grad_B, n_adapters * r * N * 4))) {
+    return LX_ERR_ALIAS;
+  }
+  const lx::LoraBackwardArgs a{s, static_cast<const uint16_t*>(grad_y), static_cast<const uint16_t*>(x), ld_grad_y, ldx,
+                               base, ld_base, grad_x, ld_grad_x, grad_A, grad_B, workspace};
+  return from_hip(lx::launch_lora_backward(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

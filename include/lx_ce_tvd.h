@@ -538,6 +538,63 @@ lx_status lx_draft_verify(const void* target, int64_t ld_target, const void* dra
 
 /*
  * ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests at once, beside a shared projection (e.g.
+ * lx_gemm_bf16's x w^T, or the lm_head's logits), and their gradients.
+ *
+ * The T rows of x are the rows of R requests: request i is the rows
+ * req_start[i] .. req_start[i + 1] - 1 and uses adapter a = adapter[i], a scale s_a
+ * and the matrices A_a (rank_a, H) and B_a (N, rank_a).  For its rows
+ *
+ *   u = s_a x A_a^T,   y = base + u B_a^T                         (forward)
+ *   v = s_a dy B_a,    dx = base + v A_a                          (backward)
+ *   dA_a = sum v^T x,  dB_a = sum dy^T u    over the rows of every request that uses a
+ *
+ * - x (T, H), grad_y (T, N): bf16, row strides ldx, ld_grad_y.
+ * - A (n_adapters, r, H), B (n_adapters, N, r): bf16, contiguous, stacked.  Adapter a
+ *   uses the first rank[a] of the r ranks there is room for (rank NULL: all r; values
+ *   are clamped to [0, r]); what lies beyond is not used and may be anything.
+ * - scale float[n_adapters]; rank int64[n_adapters] or NULL.
+ * - adapter int64[R]: an id in [0, n_adapters); several requests may share one.
+ *   Negative: no adapter (y = base, dx = base; base NULL: 0).  n_adapters or more is a
+ *   caller error the device cannot report: the request's rows of y or grad_x are NaN, and
+ *   it takes no part in grad_A and grad_B.
+ * - req_start int64[R + 1], not decreasing; requests may be empty.  Entries are taken
+ *   within [0, T].  Rows that belong to no request are not written.
+ * - base (T, N), or (T, H) in the backward: what is added to, or NULL (0).  y may EQUAL
+ *   base (same type and row stride), and grad_x too.
+ * - y and base: LX_F32 or LX_BF16 (bf16 rounded to nearest even), each its own; grad_x,
+ *   grad_A (n_adapters, r, H) and grad_B (n_adapters, N, r) float, grad_A and grad_B
+ *   contiguous.  grad_x, grad_A, grad_B are optional (NULL: not computed), one at least is given.
+ *   grad_A and grad_B are OVERWRITTEN; ranks beyond an adapter's and adapters without rows get 0.
+ * - u and v are fp32 and enter the second products unrounded; all sums are fp32, in a fixed
+ *   order (the same bits on every call).
+ * Requirements: H, N and every row stride multiples of 8, at most 2^22; r a multiple of 8,
+ *   at most 128; T <= 2^22, R <= 2^24, 1 <= n_adapters <= 2^20; x, grad_y, A, B, base, y and
+ *   the gradients 16-byte aligned.  Any T from 1 on, any request lengths.
+ *   T == 0 or R == 0: y and grad_x are not written, grad_A and grad_B are 0.
+ * Workspace: at least lx_lora_forward_workspace_bytes(...), or
+ *   lx_lora_backward_workspace_bytes(...), bytes, 256-byte aligned, contents ignored and clobbered.
+ * Errors : LX_ERR_INVALID_ARG, LX_ERR_UNSUPPORTED_DTYPE, LX_ERR_ALIAS (an output or the
+ *   workspace overlapping anything else), LX_ERR_WORKSPACE, LX_ERR_HIP.
+ */
+size_t lx_lora_forward_workspace_bytes(int64_t T, int64_t R, int64_t H, int64_t N, int64_t r);
+
+lx_status lx_lora_forward(const void* x, int64_t ldx, const void* A, const void* B, const int64_t* adapter,
+                          const int64_t* req_start, const float* scale, const int64_t* rank, int64_t T, int64_t R,
+                          int64_t n_adapters, int64_t H, int64_t N, int64_t r, const void* base, int64_t ld_base,
+                          lx_dtype base_dt, void* y, int64_t ldy, lx_dtype y_dt, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+size_t lx_lora_backward_workspace_bytes(int64_t T, int64_t R, int64_t n_adapters, int64_t H, int64_t N, int64_t r);
+
+lx_status lx_lora_backward(const void* grad_y, int64_t ld_grad_y, const void* x, int64_t ldx, const void* A,
+                           const void* B, const int64_t* adapter, const int64_t* req_start, const float* scale,
+                           const int64_t* rank, int64_t T, int64_t R, int64_t n_adapters, int64_t H, int64_t N,
+                           int64_t r, const float* base, int64_t ld_base, float* grad_x, int64_t ld_grad_x,
+                           float* grad_A, float* grad_B, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Reference streams: the practical HBM ceilings the loss kernels are measured
  * against (not part of the loss).  They move bytes the way the loss kernels
  * do: 16-byte buffer loads and stores with the streamed-once cache policy.
