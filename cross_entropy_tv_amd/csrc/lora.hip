@@ -41,7 +41,9 @@ typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kLThreads = 256;
 constexpr int kTileRows = 32;    // rows of a tile of the matrix-core kernels
-constexpr int kDownK = 128;      // k that a wave of the down kernel takes at once
+constexpr int kDownThreads = 512;
+constexpr int kDownWaves = kDownThreads / 64;
+constexpr int kDownK = 64;       // k that a wave of the down kernel takes at once
 constexpr int kMaxSplits = 16;
 
 __device__ __forceinline__ f32x4_t mfma(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
@@ -143,6 +145,38 @@ __device__ __forceinline__ void load_low(const float* P, int splits, int64_t pla
 
 // ------------------------------------------------------------------ down: P = X M^T
 
+// u or v as the other products take it: its three bf16 terms along the ranks, U[t][term][r],
+// and along the rows, W[term][rank][Tp]; either may be nullptr.  vals: the fp32 values of
+// rows t0 .. t0 + 31 (rows behind T: 0), NT threads.
+struct Terms {
+  uint16_t *U, *W;
+  int64_t Tp;
+};
+constexpr int kValStride = kLoraMaxRank + 1;
+template <int NT>
+__device__ __forceinline__ void emit_terms(const Terms& o, const float* vals, int64_t t0, int64_t T, int r) {
+  const int r8 = r / 8;
+  if (o.U) {
+    for (int i = tid_x(); i < kTileRows * 3 * r8; i += NT) {
+      const int row = i / (3 * r8), c = i - row * (3 * r8), tm = c / r8, k0 = (c - tm * r8) * 8;
+      if (t0 + row >= T) break;
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = vals[row * kValStride + k0 + k];
+      *reinterpret_cast<u32x4_t*>(o.U + ((t0 + row) * 3 + tm) * r + k0) = terms8(v, tm);
+    }
+  }
+  if (o.W) {
+    for (int i = tid_x(); i < 3 * r * (kTileRows / 8); i += NT) {
+      const int t8 = i % (kTileRows / 8) * 8, c = i / (kTileRows / 8), tm = c / r, rho = c - tm * r;
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = vals[(t8 + k) * kValStride + rho];
+      *reinterpret_cast<u32x4_t*>(o.W + ((int64_t)tm * r + rho) * o.Tp + t0 + t8) = terms8(v, tm);
+    }
+  }
+}
+
 struct DownArgs {
   LoraSet s;
   const uint16_t* X;  // (T, K)
@@ -152,86 +186,142 @@ struct DownArgs {
   float* P;  // [splits][T][r]
   int splits;
   int64_t kslice;  // k of a split, a multiple of kDownK
+  Terms o;  // tile kernel with one split: where the result goes
 };
 
-// Long requests: a workgroup per (tile of 32 rows, split of K); its four waves take the
-// 128-k chunks of the split in turn and add up in LDS.  In a chunk a lane holds 32
-// consecutive k (64 bytes) of its row, so that four MFMAs use whole lines: their k's are
-// permuted alike in both operands.  RB: blocks of 16 ranks.
+// Long requests: a workgroup per (tile of 32 rows, split of K); its eight waves take the 64-k
+// chunks of the split in turn, each chunk requested while the one before it is multiplied, and
+// add up in LDS.  In a chunk a lane holds 16 consecutive k (32 bytes) of its row, so that the
+// four lanes of a row read whole lines: the k's of the two MFMAs are permuted alike in both
+// operands.  With one split the workgroup finishes u itself (scale, rank, terms); with several
+// it leaves its partial sums for lora_terms_kernel.  RB: blocks of 16 ranks.
 template <int RB>
-__global__ __launch_bounds__(kLThreads) void lora_down_tile_kernel(DownArgs g) {
-  __shared__ float red[3][2 * RB * 4][64];
+struct DownChunk {
+  u32x4_t x[2][2], m[RB][2];
+};
+template <int RB>
+__device__ __forceinline__ void load_chunk(DownChunk<RB>& v, const uint16_t* X, const uint32_t (&xrow)[2],
+                                           const uint16_t* M, const uint32_t (&mrow)[RB], uint32_t k, uint32_t ke) {
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const bool in = k + 8 * j < ke;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v.x[h][j] = in ? load16(X + (xrow[h] + k + 8 * j)) : zero;
+#pragma unroll
+    for (int b = 0; b < RB; ++b) v.m[b][j] = in ? load16(M + (mrow[b] + k + 8 * j)) : zero;
+  }
+}
+template <int RB>
+__device__ __forceinline__ void mul_chunk(f32x4_t (&acc)[2][RB], const DownChunk<RB>& v) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int b = 0; b < RB; ++b) acc[h][b] = mfma(v.x[h][j], v.m[b][j], acc[h][b]);
+}
+
+template <int RB>
+__global__ __launch_bounds__(kDownThreads) void lora_down_tile_kernel(DownArgs g) {
+  // each wave's sums of 32 rows x 16 RB ranks, two waves at a time in turn for RB = 8
+  __shared__ float red[RB == 8 ? 4 : 8][kTileRows * 16 * RB];
+  __shared__ float vals[kTileRows * kValStride];
   const LoraSet& s = g.s;
-  const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
+  const int tid = tid_x(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int split = (int)(bid_x() % (unsigned)g.splits);
   const int64_t r0 = (int64_t)(bid_x() / (unsigned)g.splits) * kTileRows;
   const int64_t r1 = r0 + kTileRows < s.T ? r0 + kTileRows : s.T;
   const int64_t kb = split * g.kslice, ke = kb + g.kslice < g.K ? kb + g.kslice : g.K;
-  const int c16 = lane & 15, q = lane >> 4;
-  float* P = g.P + split * s.T * s.r;
-  const uint16_t* xrow[2];
+  const int c16 = lane & 15, q = lane >> 4, r = (int)s.r;
+  const bool whole = g.splits == 1;
+  // the tile's rows and an adapter's M lie within 2^30 bytes: 32-bit offsets from uniform bases
+  const uint16_t* X = g.X + r0 * g.ldx;
+  uint32_t xrow[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int64_t row = r0 + 16 * h + c16;
-    xrow[h] = g.X + (row < s.T ? row : s.T - 1) * g.ldx;
+    const int64_t row = 16 * h + c16;
+    xrow[h] = (uint32_t)((r0 + row < s.T ? row : s.T - 1 - r0) * g.ldx);
   }
+  if (whole)
+    for (int i = tid; i < kTileRows * kValStride; i += kDownThreads) vals[i] = 0.0f;
   for (int i = max(find_request(s.start, (int)s.R, r0), 0); i < s.R && s.start[i] < r1; ++i) {
     const Part p = part_of(s, i, r0, r1);
     if (p.hi <= p.lo || p.adapter < 0) continue;
-    const uint16_t* mrow[RB];
+    const uint16_t* M = g.M + (int64_t)p.adapter * r * g.K;
+    uint32_t mrow[RB];
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
       const int rho = 16 * b + c16;
-      mrow[b] = g.M + ((int64_t)p.adapter * s.r + (rho < s.r ? rho : (int)s.r - 1)) * g.K;
+      mrow[b] = (uint32_t)((rho < r ? rho : r - 1) * g.K);
     }
     f32x4_t acc[2][RB];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int b = 0; b < RB; ++b) acc[h][b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    for (int64_t k0 = kb + wave * kDownK; k0 < ke; k0 += 4 * kDownK) {
-      const int64_t k = k0 + 32 * q;
-      const u32x4_t zero = {0u, 0u, 0u, 0u};
-      u32x4_t xv[2][4], mv[RB][4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = k + 8 * j < ke;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) xv[h][j] = in ? load16(xrow[h] + k + 8 * j) : zero;
-#pragma unroll
-        for (int b = 0; b < RB; ++b) mv[b][j] = in ? load16(mrow[b] + k + 8 * j) : zero;
+    {
+      // (chunks past the split's end load nothing and multiply zeros)
+      constexpr uint32_t kStep = kDownWaves * kDownK;
+      const uint32_t lane_k = 16 * q, end = (uint32_t)ke;
+      DownChunk<RB> c0, c1;
+      uint32_t k0 = (uint32_t)kb + wave * kDownK;
+      if (RB < 8) {
+        load_chunk<RB>(c0, X, xrow, M, mrow, k0 + lane_k, end);
+        for (; k0 < end; k0 += 2 * kStep) {
+          load_chunk<RB>(c1, X, xrow, M, mrow, k0 + kStep + lane_k, end);
+          mul_chunk<RB>(acc, c0);
+          load_chunk<RB>(c0, X, xrow, M, mrow, k0 + 2 * kStep + lane_k, end);
+          mul_chunk<RB>(acc, c1);
+        }
+      } else {
+        // (128 ranks: two chunks at once would not fit the registers)
+        for (; k0 < end; k0 += kStep) {
+          load_chunk<RB>(c0, X, xrow, M, mrow, k0 + lane_k, end);
+          mul_chunk<RB>(acc, c0);
+        }
       }
+    }
+    const int rank = rank_of(s, p.adapter);
+    const float scale = s.scale[p.adapter];
+    constexpr int kRounds = RB == 8 ? 2 : 1, kPer = kDownWaves / kRounds;
+    float sum[(kTileRows * 16 * RB + kDownThreads - 1) / kDownThreads];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+    for (int round = 0; round < kRounds; ++round) {
+      __syncthreads();  // (what was there has been read)
+      if (wave / kPer == round) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int b = 0; b < RB; ++b) acc[h][b] = mfma(xv[h][j], mv[b][j], acc[h][b]);
+          for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[wave % kPer][((h * RB + b) * 4 + e) * 64 + lane] = acc[h][b][e];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < kTileRows * 16 * RB / kDownThreads; ++n) {
+        const int f = n * kDownThreads + tid;
+        float v = round ? sum[n] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v += red[k][f];
+        sum[n] = v;
+      }
     }
-    __syncthreads();  // (the previous request's sums have been read)
-    if (wave > 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) red[wave - 1][(h * RB + b) * 4 + e][lane] = acc[h][b][e];
+    for (int n = 0; n < kTileRows * 16 * RB / kDownThreads; ++n) {
+      // place f of a wave's sums: register (h, b, e) of lane l
+      const int f = n * kDownThreads + tid, l = f & 63, e = (f >> 6) & 3, b = (f >> 8) % RB, h = (f >> 8) / RB;
+      const int row = 16 * h + 4 * (l >> 4) + e, rho = 16 * b + (l & 15);
+      const int64_t t = r0 + row;
+      if (t >= p.lo && t < p.hi && rho < r) {
+        if (whole) vals[row * kValStride + rho] = rho < rank ? scale * sum[n] : 0.0f;
+        else g.P[((int64_t)split * s.T + t) * r + rho] = sum[n];
+      }
     }
+  }
+  if (whole) {
     __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int f = (h * RB + b) * 4 + e;
-            const float v = acc[h][b][e] + red[0][f][lane] + red[1][f][lane] + red[2][f][lane];
-            const int64_t t = r0 + 16 * h + 4 * q + e;
-            const int rho = 16 * b + c16;
-            if (t >= p.lo && t < p.hi && rho < s.r) P[t * s.r + rho] = v;
-          }
-    }
+    emit_terms<kDownThreads>(g.o, vals, r0, s.T, r);
   }
 }
 
@@ -275,8 +365,9 @@ __global__ __launch_bounds__(kLThreads) void lora_down_row_kernel(DownArgs g) {
 
 struct UpArgs {
   LoraSet s;
-  const float* P;  // [splits][T][r]
+  const float* P;  // single rows: [splits][T][r]
   int splits;
+  const uint16_t* U;  // tiles: terms [T][3][r]
   const uint16_t* M;  // (n, C, r)
   int64_t C;
   bool m_clean;  // M is 0 beyond an adapter's rank (else what lies there is not used)
@@ -301,15 +392,16 @@ __device__ __forceinline__ void store4(uint16_t* p, const f32x4_t& v) {
 __device__ __forceinline__ void nan4(float* p) { *reinterpret_cast<uint4*>(p) = make_uint4(kQNaN32, kQNaN32, kQNaN32, kQNaN32); }
 __device__ __forceinline__ void nan4(uint16_t* p) { *reinterpret_cast<uint2*>(p) = make_uint2(kQNaN16 * 0x10001u, kQNaN16 * 0x10001u); }
 
-// Long requests: a wave per (tile of 32 rows, steps x 64 columns).  K is the ranks three
-// times over (hi, mid, lo terms of P), in chunks of 8: chunk c is term c / (r / 8) of
-// ranks 8 (c mod r / 8) .. + 7, so r = 16 takes two MFMAs and not three half-empty ones.
-// The tile's P terms stay in registers; M's rows are read once per tile.  Column block b
-// of a step holds columns 4 (l % 16) + b, so that a lane ends with four consecutive
-// columns: whole 256-byte (fp32) or 128-byte (bf16) pieces of 4 rows per access.
-// NM: MFMAs of a product, ceil(3 r / 32).
-template <int NM, typename YT, typename BT, bool BASE>
-__global__ __launch_bounds__(kLThreads) void lora_up_tile_kernel(UpArgs g) {
+// Long requests: a wave per (tile of 32 rows, steps x 64 columns).  The tile's terms of P
+// (U[t][term][r]) stay in registers; a block of M is read once and multiplied by the terms
+// one after the other.  With r = 16 the four k-groups of an MFMA are two terms of the 16
+// ranks, with r = 8 all three: TM terms an MFMA each, LD blocks of 32 / (terms in an MFMA)
+// ranks.  Column block b of a step holds columns 4 (l % 16) + b, so that a lane ends with
+// four consecutive columns: whole 256-byte (fp32) or 128-byte (bf16) pieces of 4 rows per
+// access.
+template <int LD, int TM, typename YT, typename BT, bool BASE>
+__global__ __attribute__((amdgpu_flat_work_group_size(kLThreads, kLThreads), amdgpu_waves_per_eu(2)))
+void lora_up_tile_kernel(UpArgs g) {
   const LoraSet& s = g.s;
   const int lane = tid_x() & 63, wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6);
   const int r = (int)s.r, r8 = r / 8;
@@ -320,67 +412,101 @@ __global__ __launch_bounds__(kLThreads) void lora_up_tile_kernel(UpArgs g) {
   const int64_t r0 = (int64_t)(bid_x() / nch) * kTileRows;
   const int64_t r1 = r0 + kTileRows < s.T ? r0 + kTileRows : s.T;
   const int c16 = lane & 15, q = lane >> 4;
-  int ck[NM];  // first rank of this lane's chunk
+  // this lane's chunk of 8 ranks in block l (-1: none), and its term in MFMA j
+  int ck[LD], term0;
+  if (TM == 1) {
+    ck[0] = 0;
+    term0 = q;
+  } else if (TM == 2) {
+    ck[0] = (q & 1) * 8;
+    term0 = q >> 1;
+  } else {
+    term0 = 0;
 #pragma unroll
-  for (int m = 0; m < NM; ++m) ck[m] = (4 * m + q) % r8 * 8;
-  YT* Y = static_cast<YT*>(g.y);
-  const BT* base = static_cast<const BT*>(g.base);
+    for (int l = 0; l < LD; ++l) ck[l] = 4 * l + q < r8 ? (4 * l + q) * 8 : -1;
+  }
+  // the tile's rows and an adapter's M lie within 2^30 bytes: 32-bit offsets from uniform bases
+  YT* Y = static_cast<YT*>(g.y) + r0 * g.ldy;
+  const BT* base = static_cast<const BT*>(g.base) + (BASE ? r0 * g.ldb : 0);
+  const uint16_t* U = g.U + r0 * 3 * r;
+  const uint32_t ldy = (uint32_t)g.ldy, ldb = (uint32_t)g.ldb, C = (uint32_t)g.C;
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
   for (int i = max(find_request(s.start, (int)s.R, r0), 0); i < s.R && s.start[i] < r1; ++i) {
     const Part p = part_of(s, i, r0, r1);
     if (p.hi <= p.lo) continue;
     const bool some = p.adapter >= 0;
     const int rank = some ? rank_of(s, p.adapter) : 0;
-    u32x4_t u[2][NM];
+    const int lo = (int)(p.lo - r0), hi = (int)(p.hi - r0);
+    u32x4_t u[2][LD][TM];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t t = r0 + 16 * h + c16;
-      const bool in = some && t >= p.lo && t < p.hi;
+      const int row = 16 * h + c16;
+      const bool in = rank > 0 && row >= lo && row < hi;
 #pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        u[h][m] = (u32x4_t){0u, 0u, 0u, 0u};
-        const int tm = (4 * m + q) / r8;
-        if (in && tm < 3) {
-          float v[8];
-          load_low(g.P, g.splits, s.T * s.r, t, r, ck[m], rank, s.scale[p.adapter], v);
-          u[h][m] = terms8(v, tm);
+      for (int l = 0; l < LD; ++l)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          const int tm = TM == 2 ? 2 * j + term0 : TM == 1 ? term0 : j;
+          u[h][l][j] = in && tm < 3 && ck[l] >= 0 ? load16(U + (uint32_t)((row * 3 + tm) * r + ck[l])) : zero;
         }
-      }
     }
     const uint16_t* M = g.M + (some ? (int64_t)p.adapter * g.C * r : 0);
     const bool mask = !g.m_clean && rank < r;
-    for (int64_t n = n0; n < n1; n += 64) {
-      const int64_t col = n + 4 * c16;
+    for (uint32_t n = (uint32_t)n0; n < (uint32_t)n1; n += 64) {
+      const uint32_t col = n + 4 * c16;
+      u32x4_t w[4][LD];
+      if (rank > 0) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t row = (col + b < C ? col + b : C - 1) * (uint32_t)r;
+#pragma unroll
+          for (int l = 0; l < LD; ++l) w[b][l] = ck[l] >= 0 ? load16(M + (row + ck[l])) : zero;
+        }
+      }
+      f32x4_t old[2][4];
+      if (BASE) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = 16 * h + 4 * q + e;
+            if (col < C && row >= lo && row < hi) old[h][e] = load4(base + (row * ldb + col));
+          }
+      }
       f32x4_t acc[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int b = 0; b < 4; ++b) acc[h][b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
       if (rank > 0) {
+        if (mask) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint16_t* row = M + (col + b < g.C ? col + b : g.C - 1) * r;
+          for (int b = 0; b < 4; ++b)
 #pragma unroll
-          for (int m = 0; m < NM; ++m) {
-            u32x4_t w = load16(row + ck[m]);
-            if (mask) w = keep_below(w, ck[m], rank);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) acc[h][b] = mfma(u[h][m], w, acc[h][b]);
-          }
+            for (int l = 0; l < LD; ++l) w[b][l] = keep_below(w[b][l], ck[l], rank);
         }
+#pragma unroll
+        for (int l = 0; l < LD; ++l)
+#pragma unroll
+          for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) acc[h][b] = mfma(u[h][l][j], w[b][l], acc[h][b]);
       }
-      if (col < g.C) {
+      if (col < C) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int64_t t = r0 + 16 * h + 4 * q + e;
-            if (t >= p.lo && t < p.hi) {
+            const int row = 16 * h + 4 * q + e;
+            if (row >= lo && row < hi) {
               if (p.adapter == kBadAdapter) {
-                nan4(Y + t * g.ldy + col);
+                nan4(Y + (row * ldy + col));
               } else {
                 f32x4_t v = {acc[h][0][e], acc[h][1][e], acc[h][2][e], acc[h][3][e]};
-                if (BASE) v += load4(base + t * g.ldb + col);
-                store4(Y + t * g.ldy + col, v);
+                if (BASE) v += old[h][e];
+                store4(Y + (row * ldy + col), v);
               }
             }
           }
@@ -389,66 +515,70 @@ __global__ __launch_bounds__(kLThreads) void lora_up_tile_kernel(UpArgs g) {
   }
 }
 
-// Requests of a few rows: a workgroup per (row, 256 columns).  G lanes share a column
-// (G the power of two from r / 8 on), each with 8 ranks; in step j of G the wave takes 64 / G columns
-// and lane j of each group keeps the sum, so a wave ends with 64 consecutive columns.
+// Requests of a few rows: a wave per (row, steps x 64 columns).  G lanes share a column (G
+// the power of two from r / 8 on), each with 8 ranks; in step j of G the wave takes 64 / G
+// columns and lane j of each group keeps the sum, so 64 consecutive columns come out at once.
+// Workgroups go column range by column range, and the rows of one range on one die (id mod
+// 8), so that rows with the same adapter find its part of M in that die's L2.
 template <int G, typename YT, typename BT, bool BASE>
 __global__ __launch_bounds__(kLThreads) void lora_up_row_kernel(UpArgs g) {
   const LoraSet& s = g.s;
   const int lane = tid_x() & 63, wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6);
-  const unsigned nch = (unsigned)((g.C + 255) / 256);
-  const int64_t t = bid_x() / nch;
-  const int64_t n0 = (int64_t)(bid_x() % nch) * 256 + wave * 64;
+  const unsigned die = bid_x() % 8u, on_die = bid_x() / 8u;
+  const int64_t t = on_die % (unsigned)s.T;
+  const int64_t ch = (int64_t)(on_die / (unsigned)s.T) * 8 + die;
+  const int64_t n0 = (ch * 4 + wave) * 64 * g.steps;
   if (n0 >= g.C) return;
+  const int64_t n1 = n0 + 64 * g.steps < g.C ? n0 + 64 * g.steps : g.C;
   const int i = find_request(s.start, (int)s.R, t);
   if (i < 0) return;
   const Part p = part_of(s, i, t, t + 1);
   if (p.hi <= p.lo) return;
   const int j0 = lane & (G - 1), cl = lane / G;
-  const int64_t mine = n0 + j0 * (64 / G) + cl;  // this lane's column in the end
   YT* y = static_cast<YT*>(g.y) + t * g.ldy;
-  if (p.adapter == kBadAdapter) {
-    if (mine < g.C) store_bits1(y + mine, kQNaN32);
-    return;
-  }
-  float out = 0.0f;
-  if (BASE && mine < g.C) out = load1(static_cast<const BT*>(g.base) + t * g.ldb + mine);
   const int rank = p.adapter >= 0 ? rank_of(s, p.adapter) : 0;
-  if (rank > 0) {
-    const int r = (int)s.r, k0 = j0 * 8;
-    const bool live = k0 < rank;
-    float u[8];
+  const int r = (int)s.r, k0 = j0 * 8;
+  const bool live = k0 < rank;
+  float u[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] = 0.0f;
-    if (live) load_low(g.P, g.splits, s.T * s.r, t, r, k0, rank, s.scale[p.adapter], u);
-    const uint16_t* M = g.M + (int64_t)p.adapter * g.C * r + (live ? k0 : 0);
-    const bool mask = !g.m_clean && live && k0 + 8 > rank;
-    float sums[G];
+  for (int e = 0; e < 8; ++e) u[e] = 0.0f;
+  if (live) load_low(g.P, g.splits, s.T * s.r, t, r, k0, rank, s.scale[p.adapter], u);
+  const uint16_t* M = g.M + (live ? (int64_t)p.adapter * g.C * r + k0 : 0);
+  const bool mask = !g.m_clean && live && k0 + 8 > rank;
+  for (int64_t n = n0; n < n1; n += 64) {
+    const int64_t mine = n + j0 * (64 / G) + cl;  // this lane's column in the end
+    float out = 0.0f;
+    if (BASE && mine < g.C) out = load1(static_cast<const BT*>(g.base) + t * g.ldb + mine);
+    if (rank > 0) {
+      u32x4_t w[G];
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const int64_t n = n0 + j * (64 / G) + cl;
-      u32x4_t w = load16(M + (n < g.C ? n : g.C - 1) * r);
-      if (mask) w = keep_below(w, k0, rank);
-      const unsigned wv[4] = {w.x, w.y, w.z, w.w};
-      float a = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        a = __builtin_fmaf(u[2 * e], __uint_as_float(wv[e] << 16), a);
-        a = __builtin_fmaf(u[2 * e + 1], __uint_as_float(wv[e] & 0xffff0000u), a);
+      for (int j = 0; j < G; ++j) {
+        const int64_t c = n + j * (64 / G) + cl;
+        w[j] = load16(M + (c < g.C ? c : g.C - 1) * r);
       }
-      sums[j] = live ? a : 0.0f;
-    }
-    float add = 0.0f;
+      float add = 0.0f;
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      float a = sums[j];
+      for (int j = 0; j < G; ++j) {
+        if (mask) w[j] = keep_below(w[j], k0, rank);
+        const unsigned wv[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        float a = 0.0f;
 #pragma unroll
-      for (int off = G / 2; off >= 1; off >>= 1) a += __shfl_xor(a, off, 64);
-      if (j == j0) add = a;
+        for (int e = 0; e < 4; ++e) {
+          a = __builtin_fmaf(u[2 * e], __uint_as_float(wv[e] << 16), a);
+          a = __builtin_fmaf(u[2 * e + 1], __uint_as_float(wv[e] & 0xffff0000u), a);
+        }
+        a = live ? a : 0.0f;
+#pragma unroll
+        for (int off = G / 2; off >= 1; off >>= 1) a += __shfl_xor(a, off, 64);
+        if (j == j0) add = a;
+      }
+      out += add;
     }
-    out += add;
+    if (mine < g.C) {
+      if (p.adapter == kBadAdapter) store_bits1(y + mine, kQNaN32);
+      else store1(y + mine, out);
+    }
   }
-  if (mine < g.C) store1(y + mine, out);
 }
 
 // ------------------------------------------------------------------ transposed adapters, terms of u and v
@@ -493,52 +623,50 @@ __global__ __launch_bounds__(kLThreads) void lora_transpose_kernel(LoraSet s, ui
   else if (at - na < nb) transpose_block<false>(s, s.B, Bt, s.N, s.r, at - na);
 }
 
-// The three terms of s_a P along the rows: W[term][rank][Tp], 0 for rows without an adapter,
-// ranks beyond the adapter's and rows behind T.  A thread takes 8 rows of one rank.
+// The terms of s_a P from the down kernels' partial sums: a workgroup per 32 rows; 0 for rows
+// without an adapter and ranks beyond the adapter's.
 struct TermArgs {
   LoraSet s;
   const float* P;
   int splits;
-  uint16_t* W;
-  int64_t Tp;
+  Terms o;
 };
-__global__ __launch_bounds__(kLThreads) void lora_terms_kernel(TermArgs g0, TermArgs g1) {
-  const int64_t half = nblocks_x() / 2;
-  const bool second = bid_x() >= half;
+__global__ __launch_bounds__(kLThreads) void lora_terms_kernel(TermArgs g0, TermArgs g1, unsigned blocks0) {
+  __shared__ float vals[kTileRows * kValStride];
+  const bool second = bid_x() >= blocks0;
   const TermArgs& g = second ? g1 : g0;
   const LoraSet& s = g.s;
-  const int r = (int)s.r;
-  const int64_t unit = ((int64_t)bid_x() - (second ? half : 0)) * kLThreads + tid_x();
-  const int64_t t0 = unit / r * 8;
-  const int rho = (int)(unit % r);
-  // (every lane of the wave takes part in the search: one request lookup per wave, then steps along it)
-  const int64_t wave_t0 = (unit & ~(int64_t)63) / r * 8;
-  int i = find_request(s.start, (int)s.R, wave_t0 < s.T ? wave_t0 : s.T - 1);
-  if (t0 >= g.Tp || !g.W) return;
-  if (i < 0) i = 0;
-  float v[8];
+  const int r = (int)s.r, r4 = r / 4;
+  const int64_t t0 = (int64_t)(bid_x() - (second ? blocks0 : 0)) * kTileRows;
+  const int first = max(find_request(s.start, (int)s.R, t0), 0);
+  for (int n = tid_x(); n < kTileRows * r4; n += kLThreads) {
+    const int row = n / r4, k0 = (n - row * r4) * 4;
+    const int64_t t = t0 + row;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    if (t < s.T) {
+      int i = first;
+      while (i + 1 < s.R && s.start[i + 1] <= t) ++i;
+      const Part p = part_of(s, i, t, t + 1);
+      if (p.hi > p.lo && p.adapter >= 0) {
+        const int rank = rank_of(s, p.adapter);
+        const float scale = s.scale[p.adapter];
+        const float* P = g.P + t * r + k0;
+        for (int sp = 0; sp < g.splits; ++sp) v += *reinterpret_cast<const f32x4_t*>(P + sp * s.T * r);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int64_t t = t0 + k;
-    v[k] = 0.0f;
-    if (t >= s.T) continue;
-    while (i + 1 < s.R && s.start[i + 1] <= t) ++i;
-    const Part p = part_of(s, i, t, t + 1);
-    if (p.hi <= p.lo || p.adapter < 0 || rho >= rank_of(s, p.adapter)) continue;
-    float a = 0.0f;
-    for (int sp = 0; sp < g.splits; ++sp) a += g.P[((int64_t)sp * s.T + t) * r + rho];
-    v[k] = a * s.scale[p.adapter];
+        for (int k = 0; k < 4; ++k) v[k] = k0 + k < rank ? scale * v[k] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) vals[row * kValStride + k0 + k] = v[k];
   }
-#pragma unroll
-  for (int tm = 0; tm < 3; ++tm)
-    *reinterpret_cast<u32x4_t*>(g.W + ((int64_t)tm * r + rho) * g.Tp + t0) = terms8(v, tm);
+  __syncthreads();
+  emit_terms<kLThreads>(g.o, vals, t0, s.T, r);
 }
 
 // ------------------------------------------------------------------ grad: W^T X over the rows of an adapter
 
-constexpr int kGradCols = 128;  // columns of X of a workgroup (32 a wave)
+constexpr int kGradCols = 256;  // columns of X of a workgroup
 constexpr int kGradRows = 64;   // rows staged at once
-constexpr int kGradStride = 288;  // bytes of a staged row: 256 and 32, so that the rows of a transposing read fall on different banks
 
 struct GradArgs {
   LoraSet s;
@@ -578,83 +706,100 @@ __device__ __forceinline__ bool next_request(const LoraSet& s, int a, int64_t t0
   return false;
 }
 
-// A workgroup per (adapter, 128 columns, split of the rows).  64 rows of X at a time go
+// A workgroup per (adapter, 256 columns, split of the rows).  64 rows of X at a time go
 // through LDS, double buffered, and are read back transposed (ds_read_b64_tr_b16: 16 lanes
 // supply a 4 x 16 block of rows k, and lane i receives its column i), which gives the MFMA
-// its 8 consecutive rows; the W terms lie along the rows already.  RB: blocks of 16 ranks.
-// TRANS: the result is (C, r), so the columns of X are the rows of the product.
+// its 8 consecutive rows; the W terms lie along the rows already.  The 16-byte pieces of a
+// staged row are swapped by (row % 4, row / 8 % 2), so that the 8 rows that 32 lanes read
+// together fall on different banks.
+// RB: blocks of 16 ranks.  The waves share the ranks first (WR groups, RBW blocks each) and
+// then the columns, so that a W term is read by as few waves as can be and serves 4 to 16
+// blocks of columns.  TRANS: the result is (C, r), so the columns of X are the rows of the
+// product.
+__device__ __forceinline__ int stage_at(int row, int piece) {
+  return row * (kGradCols * 2) + ((piece ^ (2 * (row & 3) + 8 * ((row >> 3) & 1))) << 4);
+}
 template <int RB, bool TRANS>
 __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uint8_t* lds) {
+  constexpr int WR = RB < 4 ? RB : 4, RBW = RB / WR, CB = kGradCols / 16 * WR / 4;
   const LoraSet& s = g.s;
-  const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
-  const int c16 = lane & 15, q = lane >> 4;
+  const int tid = tid_x(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, q = lane >> 4, r = (int)s.r;
+  const int wr = wave % WR, wc = wave / WR;  // ranks 16 RBW wr .., columns 16 CB wc ..
   const unsigned cols = (unsigned)((g.C + kGradCols - 1) / kGradCols);
   const int64_t c0 = (int64_t)(block % cols) * kGradCols;
   const int split = (int)(block / cols % (unsigned)g.splits);
   const int a = (int)(block / cols / (unsigned)g.splits);
   const int64_t t0 = split * g.tslice, t1 = t0 + g.tslice < s.T ? t0 + g.tslice : s.T;
-  f32x4_t acc[2][RB];
+  f32x4_t acc[CB][RBW];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < CB; ++h)
 #pragma unroll
-    for (int b = 0; b < RB; ++b) acc[h][b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-  // staging: thread tid moves 16 bytes of rows tid / 16 + 16 j
-  const int srow = tid >> 4, scol = (tid & 15) * 8;
-  const bool scol_in = c0 + scol < g.C;
+    for (int b = 0; b < RBW; ++b) acc[h][b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  // staging: thread tid moves 16 bytes of rows tid / 32 + 8 j
+  const int srow = tid >> 5, spiece = tid & 31;
+  const bool scol_in = c0 + spiece * 8 < g.C;
   const u32x4_t zero = {0u, 0u, 0u, 0u};
-  auto fetch = [&](const RowWalk& w, u32x4_t (&v)[4]) {
+  auto fetch = [&](const RowWalk& w, u32x4_t (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = w.at + srow + 16 * j;
-      v[j] = scol_in && t >= w.lo && t < w.hi ? load16(g.X + t * g.ldx + c0 + scol) : zero;
+    for (int j = 0; j < 8; ++j) {
+      const int64_t t = w.at + srow + 8 * j;
+      v[j] = scol_in && t >= w.lo && t < w.hi ? load16(g.X + t * g.ldx + c0 + spiece * 8) : zero;
     }
   };
   RowWalk w{-1, 0, 0, 0};
   bool more = next_request(s, a, t0, t1, w);
-  u32x4_t held[4];
+  u32x4_t held[8];
   if (more) fetch(w, held);
   int stage = 0;
   while (more) {
-    uint8_t* T = lds + stage * (kGradRows * kGradStride);
+    uint8_t* T = lds + stage * (kGradRows * kGradCols * 2);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<u32x4_t*>(T + (srow + 16 * j) * kGradStride + scol * 2) = held[j];
+    for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4_t*>(T + stage_at(srow + 8 * j, spiece)) = held[j];
     const RowWalk now = w;
+    // this lane's rows of W in the two k-steps: now.at + 8 q .. and 32 on (W reaches kGradRows beyond T)
+    u32x4_t wv[2][RBW][3];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int b = 0; b < RBW; ++b) {
+        const int rho = 16 * (wr * RBW + b) + c16;
+        const uint16_t* p = g.W + (int64_t)(rho < r ? rho : r - 1) * g.Tp + now.at + 32 * ks + 8 * q;
+#pragma unroll
+        for (int tm = 0; tm < 3; ++tm) wv[ks][b][tm] = load16(p + (int64_t)tm * r * g.Tp);
+      }
     w.at += kGradRows;
     if (w.at >= w.hi) more = next_request(s, a, t0, t1, w);
     if (more) fetch(w, held);
     __syncthreads();
-    const bool edge = now.at < now.lo || now.at + kGradRows > now.hi;
+    if (now.at < now.lo || now.at + kGradRows > now.hi) {
+      // rows of other requests may hold anything: neither side may keep them
+      const int begin = now.lo > now.at ? (int)(now.lo - now.at) : 0;
+      const int end = now.hi - now.at < kGradRows ? (int)(now.hi - now.at) : kGradRows;
 #pragma unroll
-    for (int ks = 0; ks < kGradRows; ks += 32) {
-      if (now.at + ks >= now.hi) break;
-      // this lane's 8 rows of W: now.at + ks + 8 q (the rows of W reach Tp, kGradRows beyond T)
-      const int64_t t = now.at + ks + 8 * q;
-      u32x4_t x[2];
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int b = 0; b < RBW; ++b)
+#pragma unroll
+          for (int tm = 0; tm < 3; ++tm)
+            wv[ks][b][tm] = keep_from(keep_below(wv[ks][b][tm], 32 * ks + 8 * q, end), 32 * ks + 8 * q, begin);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int h = 0; h < CB; ++h) {
         typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
-        const uint8_t* p = T + (ks + 8 * q + (c16 >> 2)) * kGradStride + (wave * 32 + h * 16 + 4 * (c16 & 3)) * 2;
-        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p);
-        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * kGradStride));
+        const int row = 32 * ks + 8 * q + (c16 >> 2), col = 16 * (wc * CB + h) + 4 * (c16 & 3);
+        const int in = (col & 7) * 2;
+        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(T + stage_at(row, col >> 3) + in));
+        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(T + stage_at(row + 4, col >> 3) + in));
         const s16x4_t v8[2] = {lo, hi};
-        x[h] = __builtin_bit_cast(u32x4_t, v8);
-      }
+        const u32x4_t x = __builtin_bit_cast(u32x4_t, v8);
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        const int rho = 16 * b + c16;
-        const uint16_t* wr = g.W + (int64_t)(rho < s.r ? rho : (int)s.r - 1) * g.Tp + t;
+        for (int b = 0; b < RBW; ++b)
 #pragma unroll
-        for (int tm = 0; tm < 3; ++tm) {
-          u32x4_t wv = load16(wr + (int64_t)tm * s.r * g.Tp);
-          if (edge) {
-            // rows of other requests may hold anything: neither side may keep them
-            wv = keep_below(wv, (int)(t - now.at), (int)(now.hi - now.at < kGradRows ? now.hi - now.at : kGradRows));
-            wv = keep_from(wv, (int)(t - now.at), (int)(now.lo - now.at > 0 ? now.lo - now.at : 0));
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) acc[h][b] = TRANS ? mfma(x[h], wv, acc[h][b]) : mfma(wv, x[h], acc[h][b]);
-        }
+          for (int tm = 0; tm < 3; ++tm)
+            acc[h][b] = TRANS ? mfma(x, wv[ks][b][tm], acc[h][b]) : mfma(wv[ks][b][tm], x, acc[h][b]);
       }
     }
     stage ^= 1;
@@ -663,24 +808,24 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
   const int rank = rank_of(s, a);
   float* out = g.out + (int64_t)split * s.n * s.r * g.C + (int64_t)a * s.r * g.C;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < CB; ++h)
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
+    for (int b = 0; b < RBW; ++b)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int along = c16, down = 4 * q + e;
-        const int64_t col = c0 + wave * 32 + h * 16 + (TRANS ? down : along);
-        const int rho = 16 * b + (TRANS ? along : down);
-        if (col < g.C && rho < s.r) {
+        const int64_t col = c0 + 16 * (wc * CB + h) + (TRANS ? down : along);
+        const int rho = 16 * (wr * RBW + b) + (TRANS ? along : down);
+        if (col < g.C && rho < r) {
           const float v = rho < rank ? acc[h][b][e] : 0.0f;
-          out[TRANS ? col * s.r + rho : (int64_t)rho * g.C + col] = v;
+          out[TRANS ? col * r + rho : (int64_t)rho * g.C + col] = v;
         }
       }
 }
 
 template <int RB>
 __global__ __launch_bounds__(kLThreads) void lora_grad_kernel(GradArgs ga, unsigned blocks_a, GradArgs gb) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kGradRows * kGradStride];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kGradRows * kGradCols * 2];
   if (bid_x() < blocks_a) grad_tile<RB, false>(ga, bid_x(), lds);
   else grad_tile<RB, true>(gb, bid_x() - blocks_a, lds);
 }
@@ -719,10 +864,12 @@ bool short_requests(int64_t T, int64_t R, int64_t widest) {
   return T < kShortRows * R && T * ((widest + 255) / 256) < (1 << 30);
 }
 
-// Splits of a down product's K: 512 workgroups at least where K allows ranges of 512.
+// Splits of a down product's K.  Single rows: enough for 512 workgroups where K allows ranges
+// of 512.  Tiles: one, whose workgroups finish the product themselves, unless K is long
+// (beyond 8192) and the tiles are few; then enough for 512 workgroups, of 4096 k at least.
 void down_split(int64_t T, bool rows, int64_t K, int64_t r, int& splits, int64_t& kslice) {
   const int64_t units = rows ? (T * (r / kRowRanks) + 3) / 4 : (T + kTileRows - 1) / kTileRows;
-  int64_t want = (512 + units - 1) / units, most = K / 512;
+  int64_t want = (512 + units - 1) / units, most = rows ? K / 512 : K <= 8192 ? 1 : K / 4096;
   if (want > most) want = most;
   if (want > kMaxSplits) want = kMaxSplits;
   if (want < 1) want = 1;
@@ -732,28 +879,41 @@ void down_split(int64_t T, bool rows, int64_t K, int64_t r, int& splits, int64_t
 }
 
 hipError_t launch_down(const LoraSet& s, const uint16_t* X, int64_t ldx, const uint16_t* M, int64_t K, float* P,
-                       bool rows, int& splits, hipStream_t st) {
-  DownArgs g{s, X, ldx, M, K, P, 1, 0};
+                       const Terms& o, bool rows, int& splits, hipStream_t st) {
+  DownArgs g{s, X, ldx, M, K, P, 1, 0, o};
   down_split(s.T, rows, K, s.r, g.splits, g.kslice);
   splits = g.splits;
   if (rows) {
     const int64_t units = s.T * (s.r / kRowRanks) * g.splits;
     hipLaunchKernelGGL(lora_down_row_kernel, dim3((unsigned)((units + 3) / 4)), dim3(kLThreads), 0, st, g);
   } else {
-    const dim3 grid((unsigned)((s.T + kTileRows - 1) / kTileRows * g.splits));
-    if (s.r <= 16) hipLaunchKernelGGL(lora_down_tile_kernel<1>, grid, dim3(kLThreads), 0, st, g);
-    else if (s.r <= 32) hipLaunchKernelGGL(lora_down_tile_kernel<2>, grid, dim3(kLThreads), 0, st, g);
-    else if (s.r <= 64) hipLaunchKernelGGL(lora_down_tile_kernel<4>, grid, dim3(kLThreads), 0, st, g);
-    else hipLaunchKernelGGL(lora_down_tile_kernel<8>, grid, dim3(kLThreads), 0, st, g);
+    const dim3 grid((unsigned)((s.T + kTileRows - 1) / kTileRows * g.splits)), block(kDownThreads);
+    if (s.r <= 16) hipLaunchKernelGGL(lora_down_tile_kernel<1>, grid, block, 0, st, g);
+    else if (s.r <= 32) hipLaunchKernelGGL(lora_down_tile_kernel<2>, grid, block, 0, st, g);
+    else if (s.r <= 64) hipLaunchKernelGGL(lora_down_tile_kernel<4>, grid, block, 0, st, g);
+    else hipLaunchKernelGGL(lora_down_tile_kernel<8>, grid, block, 0, st, g);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_terms(const TermArgs& a, const TermArgs& b, hipStream_t st) {
+  const unsigned tiles = (unsigned)((a.s.T + kTileRows - 1) / kTileRows);
+  const bool both = (a.o.U || a.o.W) && (b.o.U || b.o.W), one = a.o.U || a.o.W || b.o.U || b.o.W;
+  if (!one) return hipSuccess;
+  const TermArgs& f = a.o.U || a.o.W ? a : b;
+  hipLaunchKernelGGL(lora_terms_kernel, dim3(both ? 2 * tiles : tiles), dim3(kLThreads), 0, st, f, b, tiles);
   return hipGetLastError();
 }
 
 template <typename YT, typename BT, bool BASE>
 hipError_t launch_up_t(UpArgs g, bool rows, hipStream_t st) {
-  const int64_t r = g.s.r;
+  const int64_t r = g.s.r, T = g.s.T;
   if (rows) {
-    const dim3 grid((unsigned)(g.s.T * ((g.C + 255) / 256)));
+    // a wave's columns: 64, more once there are 16384 waves
+    g.steps = (int)(T * ((g.C + 63) / 64) / 16384);
+    g.steps = g.steps < 1 ? 1 : g.steps > 16 ? 16 : g.steps;
+    const int64_t ranges = (g.C + 256 * g.steps - 1) / (256 * g.steps);
+    const dim3 grid((unsigned)((ranges + 7) / 8 * 8 * T));
     if (r <= 8) hipLaunchKernelGGL((lora_up_row_kernel<1, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
     else if (r <= 16) hipLaunchKernelGGL((lora_up_row_kernel<2, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
     else if (r <= 32) hipLaunchKernelGGL((lora_up_row_kernel<4, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
@@ -762,16 +922,16 @@ hipError_t launch_up_t(UpArgs g, bool rows, hipStream_t st) {
     return hipGetLastError();
   }
   // a wave's columns: 4 steps of 64, fewer where that leaves less than 1024 workgroups
-  const int64_t tiles = (g.s.T + kTileRows - 1) / kTileRows;
+  const int64_t tiles = (T + kTileRows - 1) / kTileRows;
   g.steps = 4;
   while (g.steps > 1 && tiles * ((g.C + 256 * g.steps - 1) / (256 * g.steps)) < 1024) g.steps /= 2;
   const int64_t per = 256 * g.steps;
   const dim3 grid((unsigned)(tiles * ((g.C + per - 1) / per)));
-  if (r <= 8) hipLaunchKernelGGL((lora_up_tile_kernel<1, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
-  else if (r <= 16) hipLaunchKernelGGL((lora_up_tile_kernel<2, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
-  else if (r <= 32) hipLaunchKernelGGL((lora_up_tile_kernel<3, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
-  else if (r <= 64) hipLaunchKernelGGL((lora_up_tile_kernel<6, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
-  else hipLaunchKernelGGL((lora_up_tile_kernel<12, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
+  if (r <= 8) hipLaunchKernelGGL((lora_up_tile_kernel<1, 1, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
+  else if (r <= 16) hipLaunchKernelGGL((lora_up_tile_kernel<1, 2, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
+  else if (r <= 32) hipLaunchKernelGGL((lora_up_tile_kernel<1, 3, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
+  else if (r <= 64) hipLaunchKernelGGL((lora_up_tile_kernel<2, 3, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
+  else hipLaunchKernelGGL((lora_up_tile_kernel<4, 3, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
   return hipGetLastError();
 }
 
@@ -795,9 +955,30 @@ void grad_split(int64_t T, int64_t n, int64_t C, int& splits, int64_t& tslice) {
   splits = (int)((T + tslice - 1) / tslice);
 }
 
+struct ForwardWs {
+  float* P;     // partial sums: single rows, or several splits
+  uint16_t* U;  // tiles: the terms of u
+  bool rows;
+  size_t bytes;
+};
+ForwardWs forward_ws(void* base, int64_t T, int64_t R, int64_t H, int64_t N, int64_t r) {
+  ForwardWs w{};
+  w.rows = short_requests(T, R, N);
+  int splits;
+  int64_t ks;
+  down_split(T, w.rows, H, r, splits, ks);
+  const size_t p = w.rows || splits > 1 ? align256((size_t)splits * T * r * 4) : 0;
+  const size_t u = w.rows ? 0 : align256((size_t)3 * r * T * 2);
+  char* b = static_cast<char*>(base);
+  w.P = reinterpret_cast<float*>(b);
+  w.U = b ? reinterpret_cast<uint16_t*>(b + p) : nullptr;
+  w.bytes = p + u;
+  return w;
+}
+
 struct BackwardWs {
   float *Pu, *Pv;
-  uint16_t *At, *Bt, *Wu, *Wv;
+  uint16_t *At, *Bt, *Wu, *Wv, *Uv;
   float *partA, *partB;
   int64_t Tp;
   bool rows;
@@ -822,12 +1003,14 @@ BackwardWs backward_ws(void* base, int64_t T, int64_t R, int64_t n, int64_t H, i
   w.Tp = (T + kGradRows + 7) / 8 * 8;
   grad_split(T, n, H, w.splits_A, w.tslice_A);
   grad_split(T, n, N, w.splits_B, w.tslice_B);
-  w.Pu = reinterpret_cast<float*>(take((size_t)su * T * r * 4));
-  w.Pv = reinterpret_cast<float*>(take((size_t)sv * T * r * 4));
+  const bool pu = w.rows || su > 1, pv = w.rows || sv > 1;
+  w.Pu = pu ? reinterpret_cast<float*>(take((size_t)su * T * r * 4)) : nullptr;
+  w.Pv = pv ? reinterpret_cast<float*>(take((size_t)sv * T * r * 4)) : nullptr;
   w.At = reinterpret_cast<uint16_t*>(take((size_t)n * H * r * 2));
   w.Bt = reinterpret_cast<uint16_t*>(take((size_t)n * N * r * 2));
   w.Wu = reinterpret_cast<uint16_t*>(take((size_t)3 * r * w.Tp * 2));
   w.Wv = reinterpret_cast<uint16_t*>(take((size_t)3 * r * w.Tp * 2));
+  w.Uv = w.rows ? nullptr : reinterpret_cast<uint16_t*>(take((size_t)3 * r * T * 2));
   w.partA = w.splits_A > 1 ? reinterpret_cast<float*>(take((size_t)w.splits_A * n * r * H * 4)) : nullptr;
   w.partB = w.splits_B > 1 ? reinterpret_cast<float*>(take((size_t)w.splits_B * n * r * N * 4)) : nullptr;
   w.bytes = off;
@@ -837,10 +1020,7 @@ BackwardWs backward_ws(void* base, int64_t T, int64_t R, int64_t n, int64_t H, i
 }  // namespace
 
 size_t lora_forward_workspace_bytes(int64_t T, int64_t R, int64_t H, int64_t N, int64_t r) {
-  int splits;
-  int64_t ks;
-  down_split(T, short_requests(T, R, N), H, r, splits, ks);
-  return align256((size_t)splits * T * r * 4);
+  return forward_ws(nullptr, T, R, H, N, r).bytes;
 }
 
 size_t lora_backward_workspace_bytes(int64_t T, int64_t R, int64_t n, int64_t H, int64_t N, int64_t r) {
@@ -849,12 +1029,17 @@ size_t lora_backward_workspace_bytes(int64_t T, int64_t R, int64_t n, int64_t H,
 
 hipError_t launch_lora_forward(const LoraForwardArgs& a, hipStream_t st) {
   (void)hipGetLastError();
-  const bool rows = short_requests(a.s.T, a.s.R, a.s.N);
-  float* P = static_cast<float*>(a.workspace);
+  const LoraSet& s = a.s;
+  const ForwardWs w = forward_ws(a.workspace, s.T, s.R, s.H, s.N, s.r);
   int splits;
-  if (hipError_t e = launch_down(a.s, a.x, a.ldx, a.s.A, a.s.H, P, rows, splits, st)) return e;
-  const UpArgs g{a.s, P, splits, a.s.B, a.s.N, false, a.base, a.ldb, a.y, a.ldy, 0};
-  return a.y_dt == Dt::BF16 ? launch_up_y<uint16_t>(g, a.base_dt, rows, st) : launch_up_y<float>(g, a.base_dt, rows, st);
+  const Terms o{w.U, nullptr, 0};
+  if (hipError_t e = launch_down(s, a.x, a.ldx, s.A, s.H, w.P, o, w.rows, splits, st)) return e;
+  if (!w.rows && splits > 1) {
+    const TermArgs t{s, w.P, splits, o}, none{};
+    if (hipError_t e = launch_terms(t, none, st)) return e;
+  }
+  const UpArgs g{s, w.P, splits, w.U, s.B, s.N, false, a.base, a.ldb, a.y, a.ldy, 0};
+  return a.y_dt == Dt::BF16 ? launch_up_y<uint16_t>(g, a.base_dt, w.rows, st) : launch_up_y<float>(g, a.base_dt, w.rows, st);
 }
 
 hipError_t launch_lora_backward(const LoraBackwardArgs& a, hipStream_t st) {
@@ -876,20 +1061,24 @@ hipError_t launch_lora_backward(const LoraBackwardArgs& a, hipStream_t st) {
                        st, s, a.gx ? w.At : nullptr, w.Bt);
     if (hipError_t e = hipGetLastError()) return e;
   }
+  // u for dB; v for dx (terms along the ranks, or partial sums for single rows) and dA (terms along the rows)
   int su = 1, sv = 1;
+  const Terms ou{nullptr, a.gB ? w.Wu : nullptr, w.Tp};
+  const Terms ov{a.gx ? w.Uv : nullptr, a.gA ? w.Wv : nullptr, w.Tp};
   if (a.gB)
-    if (hipError_t e = launch_down(s, a.x, a.ldx, s.A, s.H, w.Pu, w.rows, su, st)) return e;
+    if (hipError_t e = launch_down(s, a.x, a.ldx, s.A, s.H, w.Pu, ou, w.rows, su, st)) return e;
   if (need_v)
-    if (hipError_t e = launch_down(s, a.dy, a.lddy, w.Bt, s.N, w.Pv, w.rows, sv, st)) return e;
+    if (hipError_t e = launch_down(s, a.dy, a.lddy, w.Bt, s.N, w.Pv, ov, w.rows, sv, st)) return e;
+  const bool tu = a.gB && (w.rows || su > 1), tv = need_v && (w.rows || sv > 1);
+  if (tu || tv) {
+    const TermArgs gu{s, w.Pu, su, tu ? ou : Terms{}}, gv{s, w.Pv, sv, tv ? ov : Terms{}};
+    if (hipError_t e = launch_terms(gu, gv, st)) return e;
+  }
   if (a.gx) {
-    const UpArgs g{s, w.Pv, sv, w.At, s.H, true, a.base, a.ldb, a.gx, a.ldgx, 0};
+    const UpArgs g{s, w.Pv, sv, w.Uv, w.At, s.H, true, a.base, a.ldb, a.gx, a.ldgx, 0};
     if (hipError_t e = launch_up_y<float>(g, Dt::F32, w.rows, st)) return e;
   }
   if (!a.gA && !a.gB) return hipSuccess;
-  const TermArgs tu{s, w.Pu, su, a.gB ? w.Wu : nullptr, w.Tp}, tv{s, w.Pv, sv, a.gA ? w.Wv : nullptr, w.Tp};
-  const int64_t half = (w.Tp / 8 * s.r + kLThreads - 1) / kLThreads;
-  hipLaunchKernelGGL(lora_terms_kernel, dim3((unsigned)(2 * half)), dim3(kLThreads), 0, st, tu, tv);
-  if (hipError_t e = hipGetLastError()) return e;
   const GradArgs ga{s, a.x, a.ldx, s.H, w.Wv, w.Tp, w.splits_A > 1 ? w.partA : a.gA, w.splits_A, w.tslice_A};
   const GradArgs gb{s, a.dy, a.lddy, s.N, w.Wu, w.Tp, w.splits_B > 1 ? w.partB : a.gB, w.splits_B, w.tslice_B};
   const unsigned ba = a.gA ? (unsigned)(s.n * w.splits_A * ((s.H + kGradCols - 1) / kGradCols)) : 0u;
