@@ -117,12 +117,20 @@ template <typename T, typename F>
 __device__ __forceinline__ void for_groups(const T* row, int64_t lo, int64_t hi, F f) {
   const int tid = tid_x();
   const int64_t whole = lo + (hi - lo) / 8 * 8;
+  if (whole == lo) {
+    float x[8];
+    if (tid == 0 && lo < hi) {
+      load_edge(row, lo, hi, x);
+      f(lo, x);
+    }
+    return;
+  }
   for (int64_t b = lo; b < hi; b += kVUnit * kVHold) {
     Group<T> g[kVHold];
 #pragma unroll
     for (int k = 0; k < kVHold; ++k) {
       const int64_t v = b + k * kVUnit + tid * 8;
-      if (v < whole) g[k].load(row + v);
+      g[k].load(row + (v < whole ? v : whole - 8));  // (without a condition: the loads stay in flight together)
     }
     float x[8];
 #pragma unroll

@@ -41,9 +41,7 @@ typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kLThreads = 256;
 constexpr int kTileRows = 32;    // rows of a tile of the matrix-core kernels
-constexpr int kDownThreads = 512;
-constexpr int kDownWaves = kDownThreads / 64;
-constexpr int kDownK = 64;       // k that a wave of the down kernel takes at once
+constexpr int kDownK = 128;      // k of a slice of the down kernel
 constexpr int kMaxSplits = 16;
 
 __device__ __forceinline__ f32x4_t mfma(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
@@ -145,34 +143,59 @@ __device__ __forceinline__ void load_low(const float* P, int splits, int64_t pla
 
 // ------------------------------------------------------------------ down: P = X M^T
 
-// u or v as the other products take it: its three bf16 terms along the ranks, U[t][term][r],
-// and along the rows, W[term][rank][Tp]; either may be nullptr.  vals: the fp32 values of
-// rows t0 .. t0 + 31 (rows behind T: 0), NT threads.
+// u or v as the other products take it, its three bf16 terms cut into MFMA operands of 64
+// lanes x 16 bytes (a wave's load of one is 1 KB of consecutive memory; operands loaded
+// straight from row-major arrays touch 16 rows per 16 lanes and run at a quarter of that):
+//   U: rows as operand rows, for the up product: [tile of 32 rows][half h][block l][j], where
+//      lane (row, q) of operand (l, j) holds 8 ranks of one term (up_chunk);
+//   W: rows along k, for the gradients: [tile of 32 rows][block of 16 ranks][term].
+// Either may be nullptr.
 struct Terms {
   uint16_t *U, *W;
-  int64_t Tp;
 };
-constexpr int kValStride = kLoraMaxRank + 1;
+// Operands of a tile for the up product with room for r ranks: LD blocks of ranks, TM MFMAs each.
+// r = 8: the k-groups of one MFMA are the three terms (and nothing); r = 16: two terms of 16 ranks
+// an MFMA; else one term of 32 ranks.
+__host__ __device__ constexpr int up_ld(int r) { return r <= 32 ? 1 : r <= 64 ? 2 : 4; }
+__host__ __device__ constexpr int up_tm(int r) { return r <= 8 ? 1 : r <= 16 ? 2 : 3; }
+// blocks of 16 ranks that the down and gradient kernels take
+__host__ __device__ constexpr int rank_blocks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
+// First rank (-1: none) of k-group q of block l.
+__device__ __forceinline__ int up_chunk(int r, int l, int q) {
+  if (r <= 8) return 0;
+  if (r <= 16) return (q & 1) * 8;
+  return 32 * l + 8 * q < r ? 32 * l + 8 * q : -1;
+}
+// Term (3: none) of k-group q in MFMA j.
+__device__ __forceinline__ int up_term(int r, int j, int q) { return r <= 8 ? q : r <= 16 ? (2 * j + (q >> 1)) : j; }
+
+// vals: the fp32 values of rows t0 .. t0 + 31 (t0 a multiple of 32; rows behind T: 0), row stride vs.
 template <int NT>
-__device__ __forceinline__ void emit_terms(const Terms& o, const float* vals, int64_t t0, int64_t T, int r) {
-  const int r8 = r / 8;
+__device__ __forceinline__ void emit_terms(const Terms& o, const float* vals, int vs, int64_t t0, int r) {
+  const int64_t tile = t0 / kTileRows;
   if (o.U) {
-    for (int i = tid_x(); i < kTileRows * 3 * r8; i += NT) {
-      const int row = i / (3 * r8), c = i - row * (3 * r8), tm = c / r8, k0 = (c - tm * r8) * 8;
-      if (t0 + row >= T) break;
-      float v[8];
+    const int ld = up_ld(r), tm = up_tm(r);
+    for (int i = tid_x(); i < 2 * ld * tm * 64; i += NT) {
+      const int lane = i & 63, f = i >> 6, j = f % tm, l = f / tm % ld, h = f / tm / ld;
+      const int k0 = up_chunk(r, l, lane >> 4), t = up_term(r, j, lane >> 4);
+      u32x4_t w = {0u, 0u, 0u, 0u};
+      if (k0 >= 0 && t < 3) {
+        float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = vals[row * kValStride + k0 + k];
-      *reinterpret_cast<u32x4_t*>(o.U + ((t0 + row) * 3 + tm) * r + k0) = terms8(v, tm);
+        for (int k = 0; k < 8; ++k) v[k] = vals[(16 * h + (lane & 15)) * vs + k0 + k];
+        w = terms8(v, t);
+      }
+      *reinterpret_cast<u32x4_t*>(o.U + (tile * 2 * ld * tm + f) * 512 + lane * 8) = w;
     }
   }
   if (o.W) {
-    for (int i = tid_x(); i < 3 * r * (kTileRows / 8); i += NT) {
-      const int t8 = i % (kTileRows / 8) * 8, c = i / (kTileRows / 8), tm = c / r, rho = c - tm * r;
+    const int nb = rank_blocks(r);
+    for (int i = tid_x(); i < nb * 3 * 64; i += NT) {
+      const int lane = i & 63, f = i >> 6, t = f % 3, rho = f / 3 * 16 + (lane & 15);
       float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = vals[(t8 + k) * kValStride + rho];
-      *reinterpret_cast<u32x4_t*>(o.W + ((int64_t)tm * r + rho) * o.Tp + t0 + t8) = terms8(v, tm);
+      for (int k = 0; k < 8; ++k) v[k] = rho < r ? vals[((lane >> 4) * 8 + k) * vs + rho] : 0.0f;
+      *reinterpret_cast<u32x4_t*>(o.W + (tile * nb * 3 + f) * 512 + lane * 8) = terms8(v, t);
     }
   }
 }
@@ -189,139 +212,146 @@ struct DownArgs {
   Terms o;  // tile kernel with one split: where the result goes
 };
 
-// Long requests: a workgroup per (tile of 32 rows, split of K); its eight waves take the 64-k
-// chunks of the split in turn, each chunk requested while the one before it is multiplied, and
-// add up in LDS.  In a chunk a lane holds 16 consecutive k (32 bytes) of its row, so that the
-// four lanes of a row read whole lines: the k's of the two MFMAs are permuted alike in both
-// operands.  With one split the workgroup finishes u itself (scale, rank, terms); with several
-// it leaves its partial sums for lora_terms_kernel.  RB: blocks of 16 ranks.
+// Long requests: a workgroup per (tile of 32 rows, split of K).  K goes in slices of 128 through
+// LDS, 16-byte pieces of a row swapped by its number so that the 16 rows of an operand read fall
+// on different banks.  Two slices are on their way in registers while a third is multiplied, and
+// (up to 64 ranks) two groups of four waves take every other slice each: with one workgroup per
+// compute unit, as 8192 rows make, that is what keeps enough loads in flight.  A group's four
+// waves share out the row halves and the ranks (RB = 1: the slice's k).  With one split the
+// workgroup finishes u itself (scale, rank, terms); with several it leaves its partial sums for
+// lora_terms_kernel.  RB: blocks of 16 ranks.
 template <int RB>
-struct DownChunk {
-  u32x4_t x[2][2], m[RB][2];
+struct Down {
+  static constexpr int kGroups = RB == 8 ? 1 : 2, kThreads = 256 * kGroups;
+  static constexpr int kRows = kTileRows + 16 * RB;         // staged rows: x, then M
+  static constexpr int kStage = kRows * kDownK * 2;          // bytes
+  static constexpr int kLoads = kRows * (kDownK / 8) / 256;  // 16-byte pieces of a thread and slice
+  static constexpr int kBlocks = RB == 1 ? 1 : RB / 2;       // blocks of ranks of a wave
+  static constexpr int kVs = 16 * RB + 1;                    // row stride of the fp32 result
+  // (the waves' sums lie in the stages' place, behind them the result)
+  static constexpr int kLds = 2 * kGroups * kStage;
+  static_assert(4 * kGroups * kBlocks * 4 * 64 * 4 <= kLds, "sums exceed the stages");
 };
-template <int RB>
-__device__ __forceinline__ void load_chunk(DownChunk<RB>& v, const uint16_t* X, const uint32_t (&xrow)[2],
-                                           const uint16_t* M, const uint32_t (&mrow)[RB], uint32_t k, uint32_t ke) {
-  const u32x4_t zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const bool in = k + 8 * j < ke;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) v.x[h][j] = in ? load16(X + (xrow[h] + k + 8 * j)) : zero;
-#pragma unroll
-    for (int b = 0; b < RB; ++b) v.m[b][j] = in ? load16(M + (mrow[b] + k + 8 * j)) : zero;
-  }
-}
-template <int RB>
-__device__ __forceinline__ void mul_chunk(f32x4_t (&acc)[2][RB], const DownChunk<RB>& v) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int b = 0; b < RB; ++b) acc[h][b] = mfma(v.x[h][j], v.m[b][j], acc[h][b]);
-}
 
 template <int RB>
-__global__ __launch_bounds__(kDownThreads) void lora_down_tile_kernel(DownArgs g) {
-  // each wave's sums of 32 rows x 16 RB ranks, two waves at a time in turn for RB = 8
-  __shared__ float red[RB == 8 ? 4 : 8][kTileRows * 16 * RB];
-  __shared__ float vals[kTileRows * kValStride];
+__global__ __attribute__((amdgpu_flat_work_group_size(Down<RB>::kThreads, Down<RB>::kThreads), amdgpu_waves_per_eu(2)))
+void lora_down_tile_kernel(DownArgs g) {
+  using D = Down<RB>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[D::kLds];
+  __shared__ float vals[kTileRows * D::kVs];
   const LoraSet& s = g.s;
   const int tid = tid_x(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = wave >> 2, gw = wave & 3, gt = tid & 255;
   const int split = (int)(bid_x() % (unsigned)g.splits);
   const int64_t r0 = (int64_t)(bid_x() / (unsigned)g.splits) * kTileRows;
   const int64_t r1 = r0 + kTileRows < s.T ? r0 + kTileRows : s.T;
-  const int64_t kb = split * g.kslice, ke = kb + g.kslice < g.K ? kb + g.kslice : g.K;
+  const uint32_t kb = (uint32_t)(split * g.kslice), ke = (uint32_t)(kb + g.kslice < g.K ? kb + g.kslice : g.K);
   const int c16 = lane & 15, q = lane >> 4, r = (int)s.r;
   const bool whole = g.splits == 1;
-  // the tile's rows and an adapter's M lie within 2^30 bytes: 32-bit offsets from uniform bases
-  const uint16_t* X = g.X + r0 * g.ldx;
-  uint32_t xrow[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t row = 16 * h + c16;
-    xrow[h] = (uint32_t)((r0 + row < s.T ? row : s.T - 1 - r0) * g.ldx);
-  }
   if (whole)
-    for (int i = tid; i < kTileRows * kValStride; i += kDownThreads) vals[i] = 0.0f;
+    for (int i = tid; i < kTileRows * D::kVs; i += D::kThreads) vals[i] = 0.0f;
+  // this thread's pieces of a slice: rows gt / 16 + 16 p (first the 32 of x), piece gt % 16.  The
+  // tile's rows and an adapter's M lie within 2^30 bytes: 32-bit offsets from uniform bases.
+  const int prow = gt >> 4, piece = gt & 15;
+  const uint16_t* X = g.X + r0 * g.ldx;
+  uint32_t off[D::kLoads];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int64_t row = prow + 16 * p;
+    off[p] = (uint32_t)((r0 + row < s.T ? row : s.T - 1 - r0) * g.ldx);
+  }
+#pragma unroll
+  for (int p = 2; p < D::kLoads; ++p) {
+    const int rho = prow + 16 * (p - 2);
+    off[p] = (uint32_t)((rho < r ? rho : r - 1) * g.K);
+  }
+  uint8_t* const stage0 = lds + group * 2 * D::kStage;
+  const int h = gw & 1, hb = gw >> 1;  // row half; half of the ranks (RB = 1: of the slice's k)
+  const uint32_t slices = (ke - kb + kDownK - 1) / kDownK;
+  const uint32_t rounds = (slices + D::kGroups - 1) / D::kGroups;
   for (int i = max(find_request(s.start, (int)s.R, r0), 0); i < s.R && s.start[i] < r1; ++i) {
     const Part p = part_of(s, i, r0, r1);
     if (p.hi <= p.lo || p.adapter < 0) continue;
     const uint16_t* M = g.M + (int64_t)p.adapter * r * g.K;
-    uint32_t mrow[RB];
+    f32x4_t acc[D::kBlocks];
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      const int rho = 16 * b + c16;
-      mrow[b] = (uint32_t)((rho < r ? rho : r - 1) * g.K);
-    }
-    f32x4_t acc[2][RB];
+    for (int b = 0; b < D::kBlocks; ++b) acc[b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    u32x4_t v0[D::kLoads], v1[D::kLoads];
+    // slice c of this group into registers; a piece behind the end comes from the last one in front
+    // of it (no load is conditional) and is 0 in LDS
+    auto load = [&](u32x4_t (&v)[D::kLoads], uint32_t c) {
+      const uint32_t k = kb + (c * D::kGroups + group) * kDownK + piece * 8, at = min(k, ke - 8);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int n = 0; n < 2; ++n) v[n] = load16(X + (off[n] + at));
 #pragma unroll
-      for (int b = 0; b < RB; ++b) acc[h][b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    {
-      // (chunks past the split's end load nothing and multiply zeros)
-      constexpr uint32_t kStep = kDownWaves * kDownK;
-      const uint32_t lane_k = 16 * q, end = (uint32_t)ke;
-      DownChunk<RB> c0, c1;
-      uint32_t k0 = (uint32_t)kb + wave * kDownK;
-      if (RB < 8) {
-        load_chunk<RB>(c0, X, xrow, M, mrow, k0 + lane_k, end);
-        for (; k0 < end; k0 += 2 * kStep) {
-          load_chunk<RB>(c1, X, xrow, M, mrow, k0 + kStep + lane_k, end);
-          mul_chunk<RB>(acc, c0);
-          load_chunk<RB>(c0, X, xrow, M, mrow, k0 + 2 * kStep + lane_k, end);
-          mul_chunk<RB>(acc, c1);
-        }
-      } else {
-        // (128 ranks: two chunks at once would not fit the registers)
-        for (; k0 < end; k0 += kStep) {
-          load_chunk<RB>(c0, X, xrow, M, mrow, k0 + lane_k, end);
-          mul_chunk<RB>(acc, c0);
+      for (int n = 2; n < D::kLoads; ++n) v[n] = load16(M + (off[n] + at));
+    };
+    auto put = [&](const u32x4_t (&v)[D::kLoads], uint32_t c) {
+      const bool in = kb + (c * D::kGroups + group) * kDownK + piece * 8 < ke;
+      uint8_t* T = stage0 + (c & 1) * D::kStage;
+#pragma unroll
+      for (int n = 0; n < D::kLoads; ++n) {
+        const u32x4_t z = {0u, 0u, 0u, 0u};
+        *reinterpret_cast<u32x4_t*>(T + (prow + 16 * n) * (kDownK * 2) + ((piece ^ prow) << 4)) = in ? v[n] : z;
+      }
+    };
+    auto multiply = [&](uint32_t c) {
+      const uint8_t* T = stage0 + (c & 1) * D::kStage;
+      constexpr int kSteps = kDownK / 32 / (RB == 1 ? 2 : 1);
+#pragma unroll
+      for (int n = 0; n < kSteps; ++n) {
+        const int at = ((4 * (RB == 1 ? hb * kSteps + n : n) + q) ^ c16) << 4;
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(T + (16 * h + c16) * (kDownK * 2) + at);
+#pragma unroll
+        for (int b = 0; b < D::kBlocks; ++b) {
+          const int row = kTileRows + 16 * (RB == 1 ? 0 : hb * D::kBlocks + b) + c16;
+          acc[b] = mfma(x, *reinterpret_cast<const u32x4_t*>(T + row * (kDownK * 2) + at), acc[b]);
         }
       }
+    };
+    load(v0, 0);
+    load(v1, 1);
+    __syncthreads();  // (the previous request's sums have been read)
+    for (uint32_t c = 0; c < rounds; c += 2) {
+      put(v0, c);
+      load(v0, c + 2);
+      __syncthreads();
+      multiply(c);
+      put(v1, c + 1);  // (behind the last slice: zeros)
+      load(v1, c + 3);
+      __syncthreads();
+      multiply(c + 1);
+      // (a stage is written again only after the barrier behind its reads)
     }
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int b = 0; b < D::kBlocks; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[((wave * D::kBlocks + b) * 4 + e) * 64 + lane] = acc[b][e];
+    __syncthreads();
     const int rank = rank_of(s, p.adapter);
     const float scale = s.scale[p.adapter];
-    constexpr int kRounds = RB == 8 ? 2 : 1, kPer = kDownWaves / kRounds;
-    float sum[(kTileRows * 16 * RB + kDownThreads - 1) / kDownThreads];
+    for (int f = tid; f < kTileRows * 16 * RB; f += D::kThreads) {
+      // place f: register e of lane l, block b, row half hh; summed over the waves that share it
+      const int l = f & 63, e = (f >> 6) & 3, b = (f >> 8) % RB, hh = (f >> 8) / RB;
+      float v = 0.0f;
 #pragma unroll
-    for (int round = 0; round < kRounds; ++round) {
-      __syncthreads();  // (what was there has been read)
-      if (wave / kPer == round) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) red[wave % kPer][((h * RB + b) * 4 + e) * 64 + lane] = acc[h][b][e];
+      for (int n = 0; n < D::kGroups * (RB == 1 ? 2 : 1); ++n) {
+        const int w = (RB == 1 ? n >> 1 : n) * 4 + 2 * (RB == 1 ? n & 1 : b / D::kBlocks) + hh;
+        v += red[((w * D::kBlocks + b % D::kBlocks) * 4 + e) * 64 + l];
       }
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < kTileRows * 16 * RB / kDownThreads; ++n) {
-        const int f = n * kDownThreads + tid;
-        float v = round ? sum[n] : 0.0f;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) v += red[k][f];
-        sum[n] = v;
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < kTileRows * 16 * RB / kDownThreads; ++n) {
-      // place f of a wave's sums: register (h, b, e) of lane l
-      const int f = n * kDownThreads + tid, l = f & 63, e = (f >> 6) & 3, b = (f >> 8) % RB, h = (f >> 8) / RB;
-      const int row = 16 * h + 4 * (l >> 4) + e, rho = 16 * b + (l & 15);
+      const int row = 16 * hh + 4 * (l >> 4) + e, rho = 16 * b + (l & 15);
       const int64_t t = r0 + row;
       if (t >= p.lo && t < p.hi && rho < r) {
-        if (whole) vals[row * kValStride + rho] = rho < rank ? scale * sum[n] : 0.0f;
-        else g.P[((int64_t)split * s.T + t) * r + rho] = sum[n];
+        if (whole) vals[row * D::kVs + rho] = rho < rank ? scale * v : 0.0f;
+        else g.P[((int64_t)split * s.T + t) * r + rho] = v;
       }
     }
   }
   if (whole) {
     __syncthreads();
-    emit_terms<kDownThreads>(g.o, vals, r0, s.T, r);
+    emit_terms<D::kThreads>(g.o, vals, D::kVs, r0, r);
   }
 }
 
@@ -367,7 +397,7 @@ struct UpArgs {
   LoraSet s;
   const float* P;  // single rows: [splits][T][r]
   int splits;
-  const uint16_t* U;  // tiles: terms [T][3][r]
+  const uint16_t* U;  // tiles: Terms::U
   const uint16_t* M;  // (n, C, r)
   int64_t C;
   bool m_clean;  // M is 0 beyond an adapter's rank (else what lies there is not used)
@@ -392,19 +422,17 @@ __device__ __forceinline__ void store4(uint16_t* p, const f32x4_t& v) {
 __device__ __forceinline__ void nan4(float* p) { *reinterpret_cast<uint4*>(p) = make_uint4(kQNaN32, kQNaN32, kQNaN32, kQNaN32); }
 __device__ __forceinline__ void nan4(uint16_t* p) { *reinterpret_cast<uint2*>(p) = make_uint2(kQNaN16 * 0x10001u, kQNaN16 * 0x10001u); }
 
-// Long requests: a wave per (tile of 32 rows, steps x 64 columns).  The tile's terms of P
-// (U[t][term][r]) stay in registers; a block of M is read once and multiplied by the terms
-// one after the other.  With r = 16 the four k-groups of an MFMA are two terms of the 16
-// ranks, with r = 8 all three: TM terms an MFMA each, LD blocks of 32 / (terms in an MFMA)
-// ranks.  Column block b of a step holds columns 4 (l % 16) + b, so that a lane ends with
-// four consecutive columns: whole 256-byte (fp32) or 128-byte (bf16) pieces of 4 rows per
+// Long requests: a wave per (tile of 32 rows, steps x 64 columns).  The tile's operands of P
+// (Terms::U) stay in registers; a block of M is read once and multiplied by its terms one
+// after the other.  Column block b of a step holds columns 4 (l % 16) + b, so that a lane ends
+// with four consecutive columns: whole 256-byte (fp32) or 128-byte (bf16) pieces of 4 rows per
 // access.
 template <int LD, int TM, typename YT, typename BT, bool BASE>
 __global__ __attribute__((amdgpu_flat_work_group_size(kLThreads, kLThreads), amdgpu_waves_per_eu(2)))
 void lora_up_tile_kernel(UpArgs g) {
   const LoraSet& s = g.s;
   const int lane = tid_x() & 63, wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6);
-  const int r = (int)s.r, r8 = r / 8;
+  const int r = (int)s.r;
   const int64_t per = (int64_t)4 * 64 * g.steps;
   const unsigned nch = (unsigned)((g.C + per - 1) / per);
   const int64_t n0 = (int64_t)(bid_x() % nch) * per + wave * 64 * g.steps;
@@ -412,23 +440,13 @@ void lora_up_tile_kernel(UpArgs g) {
   const int64_t r0 = (int64_t)(bid_x() / nch) * kTileRows;
   const int64_t r1 = r0 + kTileRows < s.T ? r0 + kTileRows : s.T;
   const int c16 = lane & 15, q = lane >> 4;
-  // this lane's chunk of 8 ranks in block l (-1: none), and its term in MFMA j
-  int ck[LD], term0;
-  if (TM == 1) {
-    ck[0] = 0;
-    term0 = q;
-  } else if (TM == 2) {
-    ck[0] = (q & 1) * 8;
-    term0 = q >> 1;
-  } else {
-    term0 = 0;
+  int ck[LD];  // this lane's 8 ranks of block l (none: 0, and u is 0 there)
 #pragma unroll
-    for (int l = 0; l < LD; ++l) ck[l] = 4 * l + q < r8 ? (4 * l + q) * 8 : -1;
-  }
+  for (int l = 0; l < LD; ++l) ck[l] = max(up_chunk(r, l, q), 0);
   // the tile's rows and an adapter's M lie within 2^30 bytes: 32-bit offsets from uniform bases
   YT* Y = static_cast<YT*>(g.y) + r0 * g.ldy;
   const BT* base = static_cast<const BT*>(g.base) + (BASE ? r0 * g.ldb : 0);
-  const uint16_t* U = g.U + r0 * 3 * r;
+  const uint16_t* U = g.U + r0 / kTileRows * (2 * LD * TM * 512);
   const uint32_t ldy = (uint32_t)g.ldy, ldb = (uint32_t)g.ldb, C = (uint32_t)g.C;
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   for (int i = max(find_request(s.start, (int)s.R, r0), 0); i < s.R && s.start[i] < r1; ++i) {
@@ -446,8 +464,8 @@ void lora_up_tile_kernel(UpArgs g) {
       for (int l = 0; l < LD; ++l)
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
-          const int tm = TM == 2 ? 2 * j + term0 : TM == 1 ? term0 : j;
-          u[h][l][j] = in && tm < 3 && ck[l] >= 0 ? load16(U + (uint32_t)((row * 3 + tm) * r + ck[l])) : zero;
+          const u32x4_t v = load16(U + (((h * LD + l) * TM + j) * 512 + lane * 8));
+          u[h][l][j] = in ? v : zero;
         }
     }
     const uint16_t* M = g.M + (some ? (int64_t)p.adapter * g.C * r : 0);
@@ -460,7 +478,7 @@ void lora_up_tile_kernel(UpArgs g) {
         for (int b = 0; b < 4; ++b) {
           const uint32_t row = (col + b < C ? col + b : C - 1) * (uint32_t)r;
 #pragma unroll
-          for (int l = 0; l < LD; ++l) w[b][l] = ck[l] >= 0 ? load16(M + (row + ck[l])) : zero;
+          for (int l = 0; l < LD; ++l) w[b][l] = load16(M + (row + ck[l]));
         }
       }
       f32x4_t old[2][4];
@@ -470,7 +488,8 @@ void lora_up_tile_kernel(UpArgs g) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int row = 16 * h + 4 * q + e;
-            if (col < C && row >= lo && row < hi) old[h][e] = load4(base + (row * ldb + col));
+            // (a row or column of the request for those that are not written, so that no load is conditional)
+            old[h][e] = load4(base + ((uint32_t)min(max(row, lo), hi - 1) * ldb + min(col, C - 4)));
           }
       }
       f32x4_t acc[2][4];
@@ -623,6 +642,7 @@ __global__ __launch_bounds__(kLThreads) void lora_transpose_kernel(LoraSet s, ui
   else if (at - na < nb) transpose_block<false>(s, s.B, Bt, s.N, s.r, at - na);
 }
 
+constexpr int kValStride = kLoraMaxRank + 1;
 // The terms of s_a P from the down kernels' partial sums: a workgroup per 32 rows; 0 for rows
 // without an adapter and ranks beyond the adapter's.
 struct TermArgs {
@@ -660,7 +680,7 @@ __global__ __launch_bounds__(kLThreads) void lora_terms_kernel(TermArgs g0, Term
     for (int k = 0; k < 4; ++k) vals[row * kValStride + k0 + k] = v[k];
   }
   __syncthreads();
-  emit_terms<kLThreads>(g.o, vals, t0, s.T, r);
+  emit_terms<kLThreads>(g.o, vals, kValStride, t0, r);
 }
 
 // ------------------------------------------------------------------ grad: W^T X over the rows of an adapter
@@ -672,8 +692,7 @@ struct GradArgs {
   LoraSet s;
   const uint16_t* X;  // (T, C)
   int64_t ldx, C;
-  const uint16_t* W;  // [3][r][Tp] terms
-  int64_t Tp;
+  const uint16_t* W;  // Terms::W
   float* out;  // (n, r, C) or, transposed, (n, C, r); [splits] of them when splits > 1
   int splits;
   int64_t tslice;  // rows of a split
@@ -699,7 +718,7 @@ __device__ __forceinline__ bool next_request(const LoraSet& s, int a, int64_t t0
       const Part p = part_of(s, w.i, t0, t1);
       w.lo = p.lo;
       w.hi = p.hi;
-      w.at = p.lo & ~(int64_t)7;
+      w.at = p.lo & ~(int64_t)31;
       return true;
     }
   }
@@ -709,7 +728,7 @@ __device__ __forceinline__ bool next_request(const LoraSet& s, int a, int64_t t0
 // A workgroup per (adapter, 256 columns, split of the rows).  64 rows of X at a time go
 // through LDS, double buffered, and are read back transposed (ds_read_b64_tr_b16: 16 lanes
 // supply a 4 x 16 block of rows k, and lane i receives its column i), which gives the MFMA
-// its 8 consecutive rows; the W terms lie along the rows already.  The 16-byte pieces of a
+// its 8 consecutive rows; the W terms lie along the rows already (a stage starts at a multiple of 32 rows).  The 16-byte pieces of a
 // staged row are swapped by (row % 4, row / 8 % 2), so that the 8 rows that 32 lanes read
 // together fall on different banks.
 // RB: blocks of 16 ranks.  The waves share the ranks first (WR groups, RBW blocks each) and
@@ -738,13 +757,15 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
     for (int b = 0; b < RBW; ++b) acc[h][b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   // staging: thread tid moves 16 bytes of rows tid / 32 + 8 j
   const int srow = tid >> 5, spiece = tid & 31;
-  const bool scol_in = c0 + spiece * 8 < g.C;
+  const int64_t scol = c0 + spiece * 8 < g.C ? spiece * 8 : 0;
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   auto fetch = [&](const RowWalk& w, u32x4_t (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int64_t t = w.at + srow + 8 * j;
-      v[j] = scol_in && t >= w.lo && t < w.hi ? load16(g.X + t * g.ldx + c0 + spiece * 8) : zero;
+      // (loaded without conditions, from a row of the request; columns behind the last are not stored)
+      const u32x4_t x = load16(g.X + (t < w.lo ? w.lo : t < w.hi ? t : w.hi - 1) * g.ldx + c0 + scol);
+      v[j] = t >= w.lo && t < w.hi ? x : zero;
     }
   };
   RowWalk w{-1, 0, 0, 0};
@@ -757,17 +778,15 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
 #pragma unroll
     for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4_t*>(T + stage_at(srow + 8 * j, spiece)) = held[j];
     const RowWalk now = w;
-    // this lane's rows of W in the two k-steps: now.at + 8 q .. and 32 on (W reaches kGradRows beyond T)
+    // the W operands of the two k-steps (rows now.at .. and now.at + 32 ..)
     u32x4_t wv[2][RBW][3];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int b = 0; b < RBW; ++b) {
-        const int rho = 16 * (wr * RBW + b) + c16;
-        const uint16_t* p = g.W + (int64_t)(rho < r ? rho : r - 1) * g.Tp + now.at + 32 * ks + 8 * q;
+      for (int b = 0; b < RBW; ++b)
 #pragma unroll
-        for (int tm = 0; tm < 3; ++tm) wv[ks][b][tm] = load16(p + (int64_t)tm * r * g.Tp);
-      }
+        for (int tm = 0; tm < 3; ++tm)
+          wv[ks][b][tm] = load16(g.W + (((now.at / 32 + ks) * RB + wr * RBW + b) * 3 + tm) * 512 + lane * 8);
     w.at += kGradRows;
     if (w.at >= w.hi) more = next_request(s, a, t0, t1, w);
     if (more) fetch(w, held);
@@ -887,11 +906,11 @@ hipError_t launch_down(const LoraSet& s, const uint16_t* X, int64_t ldx, const u
     const int64_t units = s.T * (s.r / kRowRanks) * g.splits;
     hipLaunchKernelGGL(lora_down_row_kernel, dim3((unsigned)((units + 3) / 4)), dim3(kLThreads), 0, st, g);
   } else {
-    const dim3 grid((unsigned)((s.T + kTileRows - 1) / kTileRows * g.splits)), block(kDownThreads);
-    if (s.r <= 16) hipLaunchKernelGGL(lora_down_tile_kernel<1>, grid, block, 0, st, g);
-    else if (s.r <= 32) hipLaunchKernelGGL(lora_down_tile_kernel<2>, grid, block, 0, st, g);
-    else if (s.r <= 64) hipLaunchKernelGGL(lora_down_tile_kernel<4>, grid, block, 0, st, g);
-    else hipLaunchKernelGGL(lora_down_tile_kernel<8>, grid, block, 0, st, g);
+    const dim3 grid((unsigned)((s.T + kTileRows - 1) / kTileRows * g.splits));
+    if (s.r <= 16) hipLaunchKernelGGL(lora_down_tile_kernel<1>, grid, dim3(Down<1>::kThreads), 0, st, g);
+    else if (s.r <= 32) hipLaunchKernelGGL(lora_down_tile_kernel<2>, grid, dim3(Down<2>::kThreads), 0, st, g);
+    else if (s.r <= 64) hipLaunchKernelGGL(lora_down_tile_kernel<4>, grid, dim3(Down<4>::kThreads), 0, st, g);
+    else hipLaunchKernelGGL(lora_down_tile_kernel<8>, grid, dim3(Down<8>::kThreads), 0, st, g);
   }
   return hipGetLastError();
 }
@@ -955,6 +974,10 @@ void grad_split(int64_t T, int64_t n, int64_t C, int& splits, int64_t& tslice) {
   splits = (int)((T + tslice - 1) / tslice);
 }
 
+size_t u_bytes(int64_t T, int64_t r) {
+  return (size_t)((T + kTileRows - 1) / kTileRows) * 2 * up_ld((int)r) * up_tm((int)r) * 1024;
+}
+
 struct ForwardWs {
   float* P;     // partial sums: single rows, or several splits
   uint16_t* U;  // tiles: the terms of u
@@ -968,7 +991,7 @@ ForwardWs forward_ws(void* base, int64_t T, int64_t R, int64_t H, int64_t N, int
   int64_t ks;
   down_split(T, w.rows, H, r, splits, ks);
   const size_t p = w.rows || splits > 1 ? align256((size_t)splits * T * r * 4) : 0;
-  const size_t u = w.rows ? 0 : align256((size_t)3 * r * T * 2);
+  const size_t u = w.rows ? 0 : align256(u_bytes(T, r));
   char* b = static_cast<char*>(base);
   w.P = reinterpret_cast<float*>(b);
   w.U = b ? reinterpret_cast<uint16_t*>(b + p) : nullptr;
@@ -980,7 +1003,6 @@ struct BackwardWs {
   float *Pu, *Pv;
   uint16_t *At, *Bt, *Wu, *Wv, *Uv;
   float *partA, *partB;
-  int64_t Tp;
   bool rows;
   int splits_A, splits_B;
   int64_t tslice_A, tslice_B;
@@ -1000,7 +1022,6 @@ BackwardWs backward_ws(void* base, int64_t T, int64_t R, int64_t n, int64_t H, i
   int64_t ks;
   down_split(T, w.rows, H, r, su, ks);
   down_split(T, w.rows, N, r, sv, ks);
-  w.Tp = (T + kGradRows + 7) / 8 * 8;
   grad_split(T, n, H, w.splits_A, w.tslice_A);
   grad_split(T, n, N, w.splits_B, w.tslice_B);
   const bool pu = w.rows || su > 1, pv = w.rows || sv > 1;
@@ -1008,9 +1029,11 @@ BackwardWs backward_ws(void* base, int64_t T, int64_t R, int64_t n, int64_t H, i
   w.Pv = pv ? reinterpret_cast<float*>(take((size_t)sv * T * r * 4)) : nullptr;
   w.At = reinterpret_cast<uint16_t*>(take((size_t)n * H * r * 2));
   w.Bt = reinterpret_cast<uint16_t*>(take((size_t)n * N * r * 2));
-  w.Wu = reinterpret_cast<uint16_t*>(take((size_t)3 * r * w.Tp * 2));
-  w.Wv = reinterpret_cast<uint16_t*>(take((size_t)3 * r * w.Tp * 2));
-  w.Uv = w.rows ? nullptr : reinterpret_cast<uint16_t*>(take((size_t)3 * r * T * 2));
+  // (a stage of the gradients may reach one tile beyond the last)
+  const size_t wb = ((size_t)((T + kTileRows - 1) / kTileRows) + 1) * rank_blocks((int)r) * 3 * 1024;
+  w.Wu = reinterpret_cast<uint16_t*>(take(wb));
+  w.Wv = reinterpret_cast<uint16_t*>(take(wb));
+  w.Uv = w.rows ? nullptr : reinterpret_cast<uint16_t*>(take(u_bytes(T, r)));
   w.partA = w.splits_A > 1 ? reinterpret_cast<float*>(take((size_t)w.splits_A * n * r * H * 4)) : nullptr;
   w.partB = w.splits_B > 1 ? reinterpret_cast<float*>(take((size_t)w.splits_B * n * r * N * 4)) : nullptr;
   w.bytes = off;
@@ -1032,7 +1055,7 @@ hipError_t launch_lora_forward(const LoraForwardArgs& a, hipStream_t st) {
   const LoraSet& s = a.s;
   const ForwardWs w = forward_ws(a.workspace, s.T, s.R, s.H, s.N, s.r);
   int splits;
-  const Terms o{w.U, nullptr, 0};
+  const Terms o{w.U, nullptr};
   if (hipError_t e = launch_down(s, a.x, a.ldx, s.A, s.H, w.P, o, w.rows, splits, st)) return e;
   if (!w.rows && splits > 1) {
     const TermArgs t{s, w.P, splits, o}, none{};
@@ -1063,8 +1086,8 @@ hipError_t launch_lora_backward(const LoraBackwardArgs& a, hipStream_t st) {
   }
   // u for dB; v for dx (terms along the ranks, or partial sums for single rows) and dA (terms along the rows)
   int su = 1, sv = 1;
-  const Terms ou{nullptr, a.gB ? w.Wu : nullptr, w.Tp};
-  const Terms ov{a.gx ? w.Uv : nullptr, a.gA ? w.Wv : nullptr, w.Tp};
+  const Terms ou{nullptr, a.gB ? w.Wu : nullptr};
+  const Terms ov{a.gx ? w.Uv : nullptr, a.gA ? w.Wv : nullptr};
   if (a.gB)
     if (hipError_t e = launch_down(s, a.x, a.ldx, s.A, s.H, w.Pu, ou, w.rows, su, st)) return e;
   if (need_v)
@@ -1079,8 +1102,8 @@ hipError_t launch_lora_backward(const LoraBackwardArgs& a, hipStream_t st) {
     if (hipError_t e = launch_up_y<float>(g, Dt::F32, w.rows, st)) return e;
   }
   if (!a.gA && !a.gB) return hipSuccess;
-  const GradArgs ga{s, a.x, a.ldx, s.H, w.Wv, w.Tp, w.splits_A > 1 ? w.partA : a.gA, w.splits_A, w.tslice_A};
-  const GradArgs gb{s, a.dy, a.lddy, s.N, w.Wu, w.Tp, w.splits_B > 1 ? w.partB : a.gB, w.splits_B, w.tslice_B};
+  const GradArgs ga{s, a.x, a.ldx, s.H, w.Wv, w.splits_A > 1 ? w.partA : a.gA, w.splits_A, w.tslice_A};
+  const GradArgs gb{s, a.dy, a.lddy, s.N, w.Wu, w.splits_B > 1 ? w.partB : a.gB, w.splits_B, w.tslice_B};
   const unsigned ba = a.gA ? (unsigned)(s.n * w.splits_A * ((s.H + kGradCols - 1) / kGradCols)) : 0u;
   const unsigned bb = a.gB ? (unsigned)(s.n * w.splits_B * ((s.N + kGradCols - 1) / kGradCols)) : 0u;
   if (s.r <= 16) hipLaunchKernelGGL(lora_grad_kernel<1>, dim3(ba + bb), dim3(kLThreads), 0, st, ga, ba, gb);
