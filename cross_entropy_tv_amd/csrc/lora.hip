@@ -877,10 +877,24 @@ __global__ __launch_bounds__(kLThreads) void lora_zero_kernel(float* a, int64_t 
 
 // ------------------------------------------------------------------ launches
 
-// Mean rows of a request below which the kernels take single rows, and not tiles of 32.
-constexpr int kShortRows = 8;
-bool short_requests(int64_t T, int64_t R, int64_t widest) {
-  return T < kShortRows * R && T * ((widest + 255) / 256) < (1 << 30);
+// Whether the kernels of single rows are taken, and not those of tiles of 32 rows: by what each
+// is estimated to cost, in us, from times measured over T = 16..2048, R = 1..256, r = 16, 64, H =
+// 4096, N = 4096 and 151936.  Single rows read an adapter once for every row, from the L2s at about 8
+// TB/s.  A tile takes the requests that share it (1 + 32 R / T on average) one after the other,
+// each a pass over the down products' axes (a split's share of them) and over the tile's columns of y.
+//   T 64, R 1 / 8 / 64: 9.4 / 9.4 / 9.3 us as rows, 13.3 / 35.6 / 236 as tiles;
+//   T 512, R 1, r 64: 37 as rows, 24 as tiles; T 1024, R 2 / 128: 35 / 38 as rows, 18 / 44 as tiles;
+//   T 64, R 1 / 8, N 151936: 43 / 43 as rows, 27 / 61 as tiles.
+bool single_rows(int64_t T, int64_t R, int64_t r, int64_t H, int64_t N, bool backward) {
+  const double read = 2.0 * (double)T * (double)r * (double)(backward ? 2 * H + N : H + N);
+  const double rows = 4.0 + read / 8.0e6;
+  double shared = 1.0 + 32.0 * (double)R / (double)T;
+  if (shared > 32.0) shared = 32.0;
+  auto pass = [](int64_t K) { return 1.0 + 3.0 * (double)(K <= 8192 ? K : 8192) / 4096.0; };
+  const double tiles = 13.0 + shared * (pass(H) + (backward ? pass(N) : 0.0)) +
+                       (shared - 1.0) * (double)T * (double)(backward ? H : N) * 8.0 / 10.0e6;
+  // (and single rows' grids stay within int32)
+  return rows < tiles && T * (((H > N ? H : N) + 255) / 256) < (1 << 30);
 }
 
 // Splits of a down product's K.  Single rows: enough for 512 workgroups where K allows ranges
@@ -986,7 +1000,7 @@ struct ForwardWs {
 };
 ForwardWs forward_ws(void* base, int64_t T, int64_t R, int64_t H, int64_t N, int64_t r) {
   ForwardWs w{};
-  w.rows = short_requests(T, R, N);
+  w.rows = single_rows(T, R, r, H, N, false);
   int splits;
   int64_t ks;
   down_split(T, w.rows, H, r, splits, ks);
@@ -1017,7 +1031,7 @@ BackwardWs backward_ws(void* base, int64_t T, int64_t R, int64_t n, int64_t H, i
     off += align256(bytes);
     return q;
   };
-  w.rows = short_requests(T, R, H > N ? H : N);
+  w.rows = single_rows(T, R, r, H, N, true);
   int su, sv;
   int64_t ks;
   down_split(T, w.rows, H, r, su, ks);

@@ -132,16 +132,47 @@ def ragged(seed, R, T):
     return [0] + sorted(int(v) for v in g.integers(0, T + 1, R - 1)) + [T]
 
 
+def path_of(c, backward=False):
+    """Which kernels a shape takes: those of tiles of 32 rows, or of single rows where the estimated time is less (what
+    the library estimates by, in us)."""
+    T, R, r, H, N = c.T, len(c.adapter), c.r, c.H, c.N
+    shared = min(1 + 32 * R / T, 32)
+    rows = 4 + 2 * T * r * (H + N + (H if backward else 0)) / 8e6
+    one = lambda K: 1 + 3 * min(K, 8192) / 4096  # noqa: E731
+    tiles = 13 + shared * (one(H) + (one(N) if backward else 0)) + (shared - 1) * T * (H if backward else N) * 8 / 10e6
+    return "single" if rows < tiles else "tiles"
+
+
+def test_the_estimate_is_the_library_s():
+    """The forward's workspace is partial sums for single rows and whole 1 KB operands for tiles of 32."""
+    for r, tm in ((8, 1), (16, 2), (32, 3)):
+        for T in range(200, 9000, 97):
+            c = Case.__new__(Case)
+            c.T, c.adapter, c.r, c.H, c.N = T, [0] * (1 + T % 5), r, 520, 1032
+            tiles = lx.lx_lora_forward_workspace_bytes(T, len(c.adapter), 520, 1032, r) == -(-T // 32) * 2 * tm * 1024
+            assert tiles == (path_of(c) == "tiles"), (r, T)
+
+
+def both_paths(rows, seed, r, n=3, rank=None, R=4, adapter=None):
+    """A case of many rows (tiles of 32) or of a few (single rows)."""
+    if rows == "tiles":
+        T = 40000 // r + 190
+        start = ragged(seed, R, T)
+        c = Case(seed, start, adapter or [(i * 2 + 1) % n for i in range(R)], n, 520, 1032, r, rank)
+    else:
+        start = ragged(seed, R, 40) if seed % 2 else list(range(22))
+        c = Case(seed, start, [i % n for i in range(len(start) - 1)], n, 200, 328, r, rank)
+    assert path_of(c) == rows and path_of(c, True) == rows
+    return c
+
+
 RANKS = [8, 16, 24, 32, 40, 48, 56, 64, 72, 96, 128]
 
 
 @pytest.mark.parametrize("r", RANKS)
 @pytest.mark.parametrize("rows", ["tiles", "single"])
 def test_ranks(r, rows):
-    if rows == "tiles":
-        c = Case(r, ragged(r, 4, 101), [1, 0, 2, 1], 3, 200, 328, r)
-    else:
-        c = Case(r, list(range(22)), [i % 3 for i in range(21)], 3, 200, 328, r)
+    c = both_paths(rows, r, r)
     check_forward(c, f"r {r} {rows}", base="f32")
     check_backward(c, f"r {r} {rows}", base=True)
 
@@ -150,10 +181,7 @@ def test_ranks(r, rows):
 @pytest.mark.parametrize("r,rank", [(8, [1, 8, 0]), (16, [9, 3, 16]), (24, [17, 24, 7]), (64, [5, 33, 62]),
                                     (128, [128, 100, 1]), (16, [-4, 99, 8])])
 def test_cut_ranks(r, rank, rows):
-    if rows == "tiles":
-        c = Case(r + 1, ragged(r, 5, 90), [2, 0, 1, 0, 2], 3, 136, 264, r, rank)
-    else:
-        c = Case(r + 1, list(range(18)), [i % 3 for i in range(17)], 3, 136, 264, r, rank)
+    c = both_paths(rows, r + 1, r, rank=rank, R=5)
     check_forward(c, f"rank {rank} {rows}", base="f32")
     check_backward(c, f"rank {rank} {rows}")
 
@@ -170,67 +198,84 @@ def test_sizes(H, N, T, R):
 @pytest.mark.parametrize("y", ["f32", "bf16"])
 @pytest.mark.parametrize("rows", ["tiles", "single"])
 def test_types(base, y, rows):
-    start = ragged(3, 3, 70) if rows == "tiles" else list(range(12))
-    c = Case(5, start, [i % 2 for i in range(len(start) - 1)], 2, 160, 392, 24)
+    c = both_paths(rows, 5, 24, n=2, R=3)
     check_forward(c, f"base {base} y {y} {rows}", base=base, y=y, pads=(8, 16, 24))
     if base == y:
         check_forward(c, f"in place {y} {rows}", base=base, y=y, pads=(0, 40, 0), in_place=True)
 
 
-def test_backward_strides_and_in_place():
-    for start in (ragged(7, 3, 70), list(range(12))):
-        c = Case(9, start, [i % 2 for i in range(len(start) - 1)], 2, 160, 392, 24)
-        check_backward(c, "strides", base=True, pads=(8, 16, 24, 32))
-        check_backward(c, "in place", base=True, pads=(0, 0, 8, 0), in_place=True)
+@pytest.mark.parametrize("rows", ["tiles", "single"])
+def test_backward_strides_and_in_place(rows):
+    c = both_paths(rows, 9, 24, n=2, R=3)
+    check_backward(c, "strides", base=True, pads=(8, 16, 24, 32))
+    check_backward(c, "in place", base=True, pads=(0, 0, 8, 0), in_place=True)
+
+
+@pytest.mark.parametrize("H,N,T,R,r", [(8, 4104, 5000, 2, 8), (4104, 8, 3000, 3, 16), (72, 2056, 2500, 5, 24),
+                                       (2056, 72, 2500, 1, 16), (128, 136, 5000, 4, 128), (1032, 1544, 1500, 40, 40)])
+def test_sizes_in_tiles(H, N, T, R, r):
+    c = Case(H + N + T, ragged(T, R, T), [i % 2 for i in range(R)], 2, H, N, r)
+    assert path_of(c) == "tiles"
+    check_forward(c, f"tiles, {T} rows {R} requests {H} x {N}")
+    check_backward(c, f"tiles, {T} rows {R} requests {H} x {N}")
 
 
 @pytest.mark.parametrize("want", [(True, False, False), (False, True, False), (False, False, True), (True, True, False),
                                   (True, False, True), (False, True, True)])
-def test_some_gradients(want):
-    c = Case(11, ragged(11, 3, 90), [0, 1, 0], 2, 136, 200, 16)
-    check_backward(c, f"only {want}", want_grads=want)
+@pytest.mark.parametrize("rows", ["tiles", "single"])
+def test_some_gradients(want, rows):
+    check_backward(both_paths(rows, 11, 16, n=2, R=3), f"only {want} {rows}", want_grads=want)
 
 
-@pytest.mark.parametrize("H", [136, 1032])
-def test_requests_of_every_kind(H):
+@pytest.mark.parametrize("rows", ["tiles", "single"])
+def test_requests_of_every_kind(rows):
     """Rows in front of the first request and behind the last, empty requests, no adapter, an id that does not exist,
     adapters without rows, a tile shared by many requests."""
-    start = [3, 3, 10, 11, 11, 40, 41, 45, 45, 77, 100]
+    scale, H, N = (25, 520, 1032) if rows == "tiles" else (1, 136, 264)
+    start = [3, 3, 10, 11, 11] + [11 + scale * k for k in (29, 30, 34, 34, 66, 89)]
     adapter = [0, 2, -1, 1, 2, 0, 4, 2, -7, 0]
-    c = Case(13, start, adapter, 4, H, 264, 16, rank=[16, 16, 5, 16], T=117)
+    c = Case(13, start, adapter, 4, H, N, 16, rank=[16, 16, 5, 16], T=start[-1] + 17)
+    assert path_of(c) == rows and path_of(c, True) == rows
     check_forward(c, "every kind", base="f32")
     _, gA, gB = check_backward(c, "every kind", base=True)
     assert (gA[1] == 0).all() and (gA[3] == 0).all() and (gB[1] == 0).all() and (gB[3] == 0).all()
-    # the same as single rows
-    start = [2] + list(range(2, 30)) + [30]
-    c = Case(14, start, [(i * 5) % 6 - 1 for i in range(len(start) - 1)], 4, H, 264, 16, rank=[16, 16, 5, 16], T=33)
+    # requests of one row, then a long one
+    start = [2] + list(range(2, 30)) + ([30] if rows == "single" else [3000])
+    c = Case(14, start, [(i * 5) % 6 - 1 for i in range(len(start) - 1)], 4, H, N, 16, rank=[16, 16, 5, 16],
+             T=start[-1] + 3)
+    assert path_of(c) == rows
     check_forward(c, "every kind, single", base="f32")
     check_backward(c, "every kind, single", base=True)
 
 
 def test_starts_outside_the_rows():
-    c = Case(15, [-5, 20, 90], [0, 1], 2, 136, 136, 8, T=64)
-    check_forward(c, "starts outside")
-    check_backward(c, "starts outside")
+    for T, H, N in ((64, 136, 136), (4200, 520, 1032)):
+        c = Case(15, [-5, 20, T + 26], [0, 1], 2, H, N, 8, T=T)
+        check_forward(c, "starts outside")
+        check_backward(c, "starts outside")
 
 
-def test_other_requests_rows_do_not_leak():
+@pytest.mark.parametrize("rows", ["tiles", "single"])
+def test_other_requests_rows_do_not_leak(rows):
     """NaN and infinities in one request's rows, or between requests, reach no other row and no other adapter."""
-    start, adapter = [5, 36, 64, 100], [0, 1, 0]
-    c = Case(17, start, adapter, 2, 264, 264, 16, T=110)
+    H, N, T = (520, 1032, 2400) if rows == "tiles" else (264, 264, 110)
+    mid, end = T - 46, T - 10
+    start, adapter = [5, 36, mid, end], [0, 1, 0]
+    c = Case(17, start, adapter, 2, H, N, 16, T=T)
+    assert path_of(c) == rows and path_of(c, True) == rows
     clean = check_forward(c, "clean").clone()
     gx, gA, gB = (g.clone() for g in check_backward(c, "clean"))
-    bad = Case(17, start, adapter, 2, 264, 264, 16, T=110)
+    bad = Case(17, start, adapter, 2, H, N, 16, T=T)
     for t in (bad.x, bad.dy):
-        t[36:64] = float("nan")
+        t[36:mid] = float("nan")
         t[40] = float("inf")
         t[:5] = float("nan")
-        t[100:] = float("inf")
-    y = torch.full((110, 264), 55.0, device=DEV)
+        t[end:] = float("inf")
+    y = torch.full((T, N), 55.0, device=DEV)
     lx.lx_lora_forward(bad.x.to(DEV), base=None, y=y, **bad.set())
-    hx, hA, hB = torch.full((110, 264), 55.0, device=DEV), torch.empty_like(gA), torch.empty_like(gB)
+    hx, hA, hB = torch.full((T, H), 55.0, device=DEV), torch.empty_like(gA), torch.empty_like(gB)
     lx.lx_lora_backward(bad.dy.to(DEV), bad.x.to(DEV), base=None, grad_x=hx, grad_A=hA, grad_B=hB, **bad.set())
-    keep = list(range(0, 36)) + list(range(64, 110))
+    keep = list(range(0, 36)) + list(range(mid, T))
     assert torch.equal(y[keep], clean[keep]) and torch.equal(hx[keep], gx[keep])
     assert torch.equal(hA[0], gA[0]) and torch.equal(hB[0], gB[0])
     assert torch.isnan(hA[1]).any() and torch.isnan(hB[1]).any()
