@@ -117,6 +117,8 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+import torch  # noqa: E402  (already loaded, see _load)
+
 
 # ------------------------------------------------------------------ marshalling helpers
 
@@ -157,10 +159,15 @@ def _rows2d(t, name):
 
 
 def _arg(t, name, dtype, shape, device):
-    """A contiguous device tensor of this dtype and shape on this device."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+    """Refuses t unless it is a contiguous tensor of this dtype and shape on this device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+# The current stream's handle, without the stream object around it (3 us a call).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _Launch:
@@ -169,32 +176,35 @@ class _Launch:
     current one, and a workspace allocated here comes from the memory of the stream that
     uses it."""
 
+    __slots__ = ("device", "stream", "guard", "ptr")
+
     def __init__(self, device, stream):
-        import torch
-        self.device, self.stream = device, stream
-        self.guard = torch.cuda.device(device)
+        self.device, self.stream, self.guard = device, stream, None
 
     def __enter__(self):
-        self.guard.__enter__()
-        self.ptr = _stream(self.stream)
+        index = self.device.index
+        if torch.cuda.current_device() != index:
+            self.guard = torch.cuda.device(index)
+            self.guard.__enter__()
+        self.ptr = _current_raw_stream(index) if self.stream is None else _stream(self.stream)
         return self
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
     def workspace(self, given, need):
-        import torch
+        """(address, bytes, the tensor that holds them) of the given workspace or of a new one."""
         if given is not None:
             if given.device != self.device:
                 raise ValueError(f"workspace must be on {self.device}")
-        elif need:
-            if self.stream is None:
+        elif self.stream is None:
+            given = torch.empty(need, dtype=torch.uint8, device=self.device)
+        else:
+            s = self.stream if hasattr(self.stream, "cuda_stream") else torch.cuda.ExternalStream(self.ptr)
+            with torch.cuda.stream(s):
                 given = torch.empty(need, dtype=torch.uint8, device=self.device)
-            else:
-                s = self.stream if hasattr(self.stream, "cuda_stream") else torch.cuda.ExternalStream(self.ptr)
-                with torch.cuda.stream(s):
-                    given = torch.empty(need, dtype=torch.uint8, device=self.device)
-        return given, 0 if given is None else given.numel() * given.element_size()
+        return given.data_ptr(), given.numel() * given.element_size(), given
 
 
 def _check(status: int, where: str) -> None:
@@ -482,7 +492,6 @@ def lx_draft_verify(target, draft, draft_tokens, draft_start, max_draft: int, te
     float32 [S]; into ``n_accepted`` int64 [S], ``tokens`` int64 [S, max_draft + 1] and
     ``logprobs`` float32 [S, max_draft + 1] or None.  The workspace (uint8 device tensor) is
     allocated here with torch when not given."""
-    import torch
     rows, V, ldt = _rows2d(target, "target")
     dt, dev, max_draft = _dtype_code(target), target.device, int(max_draft)
     N, S = draft_tokens.shape[0], u_sample.shape[0]
@@ -490,7 +499,7 @@ def lx_draft_verify(target, draft, draft_tokens, draft_start, max_draft: int, te
         raise ValueError(f"target must have a row per draft and one per sequence, {N} + {S}, got {rows}")
     ldd = V
     if draft is not None:
-        if tuple(draft.shape) != (N, V) or draft.dtype != target.dtype or draft.device != dev:
+        if draft.shape != (N, V) or draft.dtype != target.dtype or draft.device != dev:
             raise ValueError(f"draft must be ({N}, {V}), of target's dtype and on its device")
         ldd = _rows2d(draft, "draft")[2]
     f32, i64 = torch.float32, torch.int64
@@ -505,10 +514,10 @@ def lx_draft_verify(target, draft, draft_tokens, draft_start, max_draft: int, te
     if logprobs is not None:
         _arg(logprobs, "logprobs", f32, (S, max_draft + 1), dev)
     with _Launch(dev, stream) as at:
-        ws, wbytes = at.workspace(workspace, lx_draft_verify_workspace_bytes(S, max_draft, V))
+        ws, wbytes, _held = at.workspace(workspace, lx_draft_verify_workspace_bytes(S, max_draft, V))
         _check(lib.lx_draft_verify(_ptr(target), ldt, _ptr(draft), ldd, _ptr(draft_tokens), _ptr(draft_start), S, N,
                                    max_draft, V, _ptr(temperature), _ptr(u_accept), _ptr(u_sample),
-                                   _ptr(n_accepted), _ptr(tokens), _ptr(logprobs), dt, _ptr(ws), wbytes, at.ptr),
+                                   _ptr(n_accepted), _ptr(tokens), _ptr(logprobs), dt, ws, wbytes, at.ptr),
                "lx_draft_verify")
 
 
@@ -522,7 +531,6 @@ def lx_lora_backward_workspace_bytes(T: int, R: int, n_adapters: int, H: int, N:
 
 def _lora_set(x, A, B, adapter, req_start, scale, rank):
     """(T, R, n_adapters, H, N, r, device) of the arguments that both directions take, checked."""
-    import torch
     dev, bf16, i64 = x.device, torch.bfloat16, torch.int64
     if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
         raise ValueError("A must be (n_adapters, r, H) and B (n_adapters, N, r)")
@@ -541,14 +549,13 @@ def _lora_set(x, A, B, adapter, req_start, scale, rank):
 
 def _rows_of(t, name, dtypes, rows, cols, dev):
     """The row stride of a 2-D (rows, cols) device tensor with contiguous rows, of one of these dtypes."""
-    if t.dtype not in dtypes or tuple(t.shape) != (rows, cols) or t.device != dev:
+    if t.dtype not in dtypes or t.shape != (rows, cols) or t.device != dev:
         raise ValueError(f"{name} must be ({rows}, {cols}) on {dev}, {' or '.join(map(str, dtypes))}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return _rows2d(t, name)[2]
 
 
 def _bf16_rows(t, name, rows, cols, dev):
-    import torch
     return _rows_of(t, name, (torch.bfloat16,), rows, cols, dev)
 
 
@@ -558,17 +565,16 @@ def lx_lora_forward(x, A, B, adapter, req_start, scale, rank, base, y, workspace
     ``req_start`` int64 [R + 1]; ``scale`` float32 [n_adapters], ``rank`` int64 [n_adapters]
     or None; ``base`` (T, N) or None and ``y`` (T, N), float32 or bfloat16 each (``y`` may be
     ``base``).  The workspace is allocated here with torch when not given."""
-    import torch
     T, R, n, H, N, r, dev = _lora_set(x, A, B, adapter, req_start, scale, rank)
     kinds = (torch.float32, torch.bfloat16)
     ldb = N if base is None else _rows_of(base, "base", kinds, T, N, dev)
     ldy = _rows_of(y, "y", kinds, T, N, dev)
     with _Launch(dev, stream) as at:
-        ws, wbytes = at.workspace(workspace, lx_lora_forward_workspace_bytes(T, R, H, N, r))
+        ws, wbytes, _held = at.workspace(workspace, lx_lora_forward_workspace_bytes(T, R, H, N, r))
         _check(lib.lx_lora_forward(_ptr(x), _rows2d(x, "x")[2], _ptr(A), _ptr(B), _ptr(adapter), _ptr(req_start),
                                    _ptr(scale), _ptr(rank), T, R, n, H, N, r, _ptr(base), ldb,
                                    LX_F32 if base is None else _dtype_code(base), _ptr(y), ldy, _dtype_code(y),
-                                   _ptr(ws), wbytes, at.ptr), "lx_lora_forward")
+                                   ws, wbytes, at.ptr), "lx_lora_forward")
 
 
 def lx_lora_backward(grad_y, x, A, B, adapter, req_start, scale, rank, base, grad_x, grad_A, grad_B, workspace=None,
@@ -576,7 +582,6 @@ def lx_lora_backward(grad_y, x, A, B, adapter, req_start, scale, rank, base, gra
     """The gradients of lx_lora_forward: ``grad_y`` (T, N) bfloat16 and its inputs, into
     ``grad_x`` (T, H) (``base`` or 0 added; may be ``base``), ``grad_A`` and ``grad_B`` (as A
     and B), float32, each or None; grad_A and grad_B are overwritten."""
-    import torch
     T, R, n, H, N, r, dev = _lora_set(x, A, B, adapter, req_start, scale, rank)
     f32 = (torch.float32,)
     lddy = _bf16_rows(grad_y, "grad_y", T, N, dev)
@@ -587,10 +592,10 @@ def lx_lora_backward(grad_y, x, A, B, adapter, req_start, scale, rank, base, gra
     if grad_B is not None:
         _arg(grad_B, "grad_B", torch.float32, (n, N, r), dev)
     with _Launch(dev, stream) as at:
-        ws, wbytes = at.workspace(workspace, lx_lora_backward_workspace_bytes(T, R, n, H, N, r))
+        ws, wbytes, _held = at.workspace(workspace, lx_lora_backward_workspace_bytes(T, R, n, H, N, r))
         _check(lib.lx_lora_backward(_ptr(grad_y), lddy, _ptr(x), _rows2d(x, "x")[2], _ptr(A), _ptr(B), _ptr(adapter),
                                     _ptr(req_start), _ptr(scale), _ptr(rank), T, R, n, H, N, r, _ptr(base), ldb,
-                                    _ptr(grad_x), ldgx, _ptr(grad_A), _ptr(grad_B), _ptr(ws), wbytes, at.ptr),
+                                    _ptr(grad_x), ldgx, _ptr(grad_A), _ptr(grad_B), ws, wbytes, at.ptr),
                "lx_lora_backward")
 
 

@@ -111,36 +111,36 @@ __device__ __forceinline__ void load_edge(const T* row, int64_t v, int64_t end, 
   for (int k = 0; k < 8; ++k) x[k] = v + k < end ? load1(row + v + k) : ninf();
 }
 
-// Elements [lo, hi) of a row, lo a multiple of kVUnit from the row's start: f(v, x) for
-// every group of 8 of this thread, with up to kVHold groups loaded at once.
-template <typename T, typename F>
-__device__ __forceinline__ void for_groups(const T* row, int64_t lo, int64_t hi, F f) {
-  const int tid = tid_x();
-  const int64_t whole = lo + (hi - lo) / 8 * 8;
-  if (whole == lo) {
-    float x[8];
-    if (tid == 0 && lo < hi) {
-      load_edge(row, lo, hi, x);
-      f(lo, x);
-    }
-    return;
+// H groups of a thread: elements b + k kVUnit + 8 tid .. + 7 of a row of V, k < H, -inf behind its
+// end.  In two parts, so that several rows' loads can be in flight; no load is conditional.
+template <typename T, int H>
+__device__ __forceinline__ void hold(const T* row, int64_t b, int64_t V, Group<T> (&g)[H]) {
+  if (V < 8) return;
+#pragma unroll
+  for (int k = 0; k < H; ++k) {
+    const int64_t v = b + k * kVUnit + tid_x() * 8;
+    g[k].load(row + (v < V - 8 ? v : V - 8));
   }
+}
+template <typename T>
+__device__ __forceinline__ void held(const T* row, int64_t v, int64_t V, const Group<T>& g, float (&x)[8]) {
+  if (v + 8 <= V) g.get(x);
+  else load_edge(row, v, V, x);
+}
+
+// Elements [lo, hi) of a row of V, lo a multiple of kVUnit: f(v, x) for every group of 8 of this
+// thread, with kVHold groups loaded at once.
+template <typename T, typename F>
+__device__ __forceinline__ void for_groups(const T* row, int64_t lo, int64_t hi, int64_t V, F f) {
   for (int64_t b = lo; b < hi; b += kVUnit * kVHold) {
     Group<T> g[kVHold];
-#pragma unroll
-    for (int k = 0; k < kVHold; ++k) {
-      const int64_t v = b + k * kVUnit + tid * 8;
-      g[k].load(row + (v < whole ? v : whole - 8));  // (without a condition: the loads stay in flight together)
-    }
+    hold<T, kVHold>(row, b, V, g);
     float x[8];
 #pragma unroll
     for (int k = 0; k < kVHold; ++k) {
-      const int64_t v = b + k * kVUnit + tid * 8;
-      if (v < whole) {
-        g[k].get(x);
-        f(v, x);
-      } else if (v < hi) {
-        load_edge(row, v, hi, x);
+      const int64_t v = b + k * kVUnit + tid_x() * 8;
+      if (v < hi) {
+        held(row, v, V, g[k], x);
         f(v, x);
       }
     }
@@ -234,22 +234,6 @@ __device__ __forceinline__ void add8(Sum32& a, const float (&x)[8], float c) {
   a.m = mn;
   a.s = s0 + s1;
 }
-// (the maximum rises a few times in a thread's elements at most, so the rescale is a branch)
-__device__ __forceinline__ void add8(Sum64& a, const float (&x)[8], double c) {
-  const float mn = fmaxf(a.m, max8(x));
-  const double ref = (double)ref_of(mn);
-  if (mn != a.m) {
-    a.s *= exp2_64(((double)a.m - ref) * c);
-    a.m = mn;
-  }
-  double s0 = 0.0, s1 = 0.0;
-#pragma unroll
-  for (int k = 0; k < 8; k += 2) {
-    s0 += exp2_64(((double)x[k] - ref) * c);
-    s1 += exp2_64(((double)x[k + 1] - ref) * c);
-  }
-  a.s += s0 + s1;
-}
 __device__ __forceinline__ void add8(Best& a, int64_t v, const float (&x)[8]) {
   const float m = max8(x);
   if (m > a.v) {
@@ -263,28 +247,81 @@ __device__ __forceinline__ void add8(Best& a, int64_t v, const float (&x)[8]) {
 
 // ------------------------------------------------------------------ reductions over a workgroup
 
-__device__ __forceinline__ float wave_max(float v) {
+// Over the 64 lanes on the vector ALU: quad permutations and rotations inside each row of 16
+// lanes, then the gfx950 swaps of rows and of halves.  (These reductions sit one behind the
+// other on every call's critical path; through LDS permutes they took several times as long.)
+template <int CTRL>
+__device__ __forceinline__ unsigned dpp(unsigned v) {
+  return (unsigned)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
+}
+template <typename T, typename F>
+__device__ __forceinline__ T wave_all(T v, F f) {
+  constexpr int kWords = sizeof(T) / 4;
+  struct Words {
+    unsigned w[kWords];
+  };
+  auto step = [&](auto move) {
+    Words a = __builtin_bit_cast(Words, v), o;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+    for (int k = 0; k < kWords; ++k) o.w[k] = move(a.w[k]);
+    v = f(v, __builtin_bit_cast(T, o));
+  };
+  step([](unsigned u) { return dpp<0xB1>(u); });   // quad_perm [1, 0, 3, 2]
+  step([](unsigned u) { return dpp<0x4E>(u); });   // quad_perm [2, 3, 0, 1]
+  step([](unsigned u) { return dpp<0x124>(u); });  // row_ror 4
+  step([](unsigned u) { return dpp<0x128>(u); });  // row_ror 8
+  // (a swap of a value with itself leaves one row's value in the first result and the other's in the
+  // second, for the lanes of both; the elements go through scalars, which this compiler needs)
+  auto both = [&](auto swap) {
+    Words a = __builtin_bit_cast(Words, v), x, y;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const auto pr = swap(a.w[k]);
+      const unsigned lo = pr[0], hi = pr[1];
+      x.w[k] = lo;
+      y.w[k] = hi;
+    }
+    v = f(__builtin_bit_cast(T, x), __builtin_bit_cast(T, y));
+  };
+  both([](unsigned u) { return __builtin_amdgcn_permlane16_swap(u, u, false, false); });
+  both([](unsigned u) { return __builtin_amdgcn_permlane32_swap(u, u, false, false); });
   return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_all(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum32(float v) {
+  return wave_all(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  return wave_all(v, [](double a, double b) { return a + b; });
 }
 __device__ __forceinline__ unsigned wave_min_u(unsigned v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const unsigned o = __shfl_xor(v, off, 64);
-    v = o < v ? o : v;
-  }
+  return wave_all(v, [](unsigned a, unsigned b) { return a < b ? a : b; });
+}
+
+// Inclusive prefix sums over the wave: row shifts inside the rows of 16 lanes, then the
+// last lane of a row to the next row, and of the first half to the second.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_shift64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, ROWS, 0xF, true);
+  const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, ROWS, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+__device__ __forceinline__ double wave_scan64(double v) {
+  v += dpp_shift64<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8 (0 comes in)
+  v += dpp_shift64<0x112, 0xF>(v);
+  v += dpp_shift64<0x114, 0xF>(v);
+  v += dpp_shift64<0x118, 0xF>(v);
+  v += dpp_shift64<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+  v += dpp_shift64<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
   return v;
 }
 
 __device__ __forceinline__ Sum32 wave_merge(Sum32 a, float c) {
   const float m = wave_max(a.m);
-  return Sum32{m, wave_sum(a.s * exp2_hw((a.m - ref_of(m)) * c))};
+  return Sum32{m, wave_sum32(a.s * exp2_hw((a.m - ref_of(m)) * c))};
 }
 __device__ __forceinline__ Sum64 wave_merge(Sum64 a, double c) {
   const float m = wave_max(a.m);
@@ -347,22 +384,23 @@ struct Ws {
 };
 
 // Chunks of a row: whole kVUnits, `per` of them each, so that `rows` rows make enough
-// workgroups for the chip (1024) before chunks grow, and at most 8 of them (16384
-// elements): a longer chunk would only delay the decision that spares later positions.
-void chunking(int64_t rows, int64_t V, int64_t& chunk, int& K) {
+// workgroups for the chip (1024) before chunks grow, and at most `most` of them.
+void chunking(int64_t rows, int64_t V, int64_t most, int64_t& chunk, int& K) {
   const int64_t units = (V + kVUnit - 1) / kVUnit;
   int64_t per = rows * units / 1024;
-  per = per < 1 ? 1 : per > 8 ? 8 : per;
+  per = per < 1 ? 1 : per > most ? most : per;
   const int64_t least = (units + kVMaxChunks - 1) / kVMaxChunks;
-  if (per < least) per = least;
+  if (per < least) per = (least + 1) / 2 * 2;  // (whole rounds of two groups)
   chunk = per * kVUnit;
   K = (int)((units + per - 1) / per);
 }
 
 Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
   Ws w{};
-  chunking(S * L, V, w.chunk1, w.K1);
-  chunking(S, V, w.chunk2, w.K2);
+  // step 1: at most 16384 elements (a longer chunk delays the decision that spares later
+  // positions); steps 2 and 3: what a thread holds at once
+  chunking(S * L, V, 8, w.chunk1, w.K1);
+  chunking(S, V, 2, w.chunk2, w.K2);
   size_t off = 0;
   char* p = static_cast<char*>(base);
   auto take = [&](size_t bytes) {
@@ -388,6 +426,7 @@ Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
 struct Args {
   VerifyArgs a;
   Ws w;
+  bool look;  // step 1: whether to look for rejections in front (not when all workgroups run at once)
 };
 
 __global__ __launch_bounds__(kVThreads) void verify_init_kernel(int* __restrict__ first, int S, int* __restrict__ zero,
@@ -419,7 +458,7 @@ template <typename T>
 __device__ double row_sum64(const T* row, int64_t V, float m, double c, double* red) {
   const double ref = (double)ref_of(m);
   double s = 0.0;
-  for_groups(row, 0, V, [&](int64_t, const float (&x)[8]) {
+  for_groups(row, 0, V, V, [&](int64_t, const float (&x)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) s += exp2_64(((double)x[k] - ref) * c);
   });
@@ -451,25 +490,32 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
   if (j >= q.n) return;
   // a rejection before this position: nothing here is asked for (one load per
   // workgroup, so that all its threads go the same way)
-  if (tid == 0)
-    sh_flag = __hip_atomic_load(w.first + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < j;
-  __syncthreads();
-  if (sh_flag) return;
+  if (g.look && j > 0) {
+    if (tid == 0) sh_flag = __hip_atomic_load(w.first + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < j;
+    __syncthreads();
+    if (sh_flag) return;
+  }
   const Temp t = temp_of(a.temperature, i);
   const T* zr = static_cast<const T*>(a.target) + (q.first + i + j) * a.ldt;
   const bool has_d = a.draft != nullptr && !t.greedy;
   const T* ur = has_d ? static_cast<const T*>(a.draft) + (q.first + j) * a.ldd : nullptr;
   const int64_t lo = c * w.chunk1, hi = lo + w.chunk1 < a.V ? lo + w.chunk1 : a.V;
+  // what the decision needs, requested ahead of the row
+  const int64_t x = a.tokens[q.first + j];
+  const bool x_ok = x >= 0 && x < a.V;
+  const float r32 = a.u_accept[q.first + j];
+  const float zx = x_ok ? load1(zr + x) : ninf();
+  const float ux = x_ok && has_d ? load1(ur + x) : ninf();
 
   if (t.greedy) {
     Best b{ninf(), kNone};
-    for_groups(zr, lo, hi, [&](int64_t v, const float (&x)[8]) { add8(b, v, x); });
+    for_groups(zr, lo, hi, a.V, [&](int64_t v, const float (&e)[8]) { add8(b, v, e); });
     b = wave_merge(b);
     if (lane == 0) red[0][wave] = pack(b.v, b.at);
   } else {
     Sum32 st{ninf(), 0.0f}, sd{ninf(), 0.0f};
-    for_groups(zr, lo, hi, [&](int64_t, const float (&x)[8]) { add8(st, x, t.c); });
-    if (has_d) for_groups(ur, lo, hi, [&](int64_t, const float (&x)[8]) { add8(sd, x, t.c); });
+    for_groups(zr, lo, hi, a.V, [&](int64_t, const float (&e)[8]) { add8(st, e, t.c); });
+    if (has_d) for_groups(ur, lo, hi, a.V, [&](int64_t, const float (&e)[8]) { add8(sd, e, t.c); });
     st = wave_merge(st, t.c);
     if (has_d) sd = wave_merge(sd, t.c);
     if (lane == 0) {
@@ -509,8 +555,6 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
 
   // the position's last workgroup: merge the chunks and decide
   const uint64_t* parts = w.part1 + (int64_t)slot * K * kP1;
-  const int64_t x = a.tokens[q.first + j];
-  const bool x_ok = x >= 0 && x < a.V;
   if (t.greedy) {
     if (wave == 0) {
       Best b{ninf(), kNone};
@@ -549,9 +593,7 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
     }
   }
   __syncthreads();
-  const double r = (double)a.u_accept[q.first + j];
-  const float zx = x_ok ? load1(zr + x) : ninf();
-  const float ux = x_ok && has_d ? load1(ur + x) : ninf();
+  const double r = (double)r32;
   const double ez = exp2_64(((double)zx - (double)ref_of(sh_m[0])) * t.c64);
   const double eu = has_d ? exp2_64(((double)ux - (double)ref_of(sh_m[1])) * t.c64) : 1.0;
   double St = sh_s[0], Sd = has_d ? sh_s[1] : 1.0;
@@ -574,7 +616,7 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
 
 // ------------------------------------------------------------------ steps 2 and 3: the token behind the accepted ones
 
-// The masses that the token is drawn from, relative to what the callers hold.
+// The masses that the token is drawn from: p relative to mt, or max(p - q, 0).
 template <typename T>
 struct Masses {
   const T *zr, *ur;  // ur: the residual's draft row, or nullptr
@@ -582,72 +624,55 @@ struct Masses {
   double c, mt, md;  // references
   double it, id;     // residual: 1 / S_t, 1 / S_d
 
-  // masses of elements v .. v + 7 (v a multiple of 8 from the row's start)
-  __device__ __forceinline__ void get(int64_t v, double (&e)[8]) const {
-    float x[8];
-    fill(zr, v, x);
-    if (ur) {
-      float y[8];
-      fill(ur, v, y);
-      of(v, x, y, e);
-    } else {
-      of(v, x, e);
-    }
-  }
-  __device__ __forceinline__ void of(int64_t v, const float (&x)[8], double (&e)[8]) const {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = v + k == skip ? 0.0 : exp2_64(((double)x[k] - mt) * c);
-  }
-  __device__ __forceinline__ void of(int64_t, const float (&x)[8], const float (&y)[8], double (&e)[8]) const {
+  __device__ __forceinline__ void of(int64_t v, const float (&x)[8], const float (&y)[8], double (&e)[8]) const {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const double d = exp2_64(((double)x[k] - mt) * c) * it - exp2_64(((double)y[k] - md) * c) * id;
-      e[k] = d > 0.0 ? d : 0.0;
+      const double p = exp2_64(((double)x[k] - mt) * c);
+      if (ur) {
+        const double d = p * it - exp2_64(((double)y[k] - md) * c) * id;
+        e[k] = d > 0.0 ? d : 0.0;
+      } else {
+        e[k] = v + k == skip ? 0.0 : p;
+      }
     }
   }
-  __device__ __forceinline__ void fill(const T* row, int64_t v, float (&x)[8]) const {
-    if (v + 8 <= V) {
-      Group<T> g;
-      g.load(row + v);
-      g.get(x);
-    } else {
-      load_edge(row, v, V, x);
-    }
+  // of elements v .. v + 7, with the target's logits
+  __device__ __forceinline__ void get(int64_t b, float (&x)[8], double (&e)[8]) const {
+    const int64_t v = b + tid_x() * 8;
+    Group<T> g[1], d[1];
+    hold<T, 1>(zr, b, V, g);
+    if (ur) hold<T, 1>(ur, b, V, d);
+    float y[8];
+    held(zr, v, V, g[0], x);
+    if (ur) held(ur, v, V, d[0], y);
+    of(v, x, y, e);
   }
 };
-
-// Wave-wide inclusive prefix sum.
-__device__ __forceinline__ double wave_scan64(double v, int lane) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const double o = __shfl_up(v, off, 64);
-    if (lane >= off) v += o;
-  }
-  return v;
-}
 
 struct PickShared {
   double sums[kVMaxChunks];
   double wave[kVWaves];
   double before;  // the sum in front of the chosen chunk
   int chunk;
-  int found;  // token + 1 of the border's element, 0: not found
+  int found;  // 2^31 - 1 - (token + 1) of the border's element, 0: not found
   int last;   // token + 1 of the last element with mass
+  float z;    // the token's target logit
 };
 
 // The token at w of the total, by the workgroup: the chunk whose running sum first
 // exceeds w * total (sums[0..K) filled by the caller, scaled like the masses), then
 // the element.  The running sums are in vocabulary order.  Should rounding leave no
 // element above the goal, the last one with mass is the token; -1: no mass at all.
+// sh.z: its target logit.
 template <typename T>
-__device__ int64_t pick(const Masses<T>& m, PickShared& sh, int K, int64_t chunk, double w) {
+__device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int K, int64_t chunk, double w) {
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   if (wave == 0) {
     // each lane a run of consecutive chunks
     const int per = (K + 63) / 64, k0 = lane * per, k1 = k0 + per < K ? k0 + per : K;
     double own = 0.0;
     for (int k = k0; k < k1; ++k) own += sh.sums[k];
-    const double upto = wave_scan64(own, lane);
+    const double upto = wave_scan64(own);
     const double total = __shfl(upto, 63, 64);
     const double goal = w * total;
     double run = upto - own;
@@ -683,17 +708,16 @@ __device__ int64_t pick(const Masses<T>& m, PickShared& sh, int K, int64_t chunk
   double base = 0.0;
   for (int64_t b = lo; b < hi; b += kVUnit) {
     const int64_t v = b + tid * 8;
+    float x[8];
     double e[8], own = 0.0;
     int last = 0;
-    if (v < hi) {
-      m.get(v, e);
+    m.get(b, x, e);  // (0 behind the row's end, which is the only place a chunk ends short)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        own += e[k];
-        if (e[k] > 0.0) last = (int)(v + k) + 1;
-      }
+    for (int k = 0; k < 8; ++k) {
+      own += e[k];
+      if (e[k] > 0.0) last = (int)(v + k) + 1;
     }
-    const double incl = wave_scan64(own, lane);
+    const double incl = wave_scan64(own);
     if (lane == 63) sh.wave[wave] = incl;
     if (last) atomicMax(&sh.last, last);
     __syncthreads();
@@ -705,22 +729,33 @@ __device__ int64_t pick(const Masses<T>& m, PickShared& sh, int K, int64_t chunk
     }
     if (all > goal) {
       // the first element whose running sum exceeds the goal: the lowest token among the finds
-      if (v < hi && run + own > goal) {
-        int at = 0;
+      int at = 0;
+      float z = 0.0f;
+      if (run + own > goal) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           run += e[k];
-          if (!at && e[k] > 0.0 && run > goal) at = (int)(v + k) + 1;
+          if (!at && e[k] > 0.0 && run > goal) {
+            at = (int)(v + k) + 1;
+            z = x[k];
+          }
         }
         // (positive, so that atomicMax of the negative keeps the lowest)
         if (at) atomicMax(&sh.found, 0x7fffffff - at);
       }
       __syncthreads();
-      if (sh.found) return 0x7fffffff - sh.found - 1;
+      const int found = sh.found;
+      if (found) {
+        if (at && found == 0x7fffffff - at) sh.z = z;
+        __syncthreads();
+        return 0x7fffffff - found - 1;
+      }
     }
     base = all;
     __syncthreads();  // sh.wave is written again
   }
+  if (tid == 0 && sh.last > 0) sh.z = load1(m.zr + sh.last - 1);
+  __syncthreads();
   return sh.last - 1;
 }
 
@@ -736,12 +771,30 @@ __device__ __forceinline__ void write_out(const VerifyArgs& a, const Ws& w, int 
 }
 
 // log p of a token from its logit and the row's sum.
-template <typename T>
-__device__ __forceinline__ float logp_of(const T* zr, int64_t tok, float m, double s, const Temp& t) {
-  return tok < 0 ? 0.0f : (float)(((double)load1(zr + tok) - (double)m) * t.inv - log_64(s));
+__device__ __forceinline__ float logp_of(int64_t tok, float z, float m, double s, const Temp& t) {
+  return tok < 0 ? 0.0f : (float)(((double)z - (double)m) * t.inv - log_64(s));
 }
 
-template <typename T>
+// max over the workgroup of two values (red: scratch, free afterwards behind the caller's next barrier)
+__device__ __forceinline__ void block_max2(float& a, float& b, float (&red)[2][kVWaves]) {
+  a = wave_max(a);
+  b = wave_max(b);
+  if ((tid_x() & 63) == 0) {
+    red[0][tid_x() >> 6] = a;
+    red[1][tid_x() >> 6] = b;
+  }
+  __syncthreads();
+  a = red[0][0];
+  b = red[1][0];
+#pragma unroll
+  for (int k = 1; k < kVWaves; ++k) {
+    a = fmaxf(a, red[0][k]);
+    b = fmaxf(b, red[1][k]);
+  }
+}
+
+// H: groups of 8 that a thread holds (a chunk is one or more rounds of them).
+template <typename T, int H>
 __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   const VerifyArgs& a = g.a;
   const Ws& w = g.w;
@@ -749,8 +802,6 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   __shared__ double red64[2][kVWaves];
   __shared__ float red_m[2][kVWaves];
   __shared__ PickShared sh;
-  __shared__ float sh_m[2];
-  __shared__ double sh_s[2];
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   const int K = w.K2;
@@ -771,7 +822,7 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   uint64_t* part = w.part2 + ((int64_t)i * K + c) * kP2;
   if (t.greedy) {
     Best b{ninf(), kNone};
-    for_groups(zr, lo, hi, [&](int64_t v, const float (&x)[8]) { add8(b, v, x); });
+    for_groups(zr, lo, hi, a.V, [&](int64_t v, const float (&x)[8]) { add8(b, v, x); });
     b = wave_merge(b);
     if (lane == 0) red[wave] = pack(b.v, b.at);
     __syncthreads();
@@ -799,116 +850,147 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
     return;
   }
 
-  // fp64 sums of the chunk, each against its own maximum; the token left out is summed on its own
-  Sum64 st{ninf(), 0.0}, sd{ninf(), 0.0};
-  for_groups(zr, lo, hi, [&](int64_t v, const float (&x)[8]) {
-    if (skip >= v && skip < v + 8) {
-      float y[8];
+  // fp64 sums of the chunk, each against the chunk's maximum; the token left out on its own
+  float mt = ninf(), md = ninf();
+  double st = 0.0, sd = 0.0;
+  for (int64_t b = lo; b < hi; b += kVUnit * H) {
+    Group<T> gz[H], gu[H];
+    hold<T, H>(zr, b, a.V, gz);
+    if (residual) hold<T, H>(ur, b, a.V, gu);
+    float x[H][8], y[H][8];
+    float xm = ninf(), ym = ninf();
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        y[k] = v + k == skip ? ninf() : x[k];
-        if (v + k == skip) sd = Sum64{x[k], x[k] == ninf() ? 0.0 : 1.0};
+    for (int h = 0; h < H; ++h) {
+      const int64_t v = b + h * kVUnit + tid * 8;
+      held(zr, v, a.V, gz[h], x[h]);
+      if (residual) {
+        held(ur, v, a.V, gu[h], y[h]);
+        ym = fmaxf(ym, max8(y[h]));
+      } else if (skip >= v && skip < v + 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (v + k == skip) {
+            ym = x[h][k];
+            x[h][k] = ninf();
+          }
+        }
       }
-      add8(st, y, t.c64);
-    } else {
-      add8(st, x, t.c64);
+      xm = fmaxf(xm, max8(x[h]));
     }
-  });
-  if (residual) for_groups(ur, lo, hi, [&](int64_t, const float (&x)[8]) { add8(sd, x, t.c64); });
-  st = wave_merge(st, t.c64);
-  sd = wave_merge(sd, t.c64);
+    const float left_out = ym;
+    block_max2(xm, ym, red_m);
+    if (b > lo) {  // (a chunk of several rounds)
+      xm = fmaxf(xm, mt);
+      ym = fmaxf(ym, md);
+      st *= exp2_64(((double)mt - (double)ref_of(xm)) * t.c64);
+      sd *= exp2_64(((double)md - (double)ref_of(ym)) * t.c64);
+    }
+    mt = xm;
+    md = ym;
+    const double rt = (double)ref_of(mt), rd = (double)ref_of(md);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) st += exp2_64(((double)x[h][k] - rt) * t.c64);
+    if (residual) {
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sd += exp2_64(((double)y[h][k] - rd) * t.c64);
+    } else if (left_out > ninf()) {
+      sd = 1.0;
+    }
+    __syncthreads();  // (red_m is written again)
+  }
+  st = wave_sum64(st);
+  sd = wave_sum64(sd);
   if (lane == 0) {
-    red_m[0][wave] = st.m;
-    red64[0][wave] = st.s;
-    red_m[1][wave] = sd.m;
-    red64[1][wave] = sd.s;
+    red64[0][wave] = st;
+    red64[1][wave] = sd;
   }
   __syncthreads();
   if (tid == 0) {
-    float m[2];
-    double s[2];
+    st = red64[0][0];
+    sd = red64[1][0];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      m[h] = ninf();
-#pragma unroll
-      for (int k = 0; k < kVWaves; ++k) m[h] = fmaxf(m[h], red_m[h][k]);
-      s[h] = 0.0;
-#pragma unroll
-      for (int k = 0; k < kVWaves; ++k)
-        s[h] += red64[h][k] * exp2_64(((double)red_m[h][k] - (double)ref_of(m[h])) * t.c64);
+    for (int k = 1; k < kVWaves; ++k) {
+      st += red64[0][k];
+      sd += red64[1][k];
     }
-    publish(part, pack(m[0], __float_as_uint(m[1])));
-    publish(part + 1, s[0]);
-    publish(part + 2, s[1]);
+    publish(part, pack(mt, __float_as_uint(md)));
+    publish(part + 1, st);
+    publish(part + 2, sd);
     sh_flag = count_last(w.count2 + i, K);
   }
   __syncthreads();
   if (!sh_flag) return;
 
-  // the sequence's last workgroup: the row's sums
+  // the sequence's last workgroup: the row's sums.  A thread takes every kVThreads-th chunk.
   const uint64_t* parts = w.part2 + (int64_t)i * K * kP2;
-  if (wave == 0) {
-    float m0 = ninf(), m1 = ninf();
-    for (int k = lane; k < K; k += 64) {
-      const uint64_t v = fetch(parts + k * kP2);
-      m0 = fmaxf(m0, lo_of(v));
-      m1 = fmaxf(m1, __uint_as_float(hi_of(v)));
-    }
-    m0 = wave_max(m0);
-    m1 = wave_max(m1);
-    double s0 = 0.0, s1 = 0.0;
-    for (int k = lane; k < K; k += 64) {
-      const uint64_t v = fetch(parts + k * kP2);
-      const double e = fetch64(parts + k * kP2 + 1) * exp2_64(((double)lo_of(v) - (double)ref_of(m0)) * t.c64);
-      sh.sums[k] = e;
-      s0 += e;
-      s1 += fetch64(parts + k * kP2 + 2) *
-            exp2_64(((double)__uint_as_float(hi_of(v)) - (double)ref_of(m1)) * t.c64);
-    }
-    s0 = wave_sum64(s0);
-    s1 = wave_sum64(s1);
-    if (lane == 0) {
-      sh_m[0] = m0;
-      sh_m[1] = m1;
-      sh_s[0] = s0;
-      sh_s[1] = s1;
+  float m0 = ninf(), m1 = ninf();
+  uint64_t pm[kVMaxChunks / kVThreads];
+  double p0[kVMaxChunks / kVThreads], p1[kVMaxChunks / kVThreads];
+#pragma unroll
+  for (int n = 0; n < kVMaxChunks / kVThreads; ++n) {
+    const int k = tid + n * kVThreads;
+    if (k < K) {
+      pm[n] = fetch(parts + k * kP2);
+      p0[n] = fetch64(parts + k * kP2 + 1);
+      p1[n] = fetch64(parts + k * kP2 + 2);
+      m0 = fmaxf(m0, lo_of(pm[n]));
+      m1 = fmaxf(m1, __uint_as_float(hi_of(pm[n])));
     }
   }
+  block_max2(m0, m1, red_m);
+  double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+  for (int n = 0; n < kVMaxChunks / kVThreads; ++n) {
+    const int k = tid + n * kVThreads;
+    if (k < K) {
+      const double e = p0[n] * exp2_64(((double)lo_of(pm[n]) - (double)ref_of(m0)) * t.c64);
+      sh.sums[k] = e;
+      s0 += e;
+      s1 += p1[n] * exp2_64(((double)__uint_as_float(hi_of(pm[n])) - (double)ref_of(m1)) * t.c64);
+    }
+  }
+  s0 = wave_sum64(s0);
+  s1 = wave_sum64(s1);
+  if (lane == 0) {
+    red64[0][wave] = s0;
+    red64[1][wave] = s1;
+  }
   __syncthreads();
+  s0 = red64[0][0];
+  s1 = red64[1][0];
+#pragma unroll
+  for (int k = 1; k < kVWaves; ++k) {
+    s0 += red64[0][k];
+    s1 += red64[1][k];
+  }
   if (residual) {
     if (tid == 0) {
       uint64_t* st_out = w.state + (int64_t)i * kSt;
-      st_out[0] = pack(sh_m[0], __float_as_uint(sh_m[1]));
-      st_out[1] = __builtin_bit_cast(uint64_t, sh_s[0]);
-      st_out[2] = __builtin_bit_cast(uint64_t, sh_s[1]);
+      st_out[0] = pack(m0, __float_as_uint(m1));
+      st_out[1] = __builtin_bit_cast(uint64_t, s0);
+      st_out[2] = __builtin_bit_cast(uint64_t, s1);
     }
     return;
   }
-  float m = sh_m[0];
-  double s = sh_s[0];
-  int64_t left_out = skip;
-  if (skip >= 0) {
-    // with no mass beside the token left out it is drawn after all (p is 1 there)
-    if (!(s > 0.0)) left_out = -1;
-    const float mn = fmaxf(m, sh_m[1]);
-    const double full = s * exp2_64(((double)m - (double)ref_of(mn)) * t.c64) +
-                        sh_s[1] * exp2_64(((double)sh_m[1] - (double)ref_of(mn)) * t.c64);
-    if (left_out < 0) {
-      if (tid == 0 && skip < a.V) sh.sums[skip / w.chunk2] = sh_s[1];
-      __syncthreads();
-      m = mn;
-    }
-    const Masses<T> ms{zr, nullptr, a.V, left_out, t.c64, (double)ref_of(m), 0.0, 0.0, 0.0};
-    const int64_t tok = pick(ms, sh, K, w.chunk2, (double)a.u_sample[i]);
-    write_out(a, w, i, q, acc, tok, logp_of(zr, tok, mn, full, t));
-    return;
-  }
-  const Masses<T> ms{zr, nullptr, a.V, -1, t.c64, (double)ref_of(m), 0.0, 0.0, 0.0};
+  // p's sum is the token left out and the rest together; with no mass in the rest, that token is
+  // drawn after all (p is 1 there)
+  const float mn = skip >= 0 ? fmaxf(m0, m1) : m0;
+  const double full = skip >= 0 ? s0 * exp2_64(((double)m0 - (double)ref_of(mn)) * t.c64) +
+                                      s1 * exp2_64(((double)m1 - (double)ref_of(mn)) * t.c64)
+                                : s0;
+  const bool only = skip >= 0 && !(s0 > 0.0);
+  if (only && tid == 0 && skip < a.V) sh.sums[skip / w.chunk2] = s1;
+  const Masses<T> ms{zr, nullptr, a.V, only ? -1 : skip, t.c64, (double)ref_of(only ? mn : m0), 0.0, 0.0, 0.0};
+  __syncthreads();  // (sh.sums)
   const int64_t tok = pick(ms, sh, K, w.chunk2, (double)a.u_sample[i]);
-  write_out(a, w, i, q, acc, tok, logp_of(zr, tok, m, s, t));
+  write_out(a, w, i, q, acc, tok, logp_of(tok, sh.z, mn, full, t));
 }
 
-template <typename T>
+template <typename T, int H>
 __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
   const VerifyArgs& a = g.a;
   const Ws& w = g.w;
@@ -932,11 +1014,21 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
   Masses<T> ms{zr, ur, a.V, -1, t.c64, (double)ref_of(mt), (double)ref_of(md), St > 0.0 ? 1.0 / St : 0.0,
                Sd > 0.0 ? 1.0 / Sd : 0.0};
   double s = 0.0;
-  for (int64_t v = lo + tid * 8; v < hi; v += kVUnit) {
-    double e[8];
-    ms.get(v, e);
+  for (int64_t b = lo; b < hi; b += kVUnit * H) {
+    Group<T> gz[H], gu[H];
+    hold<T, H>(zr, b, a.V, gz);
+    hold<T, H>(ur, b, a.V, gu);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += e[k];
+    for (int h = 0; h < H; ++h) {
+      const int64_t v = b + h * kVUnit + tid * 8;
+      float x[8], y[8];
+      double e[8];
+      held(zr, v, a.V, gz[h], x);
+      held(ur, v, a.V, gu[h], y);
+      ms.of(v, x, y, e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += e[k];
+    }
   }
   s = wave_sum64(s);
   if (lane == 0) red64[wave] = s;
@@ -972,14 +1064,16 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
     ms.ur = nullptr;
   }
   const int64_t tok = pick(ms, sh, K, w.chunk2, (double)a.u_sample[i]);
-  write_out(a, w, i, q, acc, tok, logp_of(zr, tok, mt, St, t));
+  write_out(a, w, i, q, acc, tok, logp_of(tok, sh.z, mt, St, t));
 }
 
 template <typename T>
 hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
   (void)hipGetLastError();
-  Args g{a, verify_ws(a.workspace, a.S, a.L, a.V)};
+  Args g{a, verify_ws(a.workspace, a.S, a.L, a.V), false};
   const Ws& w = g.w;
+  // (2048 workgroups run at once: none of them could spare another anything)
+  g.look = a.S * a.L * w.K1 > 2048;
   const int64_t n = w.n_zero > a.S ? w.n_zero : a.S;
   hipLaunchKernelGGL(verify_init_kernel, dim3((unsigned)((n + kVThreads - 1) / kVThreads)), dim3(kVThreads), 0, st,
                      w.first, (int)a.S, w.count1, w.n_zero);
@@ -988,13 +1082,16 @@ hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((verify_accept_kernel<T>), dim3((unsigned)(a.S * a.L * w.K1)), dim3(kVThreads), 0, st, g);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  hipLaunchKernelGGL((verify_sums_kernel<T>), dim3((unsigned)(a.S * w.K2)), dim3(kVThreads), 0, st, g);
+  const dim3 grid((unsigned)(a.S * w.K2)), block(kVThreads);
+  const bool one = w.chunk2 == kVUnit, residual = a.L > 0 && a.draft;
+  if (one) hipLaunchKernelGGL((verify_sums_kernel<T, 1>), grid, block, 0, st, g);
+  else hipLaunchKernelGGL((verify_sums_kernel<T, 2>), grid, block, 0, st, g);
   if (hipError_t e = hipGetLastError()) return e;
-  if (a.L > 0 && a.draft) {
-    hipLaunchKernelGGL((verify_residual_kernel<T>), dim3((unsigned)(a.S * w.K2)), dim3(kVThreads), 0, st, g);
-    return hipGetLastError();
+  if (residual) {
+    if (one) hipLaunchKernelGGL((verify_residual_kernel<T, 1>), grid, block, 0, st, g);
+    else hipLaunchKernelGGL((verify_residual_kernel<T, 2>), grid, block, 0, st, g);
   }
-  return hipSuccess;
+  return hipGetLastError();
 }
 
 }  // namespace
