@@ -122,6 +122,18 @@ __device__ __forceinline__ void hold(const T* row, int64_t b, int64_t V, Group<T
     g[k].load(row + (v < V - 8 ? v : V - 8));
   }
 }
+// Hides a held group from common-subexpression elimination, so that its packed registers live
+// from one use to the next and not the (two to four times as many) widened floats.
+__device__ __forceinline__ void launder(u32x4_t& w) {
+  unsigned a = w.x, b = w.y, c = w.z, d = w.w;
+  asm volatile("" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+  w = (u32x4_t){a, b, c, d};
+}
+template <typename T>
+__device__ __forceinline__ void launder(Group<T>& g) {
+  launder(g.w);
+  if constexpr (sizeof(T) == 4) launder(g.v);
+}
 template <typename T>
 __device__ __forceinline__ void held(const T* row, int64_t v, int64_t V, const Group<T>& g, float (&x)[8]) {
   if (v + 8 <= V) g.get(x);
@@ -383,14 +395,13 @@ struct Ws {
   size_t bytes;
 };
 
-// Chunks of a row: whole kVUnits, `per` of them each, so that `rows` rows make enough
-// workgroups for the chip (1024) before chunks grow, and at most `most` of them.
-void chunking(int64_t rows, int64_t V, int64_t most, int64_t& chunk, int& K) {
+// Chunks of a row: 1, 2, 4 .. kVUnits each, as few as keep `rows` rows within `wanted`
+// workgroups, and at most `most` (but for rows of more than kVMaxChunks such chunks).
+void chunking(int64_t rows, int64_t V, int64_t wanted, int64_t most, int64_t& chunk, int& K) {
   const int64_t units = (V + kVUnit - 1) / kVUnit;
-  int64_t per = rows * units / 1024;
-  per = per < 1 ? 1 : per > most ? most : per;
-  const int64_t least = (units + kVMaxChunks - 1) / kVMaxChunks;
-  if (per < least) per = (least + 1) / 2 * 2;  // (whole rounds of two groups)
+  int64_t per = 1;
+  while (per < most && rows * ((units + per - 1) / per) > wanted) per *= 2;
+  while ((units + per - 1) / per > kVMaxChunks) per *= 2;
   chunk = per * kVUnit;
   K = (int)((units + per - 1) / per);
 }
@@ -399,8 +410,8 @@ Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
   Ws w{};
   // step 1: at most 16384 elements (a longer chunk delays the decision that spares later
   // positions); steps 2 and 3: what a thread holds at once
-  chunking(S * L, V, 8, w.chunk1, w.K1);
-  chunking(S, V, 2, w.chunk2, w.K2);
+  chunking(S * L, V, 1024, 8, w.chunk1, w.K1);
+  chunking(S, V, 1280, 4, w.chunk2, w.K2);
   size_t off = 0;
   char* p = static_cast<char*>(base);
   auto take = [&](size_t bytes) {
@@ -857,25 +868,29 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
     Group<T> gz[H], gu[H];
     hold<T, H>(zr, b, a.V, gz);
     if (residual) hold<T, H>(ur, b, a.V, gu);
-    float x[H][8], y[H][8];
-    float xm = ninf(), ym = ninf();
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int64_t v = b + h * kVUnit + tid * 8;
-      held(zr, v, a.V, gz[h], x[h]);
-      if (residual) {
-        held(ur, v, a.V, gu[h], y[h]);
-        ym = fmaxf(ym, max8(y[h]));
-      } else if (skip >= v && skip < v + 8) {
+    float xm = ninf(), ym = ninf(), x[8];
+    // (the token left out counts as -inf, on its own)
+    auto leave_out = [&](int64_t v) {
+      if (skip >= v && skip < v + 8) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (v + k == skip) {
-            ym = x[h][k];
-            x[h][k] = ninf();
+            ym = x[k];
+            x[k] = ninf();
           }
         }
       }
-      xm = fmaxf(xm, max8(x[h]));
+    };
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int64_t v = b + h * kVUnit + tid * 8;
+      held(zr, v, a.V, gz[h], x);
+      if (!residual) leave_out(v);
+      xm = fmaxf(xm, max8(x));
+      if (residual) {
+        held(ur, v, a.V, gu[h], x);
+        ym = fmaxf(ym, max8(x));
+      }
     }
     const float left_out = ym;
     block_max2(xm, ym, red_m);
@@ -889,17 +904,22 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
     md = ym;
     const double rt = (double)ref_of(mt), rd = (double)ref_of(md);
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+    for (int h = 0; h < H; ++h) {
+      const int64_t v = b + h * kVUnit + tid * 8;
+      launder(gz[h]);
+      held(zr, v, a.V, gz[h], x);
+      if (!residual) leave_out(v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) st += exp2_64(((double)x[h][k] - rt) * t.c64);
-    if (residual) {
+      for (int k = 0; k < 8; ++k) st += exp2_64(((double)x[k] - rt) * t.c64);
+      if (residual) {
+        launder(gu[h]);
+        held(ur, v, a.V, gu[h], x);
 #pragma unroll
-      for (int h = 0; h < H; ++h)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sd += exp2_64(((double)y[h][k] - rd) * t.c64);
-    } else if (left_out > ninf()) {
-      sd = 1.0;
+        for (int k = 0; k < 8; ++k) sd += exp2_64(((double)x[k] - rd) * t.c64);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // (a group at a time: registers)
     }
+    if (!residual && left_out > ninf()) sd = 1.0;
     __syncthreads();  // (red_m is written again)
   }
   st = wave_sum64(st);
@@ -1028,6 +1048,7 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
       ms.of(v, x, y, e);
 #pragma unroll
       for (int k = 0; k < 8; ++k) s += e[k];
+      __builtin_amdgcn_sched_barrier(0);  // (a group at a time: registers)
     }
   }
   s = wave_sum64(s);
@@ -1083,13 +1104,16 @@ hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
     if (hipError_t e = hipGetLastError()) return e;
   }
   const dim3 grid((unsigned)(a.S * w.K2)), block(kVThreads);
-  const bool one = w.chunk2 == kVUnit, residual = a.L > 0 && a.draft;
-  if (one) hipLaunchKernelGGL((verify_sums_kernel<T, 1>), grid, block, 0, st, g);
-  else hipLaunchKernelGGL((verify_sums_kernel<T, 2>), grid, block, 0, st, g);
+  const bool residual = a.L > 0 && a.draft;
+  const int64_t held = w.chunk2 / kVUnit;
+  if (held == 1) hipLaunchKernelGGL((verify_sums_kernel<T, 1>), grid, block, 0, st, g);
+  else if (held == 2) hipLaunchKernelGGL((verify_sums_kernel<T, 2>), grid, block, 0, st, g);
+  else hipLaunchKernelGGL((verify_sums_kernel<T, 4>), grid, block, 0, st, g);
   if (hipError_t e = hipGetLastError()) return e;
   if (residual) {
-    if (one) hipLaunchKernelGGL((verify_residual_kernel<T, 1>), grid, block, 0, st, g);
-    else hipLaunchKernelGGL((verify_residual_kernel<T, 2>), grid, block, 0, st, g);
+    if (held == 1) hipLaunchKernelGGL((verify_residual_kernel<T, 1>), grid, block, 0, st, g);
+    else if (held == 2) hipLaunchKernelGGL((verify_residual_kernel<T, 2>), grid, block, 0, st, g);
+    else hipLaunchKernelGGL((verify_residual_kernel<T, 4>), grid, block, 0, st, g);
   }
   return hipGetLastError();
 }
