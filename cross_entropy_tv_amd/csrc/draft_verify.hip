@@ -511,12 +511,11 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
   const bool has_d = a.draft != nullptr && !t.greedy;
   const T* ur = has_d ? static_cast<const T*>(a.draft) + (q.first + j) * a.ldd : nullptr;
   const int64_t lo = c * w.chunk1, hi = lo + w.chunk1 < a.V ? lo + w.chunk1 : a.V;
-  // what the decision needs, requested ahead of the row
+  // what the decision needs is requested ahead of it: the token with the row, its logits behind the row's loads
   const int64_t x = a.tokens[q.first + j];
   const bool x_ok = x >= 0 && x < a.V;
   const float r32 = a.u_accept[q.first + j];
-  const float zx = x_ok ? load1(zr + x) : ninf();
-  const float ux = x_ok && has_d ? load1(ur + x) : ninf();
+  float zx = ninf(), ux = ninf();
 
   if (t.greedy) {
     Best b{ninf(), kNone};
@@ -527,6 +526,8 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
     Sum32 st{ninf(), 0.0f}, sd{ninf(), 0.0f};
     for_groups(zr, lo, hi, a.V, [&](int64_t, const float (&e)[8]) { add8(st, e, t.c); });
     if (has_d) for_groups(ur, lo, hi, a.V, [&](int64_t, const float (&e)[8]) { add8(sd, e, t.c); });
+    if (x_ok) zx = load1(zr + x);
+    if (x_ok && has_d) ux = load1(ur + x);
     st = wave_merge(st, t.c);
     if (has_d) sd = wave_merge(sd, t.c);
     if (lane == 0) {
@@ -665,18 +666,19 @@ struct PickShared {
   double wave[kVWaves];
   double before;  // the sum in front of the chosen chunk
   int chunk;
-  int found;  // 2^31 - 1 - (token + 1) of the border's element, 0: not found
-  int last;   // token + 1 of the last element with mass
-  float z;    // the token's target logit
+  int found[kVWaves];  // token + 1 of a wave's first element above the goal, 0: none
+  int last[kVWaves];   // token + 1 of its last element with mass
+  float z[kVWaves];    // target logit of the former
 };
 
 // The token at w of the total, by the workgroup: the chunk whose running sum first
 // exceeds w * total (sums[0..K) filled by the caller, scaled like the masses), then
 // the element.  The running sums are in vocabulary order.  Should rounding leave no
 // element above the goal, the last one with mass is the token; -1: no mass at all.
-// sh.z: its target logit.
+// z: its target logit.  (The finds are gathered by ballots: LDS atomics of 64 lanes on one
+// word are taken lane by lane.)
 template <typename T>
-__device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int K, int64_t chunk, double w) {
+__device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int K, int64_t chunk, double w, float& z) {
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   if (wave == 0) {
     // each lane a run of consecutive chunks
@@ -708,20 +710,19 @@ __device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int 
       sh.chunk = hit ? at_h : some ? last_l : -1;
       // (no running sum above the goal: a goal no sum of the chunk exceeds, so that its last element is taken)
       sh.before = hit ? goal - before_h : __builtin_inf();
-      sh.found = 0;
-      sh.last = 0;
     }
   }
   __syncthreads();
+  z = 0.0f;
   if (sh.chunk < 0) return -1;
   const double goal = sh.before;
   const int64_t lo = sh.chunk * chunk, hi = lo + chunk < m.V ? lo + chunk : m.V;
   double base = 0.0;
+  int last = 0;
   for (int64_t b = lo; b < hi; b += kVUnit) {
     const int64_t v = b + tid * 8;
     float x[8];
     double e[8], own = 0.0;
-    int last = 0;
     m.get(b, x, e);  // (0 behind the row's end, which is the only place a chunk ends short)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -730,7 +731,6 @@ __device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int 
     }
     const double incl = wave_scan64(own);
     if (lane == 63) sh.wave[wave] = incl;
-    if (last) atomicMax(&sh.last, last);
     __syncthreads();
     double run = base + incl - own, all = base;
 #pragma unroll
@@ -741,33 +741,43 @@ __device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int 
     if (all > goal) {
       // the first element whose running sum exceeds the goal: the lowest token among the finds
       int at = 0;
-      float z = 0.0f;
+      float zx = 0.0f;
       if (run + own > goal) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           run += e[k];
           if (!at && e[k] > 0.0 && run > goal) {
             at = (int)(v + k) + 1;
-            z = x[k];
+            zx = x[k];
           }
         }
-        // (positive, so that atomicMax of the negative keeps the lowest)
-        if (at) atomicMax(&sh.found, 0x7fffffff - at);
+      }
+      const unsigned long long hit = __ballot(at != 0);
+      if (lane == (hit ? __builtin_ctzll(hit) : 0)) {
+        sh.found[wave] = at;
+        sh.z[wave] = zx;
       }
       __syncthreads();
-      const int found = sh.found;
-      if (found) {
-        if (at && found == 0x7fffffff - at) sh.z = z;
-        __syncthreads();
-        return 0x7fffffff - found - 1;
+#pragma unroll
+      for (int k = 0; k < kVWaves; ++k) {
+        if (sh.found[k]) {
+          z = sh.z[k];
+          return sh.found[k] - 1;
+        }
       }
     }
     base = all;
     __syncthreads();  // sh.wave is written again
   }
-  if (tid == 0 && sh.last > 0) sh.z = load1(m.zr + sh.last - 1);
+  // (a thread's last element with mass: lanes and waves hold ascending runs inside a pass only, so the largest)
+  last = wave_all(last, [](int p, int q) { return p > q ? p : q; });
+  if (lane == 0) sh.last[wave] = last;
   __syncthreads();
-  return sh.last - 1;
+  last = sh.last[0];
+#pragma unroll
+  for (int k = 1; k < kVWaves; ++k) last = sh.last[k] > last ? sh.last[k] : last;
+  z = last > 0 ? load1(m.zr + last - 1) : 0.0f;
+  return last - 1;
 }
 
 // The outputs of sequence i: the accepted tokens, the drawn one, -1 behind it.
@@ -820,6 +830,7 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   const Seq q = seq_of(a, i);
   const Temp t = temp_of(a.temperature, i);
   const int acc = min(w.first[i], q.n);
+  const float u = a.u_sample[i];
   if (!q.ok || (t.greedy && acc < q.n)) {
     if (c == 0) write_out(a, w, i, q, acc, q.ok ? w.best[(int64_t)acc * a.S + i] : -1, 0.0f);
     return;
@@ -1006,8 +1017,9 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   if (only && tid == 0 && skip < a.V) sh.sums[skip / w.chunk2] = s1;
   const Masses<T> ms{zr, nullptr, a.V, only ? -1 : skip, t.c64, (double)ref_of(only ? mn : m0), 0.0, 0.0, 0.0};
   __syncthreads();  // (sh.sums)
-  const int64_t tok = pick(ms, sh, K, w.chunk2, (double)a.u_sample[i]);
-  write_out(a, w, i, q, acc, tok, logp_of(tok, sh.z, mn, full, t));
+  float z;
+  const int64_t tok = pick(ms, sh, K, w.chunk2, (double)u, z);
+  write_out(a, w, i, q, acc, tok, logp_of(tok, z, mn, full, t));
 }
 
 template <typename T, int H>
@@ -1024,6 +1036,7 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
   const int acc = min(w.first[i], q.n);
   if (!q.ok || acc >= q.n) return;  // drawn from p in step 2
   const Temp t = temp_of(a.temperature, i);
+  const float u = a.u_sample[i];
   if (t.greedy) return;
   const uint64_t* state = w.state + (int64_t)i * kSt;
   const float mt = lo_of(state[0]), md = __uint_as_float(hi_of(state[0]));
@@ -1084,8 +1097,9 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
     __syncthreads();
     ms.ur = nullptr;
   }
-  const int64_t tok = pick(ms, sh, K, w.chunk2, (double)a.u_sample[i]);
-  write_out(a, w, i, q, acc, tok, logp_of(tok, sh.z, mt, St, t));
+  float z;
+  const int64_t tok = pick(ms, sh, K, w.chunk2, (double)u, z);
+  write_out(a, w, i, q, acc, tok, logp_of(tok, z, mt, St, t));
 }
 
 template <typename T>
