@@ -21,7 +21,7 @@
 // Three steps:
 //
 //   1. verify_accept_kernel, one workgroup per (position, sequence, chunk of the
-//      row), position by position: partial (max, sum-exp) of target and draft in
+//      row), position by position: partial sums of exponentials of target and draft in
 //      fp32; the last workgroup of a position merges them and decides.  Workgroups
 //      of positions behind a rejection already decided read nothing: they look,
 //      and never wait (the results do not depend on what they see).
@@ -48,7 +48,6 @@ namespace {
 constexpr int kVThreads = 256;
 constexpr int kVWaves = kVThreads / 64;
 constexpr int kVUnit = kVThreads * 8;  // elements that one load of every thread covers
-constexpr int kVHold = 4;              // groups of 8 elements that a thread holds at once
 constexpr int kVMaxChunks = 1024;      // chunks of a row at most (the draw keeps their sums in LDS)
 constexpr float kBorder = 0x1p-15f;
 // max(p - q, 0) sums to the total variation distance.  Below 2^-40 it is the rounding of equal rows
@@ -141,15 +140,15 @@ __device__ __forceinline__ void held(const T* row, int64_t v, int64_t V, const G
 }
 
 // Elements [lo, hi) of a row of V, lo a multiple of kVUnit: f(v, x) for every group of 8 of this
-// thread, with kVHold groups loaded at once.
-template <typename T, typename F>
+// thread, with H groups loaded at once.
+template <int H, typename T, typename F>
 __device__ __forceinline__ void for_groups(const T* row, int64_t lo, int64_t hi, int64_t V, F f) {
-  for (int64_t b = lo; b < hi; b += kVUnit * kVHold) {
-    Group<T> g[kVHold];
-    hold<T, kVHold>(row, b, V, g);
+  for (int64_t b = lo; b < hi; b += kVUnit * H) {
+    Group<T> g[H];
+    hold<T, H>(row, b, V, g);
     float x[8];
 #pragma unroll
-    for (int k = 0; k < kVHold; ++k) {
+    for (int k = 0; k < H; ++k) {
       const int64_t v = b + k * kVUnit + tid_x() * 8;
       if (v < hi) {
         held(row, v, V, g[k], x);
@@ -221,9 +220,6 @@ __device__ __forceinline__ Temp temp_of(const float* temperature, int i) {
 // A reference for exponents: the maximum, or 0 for a row without any mass (-inf - 0 = -inf: all masses 0).
 __device__ __forceinline__ float ref_of(float m) { return m == ninf() ? 0.0f : m; }
 
-struct Sum32 {
-  float m, s;  // sum of 2^((x - m) c) over what was added; m = -inf: nothing with mass
-};
 struct Sum64 {
   float m;
   double s;
@@ -234,18 +230,6 @@ struct Best {
 };
 constexpr unsigned kNone = 0xffffffffu;
 
-__device__ __forceinline__ void add8(Sum32& a, const float (&x)[8], float c) {
-  const float mn = fmaxf(a.m, max8(x));
-  const float ref = ref_of(mn);
-  float s0 = a.s * exp2_hw((a.m - ref) * c), s1 = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 8; k += 2) {
-    s0 += exp2_hw((x[k] - ref) * c);
-    s1 += exp2_hw((x[k + 1] - ref) * c);
-  }
-  a.m = mn;
-  a.s = s0 + s1;
-}
 __device__ __forceinline__ void add8(Best& a, int64_t v, const float (&x)[8]) {
   const float m = max8(x);
   if (m > a.v) {
@@ -331,10 +315,50 @@ __device__ __forceinline__ double wave_scan64(double v) {
   return v;
 }
 
-__device__ __forceinline__ Sum32 wave_merge(Sum32 a, float c) {
-  const float m = wave_max(a.m);
-  return Sum32{m, wave_sum32(a.s * exp2_hw((a.m - ref_of(m)) * c))};
+// A sum of exponentials against its maximum, as what there is beside one element at the
+// maximum: the sum is 1 + rest.  A token of probability near 1 has log p = -log(1 + rest), which
+// rest gives to its own relative precision and a rounded sum would not.
+struct Sum32 {
+  float m, rest;  // m = -inf: nothing with mass
+};
+
+// A lane's running sum: s = sum of 2^((x - m) c).
+struct LaneSum {
+  float m, s;
+};
+__device__ __forceinline__ void add8(LaneSum& a, const float (&x)[8], float c) {
+  const float mn = fmaxf(a.m, max8(x));
+  const float ref = ref_of(mn);
+  float s0 = a.s * exp2_hw((a.m - ref) * c), s1 = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    s0 += exp2_hw((x[k] - ref) * c);
+    s1 += exp2_hw((x[k + 1] - ref) * c);
+  }
+  a.m = mn;
+  a.s = s0 + s1;
 }
+
+// The wave's sum over elements [lo, hi) of a row of V, of which lane l of the workgroup's wave took
+// elements lo + k kVUnit + 8 tid .. + 7.  What a lane's sum lost below the 1 of its largest element
+// matters in one lane only, the (first) one that holds the wave's maximum: its elements are summed
+// once more, an element a lane, without it.
+template <typename T>
+__device__ __forceinline__ Sum32 wave_rest(const T* row, int64_t lo, int64_t hi, int64_t V, const LaneSum& a, float c) {
+  const int lane = tid_x() & 63;
+  const float m = wave_max(a.m), ref = ref_of(m);
+  const int top = __builtin_ctzll(__ballot(a.m == m));
+  float r = lane == top ? 0.0f : a.s * exp2_hw((a.m - ref) * c);
+  int at = 0;
+  for (int64_t b = lo + (lane >> 3) * kVUnit; b < hi; b += 8 * kVUnit) {
+    const int64_t v = b + (((tid_x() & ~63) + top) * 8 + (lane & 7));
+    const float x = v < V ? load1(row + v) : ninf();
+    at += x == m ? 1 : 0;
+    r += x == m ? 0.0f : exp2_hw((x - ref) * c);
+  }
+  return Sum32{m, wave_sum32(r) + (wave_sum32((float)at) - 1.0f)};
+}
+
 __device__ __forceinline__ Sum64 wave_merge(Sum64 a, double c) {
   const float m = wave_max(a.m);
   return Sum64{m, wave_sum64(a.s * exp2_64(((double)a.m - (double)ref_of(m)) * c))};
@@ -377,7 +401,7 @@ __device__ __forceinline__ bool count_last(int* counter, int of) {
 
 // ------------------------------------------------------------------ workspace
 
-constexpr int kP1 = 2;  // 64-bit words of a chunk's partials in step 1: (m, s) of target and of draft
+constexpr int kP1 = 2;  // 64-bit words of a chunk's partials in step 1: (m, rest) of target and of draft
 constexpr int kP2 = 3;  // in step 2: (m_t, m_d), s_t, s_d
 constexpr int kSt = 3;  // a sequence's merged sums for step 3: (m_t, m_d), s_t, s_d
 
@@ -469,7 +493,7 @@ template <typename T>
 __device__ double row_sum64(const T* row, int64_t V, float m, double c, double* red) {
   const double ref = (double)ref_of(m);
   double s = 0.0;
-  for_groups(row, 0, V, V, [&](int64_t, const float (&x)[8]) {
+  for_groups<2>(row, 0, V, V, [&](int64_t, const float (&x)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) s += exp2_64(((double)x[k] - ref) * c);
   });
@@ -483,7 +507,8 @@ __device__ double row_sum64(const T* row, int64_t V, float m, double c, double* 
   return t;
 }
 
-template <typename T>
+// H: groups of 8 that a thread holds (a chunk is one or more rounds of them).
+template <typename T, int H>
 __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
   const VerifyArgs& a = g.a;
   const Ws& w = g.w;
@@ -519,20 +544,37 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
 
   if (t.greedy) {
     Best b{ninf(), kNone};
-    for_groups(zr, lo, hi, a.V, [&](int64_t v, const float (&e)[8]) { add8(b, v, e); });
+    for_groups<H>(zr, lo, hi, a.V, [&](int64_t v, const float (&e)[8]) { add8(b, v, e); });
     b = wave_merge(b);
     if (lane == 0) red[0][wave] = pack(b.v, b.at);
   } else {
-    Sum32 st{ninf(), 0.0f}, sd{ninf(), 0.0f};
-    for_groups(zr, lo, hi, a.V, [&](int64_t, const float (&e)[8]) { add8(st, e, t.c); });
-    if (has_d) for_groups(ur, lo, hi, a.V, [&](int64_t, const float (&e)[8]) { add8(sd, e, t.c); });
+    LaneSum lt{ninf(), 0.0f}, ld{ninf(), 0.0f};
+    for (int64_t b = lo; b < hi; b += kVUnit * H) {
+      Group<T> gz[H], gu[H];
+      hold<T, H>(zr, b, a.V, gz);
+      if (has_d) hold<T, H>(ur, b, a.V, gu);
+      float e[8];
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        held(zr, b + k * kVUnit + tid * 8, a.V, gz[k], e);
+        add8(lt, e, t.c);
+      }
+      if (has_d) {
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+          held(ur, b + k * kVUnit + tid * 8, a.V, gu[k], e);
+          add8(ld, e, t.c);
+        }
+      }
+    }
     if (x_ok) zx = load1(zr + x);
     if (x_ok && has_d) ux = load1(ur + x);
-    st = wave_merge(st, t.c);
-    if (has_d) sd = wave_merge(sd, t.c);
+    const Sum32 st = wave_rest(zr, lo, hi, a.V, lt, t.c);
+    Sum32 sd{ninf(), 0.0f};
+    if (has_d) sd = wave_rest(ur, lo, hi, a.V, ld, t.c);
     if (lane == 0) {
-      red[0][wave] = pack(st.m, __float_as_uint(st.s));
-      red[1][wave] = pack(sd.m, __float_as_uint(sd.s));
+      red[0][wave] = pack(st.m, __float_as_uint(st.rest));
+      red[1][wave] = pack(sd.m, __float_as_uint(sd.rest));
     }
   }
   __syncthreads();
@@ -553,11 +595,17 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
         float m = ninf();
 #pragma unroll
         for (int k = 0; k < kVWaves; ++k) m = fmaxf(m, lo_of(red[h][k]));
-        float s = 0.0f;
+        // the rest of one wave at the maximum, and the whole sums of the others
+        float rest = 0.0f;
+        bool first = true;
 #pragma unroll
-        for (int k = 0; k < kVWaves; ++k)
-          s += __uint_as_float(hi_of(red[h][k])) * exp2_hw((lo_of(red[h][k]) - ref_of(m)) * t.c);
-        if (h == 0 || has_d) publish(part + h, pack(m, __float_as_uint(s)));
+        for (int k = 0; k < kVWaves; ++k) {
+          const float mk = lo_of(red[h][k]), rk = __uint_as_float(hi_of(red[h][k]));
+          const bool at = first && mk == m;
+          rest += at ? rk : (1.0f + rk) * exp2_hw((mk - ref_of(m)) * t.c);
+          first = first && !at;
+        }
+        if (h == 0 || has_d) publish(part + h, pack(m, __float_as_uint(rest)));
       }
     }
     sh_flag = count_last(w.count1 + slot, K);
@@ -594,7 +642,7 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
         const uint64_t v = fetch(parts + k * kP1 + h);
         const float mn = fmaxf(s.m, lo_of(v)), ref = ref_of(mn);
         s.s = s.s * exp2_64(((double)s.m - ref) * t.c64) +
-              (double)__uint_as_float(hi_of(v)) * exp2_64(((double)lo_of(v) - ref) * t.c64);
+              (1.0 + (double)__uint_as_float(hi_of(v))) * exp2_64(((double)lo_of(v) - ref) * t.c64);
         s.m = mn;
       }
       s = wave_merge(s, t.c64);
@@ -844,7 +892,7 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   uint64_t* part = w.part2 + ((int64_t)i * K + c) * kP2;
   if (t.greedy) {
     Best b{ninf(), kNone};
-    for_groups(zr, lo, hi, a.V, [&](int64_t v, const float (&x)[8]) { add8(b, v, x); });
+    for_groups<H>(zr, lo, hi, a.V, [&](int64_t v, const float (&x)[8]) { add8(b, v, x); });
     b = wave_merge(b);
     if (lane == 0) red[wave] = pack(b.v, b.at);
     __syncthreads();
@@ -1114,7 +1162,12 @@ hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
                      w.first, (int)a.S, w.count1, w.n_zero);
   if (hipError_t e = hipGetLastError()) return e;
   if (a.L > 0) {
-    hipLaunchKernelGGL((verify_accept_kernel<T>), dim3((unsigned)(a.S * a.L * w.K1)), dim3(kVThreads), 0, st, g);
+    const dim3 grid((unsigned)(a.S * a.L * w.K1)), block(kVThreads);
+    // groups held at once, two rows of them: 2 of 2-byte logits (4: 23.7 against 21.4 us at 256 x
+    // 50001, the registers halve the workgroups at once), 4 of fp32 (2: 191 against 183 us at 96 x 262144)
+    constexpr int kHold = sizeof(T) == 4 ? 4 : 2;
+    if (w.chunk1 < kHold * kVUnit) hipLaunchKernelGGL((verify_accept_kernel<T, 1>), grid, block, 0, st, g);
+    else hipLaunchKernelGGL((verify_accept_kernel<T, kHold>), grid, block, 0, st, g);
     if (hipError_t e = hipGetLastError()) return e;
   }
   const dim3 grid((unsigned)(a.S * w.K2)), block(kVThreads);

@@ -217,6 +217,29 @@ def test_comparisons_next_to_their_borders(with_draft):
         check(c, f"borders {step}")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_log_p_of_confident_tokens(dt):
+    """p from 1/2 to 1 - 1e-6: log p keeps its relative precision, not only an absolute one.  It is -log(1 + rest),
+    rest a sum of exponentials relative to the largest, each good to |a| 2^-24 + 2^-22 with a = log2 of it, below 30:
+    2^-18 relative."""
+    c = Case(59, [8] * 6, 20001, dt)
+    for i in range(len(c.start) - 1):
+        for j in range(8):
+            z = c.z[c.start[i] + i + j]
+            z[17 * i + j] = float(torch.logsumexp(z, 0)) + 2.0 * j
+            c.u[c.start[i] + j] = z
+            c.tokens[c.start[i] + j] = 17 * i + j
+    c.z = c.z.to(DT[dt]).float()
+    c.u = c.u.to(DT[dt]).float()
+    c.ua[:] = 0.0
+    n, tok, lp = c.reference()
+    assert (n == 8).all() and (-lp[:, :8]).min() < 2e-6
+    announce(f"draft_verify confident {dt}")
+    _, gtok, glp = c.run()
+    assert np.array_equal(gtok, tok)
+    assert (np.abs(glp - lp)[:, :8] <= 2.0 ** -18 * np.abs(lp[:, :8])).all()
+
+
 def test_sequences_that_do_not_fit_are_refused_alone():
     c = Case(41, [2, 2, 2, 2], 500)
     n, tok, lp = c.reference()
