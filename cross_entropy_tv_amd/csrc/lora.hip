@@ -110,19 +110,29 @@ __device__ __forceinline__ u32x4_t keep_from(u32x4_t w, int k0, int begin) {
   return (u32x4_t){v[0], v[1], v[2], v[3]};
 }
 
-// Term s (0: hi, 1: mid, 2: lo) of fp32 values cut into three bf16 terms.  A value that
-// is not finite is all in hi.
-__device__ __forceinline__ float term(float v, int s) {
-  const float hi = __uint_as_float(pack_bf16x2(v, 0.0f) << 16);
-  if (s == 0) return hi;
-  if ((__float_as_uint(hi) & 0x7f800000u) == 0x7f800000u) return 0.0f;
-  const float rest = v - hi;
-  const float mid = __uint_as_float(pack_bf16x2(rest, 0.0f) << 16);
-  return s == 1 ? mid : rest - mid;
-}
-__device__ __forceinline__ u32x4_t terms8(const float (&v)[8], int s) {
-  return (u32x4_t){pack_bf16x2(term(v[0], s), term(v[1], s)), pack_bf16x2(term(v[2], s), term(v[3], s)),
-                   pack_bf16x2(term(v[4], s), term(v[5], s)), pack_bf16x2(term(v[6], s), term(v[7], s))};
+// Eight fp32 values cut into three bf16 terms each (hi, mid, lo).  A value that is not finite is
+// all in hi.
+__device__ __forceinline__ void terms8(const float (&v)[8], u32x4_t (&t)[3]) {
+  unsigned w[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a[3][2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = v[2 * i + e];
+      const float hi = __uint_as_float(pack_bf16x2(x, 0.0f) << 16);
+      const bool finite = (__float_as_uint(hi) & 0x7f800000u) != 0x7f800000u;
+      const float rest = finite ? x - hi : 0.0f;
+      const float mid = __uint_as_float(pack_bf16x2(rest, 0.0f) << 16);
+      a[0][e] = hi;
+      a[1][e] = mid;
+      a[2][e] = rest - mid;
+    }
+#pragma unroll
+    for (int n = 0; n < 3; ++n) w[n][i] = pack_bf16x2(a[n][0], a[n][1]);
+  }
+#pragma unroll
+  for (int n = 0; n < 3; ++n) t[n] = (u32x4_t){w[n][0], w[n][1], w[n][2], w[n][3]};
 }
 
 // s_a times the sum of the down kernel's split partials, ranks k0 .. k0 + 7 of row t (0 from `rank` on).
@@ -139,6 +149,55 @@ __device__ __forceinline__ void load_low(const float* P, int splits, int64_t pla
     v[k] = k0 + k < rank ? scale * a[k] : 0.0f;
     v[4 + k] = k0 + 4 + k < rank ? scale * b[k] : 0.0f;
   }
+}
+
+// ------------------------------------------------------------------ transposed adapters
+
+// The backward's tiles take A and B the other way round: (n, R0, C0) bf16 -> (n, C0, R0), an 8 x 8
+// block a thread, with 0 where the rank axis (rows of the input if RANK_ROWS, else its columns) is at
+// the adapter's rank or beyond.
+template <bool RANK_ROWS>
+__device__ __forceinline__ void transpose_block(const LoraSet& s, const uint16_t* in, uint16_t* out, int64_t R0,
+                                                int64_t C0, int64_t at) {
+  const int64_t cb = C0 / 8, rb = R0 / 8;
+  const int64_t a = at / (cb * rb), in_a = at - a * cb * rb;
+  // neighbouring threads along the long axis
+  const int64_t b8 = RANK_ROWS ? in_a / cb : in_a % rb, c8 = RANK_ROWS ? in_a % cb : in_a / rb;
+  const int rank = rank_of(s, (int)a);
+  const int64_t r0 = b8 * 8, c0 = c8 * 8;
+  u32x4_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    w[j] = load16(in + (a * R0 + r0 + j) * C0 + c0);
+    if (RANK_ROWS) {
+      if (r0 + j >= rank) w[j] = (u32x4_t){0u, 0u, 0u, 0u};
+    } else {
+      w[j] = keep_below(w[j], (int)c0, rank);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    unsigned o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned lo = w[2 * j][c / 2], hi = w[2 * j + 1][c / 2];
+      o[j] = c & 1 ? (lo >> 16) | (hi & 0xffff0000u) : (lo & 0xffffu) | (hi << 16);
+    }
+    *reinterpret_cast<u32x4_t*>(out + (a * C0 + c0 + c) * R0 + r0) = (u32x4_t){o[0], o[1], o[2], o[3]};
+  }
+}
+
+struct TransposeArgs {
+  LoraSet s;
+  uint16_t *At, *Bt;  // nullptr: not wanted
+  unsigned blocks;    // workgroups that do this, in front of the others of the launch
+};
+__device__ __forceinline__ void transpose_blocks(const TransposeArgs& g, int64_t at) {
+  const LoraSet& s = g.s;
+  uint16_t *At = g.At, *Bt = g.Bt;
+  const int64_t na = At ? s.n * (s.r / 8) * (s.H / 8) : 0, nb = Bt ? s.n * (s.r / 8) * (s.N / 8) : 0;
+  if (at < na) transpose_block<true>(s, s.A, At, s.r, s.H, at);
+  else if (at - na < nb) transpose_block<false>(s, s.B, Bt, s.N, s.r, at - na);
 }
 
 // ------------------------------------------------------------------ down: P = X M^T
@@ -166,36 +225,56 @@ __device__ __forceinline__ int up_chunk(int r, int l, int q) {
   if (r <= 16) return (q & 1) * 8;
   return 32 * l + 8 * q < r ? 32 * l + 8 * q : -1;
 }
-// Term (3: none) of k-group q in MFMA j.
-__device__ __forceinline__ int up_term(int r, int j, int q) { return r <= 8 ? q : r <= 16 ? (2 * j + (q >> 1)) : j; }
 
 // vals: the fp32 values of rows t0 .. t0 + 31 (t0 a multiple of 32; rows behind T: 0), row stride vs.
 template <int NT>
 __device__ __forceinline__ void emit_terms(const Terms& o, const float* vals, int vs, int64_t t0, int r) {
   const int64_t tile = t0 / kTileRows;
+  u32x4_t w[4];
+  w[3] = (u32x4_t){0u, 0u, 0u, 0u};
   if (o.U) {
-    const int ld = up_ld(r), tm = up_tm(r);
-    for (int i = tid_x(); i < 2 * ld * tm * 64; i += NT) {
-      const int lane = i & 63, f = i >> 6, j = f % tm, l = f / tm % ld, h = f / tm / ld;
-      const int k0 = up_chunk(r, l, lane >> 4), t = up_term(r, j, lane >> 4);
-      u32x4_t w = {0u, 0u, 0u, 0u};
-      if (k0 >= 0 && t < 3) {
-        float v[8];
+    const int ld = up_ld(r), tm = up_tm(r), kcs = r <= 8 ? 1 : r <= 16 ? 2 : 4 * ld;  // chunks of 8 ranks
+    uint16_t* U = o.U + tile * 2 * ld * tm * 512;
+    for (int i = tid_x(); i < kTileRows * kcs; i += NT) {
+      const int row = i % kTileRows, kc = i / kTileRows, h = row >> 4, c16 = row & 15;
+      float v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = vals[(16 * h + (lane & 15)) * vs + k0 + k];
-        w = terms8(v, t);
+      for (int k = 0; k < 8; ++k) v[k] = 8 * kc < r ? vals[row * vs + 8 * kc + k] : 0.0f;
+      u32x4_t t3[3];
+      terms8(v, t3);
+#pragma unroll
+      for (int n = 0; n < 3; ++n) w[n] = t3[n];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        // operand and lane of term n of this chunk (n = 3: the zeros of the k-groups that hold no term)
+        int f, q;
+        if (r <= 8) {
+          f = h;
+          q = n;
+        } else if (r <= 16) {
+          f = 2 * h + (n >> 1);
+          q = kc + 2 * (n & 1);
+        } else {
+          if (n == 3) break;
+          f = (h * ld + kc / 4) * 3 + n;
+          q = kc % 4;
+        }
+        *reinterpret_cast<u32x4_t*>(U + f * 512 + (c16 + 16 * q) * 8) = w[n];
       }
-      *reinterpret_cast<u32x4_t*>(o.U + (tile * 2 * ld * tm + f) * 512 + lane * 8) = w;
     }
   }
   if (o.W) {
     const int nb = rank_blocks(r);
-    for (int i = tid_x(); i < nb * 3 * 64; i += NT) {
-      const int lane = i & 63, f = i >> 6, t = f % 3, rho = f / 3 * 16 + (lane & 15);
+    for (int i = tid_x(); i < nb * 64; i += NT) {
+      const int lane = i & 63, b = i >> 6, rho = 16 * b + (lane & 15);
       float v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = rho < r ? vals[((lane >> 4) * 8 + k) * vs + rho] : 0.0f;
-      *reinterpret_cast<u32x4_t*>(o.W + (tile * nb * 3 + f) * 512 + lane * 8) = terms8(v, t);
+      u32x4_t t3[3];
+      terms8(v, t3);
+#pragma unroll
+      for (int n = 0; n < 3; ++n)
+        *reinterpret_cast<u32x4_t*>(o.W + ((tile * nb + b) * 3 + n) * 512 + lane * 8) = t3[n];
     }
   }
 }
@@ -235,15 +314,20 @@ struct Down {
 
 template <int RB>
 __global__ __attribute__((amdgpu_flat_work_group_size(Down<RB>::kThreads, Down<RB>::kThreads), amdgpu_waves_per_eu(2)))
-void lora_down_tile_kernel(DownArgs g) {
+void lora_down_tile_kernel(DownArgs g, TransposeArgs tr) {
   using D = Down<RB>;
+  if (bid_x() < tr.blocks) {
+    transpose_blocks(tr, (int64_t)bid_x() * D::kThreads + tid_x());
+    return;
+  }
+  const unsigned block = bid_x() - tr.blocks;
   __shared__ __attribute__((aligned(16))) uint8_t lds[D::kLds];
   __shared__ float vals[kTileRows * D::kVs];
   const LoraSet& s = g.s;
   const int tid = tid_x(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int group = wave >> 2, gw = wave & 3, gt = tid & 255;
-  const int split = (int)(bid_x() % (unsigned)g.splits);
-  const int64_t r0 = (int64_t)(bid_x() / (unsigned)g.splits) * kTileRows;
+  const int split = (int)(block % (unsigned)g.splits);
+  const int64_t r0 = (int64_t)(block / (unsigned)g.splits) * kTileRows;
   const int64_t r1 = r0 + kTileRows < s.T ? r0 + kTileRows : s.T;
   const uint32_t kb = (uint32_t)(split * g.kslice), ke = (uint32_t)(kb + g.kslice < g.K ? kb + g.kslice : g.K);
   const int c16 = lane & 15, q = lane >> 4, r = (int)s.r;
@@ -267,8 +351,12 @@ void lora_down_tile_kernel(DownArgs g) {
   }
   uint8_t* const stage0 = lds + group * 2 * D::kStage;
   const int h = gw & 1, hb = gw >> 1;  // row half; half of the ranks (RB = 1: of the slice's k)
+  // Slices of the split, and rounds of a group.  Tiles start at different rounds and go round: all
+  // at the same slice they would ask the same few channels of the L2s for M at once (38 against 35 us
+  // at 8192 x 4096, r 64).
   const uint32_t slices = (ke - kb + kDownK - 1) / kDownK;
   const uint32_t rounds = (slices + D::kGroups - 1) / D::kGroups;
+  const uint32_t turn = (uint32_t)(r0 / kTileRows * 5 % rounds);
   for (int i = max(find_request(s.start, (int)s.R, r0), 0); i < s.R && s.start[i] < r1; ++i) {
     const Part p = part_of(s, i, r0, r1);
     if (p.hi <= p.lo || p.adapter < 0) continue;
@@ -279,15 +367,19 @@ void lora_down_tile_kernel(DownArgs g) {
     u32x4_t v0[D::kLoads], v1[D::kLoads];
     // slice c of this group into registers; a piece behind the end comes from the last one in front
     // of it (no load is conditional) and is 0 in LDS
+    auto slice_k = [&](uint32_t c) {  // (behind the last round: behind the end)
+      const uint32_t n = c < rounds ? (c + turn < rounds ? c + turn : c + turn - rounds) : rounds;
+      return kb + (n * D::kGroups + group) * kDownK + piece * 8;
+    };
     auto load = [&](u32x4_t (&v)[D::kLoads], uint32_t c) {
-      const uint32_t k = kb + (c * D::kGroups + group) * kDownK + piece * 8, at = min(k, ke - 8);
+      const uint32_t at = min(slice_k(c), ke - 8);
 #pragma unroll
       for (int n = 0; n < 2; ++n) v[n] = load16(X + (off[n] + at));
 #pragma unroll
       for (int n = 2; n < D::kLoads; ++n) v[n] = load16(M + (off[n] + at));
     };
     auto put = [&](const u32x4_t (&v)[D::kLoads], uint32_t c) {
-      const bool in = kb + (c * D::kGroups + group) * kDownK + piece * 8 < ke;
+      const bool in = slice_k(c) < ke;
       uint8_t* T = stage0 + (c & 1) * D::kStage;
 #pragma unroll
       for (int n = 0; n < D::kLoads; ++n) {
@@ -355,13 +447,12 @@ void lora_down_tile_kernel(DownArgs g) {
   }
 }
 
-// Requests of a few rows: a wave per (row, 4 ranks, split of K).
+// Requests of a few rows.  u: a wave per (row, 4 ranks, split of K), along the rows of A.
 constexpr int kRowRanks = 4;
-__global__ __launch_bounds__(kLThreads) void lora_down_row_kernel(DownArgs g) {
+__device__ __forceinline__ void down_row(const DownArgs& g, int64_t unit) {
   const LoraSet& s = g.s;
-  const int lane = tid_x() & 63, wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6);
+  const int lane = tid_x() & 63;
   const int quads = (int)(s.r / kRowRanks);
-  const int64_t unit = (int64_t)bid_x() * 4 + wave;
   const int64_t t = unit / (quads * g.splits);
   if (t >= s.T) return;
   const int in_row = (int)(unit - t * (quads * g.splits));
@@ -389,6 +480,56 @@ __global__ __launch_bounds__(kLThreads) void lora_down_row_kernel(DownArgs g) {
   for (int j = 0; j < kRowRanks; ++j) acc[j] = wave_sum(acc[j]);
   if (lane == 0)
     *reinterpret_cast<f32x4_t*>(g.P + ((int64_t)split * s.T + t) * s.r + rho) = (f32x4_t){acc[0], acc[1], acc[2], acc[3]};
+}
+
+// v: a wave per (row, 16 ranks, split of N), down the rows of B (M is (n, K, r) here): a lane takes
+// every 64th row and holds the 16 sums of its rows.
+constexpr int kRowWide = 16;
+__device__ __forceinline__ void down_row_strided(const DownArgs& g, int64_t unit) {
+  const LoraSet& s = g.s;
+  const int lane = tid_x() & 63, r = (int)s.r;
+  const int wides = (r + kRowWide - 1) / kRowWide;
+  const int64_t t = unit / (wides * g.splits);
+  if (t >= s.T) return;
+  const int in_row = (int)(unit - t * (wides * g.splits));
+  const int split = in_row / wides, rho = in_row % wides * kRowWide;
+  const int i = find_request(s.start, (int)s.R, t);
+  if (i < 0) return;
+  const Part p = part_of(s, i, t, t + 1);
+  if (p.hi <= p.lo || p.adapter < 0 || rho >= rank_of(s, p.adapter)) return;
+  const int64_t kb = split * g.kslice, ke = kb + g.kslice < g.K ? kb + g.kslice : g.K;
+  const uint16_t* x = g.X + t * g.ldx;
+  const int next = rho + 8 < r ? 8 : 0;  // (8 ranks: the second half is the first again and not stored)
+  const uint16_t* m = g.M + (int64_t)p.adapter * g.K * r + rho;
+  float acc[kRowWide];
+#pragma unroll
+  for (int j = 0; j < kRowWide; ++j) acc[j] = 0.0f;
+#pragma unroll 4
+  for (int64_t k = kb + lane; k < ke; k += 64) {
+    const float xv = load1(x + k);
+    float a[8], b[8];
+    load8(m + k * r, a);
+    load8(m + k * r + next, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      acc[e] = __builtin_fmaf(xv, a[e], acc[e]);
+      acc[8 + e] = __builtin_fmaf(xv, b[e], acc[8 + e]);
+    }
+  }
+  float mine = 0.0f;  // lane j keeps sum j
+#pragma unroll
+  for (int j = 0; j < kRowWide; ++j) {
+    const float v = wave_sum(acc[j]);
+    mine = lane == j ? v : mine;
+  }
+  if (lane < kRowWide && rho + lane < r) g.P[((int64_t)split * s.T + t) * r + rho + lane] = mine;
+}
+
+// Both in one launch (blocks of four waves, blocks_u of them for u).
+__global__ __launch_bounds__(kLThreads) void lora_down_row_kernel(DownArgs u, unsigned blocks_u, DownArgs v) {
+  const int wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6);
+  if (bid_x() < blocks_u) down_row(u, (int64_t)bid_x() * 4 + wave);
+  else down_row_strided(v, (int64_t)(bid_x() - blocks_u) * 4 + wave);
 }
 
 // ------------------------------------------------------------------ up: Y = base + P M^T
@@ -534,25 +675,97 @@ void lora_up_tile_kernel(UpArgs g) {
   }
 }
 
-// Requests of a few rows: a wave per (row, steps x 64 columns).  G lanes share a column (G
-// the power of two from r / 8 on), each with 8 ranks; in step j of G the wave takes 64 / G
-// columns and lane j of each group keeps the sum, so 64 consecutive columns come out at once.
-// Workgroups go column range by column range, and the rows of one range on one die (id mod
+// Requests of a few rows: a wave per (row, steps x 64 columns).  Up to 32 ranks (CH chunks of 8) a
+// lane takes a whole column, 16 CH bytes of M; beyond, lanes share a column (the next
+// kernel).  Workgroups go column range by column range, and the rows of one range on one die (id mod
 // 8), so that rows with the same adapter find its part of M in that die's L2.
+struct RowPlace {
+  int64_t t, n0, n1;
+  Part p;
+  bool ok;
+};
+__device__ __forceinline__ RowPlace row_place(const UpArgs& g, int columns) {
+  const LoraSet& s = g.s;
+  const int wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6);
+  const unsigned die = bid_x() % 8u, on_die = bid_x() / 8u;
+  RowPlace o{};
+  o.t = on_die % (unsigned)s.T;
+  const int64_t ch = (int64_t)(on_die / (unsigned)s.T) * 8 + die;
+  o.n0 = (ch * 4 + wave) * columns * g.steps;
+  if (o.n0 >= g.C) return o;
+  o.n1 = o.n0 + columns * g.steps < g.C ? o.n0 + columns * g.steps : g.C;
+  const int i = find_request(s.start, (int)s.R, o.t);
+  if (i < 0) return o;
+  o.p = part_of(s, i, o.t, o.t + 1);
+  o.ok = o.p.hi > o.p.lo;
+  return o;
+}
+
+template <int CH, typename YT, typename BT, bool BASE>
+__global__ __launch_bounds__(kLThreads) void lora_up_lane_kernel(UpArgs g) {
+  const LoraSet& s = g.s;
+  const int lane = tid_x() & 63, r = (int)s.r;
+  const RowPlace o = row_place(g, 64);
+  if (!o.ok) return;
+  const int a = o.p.adapter, rank = a >= 0 ? rank_of(s, a) : 0;
+  YT* y = static_cast<YT*>(g.y) + o.t * g.ldy;
+  const BT* base = static_cast<const BT*>(g.base) + (BASE ? o.t * g.ldb : 0);
+  // the row's u, the same in every lane
+  float u[CH][8];
+  int kc[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    kc[c] = 8 * c < r ? 8 * c : 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[c][e] = 0.0f;
+    if (8 * c < rank) load_low(g.P, g.splits, s.T * s.r, o.t, r, 8 * c, rank, s.scale[a], u[c]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      u[c][e] = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(u[c][e])));
+  }
+  const uint16_t* M = g.M + (a >= 0 ? (int64_t)a * g.C * r : 0);
+  const bool mask = rank < r;
+  for (int64_t n = o.n0; n < o.n1; n += 64) {
+    const uint32_t col = (uint32_t)n + lane, at = min(col, (uint32_t)g.C - 1);
+    float out = 0.0f;
+    if (BASE) out = load1(base + at);
+    if (rank > 0) {
+      u32x4_t w[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) w[c] = load16(M + (at * (uint32_t)r + kc[c]));
+      float sum[CH];  // (a sum of every chunk: shorter chains)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (mask) w[c] = keep_below(w[c], kc[c], rank);
+        const unsigned wv[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        sum[c] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum[c] = __builtin_fmaf(u[c][2 * e], __uint_as_float(wv[e] << 16), sum[c]);
+          sum[c] = __builtin_fmaf(u[c][2 * e + 1], __uint_as_float(wv[e] & 0xffff0000u), sum[c]);
+        }
+      }
+#pragma unroll
+      for (int c = 1; c < CH; ++c) sum[0] += sum[c];
+      out += sum[0];
+    }
+    if (col < g.C) {
+      if (a == kBadAdapter) store_bits1(y + col, kQNaN32);
+      else store1(y + col, out);
+    }
+  }
+}
+
+// More ranks: G lanes (8 or 16) share a column, each with 8 ranks; in step j of G the wave takes
+// 64 / G columns and lane j of each group keeps the sum, so 64 consecutive columns come out at once.
 template <int G, typename YT, typename BT, bool BASE>
 __global__ __launch_bounds__(kLThreads) void lora_up_row_kernel(UpArgs g) {
   const LoraSet& s = g.s;
-  const int lane = tid_x() & 63, wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6);
-  const unsigned die = bid_x() % 8u, on_die = bid_x() / 8u;
-  const int64_t t = on_die % (unsigned)s.T;
-  const int64_t ch = (int64_t)(on_die / (unsigned)s.T) * 8 + die;
-  const int64_t n0 = (ch * 4 + wave) * 64 * g.steps;
-  if (n0 >= g.C) return;
-  const int64_t n1 = n0 + 64 * g.steps < g.C ? n0 + 64 * g.steps : g.C;
-  const int i = find_request(s.start, (int)s.R, t);
-  if (i < 0) return;
-  const Part p = part_of(s, i, t, t + 1);
-  if (p.hi <= p.lo) return;
+  const int lane = tid_x() & 63;
+  const RowPlace o = row_place(g, 64);
+  if (!o.ok) return;
+  const Part& p = o.p;
+  const int64_t t = o.t;
   const int j0 = lane & (G - 1), cl = lane / G;
   YT* y = static_cast<YT*>(g.y) + t * g.ldy;
   const int rank = p.adapter >= 0 ? rank_of(s, p.adapter) : 0;
@@ -563,8 +776,8 @@ __global__ __launch_bounds__(kLThreads) void lora_up_row_kernel(UpArgs g) {
   for (int e = 0; e < 8; ++e) u[e] = 0.0f;
   if (live) load_low(g.P, g.splits, s.T * s.r, t, r, k0, rank, s.scale[p.adapter], u);
   const uint16_t* M = g.M + (live ? (int64_t)p.adapter * g.C * r + k0 : 0);
-  const bool mask = !g.m_clean && live && k0 + 8 > rank;
-  for (int64_t n = n0; n < n1; n += 64) {
+  const bool mask = live && k0 + 8 > rank;
+  for (int64_t n = o.n0; n < o.n1; n += 64) {
     const int64_t mine = n + j0 * (64 / G) + cl;  // this lane's column in the end
     float out = 0.0f;
     if (BASE && mine < g.C) out = load1(static_cast<const BT*>(g.base) + t * g.ldb + mine);
@@ -600,47 +813,48 @@ __global__ __launch_bounds__(kLThreads) void lora_up_row_kernel(UpArgs g) {
   }
 }
 
-// ------------------------------------------------------------------ transposed adapters, terms of u and v
-
-// (n, R0, C0) bf16 -> (n, C0, R0), 8 x 8 blocks a thread, with 0 where the rank axis (rows of
-// the input if RANK_ROWS, else its columns) is at the adapter's rank or beyond.
-template <bool RANK_ROWS>
-__device__ __forceinline__ void transpose_block(const LoraSet& s, const uint16_t* in, uint16_t* out, int64_t R0,
-                                                int64_t C0, int64_t at) {
-  const int64_t cb = C0 / 8, rb = R0 / 8;
-  const int64_t a = at / (cb * rb), in_a = at - a * cb * rb;
-  // neighbouring threads along the long axis
-  const int64_t b8 = RANK_ROWS ? in_a / cb : in_a % rb, c8 = RANK_ROWS ? in_a % cb : in_a / rb;
-  const int rank = rank_of(s, (int)a);
-  const int64_t r0 = b8 * 8, c0 = c8 * 8;
-  u32x4_t w[8];
+// dx of single rows: M is A as it lies, (n, r, C), so a lane takes 8 columns and adds up the ranks,
+// 1 KB of A's row a wave and rank.
+template <bool BASE>
+__global__ __launch_bounds__(kLThreads) void lora_up_strided_kernel(UpArgs g) {
+  const LoraSet& s = g.s;
+  const int lane = tid_x() & 63, r = (int)s.r;
+  const RowPlace o = row_place(g, 512);
+  if (!o.ok) return;
+  const int a = o.p.adapter, rank = a >= 0 ? rank_of(s, a) : 0;
+  const int64_t col = o.n0 + lane * 8, at = col < g.C ? col : 0;
+  // lane l holds v of ranks l and l + 64
+  float v[2] = {0.0f, 0.0f};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    w[j] = load16(in + (a * R0 + r0 + j) * C0 + c0);
-    if (RANK_ROWS) {
-      if (r0 + j >= rank) w[j] = (u32x4_t){0u, 0u, 0u, 0u};
-    } else {
-      w[j] = keep_below(w[j], (int)c0, rank);
+  for (int h = 0; h < 2; ++h) {
+    const int rho = lane + 64 * h;
+    if (rho < rank) {
+      for (int sp = 0; sp < g.splits; ++sp) v[h] += g.P[((int64_t)sp * s.T + o.t) * r + rho];
+      v[h] *= s.scale[a];
     }
   }
+  const float* base = static_cast<const float*>(g.base) + (BASE ? o.t * g.ldb : 0);
+  float* y = static_cast<float*>(g.y) + o.t * g.ldy;
+  float out[8];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    unsigned o[4];
+  for (int e = 0; e < 8; ++e) out[e] = 0.0f;
+  if (BASE) load8(base + at, out);
+  const uint16_t* M = g.M + (a >= 0 ? (int64_t)a * r * g.C : 0) + at;
+#pragma unroll 8
+  for (int rho = 0; rho < rank; ++rho) {
+    const float vr = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(rho < 64 ? v[0] : v[1]), rho & 63));
+    float w[8];
+    load8(M + (int64_t)rho * g.C, w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned lo = w[2 * j][c / 2], hi = w[2 * j + 1][c / 2];
-      o[j] = c & 1 ? (lo >> 16) | (hi & 0xffff0000u) : (lo & 0xffffu) | (hi << 16);
-    }
-    *reinterpret_cast<u32x4_t*>(out + (a * C0 + c0 + c) * R0 + r0) = (u32x4_t){o[0], o[1], o[2], o[3]};
+    for (int e = 0; e < 8; ++e) out[e] = __builtin_fmaf(vr, w[e], out[e]);
+  }
+  if (col < g.C) {
+    if (a == kBadAdapter) store_bits8(y + col, kQNaN32);
+    else store8(y + col, out);
   }
 }
 
-__global__ __launch_bounds__(kLThreads) void lora_transpose_kernel(LoraSet s, uint16_t* At, uint16_t* Bt) {
-  const int64_t na = At ? s.n * (s.r / 8) * (s.H / 8) : 0, nb = Bt ? s.n * (s.r / 8) * (s.N / 8) : 0;
-  const int64_t at = (int64_t)bid_x() * kLThreads + tid_x();
-  if (at < na) transpose_block<true>(s, s.A, At, s.r, s.H, at);
-  else if (at - na < nb) transpose_block<false>(s, s.B, Bt, s.N, s.r, at - na);
-}
+// ------------------------------------------------------------------ terms of u and v from partial sums
 
 constexpr int kValStride = kLoraMaxRank + 1;
 // The terms of s_a P from the down kernels' partial sums: a workgroup per 32 rows; 0 for rows
@@ -696,34 +910,46 @@ struct GradArgs {
   float* out;  // (n, r, C) or, transposed, (n, C, r); [splits] of them when splits > 1
   int splits;
   int64_t tslice;  // rows of a split
+  float* P;  // v in the same pass (TRANS): partial sums [blocks of columns][T][r], or nullptr
 };
 
-// The next kGradRows rows of adapter `a` within [t0, t1): requests in order.
-struct RowWalk {
-  int i;
-  int64_t lo, hi, at;  // rows of the current request, and the first of the next stage
+// Rows of one request, and the first row of a stage of them.
+struct Stage {
+  int lo, hi, at;
 };
-__device__ __forceinline__ bool next_request(const LoraSet& s, int a, int64_t t0, int64_t t1, RowWalk& w) {
-  const int lane = tid_x() & 63;
-  for (int i = w.i + 1; i < s.R; i += 64) {
-    const int mine = i + lane;
+// The stages of adapter a within [t0, t1): its requests in order, 64 requests looked at together (each
+// lane keeps one's rows), so that going on to the next takes no load.
+struct RowWalk {
+  int base, lo, hi;          // requests base .. + 63; the rows of this lane's
+  unsigned long long left;   // those of the adapter that are still to come
+  Stage now;
+
+  __device__ __forceinline__ void look(const LoraSet& s, int a, int64_t t0, int64_t t1) {
+    const int i = base + (tid_x() & 63);
     bool hit = false;
-    if (mine < s.R) {
-      const Part p = part_of(s, mine, t0, t1);
+    lo = hi = 0;
+    if (i < s.R) {
+      const Part p = part_of(s, i, t0, t1);
       hit = p.adapter == a && p.hi > p.lo;
+      lo = (int)p.lo;
+      hi = (int)p.hi;
     }
-    const unsigned long long b = __ballot(hit);
-    if (b) {
-      w.i = __builtin_amdgcn_readfirstlane(i + __builtin_ctzll(b));
-      const Part p = part_of(s, w.i, t0, t1);
-      w.lo = p.lo;
-      w.hi = p.hi;
-      w.at = p.lo & ~(int64_t)31;
-      return true;
-    }
+    left = __ballot(hit);
   }
-  return false;
-}
+  __device__ __forceinline__ bool next_request(const LoraSet& s, int a, int64_t t0, int64_t t1) {
+    while (!left) {
+      base += 64;
+      if (base >= s.R) return false;
+      look(s, a, t0, t1);
+    }
+    const int i = __builtin_ctzll(left);
+    left &= left - 1;
+    now.lo = __builtin_amdgcn_readlane(lo, i);
+    now.hi = __builtin_amdgcn_readlane(hi, i);
+    now.at = now.lo & ~31;
+    return true;
+  }
+};
 
 // A workgroup per (adapter, 256 columns, split of the rows).  64 rows of X at a time go
 // through LDS, double buffered, and are read back transposed (ds_read_b64_tr_b16: 16 lanes
@@ -735,10 +961,13 @@ __device__ __forceinline__ bool next_request(const LoraSet& s, int a, int64_t t0
 // then the columns, so that a W term is read by as few waves as can be and serves 4 to 16
 // blocks of columns.  TRANS: the result is (C, r), so the columns of X are the rows of the
 // product.
+// VP: X is dy, and the pass that adds up dB also multiplies each staged row by its columns' rows of
+// B (in registers), so that dy is read once: v = dy B comes out as partial sums of 256 columns.  They
+// take r / 64 of dy's bytes to write and to read, so up to 16 ranks.
 __device__ __forceinline__ int stage_at(int row, int piece) {
   return row * (kGradCols * 2) + ((piece ^ (2 * (row & 3) + 8 * ((row >> 3) & 1))) << 4);
 }
-template <int RB, bool TRANS>
+template <int RB, bool TRANS, bool VP = false>
 __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uint8_t* lds) {
   constexpr int WR = RB < 4 ? RB : 4, RBW = RB / WR, CB = kGradCols / 16 * WR / 4;
   const LoraSet& s = g.s;
@@ -759,25 +988,45 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
   const int srow = tid >> 5, spiece = tid & 31;
   const int64_t scol = c0 + spiece * 8 < g.C ? spiece * 8 : 0;
   const u32x4_t zero = {0u, 0u, 0u, 0u};
-  auto fetch = [&](const RowWalk& w, u32x4_t (&v)[8]) {
+  // (loaded without conditions, from a row of the request, and cut where the stage is written: a
+  // select here would have to wait for the load; columns behind the last are not stored)
+  const uint32_t ldx = (uint32_t)g.ldx;
+  auto fetch = [&](const Stage& w, u32x4_t (&v)[8]) {
+    const uint16_t* X = g.X + w.at * g.ldx + c0;
+    const int lo = max(w.lo - w.at, 0), hi = min(w.hi - w.at, kGradRows) - 1;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t t = w.at + srow + 8 * j;
-      // (loaded without conditions, from a row of the request; columns behind the last are not stored)
-      const u32x4_t x = load16(g.X + (t < w.lo ? w.lo : t < w.hi ? t : w.hi - 1) * g.ldx + c0 + scol);
-      v[j] = t >= w.lo && t < w.hi ? x : zero;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = load16(X + ((uint32_t)min(max(srow + 8 * j, lo), hi) * ldx + (uint32_t)scol));
   };
-  RowWalk w{-1, 0, 0, 0};
-  bool more = next_request(s, a, t0, t1, w);
+  // B's rows c0 .. c0 + 255 as operands: column rho, 8 consecutive rows of k-step ks
+  u32x4_t bv[VP ? kGradCols / 32 : 1];
+  if (VP) {
+    static_assert(!VP || RB == 1, "one block of ranks");
+    const int rho = min(c16, r - 1);
+#pragma unroll
+    for (int ks = 0; ks < kGradCols / 32; ++ks) {
+      unsigned e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t col = c0 + 32 * ks + 8 * q + k;
+        const unsigned v = s.B[((int64_t)a * g.C + (col < g.C ? col : g.C - 1)) * r + rho];
+        e[k] = col < g.C ? v : 0u;
+      }
+      bv[ks] = (u32x4_t){e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+    }
+  }
+  RowWalk w{-64, 0, 0, 0ull, Stage{0, 0, 0}};
+  bool more = w.next_request(s, a, t0, t1);
   u32x4_t held[8];
-  if (more) fetch(w, held);
+  if (more) fetch(w.now, held);
   int stage = 0;
   while (more) {
     uint8_t* T = lds + stage * (kGradRows * kGradCols * 2);
+    const Stage now = w.now;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4_t*>(T + stage_at(srow + 8 * j, spiece)) = held[j];
-    const RowWalk now = w;
+    for (int j = 0; j < 8; ++j) {
+      const int t = now.at + srow + 8 * j;
+      *reinterpret_cast<u32x4_t*>(T + stage_at(srow + 8 * j, spiece)) = t >= now.lo && t < now.hi ? held[j] : zero;
+    }
     // the W operands of the two k-steps (rows now.at .. and now.at + 32 ..)
     u32x4_t wv[2][RBW][3];
 #pragma unroll
@@ -786,15 +1035,15 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
       for (int b = 0; b < RBW; ++b)
 #pragma unroll
         for (int tm = 0; tm < 3; ++tm)
-          wv[ks][b][tm] = load16(g.W + (((now.at / 32 + ks) * RB + wr * RBW + b) * 3 + tm) * 512 + lane * 8);
-    w.at += kGradRows;
-    if (w.at >= w.hi) more = next_request(s, a, t0, t1, w);
-    if (more) fetch(w, held);
+          wv[ks][b][tm] = load16(g.W + (((int64_t)(now.at / 32 + ks) * RB + wr * RBW + b) * 3 + tm) * 512 + lane * 8);
+    // (behind the last stage its own rows once more, so that the loads are not conditional)
+    if (w.now.at + kGradRows < w.now.hi) w.now.at += kGradRows;
+    else more = w.next_request(s, a, t0, t1);
+    fetch(w.now, held);
     __syncthreads();
     if (now.at < now.lo || now.at + kGradRows > now.hi) {
       // rows of other requests may hold anything: neither side may keep them
-      const int begin = now.lo > now.at ? (int)(now.lo - now.at) : 0;
-      const int end = now.hi - now.at < kGradRows ? (int)(now.hi - now.at) : kGradRows;
+      const int begin = max(now.lo - now.at, 0), end = min(now.hi - now.at, kGradRows);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -821,8 +1070,20 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
             acc[h][b] = TRANS ? mfma(x, wv[ks][b][tm], acc[h][b]) : mfma(wv[ks][b][tm], x, acc[h][b]);
       }
     }
-    stage ^= 1;
-    // (the stage written next was last read before the barrier above)
+    if (VP) {
+      // rows 16 wave .. + 15 of the stage
+      f32x4_t vp = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < kGradCols / 32; ++ks)
+        vp = mfma(*reinterpret_cast<const u32x4_t*>(T + stage_at(16 * wave + c16, 4 * ks + q)), bv[ks], vp);
+      float* P = g.P + (int64_t)(block % cols) * s.T * r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = now.at + 16 * wave + 4 * q + e;
+        if (t >= now.lo && t < now.hi && c16 < r) P[(int64_t)t * r + c16] = vp[e];
+      }
+    }
+    stage ^= 1;  // (a stage is written again only behind the next barrier, which is behind its reads)
   }
   const int rank = rank_of(s, a);
   float* out = g.out + (int64_t)split * s.n * s.r * g.C + (int64_t)a * s.r * g.C;
@@ -847,6 +1108,24 @@ __global__ __launch_bounds__(kLThreads) void lora_grad_kernel(GradArgs ga, unsig
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kGradRows * kGradCols * 2];
   if (bid_x() < blocks_a) grad_tile<RB, false>(ga, bid_x(), lds);
   else grad_tile<RB, true>(gb, bid_x() - blocks_a, lds);
+}
+
+__global__ __launch_bounds__(kLThreads) void lora_grad_v_kernel(GradArgs g) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kGradRows * kGradCols * 2];
+  grad_tile<1, true, true>(g, bid_x(), lds);
+}
+
+// The partial sums of the column blocks, [n][plane], added up in order to [parts][plane]: part p takes
+// per of them.
+__global__ __launch_bounds__(kLThreads) void lora_reduce_kernel(const float* P, int n, int64_t plane, int per, float* out) {
+  const int64_t quads = plane / 4, at = (int64_t)bid_x() * kLThreads + tid_x();
+  const int64_t part = at / quads, i = at - part * quads;
+  const int k0 = (int)part * per, k1 = min(k0 + per, n);
+  if (k0 >= n) return;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int k = k0; k < k1; ++k) v += reinterpret_cast<const f32x4_t*>(P + k * plane)[i];
+  reinterpret_cast<f32x4_t*>(out + part * plane)[i] = v;
 }
 
 // out = the sum of the splits' partials, in split order.
@@ -897,12 +1176,12 @@ bool single_rows(int64_t T, int64_t R, int64_t r, int64_t H, int64_t N, bool bac
   return rows < tiles && T * (((H > N ? H : N) + 255) / 256) < (1 << 30);
 }
 
-// Splits of a down product's K.  Single rows: enough for 512 workgroups where K allows ranges
-// of 512.  Tiles: one, whose workgroups finish the product themselves, unless K is long
+// Splits of a down product's K.  Single rows (units: waves a row): enough for 512 workgroups where K
+// allows ranges of 512.  Tiles: one, whose workgroups finish the product themselves, unless K is long
 // (beyond 8192) and the tiles are few; then enough for 512 workgroups, of 4096 k at least.
-void down_split(int64_t T, bool rows, int64_t K, int64_t r, int& splits, int64_t& kslice) {
-  const int64_t units = rows ? (T * (r / kRowRanks) + 3) / 4 : (T + kTileRows - 1) / kTileRows;
-  int64_t want = (512 + units - 1) / units, most = rows ? K / 512 : K <= 8192 ? 1 : K / 4096;
+void down_split(int64_t T, bool rows, int64_t K, int64_t units, int& splits, int64_t& kslice) {
+  const int64_t groups = rows ? (T * units + 3) / 4 : (T + kTileRows - 1) / kTileRows;
+  int64_t want = (512 + groups - 1) / groups, most = rows ? K / 512 : K <= 8192 ? 1 : K / 4096;
   if (want > most) want = most;
   if (want > kMaxSplits) want = kMaxSplits;
   if (want < 1) want = 1;
@@ -910,23 +1189,34 @@ void down_split(int64_t T, bool rows, int64_t K, int64_t r, int& splits, int64_t
   kslice = (per + kDownK - 1) / kDownK * kDownK;
   splits = (int)((K + kslice - 1) / kslice);
 }
+int64_t quads_of(int64_t r) { return r / kRowRanks; }
+int64_t wides_of(int64_t r) { return (r + kRowWide - 1) / kRowWide; }
 
-hipError_t launch_down(const LoraSet& s, const uint16_t* X, int64_t ldx, const uint16_t* M, int64_t K, float* P,
-                       const Terms& o, bool rows, int& splits, hipStream_t st) {
-  DownArgs g{s, X, ldx, M, K, P, 1, 0, o};
-  down_split(s.T, rows, K, s.r, g.splits, g.kslice);
-  splits = g.splits;
-  if (rows) {
-    const int64_t units = s.T * (s.r / kRowRanks) * g.splits;
-    hipLaunchKernelGGL(lora_down_row_kernel, dim3((unsigned)((units + 3) / 4)), dim3(kLThreads), 0, st, g);
-  } else {
-    const dim3 grid((unsigned)((s.T + kTileRows - 1) / kTileRows * g.splits));
-    if (s.r <= 16) hipLaunchKernelGGL(lora_down_tile_kernel<1>, grid, dim3(Down<1>::kThreads), 0, st, g);
-    else if (s.r <= 32) hipLaunchKernelGGL(lora_down_tile_kernel<2>, grid, dim3(Down<2>::kThreads), 0, st, g);
-    else if (s.r <= 64) hipLaunchKernelGGL(lora_down_tile_kernel<4>, grid, dim3(Down<4>::kThreads), 0, st, g);
-    else hipLaunchKernelGGL(lora_down_tile_kernel<8>, grid, dim3(Down<8>::kThreads), 0, st, g);
-  }
+// u and, when v.P is given, v of single rows.
+hipError_t launch_down_rows(const DownArgs& u, bool want_u, const DownArgs& v, bool want_v, hipStream_t st) {
+  const unsigned bu = want_u ? (unsigned)((u.s.T * quads_of(u.s.r) * u.splits + 3) / 4) : 0u;
+  const unsigned bv = want_v ? (unsigned)((v.s.T * wides_of(v.s.r) * v.splits + 3) / 4) : 0u;
+  if (bu + bv == 0) return hipSuccess;
+  hipLaunchKernelGGL(lora_down_row_kernel, dim3(bu + bv), dim3(kLThreads), 0, st, u, bu, v);
   return hipGetLastError();
+}
+
+template <int RB>
+hipError_t launch_down_t(const DownArgs& g, TransposeArgs tr, bool product, hipStream_t st) {
+  const int64_t blocks = tr.s.n * (tr.s.r / 8) * ((tr.At ? tr.s.H / 8 : 0) + (tr.Bt ? tr.s.N / 8 : 0));
+  tr.blocks = (unsigned)((blocks + Down<RB>::kThreads - 1) / Down<RB>::kThreads);
+  const unsigned tiles = product ? (unsigned)((g.s.T + kTileRows - 1) / kTileRows * g.splits) : 0u;
+  if (tr.blocks + tiles == 0) return hipSuccess;
+  hipLaunchKernelGGL(lora_down_tile_kernel<RB>, dim3(tr.blocks + tiles), dim3(Down<RB>::kThreads), 0, st, g, tr);
+  return hipGetLastError();
+}
+// A product of tiles (if wanted), and the transposes of tr in the same launch.
+hipError_t launch_down_tiles(const DownArgs& g, bool product, const TransposeArgs& tr, hipStream_t st) {
+  const int64_t r = g.s.r;
+  if (r <= 16) return launch_down_t<1>(g, tr, product, st);
+  if (r <= 32) return launch_down_t<2>(g, tr, product, st);
+  if (r <= 64) return launch_down_t<4>(g, tr, product, st);
+  return launch_down_t<8>(g, tr, product, st);
 }
 
 hipError_t launch_terms(const TermArgs& a, const TermArgs& b, hipStream_t st) {
@@ -938,18 +1228,33 @@ hipError_t launch_terms(const TermArgs& a, const TermArgs& b, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Single rows: `columns` a wave and step; more steps once there are 16384 waves.
+dim3 up_rows_grid(UpArgs& g, int64_t columns) {
+  const int64_t T = g.s.T;
+  g.steps = (int)(T * ((g.C + columns - 1) / columns) / 16384);
+  g.steps = g.steps < 1 ? 1 : g.steps > 16 ? 16 : g.steps;
+  const int64_t ranges = (g.C + 4 * columns * g.steps - 1) / (4 * columns * g.steps);
+  return dim3((unsigned)((ranges + 7) / 8 * 8 * T));
+}
+
+hipError_t launch_up_strided(UpArgs g, hipStream_t st) {
+  const int64_t T = g.s.T;
+  g.steps = 1;
+  const int64_t ranges = (g.C + 2047) / 2048;
+  const dim3 grid((unsigned)((ranges + 7) / 8 * 8 * T));
+  if (g.base) hipLaunchKernelGGL(lora_up_strided_kernel<true>, grid, dim3(kLThreads), 0, st, g);
+  else hipLaunchKernelGGL(lora_up_strided_kernel<false>, grid, dim3(kLThreads), 0, st, g);
+  return hipGetLastError();
+}
+
 template <typename YT, typename BT, bool BASE>
 hipError_t launch_up_t(UpArgs g, bool rows, hipStream_t st) {
   const int64_t r = g.s.r, T = g.s.T;
   if (rows) {
-    // a wave's columns: 64, more once there are 16384 waves
-    g.steps = (int)(T * ((g.C + 63) / 64) / 16384);
-    g.steps = g.steps < 1 ? 1 : g.steps > 16 ? 16 : g.steps;
-    const int64_t ranges = (g.C + 256 * g.steps - 1) / (256 * g.steps);
-    const dim3 grid((unsigned)((ranges + 7) / 8 * 8 * T));
-    if (r <= 8) hipLaunchKernelGGL((lora_up_row_kernel<1, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
-    else if (r <= 16) hipLaunchKernelGGL((lora_up_row_kernel<2, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
-    else if (r <= 32) hipLaunchKernelGGL((lora_up_row_kernel<4, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
+    const dim3 grid = up_rows_grid(g, 64);
+    if (r <= 8) hipLaunchKernelGGL((lora_up_lane_kernel<1, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
+    else if (r <= 16) hipLaunchKernelGGL((lora_up_lane_kernel<2, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
+    else if (r <= 32) hipLaunchKernelGGL((lora_up_lane_kernel<4, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
     else if (r <= 64) hipLaunchKernelGGL((lora_up_row_kernel<8, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
     else hipLaunchKernelGGL((lora_up_row_kernel<16, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
     return hipGetLastError();
@@ -996,15 +1301,15 @@ struct ForwardWs {
   float* P;     // partial sums: single rows, or several splits
   uint16_t* U;  // tiles: the terms of u
   bool rows;
+  int splits;
+  int64_t kslice;
   size_t bytes;
 };
 ForwardWs forward_ws(void* base, int64_t T, int64_t R, int64_t H, int64_t N, int64_t r) {
   ForwardWs w{};
   w.rows = single_rows(T, R, r, H, N, false);
-  int splits;
-  int64_t ks;
-  down_split(T, w.rows, H, r, splits, ks);
-  const size_t p = w.rows || splits > 1 ? align256((size_t)splits * T * r * 4) : 0;
+  down_split(T, w.rows, H, quads_of(r), w.splits, w.kslice);
+  const size_t p = w.rows || w.splits > 1 ? align256((size_t)w.splits * T * r * 4) : 0;
   const size_t u = w.rows ? 0 : align256(u_bytes(T, r));
   char* b = static_cast<char*>(base);
   w.P = reinterpret_cast<float*>(b);
@@ -1013,11 +1318,21 @@ ForwardWs forward_ws(void* base, int64_t T, int64_t R, int64_t H, int64_t N, int
   return w;
 }
 
+// Whether dB's pass over dy forms v as well: up to 16 ranks and from 2^28 bytes of dy on.  2048 x
+// 151936: 300 us in two passes, 242 in one; but 4096 x 4096 69 and 79, 8192 x 4096 88 and 99 (its
+// launches follow one another, and the pass holds fewer workgroups at once); r 32, 2048 x 151936: 336
+// and 606 (registers).
+bool one_pass_over_dy(int64_t T, int64_t N, int64_t r) { return r <= 16 && T * N * 2 >= (1 << 28); }
+constexpr int kReduceParts = 16;
+
 struct BackwardWs {
   float *Pu, *Pv;
   uint16_t *At, *Bt, *Wu, *Wv, *Uv;
   float *partA, *partB;
+  float* Pf;  // v's partial sums of dB's pass
   bool rows;
+  int splits_u, splits_v;
+  int64_t kslice_u, kslice_v;
   int splits_A, splits_B;
   int64_t tslice_A, tslice_B;
   size_t bytes;
@@ -1032,26 +1347,45 @@ BackwardWs backward_ws(void* base, int64_t T, int64_t R, int64_t n, int64_t H, i
     return q;
   };
   w.rows = single_rows(T, R, r, H, N, true);
-  int su, sv;
-  int64_t ks;
-  down_split(T, w.rows, H, r, su, ks);
-  down_split(T, w.rows, N, r, sv, ks);
+  down_split(T, w.rows, H, quads_of(r), w.splits_u, w.kslice_u);
+  down_split(T, w.rows, N, wides_of(r), w.splits_v, w.kslice_v);
   grad_split(T, n, H, w.splits_A, w.tslice_A);
   grad_split(T, n, N, w.splits_B, w.tslice_B);
-  const bool pu = w.rows || su > 1, pv = w.rows || sv > 1;
-  w.Pu = pu ? reinterpret_cast<float*>(take((size_t)su * T * r * 4)) : nullptr;
-  w.Pv = pv ? reinterpret_cast<float*>(take((size_t)sv * T * r * 4)) : nullptr;
-  w.At = reinterpret_cast<uint16_t*>(take((size_t)n * H * r * 2));
-  w.Bt = reinterpret_cast<uint16_t*>(take((size_t)n * N * r * 2));
+  const bool fused = !w.rows && one_pass_over_dy(T, N, r);
+  const int parts = fused && kReduceParts > w.splits_v ? kReduceParts : w.splits_v;
+  if (w.rows || w.splits_u > 1) w.Pu = reinterpret_cast<float*>(take((size_t)w.splits_u * T * r * 4));
+  if (w.rows || fused || w.splits_v > 1) w.Pv = reinterpret_cast<float*>(take((size_t)parts * T * r * 4));
+  if (!w.rows) {
+    w.At = reinterpret_cast<uint16_t*>(take((size_t)n * H * r * 2));
+    w.Uv = reinterpret_cast<uint16_t*>(take(u_bytes(T, r)));
+    // B the other way round, or (one pass over dy) v's partial sums: never both
+    const size_t bt = (size_t)n * N * r * 2, pf = fused ? (size_t)((N + kGradCols - 1) / kGradCols) * T * r * 4 : 0;
+    char* q = take(bt > pf ? bt : pf);
+    w.Bt = reinterpret_cast<uint16_t*>(q);
+    w.Pf = fused ? reinterpret_cast<float*>(q) : nullptr;
+  }
   // (a stage of the gradients may reach one tile beyond the last)
   const size_t wb = ((size_t)((T + kTileRows - 1) / kTileRows) + 1) * rank_blocks((int)r) * 3 * 1024;
   w.Wu = reinterpret_cast<uint16_t*>(take(wb));
   w.Wv = reinterpret_cast<uint16_t*>(take(wb));
-  w.Uv = w.rows ? nullptr : reinterpret_cast<uint16_t*>(take(u_bytes(T, r)));
   w.partA = w.splits_A > 1 ? reinterpret_cast<float*>(take((size_t)w.splits_A * n * r * H * 4)) : nullptr;
   w.partB = w.splits_B > 1 ? reinterpret_cast<float*>(take((size_t)w.splits_B * n * r * N * 4)) : nullptr;
   w.bytes = off;
   return w;
+}
+
+template <int RB>
+hipError_t launch_grad_t(const GradArgs& ga, unsigned ba, const GradArgs& gb, unsigned bb, hipStream_t st) {
+  if (ba + bb == 0) return hipSuccess;
+  hipLaunchKernelGGL(lora_grad_kernel<RB>, dim3(ba + bb), dim3(kLThreads), 0, st, ga, ba, gb);
+  return hipGetLastError();
+}
+hipError_t launch_grad(const GradArgs& ga, unsigned ba, const GradArgs& gb, unsigned bb, hipStream_t st) {
+  const int64_t r = ga.s.r;
+  if (r <= 16) return launch_grad_t<1>(ga, ba, gb, bb, st);
+  if (r <= 32) return launch_grad_t<2>(ga, ba, gb, bb, st);
+  if (r <= 64) return launch_grad_t<4>(ga, ba, gb, bb, st);
+  return launch_grad_t<8>(ga, ba, gb, bb, st);
 }
 
 }  // namespace
@@ -1068,14 +1402,19 @@ hipError_t launch_lora_forward(const LoraForwardArgs& a, hipStream_t st) {
   (void)hipGetLastError();
   const LoraSet& s = a.s;
   const ForwardWs w = forward_ws(a.workspace, s.T, s.R, s.H, s.N, s.r);
-  int splits;
   const Terms o{w.U, nullptr};
-  if (hipError_t e = launch_down(s, a.x, a.ldx, s.A, s.H, w.P, o, w.rows, splits, st)) return e;
-  if (!w.rows && splits > 1) {
-    const TermArgs t{s, w.P, splits, o}, none{};
-    if (hipError_t e = launch_terms(t, none, st)) return e;
+  const DownArgs d{s, a.x, a.ldx, s.A, s.H, w.P, w.splits, w.kslice, o};
+  if (w.rows) {
+    if (hipError_t e = launch_down_rows(d, true, DownArgs{}, false, st)) return e;
+  } else {
+    const TransposeArgs none{s, nullptr, nullptr, 0};
+    if (hipError_t e = launch_down_tiles(d, true, none, st)) return e;
+    if (w.splits > 1) {
+      const TermArgs t{s, w.P, w.splits, o}, no{};
+      if (hipError_t e = launch_terms(t, no, st)) return e;
+    }
   }
-  const UpArgs g{s, w.P, splits, w.U, s.B, s.N, false, a.base, a.ldb, a.y, a.ldy, 0};
+  const UpArgs g{s, w.P, w.splits, w.U, s.B, s.N, false, a.base, a.ldb, a.y, a.ldy, 0};
   return a.y_dt == Dt::BF16 ? launch_up_y<uint16_t>(g, a.base_dt, w.rows, st) : launch_up_y<float>(g, a.base_dt, w.rows, st);
 }
 
@@ -1092,39 +1431,56 @@ hipError_t launch_lora_backward(const LoraBackwardArgs& a, hipStream_t st) {
   }
   const BackwardWs w = backward_ws(a.workspace, s.T, s.R, s.n, s.H, s.N, s.r);
   const bool need_v = a.gx || a.gA;
-  if (need_v) {
-    const int64_t blocks = s.n * (s.r / 8) * ((a.gx ? s.H / 8 : 0) + s.N / 8);
-    hipLaunchKernelGGL(lora_transpose_kernel, dim3((unsigned)((blocks + kLThreads - 1) / kLThreads)), dim3(kLThreads), 0,
-                       st, s, a.gx ? w.At : nullptr, w.Bt);
-    if (hipError_t e = hipGetLastError()) return e;
-  }
-  // u for dB; v for dx (terms along the ranks, or partial sums for single rows) and dA (terms along the rows)
-  int su = 1, sv = 1;
+  const bool one_pass = w.Pf && a.gB && need_v;  // v in dB's pass over dy
+  // u for dB (terms along the rows); v for dx (terms along the ranks, or partial sums for single rows) and dA
   const Terms ou{nullptr, a.gB ? w.Wu : nullptr};
   const Terms ov{a.gx ? w.Uv : nullptr, a.gA ? w.Wv : nullptr};
-  if (a.gB)
-    if (hipError_t e = launch_down(s, a.x, a.ldx, s.A, s.H, w.Pu, ou, w.rows, su, st)) return e;
-  if (need_v)
-    if (hipError_t e = launch_down(s, a.dy, a.lddy, w.Bt, s.N, w.Pv, ov, w.rows, sv, st)) return e;
-  const bool tu = a.gB && (w.rows || su > 1), tv = need_v && (w.rows || sv > 1);
-  if (tu || tv) {
-    const TermArgs gu{s, w.Pu, su, tu ? ou : Terms{}}, gv{s, w.Pv, sv, tv ? ov : Terms{}};
+  const DownArgs du{s, a.x, a.ldx, s.A, s.H, w.Pu, w.splits_u, w.kslice_u, ou};
+  int splits_v = w.splits_v;
+  if (w.rows) {
+    const DownArgs dv{s, a.dy, a.lddy, s.B, s.N, w.Pv, splits_v, w.kslice_v, Terms{}};
+    if (hipError_t e = launch_down_rows(du, a.gB != nullptr, dv, need_v, st)) return e;
+    const TermArgs tu{s, w.Pu, w.splits_u, ou}, tv{s, w.Pv, splits_v, Terms{nullptr, ov.W}};
+    if (hipError_t e = launch_terms(tu, tv, st)) return e;
+  } else {
+    const TransposeArgs tr{s, a.gx ? w.At : nullptr, need_v && !one_pass ? w.Bt : nullptr, 0};
+    if (hipError_t e = launch_down_tiles(du, a.gB != nullptr, tr, st)) return e;
+    const bool tu = a.gB && w.splits_u > 1;
+    if (need_v && !one_pass) {
+      const DownArgs dv{s, a.dy, a.lddy, w.Bt, s.N, w.Pv, splits_v, w.kslice_v, ov};
+      if (hipError_t e = launch_down_tiles(dv, true, TransposeArgs{s, nullptr, nullptr, 0}, st)) return e;
+    }
+    const TermArgs gu{s, w.Pu, w.splits_u, tu ? ou : Terms{}};
+    const TermArgs gv{s, w.Pv, splits_v, need_v && !one_pass && splits_v > 1 ? ov : Terms{}};
     if (hipError_t e = launch_terms(gu, gv, st)) return e;
   }
-  if (a.gx) {
-    const UpArgs g{s, w.Pv, sv, w.Uv, w.At, s.H, true, a.base, a.ldb, a.gx, a.ldgx, 0};
-    if (hipError_t e = launch_up_y<float>(g, Dt::F32, w.rows, st)) return e;
+  const int64_t cols_A = (s.H + kGradCols - 1) / kGradCols, cols_B = (s.N + kGradCols - 1) / kGradCols;
+  const GradArgs ga{s, a.x, a.ldx, s.H, w.Wv, w.splits_A > 1 ? w.partA : a.gA, w.splits_A, w.tslice_A, nullptr};
+  const GradArgs gb{s, a.dy, a.lddy, s.N, w.Wu, w.splits_B > 1 ? w.partB : a.gB, w.splits_B, w.tslice_B, w.Pf};
+  const unsigned ba = a.gA ? (unsigned)(s.n * w.splits_A * cols_A) : 0u;
+  const unsigned bb = a.gB ? (unsigned)(s.n * w.splits_B * cols_B) : 0u;
+  if (one_pass) {
+    hipLaunchKernelGGL(lora_grad_v_kernel, dim3(bb), dim3(kLThreads), 0, st, gb);
+    if (hipError_t e = hipGetLastError()) return e;
+    const float* P = w.Pf;
+    splits_v = (int)cols_B;
+    if (splits_v > kReduceParts) {
+      const int per = (splits_v + kReduceParts - 1) / kReduceParts;
+      splits_v = (splits_v + per - 1) / per;
+      const int64_t threads = splits_v * (s.T * s.r / 4);
+      hipLaunchKernelGGL(lora_reduce_kernel, dim3((unsigned)((threads + kLThreads - 1) / kLThreads)), dim3(kLThreads), 0,
+                         st, P, (int)cols_B, s.T * s.r, per, w.Pv);
+      if (hipError_t e = hipGetLastError()) return e;
+      P = w.Pv;
+    }
+    const TermArgs gv{s, P, splits_v, ov}, no{};
+    if (hipError_t e = launch_terms(gv, no, st)) return e;
   }
-  if (!a.gA && !a.gB) return hipSuccess;
-  const GradArgs ga{s, a.x, a.ldx, s.H, w.Wv, w.splits_A > 1 ? w.partA : a.gA, w.splits_A, w.tslice_A};
-  const GradArgs gb{s, a.dy, a.lddy, s.N, w.Wu, w.splits_B > 1 ? w.partB : a.gB, w.splits_B, w.tslice_B};
-  const unsigned ba = a.gA ? (unsigned)(s.n * w.splits_A * ((s.H + kGradCols - 1) / kGradCols)) : 0u;
-  const unsigned bb = a.gB ? (unsigned)(s.n * w.splits_B * ((s.N + kGradCols - 1) / kGradCols)) : 0u;
-  if (s.r <= 16) hipLaunchKernelGGL(lora_grad_kernel<1>, dim3(ba + bb), dim3(kLThreads), 0, st, ga, ba, gb);
-  else if (s.r <= 32) hipLaunchKernelGGL(lora_grad_kernel<2>, dim3(ba + bb), dim3(kLThreads), 0, st, ga, ba, gb);
-  else if (s.r <= 64) hipLaunchKernelGGL(lora_grad_kernel<4>, dim3(ba + bb), dim3(kLThreads), 0, st, ga, ba, gb);
-  else hipLaunchKernelGGL(lora_grad_kernel<8>, dim3(ba + bb), dim3(kLThreads), 0, st, ga, ba, gb);
-  if (hipError_t e = hipGetLastError()) return e;
+  if (a.gx) {
+    UpArgs g{s, w.Pv, splits_v, w.Uv, w.rows ? s.A : w.At, s.H, true, a.base, a.ldb, a.gx, a.ldgx, 0};
+    if (hipError_t e = w.rows ? launch_up_strided(g, st) : launch_up_y<float>(g, Dt::F32, false, st)) return e;
+  }
+  if (hipError_t e = launch_grad(ga, ba, gb, one_pass ? 0u : bb, st)) return e;
   const SplitSum sa{w.partA, a.gA, s.n * s.r * s.H, a.gA ? w.splits_A : 0};
   const SplitSum sb{w.partB, a.gB, s.n * s.r * s.N, a.gB ? w.splits_B : 0};
   if (sa.splits > 1 || sb.splits > 1) {
