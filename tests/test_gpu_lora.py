@@ -364,3 +364,38 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for a, b in zip(got, (y, gx, gA, gB)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,R,n,H,N,r", [(1300, 3, 2, 9000, 264, 16), (1300, 2, 2, 264, 20008, 40)])
+def test_long_axis_splits_in_tiles(T, R, n, H, N, r):
+    """Beyond 8192 terms a down product of few tiles is cut into ranges whose sums are added in order."""
+    c = Case(T + H, ragged(T + H, R, T), [i % n for i in range(R)], n, H, N, r)
+    assert path_of(c) == "tiles" and path_of(c, True) == "tiles"
+    check_forward(c, "long H, tiles", base="f32")
+    check_backward(c, "long H, tiles", base=True)
+
+
+@pytest.mark.parametrize("T,R,N,r,rank", [(1100, 3, 131080, 16, None), (4100, 9, 32776, 16, [16, 3, 0]),
+                                          (34000, 700, 4040, 8, [8, 8, 5])])
+def test_a_large_dy(T, R, N, r, rank):
+    """From 2^28 bytes of dy on: v is formed in dB's pass over dy.  Odd sizes, tiles that requests share, ranks cut."""
+    assert T * N * 2 >= 2 ** 28
+    c = Case(T, ragged(T, R, T), [(i * 7) % 4 - (i % 5 == 4) for i in range(R)], 4, 136, N, r,
+             None if rank is None else rank + [r], T=T + 5)
+    c.adapter[1] = -1
+    assert path_of(c, True) == "tiles"
+    gx, gA, gB = check_backward(c, "a large dy", base=True, pads=(8, 16, 8, 24))
+    again = check_backward(c, "a large dy, without dx", want_grads=(False, True, True))
+    assert torch.equal(again[1], gA) and torch.equal(again[2], gB)
+    # NaN and infinities of one adapter's rows stay with it
+    bad = int(np.argmax([c.start[i + 1] - c.start[i] if c.adapter[i] == 2 else 0 for i in range(R)]))
+    lo, hi = c.start[bad], c.start[bad + 1]
+    c.dy[lo:hi], c.dy[T:] = float("nan"), float("inf")
+    c.x[T:] = float("nan")
+    hx, hA, hB = torch.full_like(gx, 55.0), torch.empty_like(gA), torch.empty_like(gB)
+    lx.lx_lora_backward(c.dy.to(DEV), c.x.to(DEV), base=c.base_x.to(DEV), grad_x=hx, grad_A=hA, grad_B=hB, **c.set())
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[lo:hi] = False
+    assert torch.equal(hx[:T][keep], gx[:T][keep])
+    others = [a for a in range(4) if a != 2]
+    assert torch.equal(hA[others], gA[others]) and torch.equal(hB[others], gB[others])
