@@ -182,6 +182,27 @@ __device__ __forceinline__ double exp2_64(double t) {
   return __builtin_ldexp(s, (int)n);
 }
 
+// The same for the passes over whole rows, with 2^(j / 64) from a table in LDS: t = k / 64 + f with |f| <=
+// 1/128 leaves 5 powers (|f ln 2| <= 0.0054: the rest is below 4e-17), two thirds of the instructions.  k
+// comes from adding 1.5 2^46, whose last place is 1/64.
+constexpr int kExpTable = 64;
+__device__ __forceinline__ void exp_table(double (&tab)[kExpTable]) {
+  if (tid_x() < kExpTable) tab[tid_x()] = exp2_64(((double)(int)tid_x() - kExpTable) / kExpTable) * 2.0;
+}
+__device__ __forceinline__ double exp2_64(double t, const double (&tab)[kExpTable]) {
+  constexpr double l = kLn2, round = 0x1.8p46;
+  t = __builtin_fmax(t, -1100.0);
+  const double u = t + round, f = t - (u - round);
+  const int k = (int)(unsigned)__builtin_bit_cast(uint64_t, u);
+  double s = l * l * l * l * l / 120.0;
+  s = __builtin_fma(s, f, l * l * l * l / 24.0);
+  s = __builtin_fma(s, f, l * l * l / 6.0);
+  s = __builtin_fma(s, f, l * l / 2.0);
+  s = __builtin_fma(s, f, l);
+  const double e = tab[k & (kExpTable - 1)];
+  return __builtin_ldexp(__builtin_fma(e, s * f, e), k >> 6);
+}
+
 // log s for 0 < s < inf: s = 2^k m with m in [1/sqrt 2, sqrt 2), and log m = 2 atanh(y),
 // y = (m - 1) / (m + 1), |y| <= 0.1716, by its series to y^19 (the rest is below 1e-17).
 __device__ __forceinline__ double log_64(double s) {
@@ -683,29 +704,19 @@ struct Masses {
   int64_t V, skip;   // skip: a token left out, or -1
   double c, mt, md;  // references
   double it, id;     // residual: 1 / S_t, 1 / S_d
+  const double (&tab)[kExpTable];
 
   __device__ __forceinline__ void of(int64_t v, const float (&x)[8], const float (&y)[8], double (&e)[8]) const {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const double p = exp2_64(((double)x[k] - mt) * c);
+      const double p = exp2_64(((double)x[k] - mt) * c, tab);
       if (ur) {
-        const double d = p * it - exp2_64(((double)y[k] - md) * c) * id;
+        const double d = p * it - exp2_64(((double)y[k] - md) * c, tab) * id;
         e[k] = d > 0.0 ? d : 0.0;
       } else {
         e[k] = v + k == skip ? 0.0 : p;
       }
     }
-  }
-  // of elements v .. v + 7, with the target's logits
-  __device__ __forceinline__ void get(int64_t b, float (&x)[8], double (&e)[8]) const {
-    const int64_t v = b + tid_x() * 8;
-    Group<T> g[1], d[1];
-    hold<T, 1>(zr, b, V, g);
-    if (ur) hold<T, 1>(ur, b, V, d);
-    float y[8];
-    held(zr, v, V, g[0], x);
-    if (ur) held(ur, v, V, d[0], y);
-    of(v, x, y, e);
   }
 };
 
@@ -725,7 +736,7 @@ struct PickShared {
 // element above the goal, the last one with mass is the token; -1: no mass at all.
 // z: its target logit.  (The finds are gathered by ballots: LDS atomics of 64 lanes on one
 // word are taken lane by lane.)
-template <typename T>
+template <int H, typename T>
 __device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int K, int64_t chunk, double w, float& z) {
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   if (wave == 0) {
@@ -767,11 +778,23 @@ __device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int 
   const int64_t lo = sh.chunk * chunk, hi = lo + chunk < m.V ? lo + chunk : m.V;
   double base = 0.0;
   int last = 0;
-  for (int64_t b = lo; b < hi; b += kVUnit) {
+  Group<T> gz[H], gu[H];
+  for (int64_t b = lo, n = 0; b < hi; b += kVUnit, ++n) {
+    if (n % H == 0) {
+      hold<T, H>(m.zr, b, m.V, gz);
+      if (m.ur) hold<T, H>(m.ur, b, m.V, gu);
+    }
     const int64_t v = b + tid * 8;
-    float x[8];
+    float x[8], y[8];
     double e[8], own = 0.0;
-    m.get(b, x, e);  // (0 behind the row's end, which is the only place a chunk ends short)
+    held(m.zr, v, m.V, gz[0], x);
+    if (m.ur) held(m.ur, v, m.V, gu[0], y);
+#pragma unroll
+    for (int h = 1; h < H; ++h) {
+      gz[h - 1] = gz[h];
+      gu[h - 1] = gu[h];
+    }
+    m.of(v, x, y, e);  // (0 behind the row's end, which is the only place a chunk ends short)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       own += e[k];
@@ -870,6 +893,7 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   __shared__ uint64_t red[kVWaves];
   __shared__ double red64[2][kVWaves];
   __shared__ float red_m[2][kVWaves];
+  __shared__ double tab[kExpTable];
   __shared__ PickShared sh;
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
@@ -920,81 +944,70 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
     return;
   }
 
-  // fp64 sums of the chunk, each against the chunk's maximum; the token left out on its own
+  // fp64 sums of the chunk, each thread's against its own maximum (no thread waits for another's
+  // loads); the token left out on its own
   float mt = ninf(), md = ninf();
   double st = 0.0, sd = 0.0;
+  exp_table(tab);
+  __syncthreads();
+  if (tid == 0 && skip >= lo && skip < hi) {
+    md = load1(zr + skip);
+    sd = md > ninf() ? 1.0 : 0.0;
+  }
   for (int64_t b = lo; b < hi; b += kVUnit * H) {
     Group<T> gz[H], gu[H];
     hold<T, H>(zr, b, a.V, gz);
     if (residual) hold<T, H>(ur, b, a.V, gu);
-    float xm = ninf(), ym = ninf(), x[8];
-    // (the token left out counts as -inf, on its own)
-    auto leave_out = [&](int64_t v) {
-      if (skip >= v && skip < v + 8) {
+    auto add = [&](const T* row, Group<T>(&g)[H], float& m, double& s, bool target) {
+      float top = m, x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (v + k == skip) {
-            ym = x[k];
-            x[k] = ninf();
-          }
+      for (int h = 0; h < H; ++h) {
+        const int64_t v = b + h * kVUnit + tid * 8;
+        held(row, v, a.V, g[h], x);
+        top = fmaxf(top, max8(x));
+      }
+      const double ref = (double)ref_of(top);
+      if (b > lo) s *= exp2_64(((double)m - ref) * t.c64, tab);
+      m = top;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const int64_t v = b + h * kVUnit + tid * 8;
+        launder(g[h]);
+        held(row, v, a.V, g[h], x);
+        if (target && skip >= v && skip < v + 8) {  // (the token left out)
+          const int out = (int)(skip - v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = k == out ? ninf() : x[k];
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += exp2_64(((double)x[k] - ref) * t.c64, tab);
+        asm volatile("" : "+v"(s));  // (now: what a sum waits for is not kept for several groups)
+        __builtin_amdgcn_sched_barrier(0);  // (a group at a time: registers)
       }
     };
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int64_t v = b + h * kVUnit + tid * 8;
-      held(zr, v, a.V, gz[h], x);
-      if (!residual) leave_out(v);
-      xm = fmaxf(xm, max8(x));
-      if (residual) {
-        held(ur, v, a.V, gu[h], x);
-        ym = fmaxf(ym, max8(x));
-      }
-    }
-    const float left_out = ym;
-    block_max2(xm, ym, red_m);
-    if (b > lo) {  // (a chunk of several rounds)
-      xm = fmaxf(xm, mt);
-      ym = fmaxf(ym, md);
-      st *= exp2_64(((double)mt - (double)ref_of(xm)) * t.c64);
-      sd *= exp2_64(((double)md - (double)ref_of(ym)) * t.c64);
-    }
-    mt = xm;
-    md = ym;
-    const double rt = (double)ref_of(mt), rd = (double)ref_of(md);
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int64_t v = b + h * kVUnit + tid * 8;
-      launder(gz[h]);
-      held(zr, v, a.V, gz[h], x);
-      if (!residual) leave_out(v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) st += exp2_64(((double)x[k] - rt) * t.c64);
-      if (residual) {
-        launder(gu[h]);
-        held(ur, v, a.V, gu[h], x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sd += exp2_64(((double)x[k] - rd) * t.c64);
-      }
-      __builtin_amdgcn_sched_barrier(0);  // (a group at a time: registers)
-    }
-    if (!residual && left_out > ninf()) sd = 1.0;
-    __syncthreads();  // (red_m is written again)
+    add(zr, gz, mt, st, !residual);
+    if (residual) add(ur, gu, md, sd, false);
   }
-  st = wave_sum64(st);
-  sd = wave_sum64(sd);
+  const Sum64 wt = wave_merge(Sum64{mt, st}, t.c64), wd = wave_merge(Sum64{md, sd}, t.c64);
   if (lane == 0) {
-    red64[0][wave] = st;
-    red64[1][wave] = sd;
+    red_m[0][wave] = wt.m;
+    red_m[1][wave] = wd.m;
+    red64[0][wave] = wt.s;
+    red64[1][wave] = wd.s;
   }
   __syncthreads();
   if (tid == 0) {
-    st = red64[0][0];
-    sd = red64[1][0];
+    mt = md = ninf();
 #pragma unroll
-    for (int k = 1; k < kVWaves; ++k) {
-      st += red64[0][k];
-      sd += red64[1][k];
+    for (int k = 0; k < kVWaves; ++k) {
+      mt = fmaxf(mt, red_m[0][k]);
+      md = fmaxf(md, red_m[1][k]);
+    }
+    st = sd = 0.0;
+#pragma unroll
+    for (int k = 0; k < kVWaves; ++k) {
+      st += red64[0][k] * exp2_64(((double)red_m[0][k] - (double)ref_of(mt)) * t.c64, tab);
+      sd += red64[1][k] * exp2_64(((double)red_m[1][k] - (double)ref_of(md)) * t.c64, tab);
     }
     publish(part, pack(mt, __float_as_uint(md)));
     publish(part + 1, st);
@@ -1063,10 +1076,11 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
                                 : s0;
   const bool only = skip >= 0 && !(s0 > 0.0);
   if (only && tid == 0 && skip < a.V) sh.sums[skip / w.chunk2] = s1;
-  const Masses<T> ms{zr, nullptr, a.V, only ? -1 : skip, t.c64, (double)ref_of(only ? mn : m0), 0.0, 0.0, 0.0};
+  const Masses<T> ms{zr, nullptr, a.V, only ? -1 : skip, t.c64, (double)ref_of(only ? mn : m0), 0.0, 0.0, 0.0,
+                     tab};
   __syncthreads();  // (sh.sums)
   float z;
-  const int64_t tok = pick(ms, sh, K, w.chunk2, (double)u, z);
+  const int64_t tok = pick<H>(ms, sh, K, w.chunk2, (double)u, z);
   write_out(a, w, i, q, acc, tok, logp_of(tok, z, mn, full, t));
 }
 
@@ -1075,6 +1089,7 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
   const VerifyArgs& a = g.a;
   const Ws& w = g.w;
   __shared__ double red64[kVWaves];
+  __shared__ double tab[kExpTable];
   __shared__ PickShared sh;
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
@@ -1093,7 +1108,9 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
   const T* ur = static_cast<const T*>(a.draft) + (q.first + acc) * a.ldd;
   const int64_t lo = c * w.chunk2, hi = lo + w.chunk2 < a.V ? lo + w.chunk2 : a.V;
   Masses<T> ms{zr, ur, a.V, -1, t.c64, (double)ref_of(mt), (double)ref_of(md), St > 0.0 ? 1.0 / St : 0.0,
-               Sd > 0.0 ? 1.0 / Sd : 0.0};
+               Sd > 0.0 ? 1.0 / Sd : 0.0, tab};
+  exp_table(tab);
+  __syncthreads();
   double s = 0.0;
   for (int64_t b = lo; b < hi; b += kVUnit * H) {
     Group<T> gz[H], gu[H];
@@ -1109,6 +1126,7 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
       ms.of(v, x, y, e);
 #pragma unroll
       for (int k = 0; k < 8; ++k) s += e[k];
+      asm volatile("" : "+v"(s));
       __builtin_amdgcn_sched_barrier(0);  // (a group at a time: registers)
     }
   }
@@ -1146,7 +1164,7 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
     ms.ur = nullptr;
   }
   float z;
-  const int64_t tok = pick(ms, sh, K, w.chunk2, (double)u, z);
+  const int64_t tok = pick<H>(ms, sh, K, w.chunk2, (double)u, z);
   write_out(a, w, i, q, acc, tok, logp_of(tok, z, mt, St, t));
 }
 
@@ -1173,14 +1191,16 @@ hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.S * w.K2)), block(kVThreads);
   const bool residual = a.L > 0 && a.draft;
   const int64_t held = w.chunk2 / kVUnit;
+  // (fp32: a chunk of 4 in two rounds of 2; 4 held took 75 and 57 us where 2 take 58 and 49, 96 x 262144)
+  constexpr int kMost = sizeof(T) == 4 ? 2 : 4;
   if (held == 1) hipLaunchKernelGGL((verify_sums_kernel<T, 1>), grid, block, 0, st, g);
   else if (held == 2) hipLaunchKernelGGL((verify_sums_kernel<T, 2>), grid, block, 0, st, g);
-  else hipLaunchKernelGGL((verify_sums_kernel<T, 4>), grid, block, 0, st, g);
+  else hipLaunchKernelGGL((verify_sums_kernel<T, kMost>), grid, block, 0, st, g);
   if (hipError_t e = hipGetLastError()) return e;
   if (residual) {
     if (held == 1) hipLaunchKernelGGL((verify_residual_kernel<T, 1>), grid, block, 0, st, g);
     else if (held == 2) hipLaunchKernelGGL((verify_residual_kernel<T, 2>), grid, block, 0, st, g);
-    else hipLaunchKernelGGL((verify_residual_kernel<T, 4>), grid, block, 0, st, g);
+    else hipLaunchKernelGGL((verify_residual_kernel<T, kMost>), grid, block, 0, st, g);
   }
   return hipGetLastError();
 }
