@@ -674,6 +674,7 @@ lx_status lx_draft_verify(const void* target, int64_t ld_target, const void* dra
       !aligned(n_accepted, 8) || !aligned(tokens, 8) || !aligned(logprobs, 4))
     return LX_ERR_INVALID_ARG;
   const size_t need = lx::verify_workspace_bytes(S, max_draft, V);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
   // 0..6 inputs (may overlap each other), 7..10 outputs and the workspace
   const Span sp[11] = {span(target, strided_bytes(N + S, V, ld_target, es)),
                        span(has_d ? draft : nullptr, has_d ? strided_bytes(N, V, ld_draft, es) : 0),
@@ -684,7 +685,6 @@ lx_status lx_draft_verify(const void* target, int64_t ld_target, const void* dra
   for (int o = 7; o < 11; ++o)
     for (int i = 0; i < 11; ++i)
       if (i != o && overlaps(sp[o], sp[i])) return LX_ERR_ALIAS;
-  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
   lx::VerifyArgs a{};
   a.target = target;
   a.draft = has_d ? draft : nullptr;
@@ -727,6 +727,7 @@ lx_status lx_lora_forward(const void* x, int64_t ldx, const void* A, const void*
   if (!ld_ok(ldx, H) || !ld_ok(ldy, N) || (base && !ld_ok(ld_base, N))) return LX_ERR_INVALID_ARG;
   if (!x || !y || !lora_set_ok(s) || !aligned(x, 16) || !aligned(y, 16) || !aligned(base, 16)) return LX_ERR_INVALID_ARG;
   const size_t need = lx::lora_forward_workspace_bytes(T, R, H, N, r);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
   const int ys = esize_of(y_dt), bs = base ? esize_of(base_dt) : 0;
   const Span out[2] = {span(y, strided_bytes(T, N, ldy, ys)), span(workspace, (int64_t)need)};
   const Span ins[7] = {span(x, strided_bytes(T, H, ldx, 2)), span(A, n_adapters * r * H * 2),
@@ -739,7 +740,6 @@ lx_status lx_lora_forward(const void* x, int64_t ldx, const void* A, const void*
   // y may be base itself (every element is read before it is written)
   const bool in_place = base == y && base_dt == y_dt && ld_base == ldy;
   if ((!in_place && overlaps(out[0], sb)) || overlaps(out[1], sb) || overlaps(out[0], out[1])) return LX_ERR_ALIAS;
-  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
   const lx::LoraForwardArgs a{s, static_cast<const uint16_t*>(x), ldx, base, ld_base, dt_of(base_dt), y, ldy,
                               dt_of(y_dt), workspace};
   return from_hip(lx::launch_lora_forward(a, static_cast<hipStream_t>(stream)));
@@ -768,6 +768,7 @@ lx_status lx_lora_backward(const void* grad_y, int64_t ld_grad_y, const void* x,
       return LX_ERR_INVALID_ARG;
     if (!grad_y || !x || !lora_set_ok(s) || !aligned(grad_y, 16) || !aligned(x, 16)) return LX_ERR_INVALID_ARG;
     need = lx::lora_backward_workspace_bytes(T, R, n_adapters, H, N, r);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
     const Span out[4] = {span(grad_x, grad_x ? strided_bytes(T, H, ld_grad_x, 4) : 0),
                          span(grad_A, n_adapters * r * H * 4), span(grad_B, n_adapters * r * N * 4),
                          span(workspace, (int64_t)need)};
@@ -783,7 +784,6 @@ lx_status lx_lora_backward(const void* grad_y, int64_t ld_grad_y, const void* x,
       if (!(o == 0 && in_place) && overlaps(out[o], sb)) return LX_ERR_ALIAS;
     }
     if (any_overlap(out, 4)) return LX_ERR_ALIAS;
-    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
   } else if (overlaps(span(grad_A, n_adapters * r * H * 4), span(grad_B, n_adapters * r * N * 4))) {
     return LX_ERR_ALIAS;
   }

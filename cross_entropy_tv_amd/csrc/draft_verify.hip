@@ -28,8 +28,11 @@
 //   2. verify_sums_kernel, one workgroup per (sequence, chunk) of the one row that
 //      the token is drawn from: fp64 sums of the masses.  Where they need no draft
 //      the last workgroup draws.
-//   3. verify_residual_kernel (draft logits): the fp64 sums of max(p - q, 0), and
+//   3. verify_draw_kernel (draft logits): the fp64 sums of max(p - q, 0), and
 //      the draw by the last workgroup.
+//
+// A few sequences, whose rows all fit on the chip at once, are bound by latency instead: two steps,
+// verify_rows_kernel with fp64 sums of every position and of the row behind the drafts, and the draw.
 //
 // Precision.  An answer here is a whole number that a comparison decides, so the
 // values compared are held tighter than the rounding of the logits would ask
@@ -137,6 +140,15 @@ template <typename T>
 __device__ __forceinline__ void held(const T* row, int64_t v, int64_t V, const Group<T>& g, float (&x)[8]) {
   if (v + 8 <= V) g.get(x);
   else load_edge(row, v, V, x);
+}
+
+// Element `at` (-1: none) of v .. v + 7 has no mass.
+__device__ __forceinline__ void leave_out(int64_t v, int64_t at, float (&x)[8]) {
+  if (at >= v && at < v + 8) {
+    const int out = (int)(at - v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = k == out ? ninf() : x[k];
+  }
 }
 
 // Elements [lo, hi) of a row of V, lo a multiple of kVUnit: f(v, x) for every group of 8 of this
@@ -423,16 +435,17 @@ __device__ __forceinline__ bool count_last(int* counter, int of) {
 // ------------------------------------------------------------------ workspace
 
 constexpr int kP1 = 2;  // 64-bit words of a chunk's partials in step 1: (m, rest) of target and of draft
-constexpr int kP2 = 3;  // in step 2: (m_t, m_d), s_t, s_d
-constexpr int kSt = 3;  // a sequence's merged sums for step 3: (m_t, m_d), s_t, s_d
+constexpr int kP2 = 3;  // in step 2 (and of verify_rows): (m_t, m_d), s_t, s_d
+constexpr int kSt = 3;  // merged sums for the draw: (m_t, m_d), s_t, s_d
 
 struct Ws {
   int* first;      // [S] the first rejected position, or INT_MAX
-  int* count1;     // [L][S] arrivals of step 1
+  bool direct;     // verify_rows: positions P = L + 1 and part2, state [P][S]; else P = L
+  int* count1;     // [P][S] arrivals of step 1
   int* count2;     // [S]
   int* count3;     // [S]
-  int* best;       // [L][S] greedy: the target's token
-  float* logp;     // [L][S] log p of the drafted token
+  int* best;       // [P][S] greedy: the target's token
+  float* logp;     // [P][S] log p of the drafted token
   uint64_t *part1, *part2, *part3, *state;
   int K1, K2;
   int64_t chunk1, chunk2;
@@ -451,11 +464,20 @@ void chunking(int64_t rows, int64_t V, int64_t wanted, int64_t most, int64_t& ch
   K = (int)((units + per - 1) / per);
 }
 
+// Whether verify_rows takes the first two steps' place: while the fp64 masses of all rows (about 1.6e12 a
+// second at best) cost less than the second step's launch and way through memory.  Sequences of 4 drafts,
+// V = 151936, two launches against three: 19 and 24 us for 1, 27 and 38 for 4, 46 and 56 for 16, 66 and 64
+// for 32; without draft logits 22 and 26 for 4, 34 and 36 for 16, 44 and 38 for 32.  Without drafts (64
+// rows: 28 and 27) the second step is the only one.
+bool direct_rows(int64_t S, int64_t L, int64_t V) { return L > 0 && S * (L + 1) * V <= (1 << 24); }
+
 Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
   Ws w{};
+  w.direct = direct_rows(S, L, V);
+  const int64_t P = w.direct ? L + 1 : L;
   // step 1: at most 16384 elements (a longer chunk delays the decision that spares later
   // positions); steps 2 and 3: what a thread holds at once
-  chunking(S * L, V, 1024, 8, w.chunk1, w.K1);
+  chunking(S * P, V, 1024, 8, w.chunk1, w.K1);
   chunking(S, V, 1280, 4, w.chunk2, w.K2);
   size_t off = 0;
   char* p = static_cast<char*>(base);
@@ -465,16 +487,16 @@ Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
     return q;
   };
   w.first = reinterpret_cast<int*>(take((size_t)S * 4));
-  w.n_zero = S * L + 2 * S;
+  w.n_zero = S * P + 2 * S;
   w.count1 = reinterpret_cast<int*>(take((size_t)w.n_zero * 4));
-  w.count2 = w.count1 ? w.count1 + S * L : nullptr;
+  w.count2 = w.count1 ? w.count1 + S * P : nullptr;
   w.count3 = w.count1 ? w.count2 + S : nullptr;
-  w.best = reinterpret_cast<int*>(take((size_t)S * L * 4));
-  w.logp = reinterpret_cast<float*>(take((size_t)S * L * 4));
-  w.part1 = reinterpret_cast<uint64_t*>(take((size_t)S * L * w.K1 * kP1 * 8));
-  w.part2 = reinterpret_cast<uint64_t*>(take((size_t)S * w.K2 * kP2 * 8));
+  w.best = reinterpret_cast<int*>(take((size_t)S * P * 4));
+  w.logp = reinterpret_cast<float*>(take((size_t)S * P * 4));
+  w.part1 = reinterpret_cast<uint64_t*>(w.direct ? nullptr : take((size_t)S * P * w.K1 * kP1 * 8));
+  w.part2 = reinterpret_cast<uint64_t*>(take((size_t)(w.direct ? S * P * w.K1 : S * w.K2) * kP2 * 8));
   w.part3 = reinterpret_cast<uint64_t*>(take((size_t)S * w.K2 * 8));
-  w.state = reinterpret_cast<uint64_t*>(take((size_t)S * kSt * 8));
+  w.state = reinterpret_cast<uint64_t*>(take((size_t)(w.direct ? S * P : S) * kSt * 8));
   w.bytes = off;
   return w;
 }
@@ -695,13 +717,189 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
   }
 }
 
+// ------------------------------------------------------------------ steps 1 and 2 in one
+
+// A thread's fp64 sum over its H groups of a round, against its own maximum (no thread waits for
+// another's loads).  out_at: an element left out, or -1.
+template <int H, typename T>
+__device__ __forceinline__ void add_round(const T* row, int64_t b, int64_t V, Group<T> (&g)[H], double c, int64_t out_at,
+                                          const double (&tab)[kExpTable], Sum64& a) {
+  float top = a.m, x[8];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    held(row, b + h * kVUnit + tid_x() * 8, V, g[h], x);
+    top = fmaxf(top, max8(x));
+  }
+  const double ref = (double)ref_of(top);
+  double s = a.s * exp2_64(((double)a.m - ref) * c, tab);
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    const int64_t v = b + h * kVUnit + tid_x() * 8;
+    launder(g[h]);
+    held(row, v, V, g[h], x);
+    leave_out(v, out_at, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += exp2_64(((double)x[k] - ref) * c, tab);
+    asm volatile("" : "+v"(s));  // (now: what a sum waits for is not kept for several groups)
+    __builtin_amdgcn_sched_barrier(0);  // (a group at a time: registers)
+  }
+  a.m = top;
+  a.s = s;
+}
+
+// Steps 1 and 2 of few rows: fp64 sums of every position's rows and of the row behind the last draft.
+template <typename T, int H>
+__global__ __launch_bounds__(kVThreads) void verify_rows_kernel(Args g) {
+  const VerifyArgs& a = g.a;
+  const Ws& w = g.w;
+  __shared__ uint64_t red[kVWaves];
+  __shared__ Sum64 red64[2][kVWaves];
+  __shared__ double tab[kExpTable];
+  __shared__ int sh_flag;
+  const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
+  const int K = w.K1;
+  const int c = (int)(bid_x() % (unsigned)K);
+  const unsigned slot = bid_x() / (unsigned)K;
+  const int i = (int)(slot % (unsigned)a.S), j = (int)(slot / (unsigned)a.S);
+  const Seq q = seq_of(a, i);
+  if (j > q.n || !q.ok) return;
+  const Temp t = temp_of(a.temperature, i);
+  const bool drafted = j < q.n;  // else the row behind the last draft, which only the draw asks for
+  const T* zr = static_cast<const T*>(a.target) + (q.first + i + j) * a.ldt;
+  const bool has_d = drafted && a.draft != nullptr && !t.greedy;
+  const T* ur = has_d ? static_cast<const T*>(a.draft) + (q.first + j) * a.ldd : nullptr;
+  const int64_t lo = c * w.chunk1, hi = lo + w.chunk1 < a.V ? lo + w.chunk1 : a.V;
+  // what the decision needs is requested ahead of it: the token with the row, its logits behind the row's loads
+  const int64_t x = drafted ? a.tokens[q.first + j] : -1;
+  const bool x_ok = x >= 0 && x < a.V;
+  const double r = drafted ? (double)a.u_accept[q.first + j] : 0.0;
+  float zx = ninf(), ux = ninf();
+  uint64_t* part = w.part2 + ((int64_t)slot * K + c) * kP2;
+
+  if (t.greedy) {
+    Best b{ninf(), kNone};
+    for_groups<H>(zr, lo, hi, a.V, [&](int64_t v, const float (&e)[8]) { add8(b, v, e); });
+    b = wave_merge(b);
+    if (lane == 0) red[wave] = pack(b.v, b.at);
+    __syncthreads();
+    if (tid == 0) {
+      b = Best{ninf(), kNone};
+#pragma unroll
+      for (int k = 0; k < kVWaves; ++k) {  // waves hold ascending runs only inside a pass: compare places too
+        const float v = lo_of(red[k]);
+        const unsigned at = hi_of(red[k]);
+        if (v > b.v || (v == b.v && at < b.at)) b = Best{v, at};
+      }
+      publish(part, pack(b.v, b.at));
+    }
+  } else {
+    // (a draft without a distribution is on its own in the sums: it is left out of the draw)
+    const int64_t out_at = drafted && !a.draft ? x : -1;
+    exp_table(tab);
+    __syncthreads();
+    Sum64 st{ninf(), 0.0}, sd{ninf(), 0.0};
+    for (int64_t b = lo; b < hi; b += kVUnit * H) {
+      Group<T> gz[H], gu[H];
+      hold<T, H>(zr, b, a.V, gz);
+      if (has_d) hold<T, H>(ur, b, a.V, gu);
+      add_round<H>(zr, b, a.V, gz, t.c64, out_at, tab, st);
+      if (has_d) add_round<H>(ur, b, a.V, gu, t.c64, -1, tab, sd);
+    }
+    if (x_ok) zx = load1(zr + x);
+    if (x_ok && has_d) ux = load1(ur + x);
+    st = wave_merge(st, t.c64);
+    if (has_d) sd = wave_merge(sd, t.c64);
+    if (lane == 0) {
+      red64[0][wave] = st;
+      red64[1][wave] = sd;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      float m[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h && !has_d) break;
+        m[h] = red64[h][0].m;
+#pragma unroll
+        for (int k = 1; k < kVWaves; ++k) m[h] = fmaxf(m[h], red64[h][k].m);
+        double sum = 0.0;
+#pragma unroll
+        for (int k = 0; k < kVWaves; ++k)
+          sum += red64[h][k].s * exp2_64(((double)red64[h][k].m - (double)ref_of(m[h])) * t.c64, tab);
+        publish(part + 1 + h, sum);
+      }
+      publish(part, pack(m[0], has_d ? __float_as_uint(m[1]) : 0u));
+    }
+  }
+  if (tid == 0) sh_flag = count_last(w.count1 + slot, K);
+  __syncthreads();
+  if (!sh_flag) return;
+
+  // the position's last workgroup: merge the chunks and decide
+  const uint64_t* parts = w.part2 + (int64_t)slot * K * kP2;
+  if (t.greedy) {
+    if (wave == 0) {
+      Best b{ninf(), kNone};
+      for (int k = lane; k < K; k += 64) {
+        const uint64_t v = fetch(parts + k * kP2);
+        if (lo_of(v) > b.v || (lo_of(v) == b.v && hi_of(v) < b.at)) b = Best{lo_of(v), hi_of(v)};
+      }
+      b = wave_merge(b);
+      if (lane == 0) {
+        // a row with no mass has no largest logit: nothing is accepted, no token drawn
+        const int at = b.v == ninf() ? -1 : (int)b.at;
+        w.best[slot] = at;
+        w.logp[slot] = 0.0f;
+        if (drafted && (!x_ok || x != at))
+          __hip_atomic_fetch_min(w.first + i, j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    return;
+  }
+  if (wave < (has_d ? 2 : 1)) {  // the first wave the target's, the second the draft's
+    Sum64 s{ninf(), 0.0};
+    for (int k = lane; k < K; k += 64) {
+      const uint64_t v = fetch(parts + k * kP2);
+      const double e = fetch64(parts + k * kP2 + 1 + wave);
+      const float m = wave ? __uint_as_float(hi_of(v)) : lo_of(v), mn = fmaxf(s.m, m);
+      const double ref = (double)ref_of(mn);
+      s.s = s.s * exp2_64(((double)s.m - ref) * t.c64, tab) + e * exp2_64(((double)m - ref) * t.c64, tab);
+      s.m = mn;
+    }
+    s = wave_merge(s, t.c64);
+    if (lane == 0) red64[wave][0] = s;
+  }
+  __syncthreads();
+  if (tid > 0) return;
+  const float mt = red64[0][0].m, md = has_d ? red64[1][0].m : ninf();
+  const double ez = exp2_64(((double)zx - (double)ref_of(mt)) * t.c64, tab);
+  // (the token left out of the target's sum is part of p)
+  double St = red64[0][0].s, Sd = 1.0, eu = 1.0;
+  if (drafted && !a.draft) St += ez;
+  if (has_d) {
+    Sd = red64[1][0].s;
+    eu = exp2_64(((double)ux - (double)ref_of(md)) * t.c64, tab);
+  }
+  uint64_t* state = w.state + (int64_t)slot * kSt;
+  state[0] = pack(mt, __float_as_uint(md));
+  state[1] = __builtin_bit_cast(uint64_t, St);
+  state[2] = __builtin_bit_cast(uint64_t, Sd);
+  if (!drafted) return;
+  // r q < p with p = ez / St and q = eu / Sd (q = 1 without draft logits), multiplied out;
+  // a row without mass has p = 0 or q = 0
+  const bool pz = ez > 0.0 && St > 0.0, qz = eu > 0.0 && Sd > 0.0;
+  const bool accept = pz && (!qz || r * eu * St < ez * Sd);
+  w.logp[slot] = pz ? (float)(((double)zx - (double)mt) * t.inv - log_64(St)) : ninf();
+  if (!accept) __hip_atomic_fetch_min(w.first + i, j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // ------------------------------------------------------------------ steps 2 and 3: the token behind the accepted ones
 
-// The masses that the token is drawn from: p relative to mt, or max(p - q, 0).
-template <typename T>
+// The masses that the token is drawn from: max(p - q, 0) (RES), or p relative to mt.
+template <typename T, bool RES>
 struct Masses {
-  const T *zr, *ur;  // ur: the residual's draft row, or nullptr
-  int64_t V, skip;   // skip: a token left out, or -1
+  const T *zr, *ur;  // ur: the draft's row (RES)
+  int64_t V, skip;   // skip: a token left out, or -1 (not RES)
   double c, mt, md;  // references
   double it, id;     // residual: 1 / S_t, 1 / S_d
   const double (&tab)[kExpTable];
@@ -710,19 +908,28 @@ struct Masses {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const double p = exp2_64(((double)x[k] - mt) * c, tab);
-      if (ur) {
+      if (RES) {
         const double d = p * it - exp2_64(((double)y[k] - md) * c, tab) * id;
         e[k] = d > 0.0 ? d : 0.0;
       } else {
-        e[k] = v + k == skip ? 0.0 : p;
+        e[k] = p;
       }
     }
   }
+  // of a held group (its target logits in x)
+  __device__ __forceinline__ void of(int64_t v, const Group<T>& z, const Group<T>& u, float (&x)[8], double (&e)[8]) const {
+    float y[8];
+    held(zr, v, V, z, x);
+    if (RES) held(ur, v, V, u, y);
+    if (!RES) leave_out(v, skip, x);
+    of(v, x, y, e);
+  }
 };
 
+constexpr int kMaxHold = 4;
 struct PickShared {
   double sums[kVMaxChunks];
-  double wave[kVWaves];
+  double wave[kMaxHold][kVWaves];
   double before;  // the sum in front of the chosen chunk
   int chunk;
   int found[kVWaves];  // token + 1 of a wave's first element above the goal, 0: none
@@ -736,8 +943,8 @@ struct PickShared {
 // element above the goal, the last one with mass is the token; -1: no mass at all.
 // z: its target logit.  (The finds are gathered by ballots: LDS atomics of 64 lanes on one
 // word are taken lane by lane.)
-template <int H, typename T>
-__device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int K, int64_t chunk, double w, float& z) {
+template <int H, typename T, bool RES>
+__device__ __forceinline__ int64_t pick(const Masses<T, RES>& m, PickShared& sh, int K, int64_t chunk, double w, float& z) {
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   if (wave == 0) {
     // each lane a run of consecutive chunks
@@ -777,70 +984,95 @@ __device__ __forceinline__ int64_t pick(const Masses<T>& m, PickShared& sh, int 
   const double goal = sh.before;
   const int64_t lo = sh.chunk * chunk, hi = lo + chunk < m.V ? lo + chunk : m.V;
   double base = 0.0;
-  int last = 0;
-  Group<T> gz[H], gu[H];
-  for (int64_t b = lo, n = 0; b < hi; b += kVUnit, ++n) {
-    if (n % H == 0) {
-      hold<T, H>(m.zr, b, m.V, gz);
-      if (m.ur) hold<T, H>(m.ur, b, m.V, gu);
-    }
-    const int64_t v = b + tid * 8;
-    float x[8], y[8];
-    double e[8], own = 0.0;
-    held(m.zr, v, m.V, gz[0], x);
-    if (m.ur) held(m.ur, v, m.V, gu[0], y);
+  for (int64_t b = lo; b < hi; b += kVUnit * H) {
+    // the sums of H groups, then the elements of the one that crosses the goal
+    Group<T> gz[H], gu[H];
+    hold<T, H>(m.zr, b, m.V, gz);
+    if (RES) hold<T, H>(m.ur, b, m.V, gu);
+    float x[8];
+    double e[8], own[H], incl[H];
 #pragma unroll
-    for (int h = 1; h < H; ++h) {
-      gz[h - 1] = gz[h];
-      gu[h - 1] = gu[h];
-    }
-    m.of(v, x, y, e);  // (0 behind the row's end, which is the only place a chunk ends short)
+    for (int h = 0; h < H; ++h) {
+      const int64_t v = b + h * kVUnit + tid * 8;
+      m.of(v, gz[h], gu[h], x, e);  // (0 behind the row's end, which is the only place a chunk ends short)
+      own[h] = 0.0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      own += e[k];
-      if (e[k] > 0.0) last = (int)(v + k) + 1;
+      for (int k = 0; k < 8; ++k) own[h] += e[k];
+      asm volatile("" : "+v"(own[h]));
+      incl[h] = wave_scan64(own[h]);
+      if (lane == 63) sh.wave[h][wave] = incl[h];
+      launder(gz[h]);
+      if (RES) launder(gu[h]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    const double incl = wave_scan64(own);
-    if (lane == 63) sh.wave[wave] = incl;
     __syncthreads();
-    double run = base + incl - own, all = base;
+#pragma unroll 1
+    for (int h = 0; h < H; ++h) {
+      Group<T> z1 = gz[0], u1 = gu[0];
+      double sum = own[0], upto = incl[0];
 #pragma unroll
-    for (int k = 0; k < kVWaves; ++k) {
-      if (k < wave) run += sh.wave[k];
-      all += sh.wave[k];
-    }
-    if (all > goal) {
-      // the first element whose running sum exceeds the goal: the lowest token among the finds
-      int at = 0;
-      float zx = 0.0f;
-      if (run + own > goal) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          run += e[k];
-          if (!at && e[k] > 0.0 && run > goal) {
-            at = (int)(v + k) + 1;
-            zx = x[k];
-          }
+      for (int k = 1; k < H; ++k) {
+        if (k == h) {
+          z1 = gz[k];
+          u1 = gu[k];
+          sum = own[k];
+          upto = incl[k];
         }
       }
-      const unsigned long long hit = __ballot(at != 0);
-      if (lane == (hit ? __builtin_ctzll(hit) : 0)) {
-        sh.found[wave] = at;
-        sh.z[wave] = zx;
-      }
-      __syncthreads();
+      double run = base + upto - sum, all = base;
 #pragma unroll
       for (int k = 0; k < kVWaves; ++k) {
-        if (sh.found[k]) {
-          z = sh.z[k];
-          return sh.found[k] - 1;
-        }
+        if (k < wave) run += sh.wave[h][k];
+        all += sh.wave[h][k];
       }
+      if (all > goal) {
+        // the first element whose running sum exceeds the goal: the lowest token among the finds
+        const int64_t v = b + h * kVUnit + tid * 8;
+        int at = 0;
+        float zx = 0.0f;
+        if (run + sum > goal) {
+          m.of(v, z1, u1, x, e);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            run += e[k];
+            if (!at && e[k] > 0.0 && run > goal) {
+              at = (int)(v + k) + 1;
+              zx = x[k];
+            }
+          }
+        }
+        const unsigned long long hit = __ballot(at != 0);
+        if (lane == (hit ? __builtin_ctzll(hit) : 0)) {
+          sh.found[wave] = at;
+          sh.z[wave] = zx;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kVWaves; ++k) {
+          if (sh.found[k]) {
+            z = sh.z[k];
+            return sh.found[k] - 1;
+          }
+        }
+        __syncthreads();  // (sh.found may be written again)
+      }
+      base = all;
     }
-    base = all;
-    __syncthreads();  // sh.wave is written again
+    __syncthreads();  // (sh.wave is written again)
   }
-  // (a thread's last element with mass: lanes and waves hold ascending runs inside a pass only, so the largest)
+  // the last element with mass (lanes and waves hold ascending runs inside a pass only, so the largest)
+  int last = 0;
+  for (int64_t b = lo; b < hi; b += kVUnit) {
+    const int64_t v = b + tid * 8;
+    Group<T> z1[1], u1[1];
+    hold<T, 1>(m.zr, b, m.V, z1);
+    if (RES) hold<T, 1>(m.ur, b, m.V, u1);
+    float x[8];
+    double e[8];
+    m.of(v, z1[0], u1[0], x, e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) last = e[k] > 0.0 ? (int)(v + k) + 1 : last;
+  }
   last = wave_all(last, [](int p, int q) { return p > q ? p : q; });
   if (lane == 0) sh.last[wave] = last;
   __syncthreads();
@@ -946,49 +1178,21 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
 
   // fp64 sums of the chunk, each thread's against its own maximum (no thread waits for another's
   // loads); the token left out on its own
-  float mt = ninf(), md = ninf();
-  double st = 0.0, sd = 0.0;
+  Sum64 pt{ninf(), 0.0}, pd{ninf(), 0.0};
   exp_table(tab);
   __syncthreads();
   if (tid == 0 && skip >= lo && skip < hi) {
-    md = load1(zr + skip);
-    sd = md > ninf() ? 1.0 : 0.0;
+    pd.m = load1(zr + skip);
+    pd.s = pd.m > ninf() ? 1.0 : 0.0;
   }
   for (int64_t b = lo; b < hi; b += kVUnit * H) {
     Group<T> gz[H], gu[H];
     hold<T, H>(zr, b, a.V, gz);
     if (residual) hold<T, H>(ur, b, a.V, gu);
-    auto add = [&](const T* row, Group<T>(&g)[H], float& m, double& s, bool target) {
-      float top = m, x[8];
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const int64_t v = b + h * kVUnit + tid * 8;
-        held(row, v, a.V, g[h], x);
-        top = fmaxf(top, max8(x));
-      }
-      const double ref = (double)ref_of(top);
-      if (b > lo) s *= exp2_64(((double)m - ref) * t.c64, tab);
-      m = top;
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const int64_t v = b + h * kVUnit + tid * 8;
-        launder(g[h]);
-        held(row, v, a.V, g[h], x);
-        if (target && skip >= v && skip < v + 8) {  // (the token left out)
-          const int out = (int)(skip - v);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = k == out ? ninf() : x[k];
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s += exp2_64(((double)x[k] - ref) * t.c64, tab);
-        asm volatile("" : "+v"(s));  // (now: what a sum waits for is not kept for several groups)
-        __builtin_amdgcn_sched_barrier(0);  // (a group at a time: registers)
-      }
-    };
-    add(zr, gz, mt, st, !residual);
-    if (residual) add(ur, gu, md, sd, false);
+    add_round<H>(zr, b, a.V, gz, t.c64, skip, tab, pt);
+    if (residual) add_round<H>(ur, b, a.V, gu, t.c64, -1, tab, pd);
   }
-  const Sum64 wt = wave_merge(Sum64{mt, st}, t.c64), wd = wave_merge(Sum64{md, sd}, t.c64);
+  const Sum64 wt = wave_merge(pt, t.c64), wd = wave_merge(pd, t.c64);
   if (lane == 0) {
     red_m[0][wave] = wt.m;
     red_m[1][wave] = wd.m;
@@ -997,13 +1201,13 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   }
   __syncthreads();
   if (tid == 0) {
-    mt = md = ninf();
+    float mt = ninf(), md = ninf();
+    double st = 0.0, sd = 0.0;
 #pragma unroll
     for (int k = 0; k < kVWaves; ++k) {
       mt = fmaxf(mt, red_m[0][k]);
       md = fmaxf(md, red_m[1][k]);
     }
-    st = sd = 0.0;
 #pragma unroll
     for (int k = 0; k < kVWaves; ++k) {
       st += red64[0][k] * exp2_64(((double)red_m[0][k] - (double)ref_of(mt)) * t.c64, tab);
@@ -1076,7 +1280,7 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
                                 : s0;
   const bool only = skip >= 0 && !(s0 > 0.0);
   if (only && tid == 0 && skip < a.V) sh.sums[skip / w.chunk2] = s1;
-  const Masses<T> ms{zr, nullptr, a.V, only ? -1 : skip, t.c64, (double)ref_of(only ? mn : m0), 0.0, 0.0, 0.0,
+  const Masses<T, false> ms{zr, nullptr, a.V, only ? -1 : skip, t.c64, (double)ref_of(only ? mn : m0), 0.0, 0.0, 0.0,
                      tab};
   __syncthreads();  // (sh.sums)
   float z;
@@ -1084,8 +1288,9 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   write_out(a, w, i, q, acc, tok, logp_of(tok, z, mn, full, t));
 }
 
+// H: groups of 8 that a thread holds (a chunk is one or more rounds of them).
 template <typename T, int H>
-__global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
+__global__ __launch_bounds__(kVThreads) void verify_draw_kernel(Args g, int K) {
   const VerifyArgs& a = g.a;
   const Ws& w = g.w;
   __shared__ double red64[kVWaves];
@@ -1093,78 +1298,99 @@ __global__ __launch_bounds__(kVThreads) void verify_residual_kernel(Args g) {
   __shared__ PickShared sh;
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
-  const int K = w.K2;
   const int c = (int)(bid_x() % (unsigned)K), i = (int)(bid_x() / (unsigned)K);
   const Seq q = seq_of(a, i);
   const int acc = min(w.first[i], q.n);
-  if (!q.ok || acc >= q.n) return;  // drawn from p in step 2
+  const bool residual = a.draft != nullptr && acc < q.n;
   const Temp t = temp_of(a.temperature, i);
+  const int64_t slot = (int64_t)acc * a.S + i;
+  if (!q.ok || t.greedy || !residual) {
+    if (c > 0 || !w.direct) return;  // (drawn in step 2)
+    if (!q.ok || t.greedy) {
+      write_out(a, w, i, q, acc, q.ok ? w.best[slot] : -1, 0.0f);
+      return;
+    }
+  }
+  // sums of the rows that the token is drawn from, and of p's chunks
+  const int64_t at = w.direct ? slot : i, p_chunk = w.direct ? w.chunk1 : w.chunk2;
+  const int p_chunks = w.direct ? w.K1 : w.K2;
   const float u = a.u_sample[i];
-  if (t.greedy) return;
-  const uint64_t* state = w.state + (int64_t)i * kSt;
+  const uint64_t* state = w.state + at * kSt;
   const float mt = lo_of(state[0]), md = __uint_as_float(hi_of(state[0]));
   const double St = __builtin_bit_cast(double, state[1]), Sd = __builtin_bit_cast(double, state[2]);
   const T* zr = static_cast<const T*>(a.target) + (q.first + i + acc) * a.ldt;
-  const T* ur = static_cast<const T*>(a.draft) + (q.first + acc) * a.ldd;
-  const int64_t lo = c * w.chunk2, hi = lo + w.chunk2 < a.V ? lo + w.chunk2 : a.V;
-  Masses<T> ms{zr, ur, a.V, -1, t.c64, (double)ref_of(mt), (double)ref_of(md), St > 0.0 ? 1.0 / St : 0.0,
-               Sd > 0.0 ? 1.0 / Sd : 0.0, tab};
+  const T* ur = residual ? static_cast<const T*>(a.draft) + (q.first + acc) * a.ldd : nullptr;
+  // a rejected draft without a distribution is left out of the draw
+  const int64_t skip = !residual && acc < q.n ? a.tokens[q.first + acc] : -1;
+  const double rt = (double)ref_of(mt), rd = (double)ref_of(md);
   exp_table(tab);
   __syncthreads();
-  double s = 0.0;
-  for (int64_t b = lo; b < hi; b += kVUnit * H) {
-    Group<T> gz[H], gu[H];
-    hold<T, H>(zr, b, a.V, gz);
-    hold<T, H>(ur, b, a.V, gu);
+  float z;
+  if (residual) {
+    const int64_t lo = c * w.chunk2, hi = lo + w.chunk2 < a.V ? lo + w.chunk2 : a.V;
+    const Masses<T, true> ms{zr, ur, a.V, -1, t.c64, rt, rd, St > 0.0 ? 1.0 / St : 0.0, Sd > 0.0 ? 1.0 / Sd : 0.0, tab};
+    double s = 0.0;
+    for (int64_t b = lo; b < hi; b += kVUnit * H) {
+      Group<T> gz[H], gu[H];
+      hold<T, H>(zr, b, a.V, gz);
+      hold<T, H>(ur, b, a.V, gu);
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int64_t v = b + h * kVUnit + tid * 8;
-      float x[8], y[8];
-      double e[8];
-      held(zr, v, a.V, gz[h], x);
-      held(ur, v, a.V, gu[h], y);
-      ms.of(v, x, y, e);
+      for (int h = 0; h < H; ++h) {
+        const int64_t v = b + h * kVUnit + tid * 8;
+        float x[8], y[8];
+        double e[8];
+        held(zr, v, a.V, gz[h], x);
+        held(ur, v, a.V, gu[h], y);
+        ms.of(v, x, y, e);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s += e[k];
-      asm volatile("" : "+v"(s));
-      __builtin_amdgcn_sched_barrier(0);  // (a group at a time: registers)
+        for (int k = 0; k < 8; ++k) s += e[k];
+        asm volatile("" : "+v"(s));
+        __builtin_amdgcn_sched_barrier(0);  // (a group at a time: registers)
+      }
     }
-  }
-  s = wave_sum64(s);
-  if (lane == 0) red64[wave] = s;
-  __syncthreads();
-  if (tid == 0) {
-    double r = 0.0;
+    s = wave_sum64(s);
+    if (lane == 0) red64[wave] = s;
+    __syncthreads();
+    if (tid == 0) {
+      double r = 0.0;
 #pragma unroll
-    for (int k = 0; k < kVWaves; ++k) r += red64[k];
-    publish(w.part3 + (int64_t)i * K + c, r);
-    sh_flag = count_last(w.count3 + i, K);
-  }
-  __syncthreads();
-  if (!sh_flag) return;
-  double any = 0.0;
-  for (int k = tid; k < K; k += kVThreads) {
-    sh.sums[k] = fetch64(w.part3 + (int64_t)i * K + k);
-    any += sh.sums[k];
-  }
-  __syncthreads();
-  any = wave_sum64(any);
-  if (lane == 0) red64[wave] = any;
-  __syncthreads();
-  any = 0.0;
-#pragma unroll
-  for (int k = 0; k < kVWaves; ++k) any += red64[k];
-  if (!(any > kNothing)) {
-    // nothing in p beyond q (a draft that neither row could have produced): drawn from p
-    for (int k = tid; k < K; k += kVThreads) {
-      const uint64_t* part = w.part2 + ((int64_t)i * K + k) * kP2;
-      sh.sums[k] = __builtin_bit_cast(double, part[1]) * exp2_64(((double)lo_of(part[0]) - ms.mt) * t.c64);
+      for (int k = 0; k < kVWaves; ++k) r += red64[k];
+      publish(w.part3 + (int64_t)i * K + c, r);
+      sh_flag = count_last(w.count3 + i, K);
     }
     __syncthreads();
-    ms.ur = nullptr;
+    if (!sh_flag) return;
+    double any = 0.0;
+    for (int k = tid; k < K; k += kVThreads) {
+      sh.sums[k] = fetch64(w.part3 + (int64_t)i * K + k);
+      any += sh.sums[k];
+    }
+    __syncthreads();  // (red64 is written again)
+    any = wave_sum64(any);
+    if (lane == 0) red64[wave] = any;
+    __syncthreads();
+    any = 0.0;
+#pragma unroll
+    for (int k = 0; k < kVWaves; ++k) any += red64[k];
+    if (any > kNothing) {
+      const int64_t tok = pick<H>(ms, sh, K, w.chunk2, (double)u, z);
+      write_out(a, w, i, q, acc, tok, logp_of(tok, z, mt, St, t));
+      return;
+    }
+    // nothing in p beyond q (a draft that neither row could have produced): drawn from p
   }
-  float z;
-  const int64_t tok = pick<H>(ms, sh, K, w.chunk2, (double)u, z);
+  for (int k = tid; k < p_chunks; k += kVThreads) {
+    const uint64_t* part = w.part2 + (at * p_chunks + k) * kP2;
+    sh.sums[k] = __builtin_bit_cast(double, part[1]) * exp2_64(((double)lo_of(part[0]) - rt) * t.c64, tab);
+  }
+  __syncthreads();
+  const Masses<T, false> ms{zr, nullptr, a.V, skip, t.c64, rt, rd, 0.0, 0.0, tab};
+  int64_t tok = pick<H>(ms, sh, p_chunks, p_chunk, (double)u, z);
+  if (tok < 0 && skip >= 0 && skip < a.V && load1(zr + skip) > ninf()) {
+    // no mass but the token left out: drawn after all (p is 1 there)
+    tok = skip;
+    z = load1(zr + skip);
+  }
   write_out(a, w, i, q, acc, tok, logp_of(tok, z, mt, St, t));
 }
 
@@ -1179,29 +1405,32 @@ hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
   hipLaunchKernelGGL(verify_init_kernel, dim3((unsigned)((n + kVThreads - 1) / kVThreads)), dim3(kVThreads), 0, st,
                      w.first, (int)a.S, w.count1, w.n_zero);
   if (hipError_t e = hipGetLastError()) return e;
-  if (a.L > 0) {
-    const dim3 grid((unsigned)(a.S * a.L * w.K1)), block(kVThreads);
-    // groups held at once, two rows of them: 2 of 2-byte logits (4: 23.7 against 21.4 us at 256 x
-    // 50001, the registers halve the workgroups at once), 4 of fp32 (2: 191 against 183 us at 96 x 262144)
-    constexpr int kHold = sizeof(T) == 4 ? 4 : 2;
-    if (w.chunk1 < kHold * kVUnit) hipLaunchKernelGGL((verify_accept_kernel<T, 1>), grid, block, 0, st, g);
-    else hipLaunchKernelGGL((verify_accept_kernel<T, kHold>), grid, block, 0, st, g);
-    if (hipError_t e = hipGetLastError()) return e;
-  }
-  const dim3 grid((unsigned)(a.S * w.K2)), block(kVThreads);
-  const bool residual = a.L > 0 && a.draft;
+  const dim3 block(kVThreads), rows((unsigned)(a.S * (w.direct ? a.L + 1 : a.L) * w.K1)), draws((unsigned)(a.S * w.K2));
   const int64_t held = w.chunk2 / kVUnit;
-  // (fp32: a chunk of 4 in two rounds of 2; 4 held took 75 and 57 us where 2 take 58 and 49, 96 x 262144)
-  constexpr int kMost = sizeof(T) == 4 ? 2 : 4;
-  if (held == 1) hipLaunchKernelGGL((verify_sums_kernel<T, 1>), grid, block, 0, st, g);
-  else if (held == 2) hipLaunchKernelGGL((verify_sums_kernel<T, 2>), grid, block, 0, st, g);
-  else hipLaunchKernelGGL((verify_sums_kernel<T, kMost>), grid, block, 0, st, g);
-  if (hipError_t e = hipGetLastError()) return e;
-  if (residual) {
-    if (held == 1) hipLaunchKernelGGL((verify_residual_kernel<T, 1>), grid, block, 0, st, g);
-    else if (held == 2) hipLaunchKernelGGL((verify_residual_kernel<T, 2>), grid, block, 0, st, g);
-    else hipLaunchKernelGGL((verify_residual_kernel<T, kMost>), grid, block, 0, st, g);
+  if (w.direct) {
+    if (w.chunk1 == kVUnit) hipLaunchKernelGGL((verify_rows_kernel<T, 1>), rows, block, 0, st, g);
+    else hipLaunchKernelGGL((verify_rows_kernel<T, 2>), rows, block, 0, st, g);
+  } else {
+    if (a.L > 0) {
+      // groups held at once, two rows of them: 2 of 2-byte logits (4: 23.7 against 21.4 us at 256 x
+      // 50001, the registers halve the workgroups at once), 4 of fp32 (2: 191 against 183 us at 96 x 262144)
+      constexpr int kHold = sizeof(T) == 4 ? 4 : 2;
+      if (w.chunk1 < kHold * kVUnit) hipLaunchKernelGGL((verify_accept_kernel<T, 1>), rows, block, 0, st, g);
+      else hipLaunchKernelGGL((verify_accept_kernel<T, kHold>), rows, block, 0, st, g);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+    // (fp32: a chunk of 4 in two rounds of 2; 4 held took 75 us where 2 take 58, 96 x 262144)
+    if (held == 1) hipLaunchKernelGGL((verify_sums_kernel<T, 1>), draws, block, 0, st, g);
+    else if (held == 2 || sizeof(T) == 4) hipLaunchKernelGGL((verify_sums_kernel<T, 2>), draws, block, 0, st, g);
+    else hipLaunchKernelGGL((verify_sums_kernel<T, sizeof(T) == 4 ? 2 : 4>), draws, block, 0, st, g);
+    if (a.L == 0 || !a.draft) return hipGetLastError();
   }
+  if (hipError_t e = hipGetLastError()) return e;
+  // (without draft logits every draw is from p, by one workgroup)
+  const int K = a.draft ? w.K2 : 1;
+  const dim3 all((unsigned)(a.S * K));
+  if (held == 1) hipLaunchKernelGGL((verify_draw_kernel<T, 1>), all, block, 0, st, g, K);
+  else hipLaunchKernelGGL((verify_draw_kernel<T, 2>), all, block, 0, st, g, K);
   return hipGetLastError();
 }
 

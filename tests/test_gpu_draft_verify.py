@@ -23,6 +23,16 @@ DEV = "cuda:0"
 DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 TOL_LOGP = 2.0 ** -18
 NINF = float("-inf")
+DIRECT = 1 << 24  # up to this many positions times V the rows are summed in one step
+ROOM = {"wide": False}
+
+
+@pytest.fixture(params=[False, True], ids=["", "wide"], autouse=True)
+def room(request):
+    """Every test twice: as it is, and with room for so many drafts that a few sequences take the many ones' path."""
+    ROOM["wide"] = request.param
+    yield
+    ROOM["wide"] = False
 
 
 def rows(rng, n, V, scale=3.0):
@@ -46,6 +56,10 @@ class Case:
         self.lens, self.V, self.dt = lens, V, dt
         self.start = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
         self.max_draft = max(lens + [0]) if max_draft is None else max_draft
+        if ROOM["wide"]:
+            self.max_draft = max(self.max_draft, DIRECT // (S * V))
+            if self.max_draft > 2 ** 20:
+                pytest.skip("more room than the entry point takes")
         z = rows(rng, N + S, V).to(DT[dt]).float()
         u = rows(rng, N, V, noise)
         for i in range(S):
@@ -250,7 +264,7 @@ def test_sequences_that_do_not_fit_are_refused_alone():
         gn, gtok, glp = c2.run()
         for i in range(4):
             s, e = bad[i], bad[i + 1]
-            if not (0 <= s <= e <= 8 and e - s <= 2):
+            if not (0 <= s <= e <= 8 and e - s <= c2.max_draft):
                 assert gn[i] == -1 and (gtok[i] == -1).all() and (glp[i] == 0).all(), (bad, i)
             elif (s, e) == (c.start[i], c.start[i + 1]):
                 assert gn[i] == n[i] and np.array_equal(gtok[i], tok[i]), (bad, i)
@@ -260,7 +274,7 @@ def test_without_logprobs_and_with_a_given_workspace():
     c = Case(43, [2, 3], 1234)
     n, tok, _ = c.reference()
     out = c.outputs()
-    need = lx.lx_draft_verify_workspace_bytes(2, 3, 1234)
+    need = lx.lx_draft_verify_workspace_bytes(2, c.max_draft, 1234)
     ws = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)
     lx.lx_draft_verify(**c.inputs(), n_accepted=out[0], tokens=out[1], logprobs=None, workspace=ws)
     assert np.array_equal(out[0].cpu().numpy(), n) and np.array_equal(out[1].cpu().numpy(), tok)
@@ -282,7 +296,7 @@ def test_repeats_are_bitwise_equal_and_streams_are_kept():
 def test_captured_and_replayed():
     c = Case(53, [4, 0, 3, 2], 9001)
     a, out = c.inputs(), c.outputs()
-    ws = torch.empty(lx.lx_draft_verify_workspace_bytes(4, 4, 9001), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(lx.lx_draft_verify_workspace_bytes(4, c.max_draft, 9001), dtype=torch.uint8, device=DEV)
     call = lambda: lx.lx_draft_verify(**a, n_accepted=out[0], tokens=out[1], logprobs=out[2], workspace=ws)  # noqa: E731
     call()
     torch.cuda.synchronize()
