@@ -126,15 +126,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_DTYPE_CODES = {torch.float32: LX_F32, torch.bfloat16: LX_BF16, torch.float16: LX_F16}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return LX_BF16
-    if t.dtype == torch.float32:
-        return LX_F32
-    if t.dtype == torch.float16:
-        return LX_F16
-    raise TypeError(f"logits must be bfloat16, float16 or float32, got {t.dtype}")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {t.dtype}")
+    return code
 
 
 def _stream(stream):
@@ -170,6 +169,9 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 class _Launch:
     """The device, stream and workspace of one call: the device of its tensors is made
     current (a stream belongs to a device), the stream is the given one or that device's
@@ -183,7 +185,7 @@ class _Launch:
 
     def __enter__(self):
         index = self.device.index
-        if torch.cuda.current_device() != index:
+        if _current_device() != index:
             self.guard = torch.cuda.device(index)
             self.guard.__enter__()
         self.ptr = _current_raw_stream(index) if self.stream is None else _stream(self.stream)
@@ -200,6 +202,7 @@ class _Launch:
                 raise ValueError(f"workspace must be on {self.device}")
         elif self.stream is None:
             given = torch.empty(need, dtype=torch.uint8, device=self.device)
+            return given.data_ptr(), need, given
         else:
             s = self.stream if hasattr(self.stream, "cuda_stream") else torch.cuda.ExternalStream(self.ptr)
             with torch.cuda.stream(s):
@@ -514,7 +517,7 @@ def lx_draft_verify(target, draft, draft_tokens, draft_start, max_draft: int, te
     if logprobs is not None:
         _arg(logprobs, "logprobs", f32, (S, max_draft + 1), dev)
     with _Launch(dev, stream) as at:
-        ws, wbytes, _held = at.workspace(workspace, lx_draft_verify_workspace_bytes(S, max_draft, V))
+        ws, wbytes, _held = at.workspace(workspace, lib.lx_draft_verify_workspace_bytes(S, max_draft, V))
         _check(lib.lx_draft_verify(_ptr(target), ldt, _ptr(draft), ldd, _ptr(draft_tokens), _ptr(draft_start), S, N,
                                    max_draft, V, _ptr(temperature), _ptr(u_accept), _ptr(u_sample),
                                    _ptr(n_accepted), _ptr(tokens), _ptr(logprobs), dt, ws, wbytes, at.ptr),
@@ -529,34 +532,39 @@ def lx_lora_backward_workspace_bytes(T: int, R: int, n_adapters: int, H: int, N:
     return lib.lx_lora_backward_workspace_bytes(T, R, n_adapters, H, N, r)
 
 
-def _lora_set(x, A, B, adapter, req_start, scale, rank):
-    """(T, R, n_adapters, H, N, r, device) of the arguments that both directions take, checked."""
-    dev, bf16, i64 = x.device, torch.bfloat16, torch.int64
-    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
-        raise ValueError("A must be (n_adapters, r, H) and B (n_adapters, N, r)")
-    (n, r, H), N, R = A.shape, B.shape[1], adapter.shape[0]
-    T = x.shape[0]
-    _bf16_rows(x, "x", T, H, dev)
-    _arg(A, "A", bf16, (n, r, H), dev)
-    _arg(B, "B", bf16, (n, N, r), dev)
-    _arg(adapter, "adapter", i64, (R,), dev)
-    _arg(req_start, "req_start", i64, (R + 1,), dev)
-    _arg(scale, "scale", torch.float32, (n,), dev)
-    if rank is not None:
-        _arg(rank, "rank", i64, (n,), dev)
-    return T, R, n, H, N, r, dev
-
-
 def _rows_of(t, name, dtypes, rows, cols, dev):
     """The row stride of a 2-D (rows, cols) device tensor with contiguous rows, of one of these dtypes."""
     if t.dtype not in dtypes or t.shape != (rows, cols) or t.device != dev:
         raise ValueError(f"{name} must be ({rows}, {cols}) on {dev}, {' or '.join(map(str, dtypes))}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    return _rows2d(t, name)[2]
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return ld if rows > 1 else cols
 
 
-def _bf16_rows(t, name, rows, cols, dev):
-    return _rows_of(t, name, (torch.bfloat16,), rows, cols, dev)
+_ONLY_BF16, _ONLY_F32, _F32_OR_BF16 = (torch.bfloat16,), (torch.float32,), (torch.float32, torch.bfloat16)
+
+
+def _lora_set(x, A, B, adapter, req_start, scale, rank):
+    """(T, R, n_adapters, H, N, r, device, x's row stride, the pointers of A .. rank) of the arguments that both
+    directions take, checked."""
+    dev, bf16, i64, a, b = x.device, torch.bfloat16, torch.int64, A.shape, B.shape
+    if len(a) != 3 or len(b) != 3 or a[0] != b[0] or a[1] != b[2]:
+        raise ValueError("A must be (n_adapters, r, H) and B (n_adapters, N, r)")
+    (n, r, H), N, R, T = a, b[1], adapter.shape[0], x.shape[0]
+    ldx = _rows_of(x, "x", _ONLY_BF16, T, H, dev)
+    _arg(A, "A", bf16, a, dev)
+    _arg(B, "B", bf16, b, dev)
+    _arg(adapter, "adapter", i64, (R,), dev)
+    _arg(req_start, "req_start", i64, (R + 1,), dev)
+    _arg(scale, "scale", torch.float32, (n,), dev)
+    if rank is not None:
+        _arg(rank, "rank", i64, (n,), dev)
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor, and the others on its device")
+    return T, R, n, H, N, r, dev, ldx, (A.data_ptr(), B.data_ptr(), adapter.data_ptr(), req_start.data_ptr(),
+                                        scale.data_ptr(), None if rank is None else rank.data_ptr())
 
 
 def lx_lora_forward(x, A, B, adapter, req_start, scale, rank, base, y, workspace=None, stream=None) -> None:
@@ -565,16 +573,15 @@ def lx_lora_forward(x, A, B, adapter, req_start, scale, rank, base, y, workspace
     ``req_start`` int64 [R + 1]; ``scale`` float32 [n_adapters], ``rank`` int64 [n_adapters]
     or None; ``base`` (T, N) or None and ``y`` (T, N), float32 or bfloat16 each (``y`` may be
     ``base``).  The workspace is allocated here with torch when not given."""
-    T, R, n, H, N, r, dev = _lora_set(x, A, B, adapter, req_start, scale, rank)
-    kinds = (torch.float32, torch.bfloat16)
-    ldb = N if base is None else _rows_of(base, "base", kinds, T, N, dev)
-    ldy = _rows_of(y, "y", kinds, T, N, dev)
+    T, R, n, H, N, r, dev, ldx, set_ = _lora_set(x, A, B, adapter, req_start, scale, rank)
+    base_ptr, ldb, base_dt = None, N, LX_F32
+    if base is not None:
+        base_ptr, ldb, base_dt = base.data_ptr(), _rows_of(base, "base", _F32_OR_BF16, T, N, dev), _dtype_code(base)
+    ldy = _rows_of(y, "y", _F32_OR_BF16, T, N, dev)
     with _Launch(dev, stream) as at:
-        ws, wbytes, _held = at.workspace(workspace, lx_lora_forward_workspace_bytes(T, R, H, N, r))
-        _check(lib.lx_lora_forward(_ptr(x), _rows2d(x, "x")[2], _ptr(A), _ptr(B), _ptr(adapter), _ptr(req_start),
-                                   _ptr(scale), _ptr(rank), T, R, n, H, N, r, _ptr(base), ldb,
-                                   LX_F32 if base is None else _dtype_code(base), _ptr(y), ldy, _dtype_code(y),
-                                   ws, wbytes, at.ptr), "lx_lora_forward")
+        ws, wbytes, _held = at.workspace(workspace, lib.lx_lora_forward_workspace_bytes(T, R, H, N, r))
+        _check(lib.lx_lora_forward(x.data_ptr(), ldx, *set_, T, R, n, H, N, r, base_ptr, ldb, base_dt, y.data_ptr(), ldy,
+                                   _dtype_code(y), ws, wbytes, at.ptr), "lx_lora_forward")
 
 
 def lx_lora_backward(grad_y, x, A, B, adapter, req_start, scale, rank, base, grad_x, grad_A, grad_B, workspace=None,
@@ -582,19 +589,17 @@ def lx_lora_backward(grad_y, x, A, B, adapter, req_start, scale, rank, base, gra
     """The gradients of lx_lora_forward: ``grad_y`` (T, N) bfloat16 and its inputs, into
     ``grad_x`` (T, H) (``base`` or 0 added; may be ``base``), ``grad_A`` and ``grad_B`` (as A
     and B), float32, each or None; grad_A and grad_B are overwritten."""
-    T, R, n, H, N, r, dev = _lora_set(x, A, B, adapter, req_start, scale, rank)
-    f32 = (torch.float32,)
-    lddy = _bf16_rows(grad_y, "grad_y", T, N, dev)
-    ldb = H if base is None else _rows_of(base, "base", f32, T, H, dev)
-    ldgx = H if grad_x is None else _rows_of(grad_x, "grad_x", f32, T, H, dev)
+    T, R, n, H, N, r, dev, ldx, set_ = _lora_set(x, A, B, adapter, req_start, scale, rank)
+    lddy = _rows_of(grad_y, "grad_y", _ONLY_BF16, T, N, dev)
+    ldb = H if base is None else _rows_of(base, "base", _ONLY_F32, T, H, dev)
+    ldgx = H if grad_x is None else _rows_of(grad_x, "grad_x", _ONLY_F32, T, H, dev)
     if grad_A is not None:
         _arg(grad_A, "grad_A", torch.float32, (n, r, H), dev)
     if grad_B is not None:
         _arg(grad_B, "grad_B", torch.float32, (n, N, r), dev)
     with _Launch(dev, stream) as at:
-        ws, wbytes, _held = at.workspace(workspace, lx_lora_backward_workspace_bytes(T, R, n, H, N, r))
-        _check(lib.lx_lora_backward(_ptr(grad_y), lddy, _ptr(x), _rows2d(x, "x")[2], _ptr(A), _ptr(B), _ptr(adapter),
-                                    _ptr(req_start), _ptr(scale), _ptr(rank), T, R, n, H, N, r, _ptr(base), ldb,
+        ws, wbytes, _held = at.workspace(workspace, lib.lx_lora_backward_workspace_bytes(T, R, n, H, N, r))
+        _check(lib.lx_lora_backward(grad_y.data_ptr(), lddy, x.data_ptr(), ldx, *set_, T, R, n, H, N, r, _ptr(base), ldb,
                                     _ptr(grad_x), ldgx, _ptr(grad_A), _ptr(grad_B), ws, wbytes, at.ptr),
                "lx_lora_backward")
 

@@ -756,6 +756,101 @@ __global__ __launch_bounds__(kLThreads) void lora_up_lane_kernel(UpArgs g) {
   }
 }
 
+// The same with u formed by every workgroup itself, its waves sharing out the ranks: a few rows are bound by
+// the launches, and A's part is read from the L2s once for every 256 steps columns of a row.
+struct RowArgs {
+  const uint16_t *X, *A;
+  int64_t ldx, K;
+};
+template <int CH, typename YT, typename BT, bool BASE>
+__global__ __launch_bounds__(kLThreads) void lora_row_kernel(UpArgs g, RowArgs d) {
+  __shared__ float sh[8 * CH];
+  const LoraSet& s = g.s;
+  const int lane = tid_x() & 63, wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6), r = (int)s.r;
+  const int64_t t = bid_x() % (unsigned)s.T;
+  const int64_t wide = 64 * g.steps, n0 = ((int64_t)(bid_x() / (unsigned)s.T) * 4 + wave) * wide;
+  const int64_t n1 = n0 + wide < g.C ? n0 + wide : g.C;
+  const int i = find_request(s.start, (int)s.R, t);
+  if (i < 0) return;
+  const Part p = part_of(s, i, t, t + 1);
+  if (p.hi <= p.lo) return;
+  const int a = p.adapter, rank = a >= 0 ? rank_of(s, a) : 0;
+  YT* y = static_cast<YT*>(g.y) + t * g.ldy;
+  const BT* base = static_cast<const BT*>(g.base) + (BASE ? t * g.ldb : 0);
+  const uint16_t* M = g.M + (a >= 0 ? (int64_t)a * g.C * r : 0);
+  u32x4_t w[CH];
+  float old = 0.0f;
+  auto load = [&](int64_t n) {
+    const uint32_t at = min((uint32_t)n + lane, (uint32_t)g.C - 1);
+    if (BASE) old = load1(base + at);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) w[c] = load16(M + (at * (uint32_t)r + (8 * c < r ? 8 * c : 0)));
+  };
+  load(n0);  // (ahead of u)
+  if (rank > 0) {
+    // ranks 2 CH wave .. of u
+    const uint16_t *x = d.X + t * d.ldx, *m = d.A + (int64_t)a * r * d.K;
+    float acc[2 * CH];
+#pragma unroll
+    for (int j = 0; j < 2 * CH; ++j) acc[j] = 0.0f;
+#pragma unroll 2
+    for (int64_t k = lane * 8; k < d.K; k += 512) {
+      float xv[8], mv[8];
+      load8(x + k, xv);
+#pragma unroll
+      for (int j = 0; j < 2 * CH; ++j) {
+        const int rho = min(2 * CH * wave + j, r - 1);
+        load8(m + rho * d.K + k, mv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[j] = __builtin_fmaf(xv[e], mv[e], acc[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * CH; ++j) {
+      const float v = wave_sum(acc[j]);
+      const int rho = 2 * CH * wave + j;
+      if (lane == 0) sh[rho] = rho < rank ? s.scale[a] * v : 0.0f;
+    }
+  }
+  __syncthreads();
+  float u[CH][8];
+  if (rank > 0) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        u[c][e] = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sh[8 * c + e])));
+  }
+  const bool mask = rank < r;
+  for (int64_t n = n0; n < n1; n += 64) {
+    float out = old;
+    if (rank > 0) {
+      float sum[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (mask) w[c] = keep_below(w[c], 8 * c, rank);
+        const unsigned wv[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        sum[c] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum[c] = __builtin_fmaf(u[c][2 * e], __uint_as_float(wv[e] << 16), sum[c]);
+          sum[c] = __builtin_fmaf(u[c][2 * e + 1], __uint_as_float(wv[e] & 0xffff0000u), sum[c]);
+        }
+        if (8 * c >= r) sum[c] = 0.0f;  // (24 ranks: the last chunk is the first again)
+      }
+#pragma unroll
+      for (int c = 1; c < CH; ++c) sum[0] += sum[c];
+      out += sum[0];
+    }
+    const int64_t col = n + lane;
+    if (col < g.C) {
+      if (a == kBadAdapter) store_bits1(y + col, kQNaN32);
+      else store1(y + col, out);
+    }
+    if (n + 64 < n1) load(n + 64);
+  }
+}
+
 // More ranks: G lanes (8 or 16) share a column, each with 8 ranks; in step j of G the wave takes
 // 64 / G columns and lane j of each group keeps the sum, so 64 consecutive columns come out at once.
 template <int G, typename YT, typename BT, bool BASE>
@@ -1247,9 +1342,25 @@ hipError_t launch_up_strided(UpArgs g, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Single rows in one launch: steps of 256 columns of a workgroup for about 256 workgroups, and whether A's part,
+// read by each of them from the L2s at about 8 TB/s, costs less than the second launch (about 4 us).
+bool one_launch(int64_t T, int64_t r, int64_t H, int64_t N, int& steps) {
+  const int64_t units = (N + 255) / 256;
+  steps = (int)((T * units + 255) / 256);
+  steps = steps > 16 ? 16 : steps;
+  return r <= 32 && T * ((units + steps - 1) / steps) * r * H * 2 <= (1 << 25);
+}
+
 template <typename YT, typename BT, bool BASE>
-hipError_t launch_up_t(UpArgs g, bool rows, hipStream_t st) {
+hipError_t launch_up_t(UpArgs g, bool rows, hipStream_t st, const RowArgs& d) {
   const int64_t r = g.s.r, T = g.s.T;
+  if (rows && d.X) {
+    const dim3 grid((unsigned)(T * ((g.C + 256 * g.steps - 1) / (256 * g.steps))));
+    if (r <= 8) hipLaunchKernelGGL((lora_row_kernel<1, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g, d);
+    else if (r <= 16) hipLaunchKernelGGL((lora_row_kernel<2, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g, d);
+    else hipLaunchKernelGGL((lora_row_kernel<4, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g, d);
+    return hipGetLastError();
+  }
   if (rows) {
     const dim3 grid = up_rows_grid(g, 64);
     if (r <= 8) hipLaunchKernelGGL((lora_up_lane_kernel<1, YT, BT, BASE>), grid, dim3(kLThreads), 0, st, g);
@@ -1274,9 +1385,10 @@ hipError_t launch_up_t(UpArgs g, bool rows, hipStream_t st) {
 }
 
 template <typename YT>
-hipError_t launch_up_y(const UpArgs& g, Dt base_dt, bool rows, hipStream_t st) {
-  if (!g.base) return launch_up_t<YT, float, false>(g, rows, st);
-  return base_dt == Dt::BF16 ? launch_up_t<YT, uint16_t, true>(g, rows, st) : launch_up_t<YT, float, true>(g, rows, st);
+hipError_t launch_up_y(const UpArgs& g, Dt base_dt, bool rows, hipStream_t st, const RowArgs& d = RowArgs{}) {
+  if (!g.base) return launch_up_t<YT, float, false>(g, rows, st, d);
+  return base_dt == Dt::BF16 ? launch_up_t<YT, uint16_t, true>(g, rows, st, d)
+                             : launch_up_t<YT, float, true>(g, rows, st, d);
 }
 
 size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -1404,7 +1516,11 @@ hipError_t launch_lora_forward(const LoraForwardArgs& a, hipStream_t st) {
   const ForwardWs w = forward_ws(a.workspace, s.T, s.R, s.H, s.N, s.r);
   const Terms o{w.U, nullptr};
   const DownArgs d{s, a.x, a.ldx, s.A, s.H, w.P, w.splits, w.kslice, o};
-  if (w.rows) {
+  RowArgs row{};
+  int steps = 0;
+  if (w.rows && one_launch(s.T, s.r, s.H, s.N, steps)) {
+    row = RowArgs{a.x, s.A, a.ldx, s.H};
+  } else if (w.rows) {
     if (hipError_t e = launch_down_rows(d, true, DownArgs{}, false, st)) return e;
   } else {
     const TransposeArgs none{s, nullptr, nullptr, 0};
@@ -1414,8 +1530,9 @@ hipError_t launch_lora_forward(const LoraForwardArgs& a, hipStream_t st) {
       if (hipError_t e = launch_terms(t, no, st)) return e;
     }
   }
-  const UpArgs g{s, w.P, w.splits, w.U, s.B, s.N, false, a.base, a.ldb, a.y, a.ldy, 0};
-  return a.y_dt == Dt::BF16 ? launch_up_y<uint16_t>(g, a.base_dt, w.rows, st) : launch_up_y<float>(g, a.base_dt, w.rows, st);
+  const UpArgs g{s, w.P, w.splits, w.U, s.B, s.N, false, a.base, a.ldb, a.y, a.ldy, steps};
+  return a.y_dt == Dt::BF16 ? launch_up_y<uint16_t>(g, a.base_dt, w.rows, st, row)
+                            : launch_up_y<float>(g, a.base_dt, w.rows, st, row);
 }
 
 hipError_t launch_lora_backward(const LoraBackwardArgs& a, hipStream_t st) {
