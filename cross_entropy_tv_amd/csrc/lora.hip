@@ -361,30 +361,37 @@ void lora_down_tile_kernel(DownArgs g, TransposeArgs tr) {
     const Part p = part_of(s, i, r0, r1);
     if (p.hi <= p.lo || p.adapter < 0) continue;
     const uint16_t* M = g.M + (int64_t)p.adapter * r * g.K;
+    const int rank = rank_of(s, p.adapter);
+    const float scale = s.scale[p.adapter];
     f32x4_t acc[D::kBlocks];
 #pragma unroll
     for (int b = 0; b < D::kBlocks; ++b) acc[b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    u32x4_t v0[D::kLoads], v1[D::kLoads];
+    // x comes from memory and is asked for four slices ahead, M from the L2s two slices ahead
+    u32x4_t xs[4][2], ms[2][D::kLoads - 2];
     // slice c of this group into registers; a piece behind the end comes from the last one in front
     // of it (no load is conditional) and is 0 in LDS
     auto slice_k = [&](uint32_t c) {  // (behind the last round: behind the end)
       const uint32_t n = c < rounds ? (c + turn < rounds ? c + turn : c + turn - rounds) : rounds;
       return kb + (n * D::kGroups + group) * kDownK + piece * 8;
     };
-    auto load = [&](u32x4_t (&v)[D::kLoads], uint32_t c) {
+    auto load_x = [&](u32x4_t (&v)[2], uint32_t c) {
       const uint32_t at = min(slice_k(c), ke - 8);
 #pragma unroll
       for (int n = 0; n < 2; ++n) v[n] = load16(X + (off[n] + at));
-#pragma unroll
-      for (int n = 2; n < D::kLoads; ++n) v[n] = load16(M + (off[n] + at));
     };
-    auto put = [&](const u32x4_t (&v)[D::kLoads], uint32_t c) {
+    auto load_m = [&](u32x4_t (&v)[D::kLoads - 2], uint32_t c) {
+      const uint32_t at = min(slice_k(c), ke - 8);
+#pragma unroll
+      for (int n = 0; n < D::kLoads - 2; ++n) v[n] = load16(M + (off[2 + n] + at));
+    };
+    auto put = [&](const u32x4_t (&vx)[2], const u32x4_t (&vm)[D::kLoads - 2], uint32_t c) {
       const bool in = slice_k(c) < ke;
       uint8_t* T = stage0 + (c & 1) * D::kStage;
 #pragma unroll
       for (int n = 0; n < D::kLoads; ++n) {
         const u32x4_t z = {0u, 0u, 0u, 0u};
-        *reinterpret_cast<u32x4_t*>(T + (prow + 16 * n) * (kDownK * 2) + ((piece ^ prow) << 4)) = in ? v[n] : z;
+        *reinterpret_cast<u32x4_t*>(T + (prow + 16 * n) * (kDownK * 2) + ((piece ^ prow) << 4)) =
+            in ? (n < 2 ? vx[n < 2 ? n : 0] : vm[n < 2 ? 0 : n - 2]) : z;
       }
     };
     auto multiply = [&](uint32_t c) {
@@ -401,20 +408,30 @@ void lora_down_tile_kernel(DownArgs g, TransposeArgs tr) {
         }
       }
     };
-    load(v0, 0);
-    load(v1, 1);
-    __syncthreads();  // (the previous request's sums have been read)
-    for (uint32_t c = 0; c < rounds; c += 2) {
-      put(v0, c);
-      load(v0, c + 2);
+    auto round = [&](int n, uint32_t c) {  // n = c % 4
+      put(xs[n], ms[n & 1], c);
+      load_m(ms[n & 1], c + 2);
+      load_x(xs[n], c + 4);
       __syncthreads();
       multiply(c);
-      put(v1, c + 1);  // (behind the last slice: zeros)
-      load(v1, c + 3);
-      __syncthreads();
-      multiply(c + 1);
       // (a stage is written again only after the barrier behind its reads)
+    };
+    // (in the loop's order, so that its waits are the same from the first round on)
+    load_x(xs[0], 0);
+    load_x(xs[1], 1);
+    load_m(ms[0], 0);
+    load_x(xs[2], 2);
+    load_m(ms[1], 1);
+    load_x(xs[3], 3);
+    __syncthreads();  // (the previous request's sums have been read)
+    uint32_t c = 0;
+    for (; c + 4 <= rounds; c += 4) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) round(n, c + n);
     }
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+      if (c + n < rounds) round(n, c + n);
     __syncthreads();
     float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
@@ -422,8 +439,6 @@ void lora_down_tile_kernel(DownArgs g, TransposeArgs tr) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) red[((wave * D::kBlocks + b) * 4 + e) * 64 + lane] = acc[b][e];
     __syncthreads();
-    const int rank = rank_of(s, p.adapter);
-    const float scale = s.scale[p.adapter];
     for (int f = tid; f < kTileRows * 16 * RB; f += D::kThreads) {
       // place f: register e of lane l, block b, row half hh; summed over the waves that share it
       const int l = f & 63, e = (f >> 6) & 3, b = (f >> 8) % RB, hh = (f >> 8) / RB;
