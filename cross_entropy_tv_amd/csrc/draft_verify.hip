@@ -242,7 +242,8 @@ __device__ __forceinline__ Temp temp_of(const float* temperature, int i) {
   const float t = temperature ? temperature[i] : 1.0f;
   Temp r;
   r.greedy = !(t > 0.0f);
-  const double d = r.greedy ? 1.0 : (double)t;
+  // (infinitely hot: all finite logits alike; -inf times the scale must stay -inf)
+  const double d = r.greedy ? 1.0 : (double)fminf(t, 1.0e37f);
   r.inv = 1.0 / d;
   r.c64 = kLog2e64 / d;
   // (finite also for the smallest temperatures: 0 * c must stay 0 at the largest logit)

@@ -518,8 +518,8 @@ lx_status lx_ce_tvd_linear_forward_backward(const void* x_s, const void* w_s, in
  * - A sequence whose draft_start entries decrease, leave [0, N] or span more than
  *   max_draft gives n_accepted = -1 and tokens -1.
  * - Rows behind a sequence's first rejection need not be read; whether they are
- *   does not change a result.  Comparisons that fp32 sums cannot decide are made
- *   again from fp64 sums, and the draw's running sums are fp64.
+ *   does not change a result.  Acceptance is decided from fp64 sums wherever fp32 sums
+ *   could decide it otherwise, and the draw's running sums are fp64.
  * Workspace: at least lx_draft_verify_workspace_bytes(S, max_draft, V) bytes,
  *   256-byte aligned, contents ignored and clobbered.
  * Requirements: S * (max_draft + 1) <= 2^24 and, times ceil(V / 2048), below 2^31;
@@ -569,11 +569,14 @@ lx_status lx_draft_verify(const void* target, int64_t ld_target, const void* dra
  * - u and v are fp32 and enter the second products unrounded; all sums are fp32, in a fixed
  *   order (the same bits on every call).
  * Requirements: H, N and every row stride multiples of 8, at most 2^22; r a multiple of 8,
- *   at most 128; T <= 2^22, R <= 2^24, 1 <= n_adapters <= 2^20; x, grad_y, A, B, base, y and
+ *   at most 128; T <= 2^22, R <= 2^24, 1 <= n_adapters <= 2^20, n_adapters * r * (H + N)
+ *   below 2^37; x, grad_y, A, B, base, y and
  *   the gradients 16-byte aligned.  Any T from 1 on, any request lengths.
  *   T == 0 or R == 0: y and grad_x are not written, grad_A and grad_B are 0.
  * Workspace: at least lx_lora_forward_workspace_bytes(...), or
- *   lx_lora_backward_workspace_bytes(...), bytes, 256-byte aligned, contents ignored and clobbered.
+ *   lx_lora_backward_workspace_bytes(...), bytes, 256-byte aligned, contents ignored and clobbered;
+ *   like any other, for one call at a time (calls that may run at once, two captured graphs on
+ *   two streams among them, need one each).
  * Errors : LX_ERR_INVALID_ARG, LX_ERR_UNSUPPORTED_DTYPE, LX_ERR_ALIAS (an output or the
  *   workspace overlapping anything else), LX_ERR_WORKSPACE, LX_ERR_HIP.
  */

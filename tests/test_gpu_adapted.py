@@ -221,3 +221,40 @@ def test_serving_steps():
         step()  # eager work between replays
         torch.cuda.synchronize()
     assert 0 < accepted < 5 * N
+
+
+def test_calls_at_once():
+    """Training and serving on two streams at once, each call with a workspace of its own: the results of one at a time."""
+    announce("calls at once")
+    g = np.random.default_rng(21)
+    m = Model(g, 3, 264, 2056, 16)
+    T = 400
+    x, teacher = bf16(g.standard_normal((T, 264))), bf16(g.standard_normal((T, 2056)) * 2)
+    start, adapter = i64([0, 90, 260, T]), i64([1, 0, 2])
+    target = torch.from_numpy(g.integers(0, 2056, T)).to(DEV)
+    S, L = 6, 3
+    hidden, drafted = bf16(g.standard_normal((S * (L + 1), 264)) * 2), bf16(g.standard_normal((S * L, 264)) * 2)
+    tokens = torch.from_numpy(g.integers(0, 2056, S * L)).to(DEV)
+    dstart, who = torch.arange(S + 1, device=DEV) * L, i64([0, 1, 2, -1, 1, 0])
+    ua, us = torch.rand(S * L, device=DEV), torch.rand(S, device=DEV)
+
+    def training():
+        return train(m, x, teacher, target, adapter, start, 1.0 / T, 1.0 / T)[3:]
+
+    def serving():
+        out = (torch.empty(S, dtype=torch.int64, device=DEV), torch.empty(S, L + 1, dtype=torch.int64, device=DEV),
+               torch.empty(S, L + 1, device=DEV))
+        serve(m, hidden, drafted, tokens, dstart, L, who, torch.ones(S, device=DEV), ua, us, out)
+        return out
+
+    want = training(), serving()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for k in range(8):
+        for st, run in zip(streams, (training, serving) if k % 2 else (serving, training)):
+            with torch.cuda.stream(st):
+                got.append((run is serving, run()))
+    torch.cuda.synchronize()
+    for which, out in got:
+        for a, b in zip(out, want[which]):
+            assert torch.equal(a, b)

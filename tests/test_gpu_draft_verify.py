@@ -57,9 +57,7 @@ class Case:
         self.start = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
         self.max_draft = max(lens + [0]) if max_draft is None else max_draft
         if ROOM["wide"]:
-            self.max_draft = max(self.max_draft, DIRECT // (S * V))
-            if self.max_draft > 2 ** 20:
-                pytest.skip("more room than the entry point takes")
+            self.max_draft = max(self.max_draft, min(DIRECT // (S * V), 2 ** 20))  # (the most there is room for)
         z = rows(rng, N + S, V).to(DT[dt]).float()
         u = rows(rng, N, V, noise)
         for i in range(S):
@@ -150,6 +148,25 @@ def test_strides_and_alignments(pad, offset, dt):
 @pytest.mark.parametrize("V,S", [(151936, 1), (151936, 20), (262144, 3)])
 def test_large_vocabularies(V, S):
     check(Case(17 + S, [4, 2, 5, 0][:S] * max(1, S // 4), V, "bf16"), f"{S} x {V}")
+
+
+@pytest.mark.parametrize("with_draft", [True, False], ids=["draft", "lookup"])
+def test_infinitely_hot(with_draft):
+    """T = inf: every token that is not masked is as likely as any other."""
+    V = 3000
+    c = Case(71, [3, 0, 2], V, "f32", with_draft, temps=[1.0, 1.0, 1.0])
+    c.z[:, 5:] = NINF
+    if with_draft:
+        c.u[:, 5:] = NINF  # p = q: all accepted
+    c.tokens[:] = c.tokens % 5
+    c.temps = [float("inf")] * 3
+    c.ua[:] = 0.19 if not with_draft else 0.999
+    announce(f"draft_verify infinitely hot {with_draft}")
+    n, tok, lp = c.run()
+    assert (n == c.lens).all()
+    for i in range(3):
+        assert (tok[i, :n[i]] == c.tokens[c.start[i]:c.start[i + 1]]).all() and tok[i, n[i]] == int(5 * c.us[i])
+        assert np.abs(lp[i, :n[i] + 1] + np.log(5)).max() <= TOL_LOGP
 
 
 def test_masked_vocabulary():
