@@ -442,9 +442,10 @@ constexpr int kSt = 3;  // merged sums for the draw: (m_t, m_d), s_t, s_d
 struct Ws {
   int* first;      // [S] the first rejected position, or INT_MAX
   bool direct;     // verify_rows: positions P = L + 1 and part2, state [P][S]; else P = L
-  int* count1;     // [P][S] arrivals of step 1
-  int* count2;     // [S]
-  int* count3;     // [S]
+  int* count1;     // [P][S] arrivals of step 1, `apart1` ints apart
+  int* count2;     // [S], `apart` ints apart
+  int* count3;     // [S], likewise
+  int apart, apart1;
   int* best;       // [P][S] greedy: the target's token
   float* logp;     // [P][S] log p of the drafted token
   uint64_t *part1, *part2, *part3, *state;
@@ -488,10 +489,14 @@ Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
     return q;
   };
   w.first = reinterpret_cast<int*>(take((size_t)S * 4));
-  w.n_zero = S * P + 2 * S;
+  // (a line each for a few sequences, whose workgroups all count at once: 19.6 against 17.2 us for
+  // the sums of 32 x 151936)
+  w.apart = S <= 1024 ? 32 : 1;
+  w.apart1 = S * P <= 1024 ? 32 : 1;
+  w.n_zero = S * P * w.apart1 + 2 * S * w.apart;
   w.count1 = reinterpret_cast<int*>(take((size_t)w.n_zero * 4));
-  w.count2 = w.count1 ? w.count1 + S * P : nullptr;
-  w.count3 = w.count1 ? w.count2 + S : nullptr;
+  w.count2 = w.count1 ? w.count1 + S * P * w.apart1 : nullptr;
+  w.count3 = w.count1 ? w.count2 + S * w.apart : nullptr;
   w.best = reinterpret_cast<int*>(take((size_t)S * P * 4));
   w.logp = reinterpret_cast<float*>(take((size_t)S * P * 4));
   w.part1 = reinterpret_cast<uint64_t*>(w.direct ? nullptr : take((size_t)S * P * w.K1 * kP1 * 8));
@@ -652,7 +657,7 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
         if (h == 0 || has_d) publish(part + h, pack(m, __float_as_uint(rest)));
       }
     }
-    sh_flag = count_last(w.count1 + slot, K);
+    sh_flag = count_last(w.count1 + (int64_t)slot * w.apart1, K);
   }
   __syncthreads();
   if (!sh_flag) return;
@@ -832,7 +837,7 @@ __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(Args g) {
       publish(part, pack(m[0], has_d ? __float_as_uint(m[1]) : 0u));
     }
   }
-  if (tid == 0) sh_flag = count_last(w.count1 + slot, K);
+  if (tid == 0) sh_flag = count_last(w.count1 + (int64_t)slot * w.apart1, K);
   __syncthreads();
   if (!sh_flag) return;
 
@@ -1159,7 +1164,7 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
       for (int k = 0; k < kVWaves; ++k)
         if (lo_of(red[k]) > b.v || (lo_of(red[k]) == b.v && hi_of(red[k]) < b.at)) b = Best{lo_of(red[k]), hi_of(red[k])};
       publish(part, pack(b.v, b.at));
-      sh_flag = count_last(w.count2 + i, K);
+      sh_flag = count_last(w.count2 + i * w.apart, K);
     }
     __syncthreads();
     if (!sh_flag) return;
@@ -1217,7 +1222,7 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
     publish(part, pack(mt, __float_as_uint(md)));
     publish(part + 1, st);
     publish(part + 2, sd);
-    sh_flag = count_last(w.count2 + i, K);
+    sh_flag = count_last(w.count2 + i * w.apart, K);
   }
   __syncthreads();
   if (!sh_flag) return;
@@ -1357,7 +1362,7 @@ __global__ __launch_bounds__(kVThreads) void verify_draw_kernel(Args g, int K) {
 #pragma unroll
       for (int k = 0; k < kVWaves; ++k) r += red64[k];
       publish(w.part3 + (int64_t)i * K + c, r);
-      sh_flag = count_last(w.count3 + i, K);
+      sh_flag = count_last(w.count3 + i * w.apart, K);
     }
     __syncthreads();
     if (!sh_flag) return;
