@@ -468,10 +468,10 @@ void chunking(int64_t rows, int64_t V, int64_t wanted, int64_t most, int64_t& ch
 
 // Whether verify_rows takes the first two steps' place: while the fp64 masses of all rows (about 1.6e12 a
 // second at best) cost less than the second step's launch and way through memory.  Sequences of 4 drafts,
-// V = 151936, two launches against three: 19 and 24 us for 1, 27 and 38 for 4, 46 and 56 for 16, 66 and 64
-// for 32; without draft logits 22 and 26 for 4, 34 and 36 for 16, 44 and 38 for 32.  Without drafts (64
-// rows: 28 and 27) the second step is the only one.
-bool direct_rows(int64_t S, int64_t L, int64_t V) { return L > 0 && S * (L + 1) * V <= (1 << 24); }
+// V = 151936, two launches against three: 16 and 21 us for 1, 24 and 31 for 4, 31 and 34 for 8, 45 and 44
+// for 16; without draft logits 17 and 19 for 4, 22 and 21 for 8, 34 and 26 for 16.  Without drafts (one row:
+// 14 and 12) the second step is the only one.
+bool direct_rows(int64_t S, int64_t L, int64_t V) { return L > 0 && S * (L + 1) * V <= (1 << 23); }
 
 Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
   Ws w{};

@@ -23,7 +23,7 @@ DEV = "cuda:0"
 DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 TOL_LOGP = 2.0 ** -18
 NINF = float("-inf")
-DIRECT = 1 << 24  # up to this many positions times V the rows are summed in one step
+DIRECT = 1 << 23  # up to this many positions times V the rows are summed in one step
 ROOM = {"wide": False}
 
 
