@@ -282,7 +282,8 @@ def test_other_requests_rows_do_not_leak(rows):
 
 
 @pytest.mark.parametrize("T,R,n,H,N,r", [(3000, 5, 2, 1160, 520, 16), (1300, 40, 6, 520, 2056, 64),
-                                         (2100, 1, 1, 264, 264, 128), (700, 700, 9, 264, 520, 16)])
+                                         (2100, 1, 1, 264, 264, 128), (700, 700, 9, 264, 520, 16),
+                                         (256, 256, 3, 240, 1144, 16), (256, 256, 2, 136, 488, 128)])
 def test_larger(T, R, n, H, N, r):
     """Several splits of the rows and of the long axes; more than 64 requests."""
     start = ragged(T, R, T) if R < T else list(range(T + 1))
