@@ -913,44 +913,59 @@ __global__ __launch_bounds__(kLThreads) void lora_up_row_kernel(UpArgs g) {
   }
 }
 
-// dx of single rows: M is A as it lies, (n, r, C), so a lane takes 8 columns and adds up the ranks,
-// 1 KB of A's row a wave and rank.
+// dx of single rows: M is A as it lies, (n, r, C), so a lane takes 8 columns and adds up the ranks, 1 KB of
+// A's row a wave and rank.  A workgroup per (row, 512 columns); its waves share out the ranks (a wave
+// alone with 128 ranks waits for 16 rounds of loads: 20 us for 3 rows).
 template <bool BASE>
-__global__ __launch_bounds__(kLThreads) void lora_up_strided_kernel(UpArgs g) {
+__global__ __launch_bounds__(kLThreads) void lora_up_strided_kernel(UpArgs g, unsigned ranges) {
+  constexpr int kCols = 512;
+  __shared__ float part[4][kCols];
   const LoraSet& s = g.s;
-  const int lane = tid_x() & 63, r = (int)s.r;
-  const RowPlace o = row_place(g, 512);
-  if (!o.ok) return;
-  const int a = o.p.adapter, rank = a >= 0 ? rank_of(s, a) : 0;
-  const int64_t col = o.n0 + lane * 8, at = col < g.C ? col : 0;
-  // lane l holds v of ranks l and l + 64
-  float v[2] = {0.0f, 0.0f};
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int rho = lane + 64 * h;
-    if (rho < rank) {
-      for (int sp = 0; sp < g.splits; ++sp) v[h] += g.P[((int64_t)sp * s.T + o.t) * r + rho];
-      v[h] *= s.scale[a];
-    }
+  const int tid = tid_x(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = (int)s.r;
+  // (ranges a multiple of 8, or below 8: the rows of one range on one die, for A's part in its L2)
+  const int64_t t = bid_x() / ranges, c0 = (int64_t)(bid_x() % ranges) * kCols;
+  if (c0 >= g.C) return;
+  const int i = find_request(s.start, (int)s.R, t);
+  if (i < 0) return;
+  const Part p = part_of(s, i, t, t + 1);
+  if (p.hi <= p.lo) return;
+  const int a = p.adapter, rank = a >= 0 ? rank_of(s, a) : 0;
+  const int64_t col = c0 + lane * 8, at = col < g.C ? col : 0;
+  // this wave's ranks, and (lane l) v of the l-th of them
+  const int per = (rank + 3) / 4, k0 = min(wave * per, rank), n = min(k0 + per, rank) - k0;
+  float v = 0.0f;
+  if (lane < n) {
+    for (int sp = 0; sp < g.splits; ++sp) v += g.P[((int64_t)sp * s.T + t) * r + k0 + lane];
+    v *= s.scale[a];
   }
-  const float* base = static_cast<const float*>(g.base) + (BASE ? o.t * g.ldb : 0);
-  float* y = static_cast<float*>(g.y) + o.t * g.ldy;
   float out[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] = 0.0f;
-  if (BASE) load8(base + at, out);
-  const uint16_t* M = g.M + (a >= 0 ? (int64_t)a * r * g.C : 0) + at;
+  const uint16_t* M = g.M + (a >= 0 ? ((int64_t)a * r + k0) * g.C : 0) + at;
 #pragma unroll 8
-  for (int rho = 0; rho < rank; ++rho) {
-    const float vr = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(rho < 64 ? v[0] : v[1]), rho & 63));
+  for (int k = 0; k < n; ++k) {
+    const float vr = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), k));
     float w[8];
-    load8(M + (int64_t)rho * g.C, w);
+    load8(M + (int64_t)k * g.C, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) out[e] = __builtin_fmaf(vr, w[e], out[e]);
   }
-  if (col < g.C) {
-    if (a == kBadAdapter) store_bits8(y + col, kQNaN32);
-    else store8(y + col, out);
+  f32x4_t* mine = reinterpret_cast<f32x4_t*>(part[wave] + lane * 8);
+  mine[0] = (f32x4_t){out[0], out[1], out[2], out[3]};
+  mine[1] = (f32x4_t){out[4], out[5], out[6], out[7]};
+  __syncthreads();
+  // two columns a thread (C is even)
+  const int64_t c = c0 + 2 * tid;
+  if (c >= g.C) return;
+  float* y = static_cast<float*>(g.y) + t * g.ldy + c;
+  const float* base = static_cast<const float*>(g.base) + (BASE ? t * g.ldb + c : 0);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float sum = BASE ? base[e] : 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum += part[w][2 * tid + e];
+    if (a == kBadAdapter) store_bits1(y + e, kQNaN32);
+    else y[e] = sum;
   }
 }
 
@@ -1361,13 +1376,12 @@ dim3 up_rows_grid(UpArgs& g, int64_t columns) {
   return dim3((unsigned)((ranges + 7) / 8 * 8 * T));
 }
 
-hipError_t launch_up_strided(UpArgs g, hipStream_t st) {
-  const int64_t T = g.s.T;
-  g.steps = 1;
-  const int64_t ranges = (g.C + 2047) / 2048;
-  const dim3 grid((unsigned)((ranges + 7) / 8 * 8 * T));
-  if (g.base) hipLaunchKernelGGL(lora_up_strided_kernel<true>, grid, dim3(kLThreads), 0, st, g);
-  else hipLaunchKernelGGL(lora_up_strided_kernel<false>, grid, dim3(kLThreads), 0, st, g);
+hipError_t launch_up_strided(const UpArgs& g, hipStream_t st) {
+  unsigned ranges = (unsigned)((g.C + 511) / 512);
+  if (ranges > 8) ranges = (ranges + 7) / 8 * 8;
+  const dim3 grid((unsigned)(ranges * g.s.T));
+  if (g.base) hipLaunchKernelGGL(lora_up_strided_kernel<true>, grid, dim3(kLThreads), 0, st, g, ranges);
+  else hipLaunchKernelGGL(lora_up_strided_kernel<false>, grid, dim3(kLThreads), 0, st, g, ranges);
   return hipGetLastError();
 }
 
