@@ -595,25 +595,40 @@ void lora_up_tile_kernel(UpArgs g) {
   const uint16_t* U = g.U + r0 / kTileRows * (2 * LD * TM * 512);
   const uint32_t ldy = (uint32_t)g.ldy, ldb = (uint32_t)g.ldb, C = (uint32_t)g.C;
   const u32x4_t zero = {0u, 0u, 0u, 0u};
+  __shared__ u32x4_t shared[LD == 4 ? 2 * LD * TM * 64 : 1];  // beyond 64 ranks U does not fit the registers beside M
   for (int i = max(find_request(s.start, (int)s.R, r0), 0); i < s.R && s.start[i] < r1; ++i) {
     const Part p = part_of(s, i, r0, r1);
     if (p.hi <= p.lo) continue;
     const bool some = p.adapter >= 0;
     const int rank = some ? rank_of(s, p.adapter) : 0;
     const int lo = (int)(p.lo - r0), hi = (int)(p.hi - r0);
-    u32x4_t u[2][LD][TM];
+    u32x4_t u[2][LD == 4 ? 1 : LD][TM];
+    if constexpr (LD == 4) {
+      __syncthreads();  // (the previous request's products are done)
+      for (int n = tid_x(); n < 2 * LD * TM * 64; n += kLThreads) {
+        const int row = n / (LD * TM * 64) * 16 + (n & 15);
+        const u32x4_t v = load16(U + n * 8);
+        shared[n] = rank > 0 && row >= lo && row < hi ? v : zero;
+      }
+      __syncthreads();
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = 16 * h + c16;
-      const bool in = rank > 0 && row >= lo && row < hi;
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * h + c16;
+        const bool in = rank > 0 && row >= lo && row < hi;
 #pragma unroll
-      for (int l = 0; l < LD; ++l)
+        for (int l = 0; l < LD; ++l)
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-          const u32x4_t v = load16(U + (((h * LD + l) * TM + j) * 512 + lane * 8));
-          u[h][l][j] = in ? v : zero;
-        }
+          for (int j = 0; j < TM; ++j) {
+            const u32x4_t v = load16(U + (((h * LD + l) * TM + j) * 512 + lane * 8));
+            u[h][l][j] = in ? v : zero;
+          }
+      }
     }
+    auto operand = [&](int h, int l, int j) {
+      if constexpr (LD == 4) return shared[((h * LD + l) * TM + j) * 64 + lane];
+      else return u[h][l][j];
+    };
     const uint16_t* M = g.M + (some ? (int64_t)p.adapter * g.C * r : 0);
     const bool mask = !g.m_clean && rank < r;
     for (uint32_t n = (uint32_t)n0; n < (uint32_t)n1; n += 64) {
@@ -653,11 +668,14 @@ void lora_up_tile_kernel(UpArgs g) {
 #pragma unroll
         for (int l = 0; l < LD; ++l)
 #pragma unroll
-          for (int j = 0; j < TM; ++j)
+          for (int j = 0; j < TM; ++j) {
+            const u32x4_t u0 = operand(0, l, j), u1 = operand(1, l, j);
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) acc[h][b] = mfma(u[h][l][j], w[b][l], acc[h][b]);
+            for (int b = 0; b < 4; ++b) {
+              acc[0][b] = mfma(u0, w[b][l], acc[0][b]);
+              acc[1][b] = mfma(u1, w[b][l], acc[1][b]);
+            }
+          }
       }
       if (col < C) {
 #pragma unroll
