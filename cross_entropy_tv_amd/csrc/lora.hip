@@ -19,6 +19,9 @@
 //   up     Y = base + P M^T (y from u and B; dx from v and A^T)
 //   grad   W^T X over the rows (dA from v and x; dB from u and dy)
 //
+// Long requests go in tiles of 32 rows on the matrix cores; single rows (a token of each request) are
+// vector products that read an adapter once for every row, from the L2s (single_rows decides).
+//
 // Precision.  u and v are sums of bf16 products in fp32 and stay fp32: where they
 // enter a matrix-core product they are cut into three bf16 terms (hi + mid + lo, 24
 // bits together), so the products are exact and the results as good as fp32
@@ -283,9 +286,11 @@ struct DownArgs {
 
 // Long requests: a workgroup per (tile of 32 rows, split of K).  K goes in slices of 128 through
 // LDS, 16-byte pieces of a row swapped by its number so that the 16 rows of an operand read fall
-// on different banks.  Two slices are on their way in registers while a third is multiplied, and
+// on different banks.  x is on its way in registers four slices ahead and M two, and
 // (up to 64 ranks) two groups of four waves take every other slice each: with one workgroup per
-// compute unit, as 8192 rows make, that is what keeps enough loads in flight.  A group's four
+// compute unit, as 8192 rows make, that is what keeps enough loads in flight.  Bound by reading x and
+// by the steps between barriers: 31 us at 8192 x 4096, r 64 (67 MB of x: 2.2 TB/s; about 10 us of it
+// start and end, 1.3 us every two slices), 17 us at 4096 x 4096, r 16.  A group's four
 // waves share out the row halves and the ranks (RB = 1: the slice's k).  With one split the
 // workgroup finishes u itself (scale, rank, terms); with several it leaves its partial sums for
 // lora_terms_kernel.  RB: blocks of 16 ranks.
@@ -452,7 +457,8 @@ void lora_down_tile_kernel(DownArgs g, TransposeArgs tr) {
   }
 }
 
-// Requests of a few rows.  u: a wave per (row, 4 ranks, split of K), along the rows of A.
+// Requests of a few rows.  u: a wave per (row, 4 ranks, split of K), along the rows of A.  Bound by latency:
+// 4 us for 64 rows of 4096, r 16, and by the L2s (8 TB/s) for more.
 constexpr int kRowRanks = 4;
 __device__ __forceinline__ void down_row(const DownArgs& g, int64_t unit) {
   const LoraSet& s = g.s;
@@ -572,7 +578,8 @@ __device__ __forceinline__ void nan4(uint16_t* p) { *reinterpret_cast<uint2*>(p)
 // (Terms::U) stay in registers; a block of M is read once and multiplied by its terms one
 // after the other.  Column block b of a step holds columns 4 (l % 16) + b, so that a lane ends
 // with four consecutive columns: whole 256-byte (fp32) or 128-byte (bf16) pieces of 4 rows per
-// access.
+// access.  Bound by reading base and writing y: 62 to 69 us for 268 MB at 8192 x 4096 fp32, r 64 (4.1
+// TB/s where a copy reaches 4.7).
 template <int LD, int TM, typename YT, typename BT, bool BASE>
 __global__ __attribute__((amdgpu_flat_work_group_size(kLThreads, kLThreads), amdgpu_waves_per_eu(2)))
 void lora_up_tile_kernel(UpArgs g) {
@@ -699,8 +706,9 @@ void lora_up_tile_kernel(UpArgs g) {
 }
 
 // Requests of a few rows: a wave per (row, steps x 64 columns).  Up to 32 ranks (CH chunks of 8) a
-// lane takes a whole column, 16 CH bytes of M; beyond, lanes share a column (the next
-// kernel).  Workgroups go column range by column range, and the rows of one range on one die (id mod
+// lane takes a whole column, 16 CH bytes of M; beyond, lanes share a column (lora_up_row_kernel).
+// Bound by reading M from the L2s, once a row, beside base and y: 64 x 151936, fp32 to bf16, r 16,
+// 29.5 us (369 MB, 311 of them M's).  Workgroups go column range by column range, and the rows of one range on one die (id mod
 // 8), so that rows with the same adapter find its part of M in that die's L2.
 struct RowPlace {
   int64_t t, n0, n1;
@@ -780,7 +788,8 @@ __global__ __launch_bounds__(kLThreads) void lora_up_lane_kernel(UpArgs g) {
 }
 
 // The same with u formed by every workgroup itself, its waves sharing out the ranks: a few rows are bound by
-// the launches, and A's part is read from the L2s once for every 256 steps columns of a row.
+// the launches, and A's part is read from the L2s once for every 256 steps columns of a row.  4096 x 4096,
+// r 16: 6.2 us for one row, 8 for 64 (in two launches 11 and 11).
 struct RowArgs {
   const uint16_t *X, *A;
   int64_t ldx, K;
@@ -1117,6 +1126,9 @@ struct RowWalk {
 // VP: X is dy, and the pass that adds up dB also multiplies each staged row by its columns' rows of
 // B (in registers), so that dy is read once: v = dy B comes out as partial sums of 256 columns.  They
 // take r / 64 of dy's bytes to write and to read, so up to 16 ranks.
+// Bound by reading x and dy between barriers, two workgroups a compute unit (LDS): 41 us for both of 8192 x 4096,
+// r 64 (134 MB: 3.3 TB/s), 19 us for 4096 x 4096 of 4 adapters, r 16; dy of 2048 x 151936 with v 159 us
+// (622 MB: 3.9 TB/s).  W's terms asked for a stage ahead, and x two stages ahead, took longer (registers).
 __device__ __forceinline__ int stage_at(int row, int piece) {
   return row * (kGradCols * 2) + ((piece ^ (2 * (row & 3) + 8 * ((row >> 3) & 1))) << 4);
 }
