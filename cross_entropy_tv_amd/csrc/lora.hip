@@ -1153,7 +1153,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
   const int srow = tid >> 5, spiece = tid & 31;
   const int64_t scol = c0 + spiece * 8 < g.C ? spiece * 8 : 0;
   const u32x4_t zero = {0u, 0u, 0u, 0u};
-  // (loaded without conditions, from a row of the request, and cut where the stage is written: a
+  // (loaded without conditions, from rows between the stage's first and last, and cut where it is written: a
   // select here would have to wait for the load; columns behind the last are not stored)
   const uint32_t ldx = (uint32_t)g.ldx;
   auto fetch = [&](const Stage& w, u32x4_t (&v)[8]) {
@@ -1330,7 +1330,7 @@ __global__ __launch_bounds__(kLThreads) void lora_zero_kernel(float* a, int64_t 
 // 4096, N = 4096 and 151936.  Single rows read an adapter once for every row, from the L2s at about 8
 // TB/s.  A tile takes the requests that share it (1 + 32 R / T on average) one after the other,
 // each a pass over the down products' axes (a split's share of them) and over the tile's columns of y.
-//   T 64, R 1 / 8 / 64: 9.4 / 9.4 / 9.3 us as rows, 13.3 / 35.6 / 236 as tiles;
+//   T 64, R 1 / 8 / 64: 9.4 / 9.4 / 9.3 us as rows (in two launches), 13.3 / 35.6 / 236 as tiles;
 //   T 512, R 1, r 64: 37 as rows, 24 as tiles; T 1024, R 2 / 128: 35 / 38 as rows, 18 / 44 as tiles;
 //   T 64, R 1 / 8, N 151936: 43 / 43 as rows, 27 / 61 as tiles.
 bool single_rows(int64_t T, int64_t R, int64_t r, int64_t H, int64_t N, bool backward) {
