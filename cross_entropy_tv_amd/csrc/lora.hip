@@ -1333,14 +1333,17 @@ __global__ __launch_bounds__(kLThreads) void lora_zero_kernel(float* a, int64_t 
 //   T 64, R 1 / 8 / 64: 9.4 / 9.4 / 9.3 us as rows (in two launches), 13.3 / 35.6 / 236 as tiles;
 //   T 512, R 1, r 64: 37 as rows, 24 as tiles; T 1024, R 2 / 128: 35 / 38 as rows, 18 / 44 as tiles;
 //   T 64, R 1 / 8, N 151936: 43 / 43 as rows, 27 / 61 as tiles.
+// Beyond 64 ranks tiles take about twice as long (T 256, R 13, 2048 x 1024: 33 us with r 64, 75 with 128, where rows
+// take 14 and 24).
 bool single_rows(int64_t T, int64_t R, int64_t r, int64_t H, int64_t N, bool backward) {
   const double read = 2.0 * (double)T * (double)r * (double)(backward ? 2 * H + N : H + N);
   const double rows = 4.0 + read / 8.0e6;
   double shared = 1.0 + 32.0 * (double)R / (double)T;
   if (shared > 32.0) shared = 32.0;
   auto pass = [](int64_t K) { return 1.0 + 3.0 * (double)(K <= 8192 ? K : 8192) / 4096.0; };
-  const double tiles = 13.0 + shared * (pass(H) + (backward ? pass(N) : 0.0)) +
-                       (shared - 1.0) * (double)T * (double)(backward ? H : N) * 8.0 / 10.0e6;
+  double tiles = 13.0 + shared * (pass(H) + (backward ? pass(N) : 0.0)) +
+                 (shared - 1.0) * (double)T * (double)(backward ? H : N) * 8.0 / 10.0e6;
+  if (r > 64) tiles *= 2.0;
   // (and single rows' grids stay within int32)
   return rows < tiles && T * (((H > N ? H : N) + 255) / 256) < (1 << 30);
 }

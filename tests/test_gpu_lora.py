@@ -140,12 +140,14 @@ def path_of(c, backward=False):
     rows = 4 + 2 * T * r * (H + N + (H if backward else 0)) / 8e6
     one = lambda K: 1 + 3 * min(K, 8192) / 4096  # noqa: E731
     tiles = 13 + shared * (one(H) + (one(N) if backward else 0)) + (shared - 1) * T * (H if backward else N) * 8 / 10e6
+    if r > 64:
+        tiles *= 2
     return "single" if rows < tiles else "tiles"
 
 
 def test_the_estimate_is_the_library_s():
     """The forward's workspace is partial sums for single rows and whole 1 KB operands for tiles of 32."""
-    for r, tm in ((8, 1), (16, 2), (32, 3)):
+    for r, tm in ((8, 1), (16, 2), (32, 3), (128, 12)):  # (128: 4 blocks of 32 ranks)
         for T in range(200, 9000, 97):
             c = Case.__new__(Case)
             c.T, c.adapter, c.r, c.H, c.N = T, [0] * (1 + T % 5), r, 520, 1032
@@ -156,7 +158,7 @@ def test_the_estimate_is_the_library_s():
 def both_paths(rows, seed, r, n=3, rank=None, R=4, adapter=None):
     """A case of many rows (tiles of 32) or of a few (single rows)."""
     if rows == "tiles":
-        T = 40000 // r + 190
+        T = (40000 if r <= 64 else 90000) // r + 190
         start = ragged(seed, R, T)
         c = Case(seed, start, adapter or [(i * 2 + 1) % n for i in range(R)], n, 520, 1032, r, rank)
     else:
