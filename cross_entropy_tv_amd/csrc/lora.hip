@@ -23,9 +23,10 @@
 // vector products that read an adapter once for every row, from the L2s (single_rows decides).
 //
 // Precision.  u and v are sums of bf16 products in fp32 and stay fp32: where they
-// enter a matrix-core product they are cut into three bf16 terms (hi + mid + lo, 24
-// bits together), so the products are exact and the results as good as fp32
-// arithmetic (two terms would leave 2^-17).  The extra MFMAs are on the r-sized side.
+// enter a matrix-core product they are cut into three bf16 terms (24 bits together),
+// so the products are exact and the results as good as fp32 arithmetic (two terms
+// would leave 2^-17).  The extra MFMAs are on the r-sized side.  The cut leaves no
+// term 0 (terms8), so a product with an infinity is the infinity that it should be.
 //
 // MFMA layout used throughout (v_mfma_f32_16x16x32_bf16): lane l supplies row (or
 // column) l % 16 and k = 8 (l / 16) .. + 7 of the operands; result register i of lane
@@ -103,29 +104,39 @@ __device__ __forceinline__ u32x4_t keep_below(u32x4_t w, int k0, int end) {
   return (u32x4_t){v[0], v[1], v[2], v[3]};
 }
 
-// Eight fp32 values cut into three bf16 terms each (hi, mid, lo).  A value that is not finite is
-// all in hi.
-__device__ __forceinline__ void terms8(const float (&v)[8], u32x4_t (&t)[3]) {
-  unsigned w[3][4];
+// Eight fp32 values, each cut into N bf16 terms that add up to it.  A term is the largest bf16 number strictly below
+// (in magnitude) what the terms in front of it leave, the last one is the rest: 8 bits at a time, a value's 24 bits
+// fit three terms, a fourth splits the third.  So the terms of a value other than 0 are all of its sign and none of
+// them is 0 (from 2^-87 on; below, the last ones run out of exponents), which keeps its product with an infinity that
+// infinity (rounded terms of either sign, or 0, would make it NaN), and none exceeds a finite value.  A value that is
+// not finite is all of its terms.
+__device__ __forceinline__ unsigned bf16_below(unsigned f32bits) {
+  return f32bits & 0x7fffffffu ? (f32bits - 1u) & 0xffff0000u : f32bits;
+}
+template <int N>
+__device__ __forceinline__ void terms8(const float (&v)[8], u32x4_t (&t)[N]) {
+  unsigned w[N][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float a[3][2];
+    unsigned a[2][N];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float x = v[2 * i + e];
-      const float hi = __uint_as_float(pack_bf16x2(x, 0.0f) << 16);
-      const bool finite = (__float_as_uint(hi) & 0x7f800000u) != 0x7f800000u;
-      const float rest = finite ? x - hi : 0.0f;
-      const float mid = __uint_as_float(pack_bf16x2(rest, 0.0f) << 16);
-      a[0][e] = hi;
-      a[1][e] = mid;
-      a[2][e] = rest - mid;
+      const unsigned x = __float_as_uint(v[2 * i + e]);
+      const bool finite = (x & 0x7f800000u) != 0x7f800000u;
+      const unsigned whole = (x & 0x7fffffffu) > 0x7f800000u ? x | 0x400000u : x;  // (a NaN in its upper half, too)
+      unsigned rest = x;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const unsigned term = n < N - 1 ? bf16_below(rest) : rest;
+        if (n < N - 1) rest = __float_as_uint(__uint_as_float(rest) - __uint_as_float(term));
+        a[e][n] = finite ? term : whole;
+      }
     }
 #pragma unroll
-    for (int n = 0; n < 3; ++n) w[n][i] = pack_bf16x2(a[n][0], a[n][1]);
+    for (int n = 0; n < N; ++n) w[n][i] = a[0][n] >> 16 | (a[1][n] & 0xffff0000u);
   }
 #pragma unroll
-  for (int n = 0; n < 3; ++n) t[n] = (u32x4_t){w[n][0], w[n][1], w[n][2], w[n][3]};
+  for (int n = 0; n < N; ++n) t[n] = (u32x4_t){w[n][0], w[n][1], w[n][2], w[n][3]};
 }
 
 // s_a times the sum of the down kernel's split partials, ranks k0 .. k0 + 7 of row t (0 from `rank` on).
@@ -195,7 +206,7 @@ __device__ __forceinline__ void transpose_blocks(const TransposeArgs& g, int64_t
 
 // ------------------------------------------------------------------ down: P = X M^T
 
-// u or v as the other products take it, its three bf16 terms cut into MFMA operands of 64
+// u or v as the other products take it, its bf16 terms cut into MFMA operands of 64
 // lanes x 16 bytes (a wave's load of one is 1 KB of consecutive memory; operands loaded
 // straight from row-major arrays touch 16 rows per 16 lanes and run at a quarter of that):
 //   U: rows as operand rows, for the up product: [tile of 32 rows][half h][block l][j], where
@@ -206,8 +217,8 @@ struct Terms {
   uint16_t *U, *W;
 };
 // Operands of a tile for the up product with room for r ranks: LD blocks of ranks, TM MFMAs each.
-// r = 8: the k-groups of one MFMA are the three terms (and nothing); r = 16: two terms of 16 ranks
-// an MFMA; else one term of 32 ranks.
+// r = 8: the four k-groups of one MFMA are four terms; r = 16: two terms of 16 ranks an MFMA, four in two; else
+// one term of 32 ranks, three MFMAs.
 __host__ __device__ constexpr int up_ld(int r) { return r <= 32 ? 1 : r <= 64 ? 2 : 4; }
 __host__ __device__ constexpr int up_tm(int r) { return r <= 8 ? 1 : r <= 16 ? 2 : 3; }
 // blocks of 16 ranks that the down and gradient kernels take
@@ -223,8 +234,6 @@ __device__ __forceinline__ int up_chunk(int r, int l, int q) {
 template <int NT>
 __device__ __forceinline__ void emit_terms(const Terms& o, const float* vals, int vs, int64_t t0, int r) {
   const int64_t tile = t0 / kTileRows;
-  u32x4_t w[4];
-  w[3] = (u32x4_t){0u, 0u, 0u, 0u};
   if (o.U) {
     const int ld = up_ld(r), tm = up_tm(r), kcs = r <= 8 ? 1 : r <= 16 ? 2 : 4 * ld;  // chunks of 8 ranks
     uint16_t* U = o.U + tile * 2 * ld * tm * 512;
@@ -233,26 +242,23 @@ __device__ __forceinline__ void emit_terms(const Terms& o, const float* vals, in
       float v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = 8 * kc < r ? vals[row * vs + 8 * kc + k] : 0.0f;
-      u32x4_t t3[3];
-      terms8(v, t3);
+      // operand and lane (k-group q) of term n of this chunk
+      auto put = [&](int f, int q, const u32x4_t& w) {
+        *reinterpret_cast<u32x4_t*>(U + f * 512 + (c16 + 16 * q) * 8) = w;
+      };
+      if (r <= 16) {
+        u32x4_t t4[4];
+        terms8(v, t4);
 #pragma unroll
-      for (int n = 0; n < 3; ++n) w[n] = t3[n];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        // operand and lane of term n of this chunk (n = 3: the zeros of the k-groups that hold no term)
-        int f, q;
-        if (r <= 8) {
-          f = h;
-          q = n;
-        } else if (r <= 16) {
-          f = 2 * h + (n >> 1);
-          q = kc + 2 * (n & 1);
-        } else {
-          if (n == 3) break;
-          f = (h * ld + kc / 4) * 3 + n;
-          q = kc % 4;
+        for (int n = 0; n < 4; ++n) {
+          if (r <= 8) put(h, n, t4[n]);
+          else put(2 * h + (n >> 1), kc + 2 * (n & 1), t4[n]);
         }
-        *reinterpret_cast<u32x4_t*>(U + f * 512 + (c16 + 16 * q) * 8) = w[n];
+      } else {
+        u32x4_t t3[3];
+        terms8(v, t3);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) put((h * ld + kc / 4) * 3 + n, kc % 4, t3[n]);
       }
     }
   }
@@ -593,9 +599,16 @@ void lora_up_tile_kernel(UpArgs g) {
   const int64_t r0 = (int64_t)(bid_x() / nch) * kTileRows;
   const int64_t r1 = r0 + kTileRows < s.T ? r0 + kTileRows : s.T;
   const int c16 = lane & 15, q = lane >> 4;
-  int ck[LD];  // this lane's 8 ranks of block l (none: 0, and u is 0 there)
+  // this lane's 8 ranks of block l, and how they count against an adapter's rank; none (u is 0 there): the first 8
+  // are loaded and made 0, so that no infinity among them meets the 0
+  int ck[LD], first[LD];
 #pragma unroll
-  for (int l = 0; l < LD; ++l) ck[l] = max(up_chunk(r, l, q), 0);
+  for (int l = 0; l < LD; ++l) {
+    const int c = up_chunk(r, l, q);
+    ck[l] = TM == 3 ? max(c, 0) : c;
+    first[l] = TM == 3 && c < 0 ? r : c;
+  }
+  const bool some_none = TM == 3 && r < 32 * LD;
   // the tile's rows and an adapter's M lie within 2^30 bytes: 32-bit offsets from uniform bases
   YT* Y = static_cast<YT*>(g.y) + r0 * g.ldy;
   const BT* base = static_cast<const BT*>(g.base) + (BASE ? r0 * g.ldb : 0);
@@ -637,7 +650,7 @@ void lora_up_tile_kernel(UpArgs g) {
       else return u[h][l][j];
     };
     const uint16_t* M = g.M + (some ? (int64_t)p.adapter * g.C * r : 0);
-    const bool mask = !g.m_clean && rank < r;
+    const bool mask = some_none || (!g.m_clean && rank < r);
     for (uint32_t n = (uint32_t)n0; n < (uint32_t)n1; n += 64) {
       const uint32_t col = n + 4 * c16;
       u32x4_t w[4][LD];
@@ -670,7 +683,7 @@ void lora_up_tile_kernel(UpArgs g) {
 #pragma unroll
           for (int b = 0; b < 4; ++b)
 #pragma unroll
-            for (int l = 0; l < LD; ++l) w[b][l] = keep_below(w[b][l], ck[l], rank);
+            for (int l = 0; l < LD; ++l) w[b][l] = keep_below(w[b][l], first[l], rank);
         }
 #pragma unroll
         for (int l = 0; l < LD; ++l)
@@ -775,6 +788,7 @@ __global__ __launch_bounds__(kLThreads) void lora_up_lane_kernel(UpArgs g) {
           sum[c] = __builtin_fmaf(u[c][2 * e], __uint_as_float(wv[e] << 16), sum[c]);
           sum[c] = __builtin_fmaf(u[c][2 * e + 1], __uint_as_float(wv[e] & 0xffff0000u), sum[c]);
         }
+        if (c == 3 && r == 24) sum[c] = 0.0f;  // (the last chunk is the first again)
       }
 #pragma unroll
       for (int c = 1; c < CH; ++c) sum[0] += sum[c];
@@ -1154,7 +1168,8 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
   const int64_t scol = c0 + spiece * 8 < g.C ? spiece * 8 : 0;
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   // (loaded without conditions, from rows between the stage's first and last, and cut where it is written: a
-  // select here would have to wait for the load; columns behind the last are not stored)
+  // select here would have to wait for the load; columns behind the last are 0, as B's rows there are for v)
+  const bool scol_in = c0 + spiece * 8 < g.C;
   const uint32_t ldx = (uint32_t)g.ldx;
   auto fetch = [&](const Stage& w, u32x4_t (&v)[8]) {
     const uint16_t* X = g.X + w.at * g.ldx + c0;
@@ -1188,7 +1203,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
   while (more) {
     uint8_t* T = lds + stage * (kGradRows * kGradCols * 2);
     const Stage now = coming;
-    const unsigned long long mine = now.rows >> srow;
+    const unsigned long long mine = scol_in ? now.rows >> srow : 0ull;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       *reinterpret_cast<u32x4_t*>(T + stage_at(srow + 8 * j, spiece)) = mine >> (8 * j) & 1 ? held[j] : zero;

@@ -567,7 +567,9 @@ lx_status lx_draft_verify(const void* target, int64_t ld_target, const void* dra
  *   contiguous.  grad_x, grad_A, grad_B are optional (NULL: not computed), one at least is given.
  *   grad_A and grad_B are OVERWRITTEN; ranks beyond an adapter's and adapters without rows get 0.
  * - u and v are fp32 and enter the second products unrounded; all sums are fp32, in a fixed
- *   order (the same bits on every call).
+ *   order (the same bits on every call).  Infinities among the inputs reach the results as the
+ *   sums above say (infinity times 0, and a sum of both signs, are NaN), those of ranks beyond an
+ *   adapter's and of other requests' rows do not; beside one, u and v below 2^-87 may count as 0.
  * Requirements: H, N and every row stride multiples of 8, at most 2^22; r a multiple of 8,
  *   at most 128; T <= 2^22, R <= 2^24, 1 <= n_adapters <= 2^20, n_adapters * r * (H + N)
  *   below 2^37; x, grad_y, A, B, base, y and
