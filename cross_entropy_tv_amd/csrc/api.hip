@@ -84,8 +84,8 @@ struct Tensor {
   int64_t ld;
 };
 
-// Sizes that lx_draft_verify takes: grids of one workgroup per (position, sequence, at
-// least 2048 logits) and tables of S * (max_draft + 1) entries stay within int32.
+// Sizes that lx_draft_verify takes: workgroups, one per (position, sequence, at least 2048
+// logits), and tables of S * (max_draft + 1) entries are counted within int32.
 bool verify_shape_ok(int64_t S, int64_t max_draft, int64_t V) {
   if (S < 0 || max_draft < 0 || V < 1 || V > (int64_t)INT_MAX || S > (1 << 24) || max_draft > (1 << 20)) return false;
   return S * (max_draft + 1) <= (1 << 24) && S * (max_draft + 1) <= (int64_t)INT_MAX / ((V + 2047) / 2048);
@@ -303,8 +303,8 @@ lx_status forward_backward_impl(Tensor zs, Tensor us, const int64_t* target, int
   return from_hip(lx::launch_backward(b, dt_of(dt), st));
 }
 
-// Sizes that the low-rank adapters take: operand rows of whole 16 bytes, grids and
-// tables within int32.
+// Sizes that the low-rank adapters take: operand rows of whole 16 bytes, workgroups and
+// tables counted within int32.
 bool lora_shape_ok(int64_t T, int64_t R, int64_t n, int64_t H, int64_t N, int64_t r) {
   if (T < 0 || T > (1 << 22) || R < 0 || R > (1 << 24) || n < 1 || n > (1 << 20)) return false;
   if (H < 8 || H % 8 || H > lx::kGemmMaxLd || N < 8 || N % 8 || N > lx::kGemmMaxLd) return false;

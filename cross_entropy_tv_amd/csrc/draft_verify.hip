@@ -570,8 +570,8 @@ __global__ __launch_bounds__(kVThreads) void verify_accept_kernel(Args g) {
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   const int K = w.K1;
-  const int c = (int)(bid_x() % (unsigned)K);
-  const unsigned slot = bid_x() / (unsigned)K;  // position-major: all first positions, then all second ones, ...
+  const int c = (int)(large_bid() % (unsigned)K);
+  const unsigned slot = large_bid() / (unsigned)K;  // position-major: all first positions, then all second ones, ...
   const int i = (int)(slot % (unsigned)a.S), j = (int)(slot / (unsigned)a.S);
   const Seq q = seq_of(a, i);
   if (j >= q.n) return;
@@ -767,8 +767,8 @@ __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(Args g) {
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   const int K = w.K1;
-  const int c = (int)(bid_x() % (unsigned)K);
-  const unsigned slot = bid_x() / (unsigned)K;
+  const int c = (int)(large_bid() % (unsigned)K);
+  const unsigned slot = large_bid() / (unsigned)K;
   const int i = (int)(slot % (unsigned)a.S), j = (int)(slot / (unsigned)a.S);
   const Seq q = seq_of(a, i);
   if (j > q.n || !q.ok) return;
@@ -1141,7 +1141,8 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   const int K = w.K2;
-  const int c = (int)(bid_x() % (unsigned)K), i = (int)(bid_x() / (unsigned)K);
+  const int c = (int)(large_bid() % (unsigned)K), i = (int)(large_bid() / (unsigned)K);
+  if (i >= a.S) return;
   const Seq q = seq_of(a, i);
   const Temp t = temp_of(a.temperature, i);
   const int acc = min(w.first[i], q.n);
@@ -1311,7 +1312,8 @@ __global__ __launch_bounds__(kVThreads) void verify_draw_kernel(Args g, int K) {
   __shared__ PickShared sh;
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
-  const int c = (int)(bid_x() % (unsigned)K), i = (int)(bid_x() / (unsigned)K);
+  const int c = (int)(large_bid() % (unsigned)K), i = (int)(large_bid() / (unsigned)K);
+  if (i >= a.S) return;
   const Seq q = seq_of(a, i);
   const int acc = min(w.first[i], q.n);
   const bool residual = a.draft != nullptr && acc < q.n;
@@ -1418,7 +1420,8 @@ hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
   hipLaunchKernelGGL(verify_init_kernel, dim3((unsigned)((n + kVThreads - 1) / kVThreads)), dim3(kVThreads), 0, st,
                      w.first, (int)a.S, w.count1, w.n_zero);
   if (hipError_t e = hipGetLastError()) return e;
-  const dim3 block(kVThreads), rows((unsigned)(a.S * (w.direct ? a.L + 1 : a.L) * w.K1)), draws((unsigned)(a.S * w.K2));
+  // (positions behind max_draft, as the last row of a large grid may have, are behind every sequence's drafts)
+  const dim3 block(kVThreads), rows = large_grid(a.S * (w.direct ? a.L + 1 : a.L) * w.K1), draws = large_grid(a.S * w.K2);
   const int64_t held = w.chunk2 / kVUnit;
   if (w.direct) {
     if (w.chunk1 == kVUnit) hipLaunchKernelGGL((verify_rows_kernel<T, 1>), rows, block, 0, st, g);
@@ -1441,7 +1444,7 @@ hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
   if (hipError_t e = hipGetLastError()) return e;
   // (without draft logits every draw is from p, by one workgroup)
   const int K = a.draft ? w.K2 : 1;
-  const dim3 all((unsigned)(a.S * K));
+  const dim3 all = large_grid(a.S * K);
   if (held == 1) hipLaunchKernelGGL((verify_draw_kernel<T, 1>), all, block, 0, st, g, K);
   else hipLaunchKernelGGL((verify_draw_kernel<T, 2>), all, block, 0, st, g, K);
   return hipGetLastError();

@@ -23,4 +23,18 @@ __device__ __forceinline__ unsigned nblocks_x() {
   return *(const unsigned*)__builtin_amdgcn_implicitarg_ptr();
 }
 
+// Large grids.  One dimension of a launch holds less than 2^32 threads (2^24 workgroups of 256), and the runtime does
+// not refuse more but launches what is left modulo 2^32.  Grids that may be larger are cut into rows of 2^20
+// workgroups (a multiple of 8: workgroup id mod 8 stays the die), and their kernels take their place from large_bid;
+// the last row's workgroups behind the end find no work at their place.
+constexpr int kGridRowBits = 20;
+__device__ __forceinline__ unsigned large_bid() {
+  return (__builtin_amdgcn_workgroup_id_y() << kGridRowBits) + __builtin_amdgcn_workgroup_id_x();
+}
+inline dim3 large_grid(int64_t workgroups) {
+  constexpr int64_t row = (int64_t)1 << kGridRowBits;
+  if (workgroups <= row) return dim3((unsigned)workgroups);
+  return dim3((unsigned)row, (unsigned)((workgroups + row - 1) / row));
+}
+
 }  // namespace lx

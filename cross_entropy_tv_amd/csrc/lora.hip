@@ -542,11 +542,13 @@ __device__ __forceinline__ void down_row_strided(const DownArgs& g, int64_t unit
   if (lane < kRowWide && rho + lane < r) g.P[((int64_t)split * s.T + t) * r + rho + lane] = mine;
 }
 
-// Both in one launch (blocks of four waves, blocks_u of them for u).
-__global__ __launch_bounds__(kLThreads) void lora_down_row_kernel(DownArgs u, unsigned blocks_u, DownArgs v) {
+// Both in one launch (blocks of four waves, blocks_u of them for u and blocks_v for v).
+__global__ __launch_bounds__(kLThreads) void lora_down_row_kernel(DownArgs u, unsigned blocks_u, DownArgs v,
+                                                                  unsigned blocks_v) {
   const int wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6);
-  if (bid_x() < blocks_u) down_row(u, (int64_t)bid_x() * 4 + wave);
-  else down_row_strided(v, (int64_t)(bid_x() - blocks_u) * 4 + wave);
+  const unsigned block = large_bid();
+  if (block < blocks_u) down_row(u, (int64_t)block * 4 + wave);
+  else if (block - blocks_u < blocks_v) down_row_strided(v, (int64_t)(block - blocks_u) * 4 + wave);
 }
 
 // ------------------------------------------------------------------ up: Y = base + P M^T
@@ -731,7 +733,7 @@ struct RowPlace {
 __device__ __forceinline__ RowPlace row_place(const UpArgs& g, int columns) {
   const LoraSet& s = g.s;
   const int wave = __builtin_amdgcn_readfirstlane(tid_x() >> 6);
-  const unsigned die = bid_x() % 8u, on_die = bid_x() / 8u;
+  const unsigned die = large_bid() % 8u, on_die = large_bid() / 8u;
   RowPlace o{};
   o.t = on_die % (unsigned)s.T;
   const int64_t ch = (int64_t)(on_die / (unsigned)s.T) * 8 + die;
@@ -964,8 +966,8 @@ __global__ __launch_bounds__(kLThreads) void lora_up_strided_kernel(UpArgs g, un
   const LoraSet& s = g.s;
   const int tid = tid_x(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = (int)s.r;
   // (ranges a multiple of 8, or below 8: the rows of one range on one die, for A's part in its L2)
-  const int64_t t = bid_x() / ranges, c0 = (int64_t)(bid_x() % ranges) * kCols;
-  if (c0 >= g.C) return;
+  const int64_t t = large_bid() / ranges, c0 = (int64_t)(large_bid() % ranges) * kCols;
+  if (c0 >= g.C || t >= s.T) return;
   const int i = find_request(s.start, (int)s.R, t);
   if (i < 0) return;
   const Part p = part_of(s, i, t, t + 1);
@@ -1157,6 +1159,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
   const int64_t c0 = (int64_t)(block % cols) * kGradCols;
   const int split = (int)(block / cols % (unsigned)g.splits);
   const int a = (int)(block / cols / (unsigned)g.splits);
+  if (a >= s.n) return;
   const int64_t t0 = split * g.tslice, t1 = t0 + g.tslice < s.T ? t0 + g.tslice : s.T;
   f32x4_t acc[CB][RBW];
 #pragma unroll
@@ -1288,15 +1291,17 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, unsigned block, uin
 }
 
 template <int RB>
-__global__ __launch_bounds__(kLThreads) void lora_grad_kernel(GradArgs ga, unsigned blocks_a, GradArgs gb) {
+__global__ __launch_bounds__(kLThreads) void lora_grad_kernel(GradArgs ga, unsigned blocks_a, GradArgs gb,
+                                                              unsigned blocks_b) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kGradRows * kGradCols * 2];
-  if (bid_x() < blocks_a) grad_tile<RB, false>(ga, bid_x(), lds);
-  else grad_tile<RB, true>(gb, bid_x() - blocks_a, lds);
+  const unsigned block = large_bid();
+  if (block < blocks_a) grad_tile<RB, false>(ga, block, lds);
+  else if (block - blocks_a < blocks_b) grad_tile<RB, true>(gb, block - blocks_a, lds);
 }
 
 __global__ __launch_bounds__(kLThreads) void lora_grad_v_kernel(GradArgs g) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kGradRows * kGradCols * 2];
-  grad_tile<1, true, true>(g, bid_x(), lds);
+  grad_tile<1, true, true>(g, large_bid(), lds);
 }
 
 // The partial sums of the column blocks, [n][plane], added up in order to [parts][plane]: part p takes
@@ -1359,7 +1364,7 @@ bool single_rows(int64_t T, int64_t R, int64_t r, int64_t H, int64_t N, bool bac
   double tiles = 13.0 + shared * (pass(H) + (backward ? pass(N) : 0.0)) +
                  (shared - 1.0) * (double)T * (double)(backward ? H : N) * 8.0 / 10.0e6;
   if (r > 64) tiles *= 2.0;
-  // (and single rows' grids stay within int32)
+  // (and single rows' workgroups are counted in 32 bits)
   return rows < tiles && T * (((H > N ? H : N) + 255) / 256) < (1 << 30);
 }
 
@@ -1384,7 +1389,7 @@ hipError_t launch_down_rows(const DownArgs& u, bool want_u, const DownArgs& v, b
   const unsigned bu = want_u ? (unsigned)((u.s.T * quads_of(u.s.r) * u.splits + 3) / 4) : 0u;
   const unsigned bv = want_v ? (unsigned)((v.s.T * wides_of(v.s.r) * v.splits + 3) / 4) : 0u;
   if (bu + bv == 0) return hipSuccess;
-  hipLaunchKernelGGL(lora_down_row_kernel, dim3(bu + bv), dim3(kLThreads), 0, st, u, bu, v);
+  hipLaunchKernelGGL(lora_down_row_kernel, large_grid((int64_t)bu + bv), dim3(kLThreads), 0, st, u, bu, v, bv);
   return hipGetLastError();
 }
 
@@ -1421,13 +1426,13 @@ dim3 up_rows_grid(UpArgs& g, int64_t columns) {
   g.steps = (int)(T * ((g.C + columns - 1) / columns) / 16384);
   g.steps = g.steps < 1 ? 1 : g.steps > 16 ? 16 : g.steps;
   const int64_t ranges = (g.C + 4 * columns * g.steps - 1) / (4 * columns * g.steps);
-  return dim3((unsigned)((ranges + 7) / 8 * 8 * T));
+  return large_grid((ranges + 7) / 8 * 8 * T);
 }
 
 hipError_t launch_up_strided(const UpArgs& g, hipStream_t st) {
   unsigned ranges = (unsigned)((g.C + 511) / 512);
   if (ranges > 8) ranges = (ranges + 7) / 8 * 8;
-  const dim3 grid((unsigned)(ranges * g.s.T));
+  const dim3 grid = large_grid(ranges * g.s.T);
   if (g.base) hipLaunchKernelGGL(lora_up_strided_kernel<true>, grid, dim3(kLThreads), 0, st, g, ranges);
   else hipLaunchKernelGGL(lora_up_strided_kernel<false>, grid, dim3(kLThreads), 0, st, g, ranges);
   return hipGetLastError();
@@ -1580,7 +1585,7 @@ BackwardWs backward_ws(void* base, int64_t T, int64_t R, int64_t n, int64_t H, i
 template <int RB>
 hipError_t launch_grad_t(const GradArgs& ga, unsigned ba, const GradArgs& gb, unsigned bb, hipStream_t st) {
   if (ba + bb == 0) return hipSuccess;
-  hipLaunchKernelGGL(lora_grad_kernel<RB>, dim3(ba + bb), dim3(kLThreads), 0, st, ga, ba, gb);
+  hipLaunchKernelGGL(lora_grad_kernel<RB>, large_grid((int64_t)ba + bb), dim3(kLThreads), 0, st, ga, ba, gb, bb);
   return hipGetLastError();
 }
 hipError_t launch_grad(const GradArgs& ga, unsigned ba, const GradArgs& gb, unsigned bb, hipStream_t st) {
@@ -1668,7 +1673,7 @@ hipError_t launch_lora_backward(const LoraBackwardArgs& a, hipStream_t st) {
   const unsigned ba = a.gA ? (unsigned)(s.n * w.splits_A * cols_A) : 0u;
   const unsigned bb = a.gB ? (unsigned)(s.n * w.splits_B * cols_B) : 0u;
   if (one_pass) {
-    hipLaunchKernelGGL(lora_grad_v_kernel, dim3(bb), dim3(kLThreads), 0, st, gb);
+    hipLaunchKernelGGL(lora_grad_v_kernel, large_grid(bb), dim3(kLThreads), 0, st, gb);
     if (hipError_t e = hipGetLastError()) return e;
     const float* P = w.Pf;
     splits_v = (int)cols_B;
