@@ -767,8 +767,8 @@ __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(Args g) {
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   const int K = w.K1;
-  const int c = (int)(large_bid() % (unsigned)K);
-  const unsigned slot = large_bid() / (unsigned)K;
+  const int c = (int)(bid_x() % (unsigned)K);
+  const unsigned slot = bid_x() / (unsigned)K;
   const int i = (int)(slot % (unsigned)a.S), j = (int)(slot / (unsigned)a.S);
   const Seq q = seq_of(a, i);
   if (j > q.n || !q.ok) return;
@@ -1141,12 +1141,13 @@ __global__ __launch_bounds__(kVThreads) void verify_sums_kernel(Args g) {
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
   const int K = w.K2;
-  const int c = (int)(large_bid() % (unsigned)K), i = (int)(large_bid() / (unsigned)K);
-  if (i >= a.S) return;
+  const int c = (int)(large_bid() % (unsigned)K), at_i = (int)(large_bid() / (unsigned)K);
+  const int i = min(at_i, (int)a.S - 1);
   const Seq q = seq_of(a, i);
   const Temp t = temp_of(a.temperature, i);
   const int acc = min(w.first[i], q.n);
   const float u = a.u_sample[i];
+  if (at_i >= a.S) return;  // (behind the loads, none of which waits for it)
   if (!q.ok || (t.greedy && acc < q.n)) {
     if (c == 0) write_out(a, w, i, q, acc, q.ok ? w.best[(int64_t)acc * a.S + i] : -1, 0.0f);
     return;
@@ -1312,13 +1313,14 @@ __global__ __launch_bounds__(kVThreads) void verify_draw_kernel(Args g, int K) {
   __shared__ PickShared sh;
   __shared__ int sh_flag;
   const int tid = tid_x(), lane = tid & 63, wave = tid >> 6;
-  const int c = (int)(large_bid() % (unsigned)K), i = (int)(large_bid() / (unsigned)K);
-  if (i >= a.S) return;
+  const int c = (int)(large_bid() % (unsigned)K), at_i = (int)(large_bid() / (unsigned)K);
+  const int i = min(at_i, (int)a.S - 1);
   const Seq q = seq_of(a, i);
   const int acc = min(w.first[i], q.n);
   const bool residual = a.draft != nullptr && acc < q.n;
   const Temp t = temp_of(a.temperature, i);
   const int64_t slot = (int64_t)acc * a.S + i;
+  if (at_i >= a.S) return;  // (behind the loads, none of which waits for it)
   if (!q.ok || t.greedy || !residual) {
     if (c > 0 || !w.direct) return;  // (drawn in step 2)
     if (!q.ok || t.greedy) {
@@ -1420,19 +1422,20 @@ hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
   hipLaunchKernelGGL(verify_init_kernel, dim3((unsigned)((n + kVThreads - 1) / kVThreads)), dim3(kVThreads), 0, st,
                      w.first, (int)a.S, w.count1, w.n_zero);
   if (hipError_t e = hipGetLastError()) return e;
-  // (positions behind max_draft, as the last row of a large grid may have, are behind every sequence's drafts)
-  const dim3 block(kVThreads), rows = large_grid(a.S * (w.direct ? a.L + 1 : a.L) * w.K1), draws = large_grid(a.S * w.K2);
+  // (verify_rows: at most 2^23 workgroups, as direct_rows says)
+  const int64_t n_rows = a.S * (w.direct ? a.L + 1 : a.L) * w.K1;
+  const dim3 block(kVThreads), draws = large_grid(a.S * w.K2);
   const int64_t held = w.chunk2 / kVUnit;
   if (w.direct) {
-    if (w.chunk1 == kVUnit) hipLaunchKernelGGL((verify_rows_kernel<T, 1>), rows, block, 0, st, g);
-    else hipLaunchKernelGGL((verify_rows_kernel<T, 2>), rows, block, 0, st, g);
+    if (w.chunk1 == kVUnit) hipLaunchKernelGGL((verify_rows_kernel<T, 1>), dim3((unsigned)n_rows), block, 0, st, g);
+    else hipLaunchKernelGGL((verify_rows_kernel<T, 2>), dim3((unsigned)n_rows), block, 0, st, g);
   } else {
     if (a.L > 0) {
       // groups held at once, two rows of them: 2 of 2-byte logits (4: 23.7 against 21.4 us at 256 x
       // 50001, the registers halve the workgroups at once), 4 of fp32 (2: 191 against 183 us at 96 x 262144)
       constexpr int kHold = sizeof(T) == 4 ? 4 : 2;
-      if (w.chunk1 < kHold * kVUnit) hipLaunchKernelGGL((verify_accept_kernel<T, 1>), rows, block, 0, st, g);
-      else hipLaunchKernelGGL((verify_accept_kernel<T, kHold>), rows, block, 0, st, g);
+      if (w.chunk1 < kHold * kVUnit) hipLaunchKernelGGL((verify_accept_kernel<T, 1>), large_grid(n_rows), block, 0, st, g);
+      else hipLaunchKernelGGL((verify_accept_kernel<T, kHold>), large_grid(n_rows), block, 0, st, g);
       if (hipError_t e = hipGetLastError()) return e;
     }
     // (fp32: a chunk of 4 in two rounds of 2; 4 held took 75 us where 2 take 58, 96 x 262144)
