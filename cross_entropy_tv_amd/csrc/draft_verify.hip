@@ -381,7 +381,9 @@ template <typename T>
 __device__ __forceinline__ Sum32 wave_rest(const T* row, int64_t lo, int64_t hi, int64_t V, const LaneSum& a, float c) {
   const int lane = tid_x() & 63;
   const float m = wave_max(a.m), ref = ref_of(m);
-  const int top = __builtin_ctzll(__ballot(a.m == m));
+  // (NaNs are assumed absent from the arithmetic here: what is compared may not decide where is read, so a lane is
+  // named in any case)
+  const int top = __builtin_ctzll(__ballot(a.m == m) | 1ull << 63);
   float r = lane == top ? 0.0f : a.s * exp2_hw((a.m - ref) * c);
   int at = 0;
   for (int64_t b = lo + (lane >> 3) * kVUnit; b < hi; b += 8 * kVUnit) {
@@ -1049,6 +1051,7 @@ __device__ __forceinline__ int64_t pick(const Masses<T, RES>& m, PickShared& sh,
               zx = x[k];
             }
           }
+          at = at <= m.V ? at : 0;  // (with NaN masses)
         }
         const unsigned long long hit = __ballot(at != 0);
         if (lane == (hit ? __builtin_ctzll(hit) : 0)) {
@@ -1082,6 +1085,7 @@ __device__ __forceinline__ int64_t pick(const Masses<T, RES>& m, PickShared& sh,
 #pragma unroll
     for (int k = 0; k < 8; ++k) last = e[k] > 0.0 ? (int)(v + k) + 1 : last;
   }
+  last = last <= m.V ? last : 0;  // (with NaN masses)
   last = wave_all(last, [](int p, int q) { return p > q ? p : q; });
   if (lane == 0) sh.last[wave] = last;
   __syncthreads();
