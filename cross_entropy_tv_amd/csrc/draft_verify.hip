@@ -457,11 +457,11 @@ struct Ws {
   size_t bytes;
 };
 
-// Chunks of a row: 1, 2, 4 .. kVUnits each, as few as keep `rows` rows within `wanted`
-// workgroups, and at most `most` (but for rows of more than kVMaxChunks such chunks).
-void chunking(int64_t rows, int64_t V, int64_t wanted, int64_t most, int64_t& chunk, int& K) {
+// Chunks of a row: `least` (a power of two) units of kVUnit elements each, or 2, 4 .. times as many, as few as keep
+// `rows` rows within `wanted` workgroups, and at most `most` (but for rows of more than kVMaxChunks such chunks).
+void chunking(int64_t rows, int64_t V, int64_t wanted, int64_t least, int64_t most, int64_t& chunk, int& K) {
   const int64_t units = (V + kVUnit - 1) / kVUnit;
-  int64_t per = 1;
+  int64_t per = least;
   while (per < most && rows * ((units + per - 1) / per) > wanted) per *= 2;
   while ((units + per - 1) / per > kVMaxChunks) per *= 2;
   chunk = per * kVUnit;
@@ -480,9 +480,11 @@ Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
   w.direct = direct_rows(S, L, V);
   const int64_t P = w.direct ? L + 1 : L;
   // step 1: at most 16384 elements (a longer chunk delays the decision that spares later
-  // positions); steps 2 and 3: what a thread holds at once
-  chunking(S * P, V, 1024, 8, w.chunk1, w.K1);
-  chunking(S, V, 1280, 4, w.chunk2, w.K2);
+  // positions), and whole rounds of what verify_accept holds (up to 4 units: with fewer, S L rows would be
+  // 1024 chunks or less of 2 units or less, and S (L + 1) V below 2^23: direct); steps 2 and 3: what a thread
+  // holds at once
+  chunking(S * P, V, 1024, w.direct ? 1 : 4, 8, w.chunk1, w.K1);
+  chunking(S, V, 1280, 1, 4, w.chunk2, w.K2);
   size_t off = 0;
   char* p = static_cast<char*>(base);
   auto take = [&](size_t bytes) {
@@ -1438,8 +1440,7 @@ hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t st) {
       // groups held at once, two rows of them: 2 of 2-byte logits (4: 23.7 against 21.4 us at 256 x
       // 50001, the registers halve the workgroups at once), 4 of fp32 (2: 191 against 183 us at 96 x 262144)
       constexpr int kHold = sizeof(T) == 4 ? 4 : 2;
-      if (w.chunk1 < kHold * kVUnit) hipLaunchKernelGGL((verify_accept_kernel<T, 1>), large_grid(n_rows), block, 0, st, g);
-      else hipLaunchKernelGGL((verify_accept_kernel<T, kHold>), large_grid(n_rows), block, 0, st, g);
+      hipLaunchKernelGGL((verify_accept_kernel<T, kHold>), large_grid(n_rows), block, 0, st, g);
       if (hipError_t e = hipGetLastError()) return e;
     }
     // (fp32: a chunk of 4 in two rounds of 2; 4 held took 75 us where 2 take 58, 96 x 262144)
