@@ -50,3 +50,22 @@ def test_nan_and_infinite_logits(dt, with_draft, temp):
         assert 0 <= a <= c.lens[i], i
         assert np.array_equal(tok[i, :a], c.tokens[s[i]:s[i] + a]) and (tok[i, a + 1:] == -1).all(), i
         assert -1 <= tok[i, a] < V, i
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("S", [9, 200, 300])
+def test_greedy_takes_the_first_of_equals(S, dt):
+    """Several tokens with the largest logit, of a drafted position and of the row behind the drafts: in one group of 8,
+    in two lanes, in two waves of which the lower one holds the later token (of the next 2048), in later rounds of a
+    chunk, in two chunks, at the end of the row.  9, 200 and 300 sequences take chunks of 1, 8 and 4 times 2048."""
+    V = 20003
+    kinds = [(17, 21), (25, 322), (1900, 2053), (2047, 2048, 4096), (4000, 6150, 6151), (100, 19000), (9000, 20002),
+             (1531, 3066, 5117, 8200)]
+    c = plain.Case(89, [1] * S, V, dt, temps=np.zeros(S, dtype=np.float32))
+    for i in range(S):
+        for j in range(2):
+            c.z[2 * i + j, list(kinds[(i + j) % len(kinds)])] = 50.0
+        k = kinds[i % len(kinds)]
+        c.tokens[i] = k[0] if i // len(kinds) % 2 == 0 else k[-1]
+    n = plain.check(c, f"ties of {S} {dt}")
+    assert 0 < n.sum() < S and np.array_equal(n, [i // len(kinds) % 2 == 0 for i in range(S)])
