@@ -185,10 +185,10 @@ class _Launch:
 
     def __enter__(self):
         index = self.device.index
-        if _current_device() != index:
+        self.ptr = _current_raw_stream(index) if self.stream is None else _stream(self.stream)
+        if _current_device() != index:  # (last: nothing behind it can fail and leave the device changed)
             self.guard = torch.cuda.device(index)
             self.guard.__enter__()
-        self.ptr = _current_raw_stream(index) if self.stream is None else _stream(self.stream)
         return self
 
     def __exit__(self, *exc):
