@@ -185,7 +185,12 @@ class _Launch:
 
     def __enter__(self):
         index = self.device.index
-        self.ptr = _current_raw_stream(index) if self.stream is None else _stream(self.stream)
+        if self.stream is None:
+            self.ptr = _current_raw_stream(index)
+        else:
+            if getattr(self.stream, "device", self.device) != self.device:
+                raise ValueError(f"stream must be one of {self.device}, got one of {self.stream.device}")
+            self.ptr = _stream(self.stream)
         if _current_device() != index:  # (last: nothing behind it can fail and leave the device changed)
             self.guard = torch.cuda.device(index)
             self.guard.__enter__()

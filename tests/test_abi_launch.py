@@ -50,3 +50,12 @@ def test_a_stream_that_is_none_leaves_the_device_as_it_was(monkeypatch):
         with lx._Launch(torch.device("cuda:1"), "no stream"):
             pass
     assert devices.current == 0
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Its kernels would run on that device, on this one's memory."""
+    devices = Devices(monkeypatch)
+    with pytest.raises(ValueError, match="stream must be one of cuda:1"):
+        with lx._Launch(torch.device("cuda:1"), Stream(0, 77)):
+            pass
+    assert devices.current == 0
