@@ -36,9 +36,10 @@
 //
 // Precision.  An answer here is a whole number that a comparison decides, so the
 // values compared are held tighter than the rounding of the logits would ask
-// for.  The acceptance compares r q(x) with p(x) from fp32 sums (good to a few
-// 2^-21) and, where the two lie within 2^-15 of each other, again from fp64 sums
-// over both rows.  The draw's running sums are fp64 throughout: with 150 000
+// for.  The acceptance compares r q(x) with p(x) from fp32 sums (of 64 elements a
+// lane at most, 48 additions one behind the other: good to 2^-18, a few 2^-21 as a
+// rule; chunks are joined in fp64) and, where the two lie within 2^-15 of each
+// other, again from fp64 sums over both rows.  The draw's running sums are fp64 throughout: with 150 000
 // tokens the borders between them lie too close for fp32 sums to tell which side
 // w * total falls on.
 #include "common.hpp"
@@ -458,12 +459,13 @@ struct Ws {
 };
 
 // Chunks of a row: `least` (a power of two) units of kVUnit elements each, or 2, 4 .. times as many, as few as keep
-// `rows` rows within `wanted` workgroups, and at most `most` (but for rows of more than kVMaxChunks such chunks).
-void chunking(int64_t rows, int64_t V, int64_t wanted, int64_t least, int64_t most, int64_t& chunk, int& K) {
+// `rows` rows within `wanted` workgroups, and at most `most` (with `fit` but for rows of more than kVMaxChunks such
+// chunks).
+void chunking(int64_t rows, int64_t V, int64_t wanted, int64_t least, int64_t most, bool fit, int64_t& chunk, int& K) {
   const int64_t units = (V + kVUnit - 1) / kVUnit;
   int64_t per = least;
   while (per < most && rows * ((units + per - 1) / per) > wanted) per *= 2;
-  while ((units + per - 1) / per > kVMaxChunks) per *= 2;
+  while (fit && (units + per - 1) / per > kVMaxChunks) per *= 2;
   chunk = per * kVUnit;
   K = (int)((units + per - 1) / per);
 }
@@ -479,12 +481,12 @@ Ws verify_ws(void* base, int64_t S, int64_t L, int64_t V) {
   Ws w{};
   w.direct = direct_rows(S, L, V);
   const int64_t P = w.direct ? L + 1 : L;
-  // step 1: at most 16384 elements (a longer chunk delays the decision that spares later
-  // positions), and whole rounds of what verify_accept holds (up to 4 units: with fewer, S L rows would be
-  // 1024 chunks or less of 2 units or less, and S (L + 1) V below 2^23: direct); steps 2 and 3: what a thread
-  // holds at once
-  chunking(S * P, V, 1024, w.direct ? 1 : 4, 8, w.chunk1, w.K1);
-  chunking(S, V, 1280, 1, 4, w.chunk2, w.K2);
+  // step 1: at most 16384 elements (a longer chunk delays the decision that spares later positions, and its fp32
+  // sums would be less good than kBorder asks for), and whole rounds of what verify_accept holds (up to 4 units:
+  // with fewer, S L rows would be 1024 chunks or less of 2 units or less, and S (L + 1) V below 2^23: direct);
+  // steps 2 and 3: what a thread holds at once
+  chunking(S * P, V, 1024, w.direct ? 1 : 4, 8, w.direct, w.chunk1, w.K1);
+  chunking(S, V, 1280, 1, 4, true, w.chunk2, w.K2);
   size_t off = 0;
   char* p = static_cast<char*>(base);
   auto take = [&](size_t bytes) {

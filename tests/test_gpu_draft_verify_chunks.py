@@ -71,3 +71,52 @@ def test_long_chunks_of_a_few_rows(S, L, V, dt, with_draft):
     c = plain.Case(103 + S, lens, V, dt, with_draft, max_draft=L)
     c.ua[::3] = np.float32(0.9999)
     plain.check(c, f"long chunks {S} {dt} {with_draft}")
+
+
+def two_levels(rows, V, level):
+    """bf16 logits of 0 at every eighth token and `level` elsewhere: added up in one place in fp32, their exponentials
+    are rounded the same way every time."""
+    t = torch.full((rows, V), level, dtype=torch.bfloat16, device=plain.DEV)
+    t[:, ::8] = 0.0
+    return t
+
+
+def of_two_levels(V, level):
+    """The sum of the exponentials."""
+    return V / 8 * (1.0 + 7.0 * np.exp(level))
+
+
+def call(z, u, token, r, w):
+    V, dev = z.shape[1], plain.DEV
+    n, tok, lp = (torch.full(s, 99, dtype=t, device=dev) for s, t in
+                  (((1,), torch.int64), ((1, 2), torch.int64), ((1, 2), torch.float32)))
+    plain.lx.lx_draft_verify(z, u, torch.tensor([token], device=dev), torch.tensor([0, 1], device=dev), 1, None,
+                             torch.tensor([r], dtype=torch.float32, device=dev),
+                             torch.tensor([w], dtype=torch.float32, device=dev), n, tok, lp)
+    return n.item(), tok[0].tolist(), lp[0].tolist()
+
+
+def test_log_p_of_a_very_long_row():
+    plain.announce("draft_verify log p, V 2^28")
+    V, level = 1 << 28, -1 / 128
+    n, tok, lp = call(two_levels(2, V, level), two_levels(1, V, level), 8 * 12345, 0.5, 0.5)
+    assert n == 1 and tok[0] == 8 * 12345
+    assert abs(lp[0] + np.log(of_two_levels(V, level))) <= plain.TOL_LOGP
+    assert abs(lp[1] + np.log(of_two_levels(V, level)) - (level if tok[1] % 8 else 0.0)) <= plain.TOL_LOGP
+
+
+def test_acceptance_over_a_very_long_row():
+    """r beyond p / q, and below it, by 2^-17."""
+    plain.announce("draft_verify acceptance, V 2^30")
+    V, zl, ul, w = (1 << 30) - 40, -1 / 64, -87 / 128, 0.3
+    z, u = two_levels(2, V, zl), two_levels(1, V, ul)
+    St, Sd = of_two_levels(V, zl), of_two_levels(V, ul)
+    ratio = Sd / St
+    n, tok, lp = call(z, u, 800, ratio * (1 - 2.0 ** -17), w)
+    assert n == 1 and tok[0] == 800 and abs(lp[0] + np.log(St)) <= plain.TOL_LOGP
+    n, tok, lp = call(z, u, 800, ratio * (1 + 2.0 ** -17), w)
+    # max(p - q, 0) is the same at every token but the eighths: the one at w of them
+    k = float(np.float32(w)) * (V // 8 * 7)
+    assert 0.4 < k % 1 < 0.6
+    assert n == 0 and tok == [int(k) // 7 * 8 + int(k) % 7 + 1, -1]
+    assert abs(lp[0] + np.log(St) - zl) <= plain.TOL_LOGP
