@@ -112,6 +112,16 @@ def _load() -> ctypes.CDLL:
     L.lx_lora_backward.argtypes = [p, i64, p, i64, p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, p, i64, p, i64, p, p, p,
                                    sz, p]
     L.lx_lora_backward.restype = i32
+    for name in ("lx_ce_kd_workspace_bytes", "lx_ce_kd_forward_backward_workspace_bytes"):
+        getattr(L, name).argtypes = [i64, i64, i32]
+        getattr(L, name).restype = sz
+    L.lx_ce_kd_forward.argtypes = [p, i64, p, p, p, p, i64, i64, i64, i64, f32, p, p, p, p, i32, p, sz, p]
+    L.lx_ce_kd_forward.restype = i32
+    L.lx_ce_kd_backward.argtypes = [p, i64, p, i64, p, p, p, i64, i64, i64, i64, f32, p, p, f32, f32, p, p, p, i32, p]
+    L.lx_ce_kd_backward.restype = i32
+    L.lx_ce_kd_forward_backward.argtypes = [p, i64, p, p, p, p, i64, i64, i64, i64, f32, p, p, p, p, p, i64, f32, f32, p, p,
+                                            p, i32, p, sz, p]
+    L.lx_ce_kd_forward_backward.restype = i32
     return L
 
 
@@ -609,6 +619,90 @@ def lx_lora_backward(grad_y, x, A, B, adapter, req_start, scale, rank, base, gra
                "lx_lora_backward")
 
 
+LX_KD_MAX_TOP, LX_KD_STATE_FLOATS = 256, 4
+
+
+def _kd_set(student, target, ids, top, lse_rest, per_row, state, grad=None):
+    """(BT, V, K, dtype code, device, student's row stride, grad's) of the arguments that the entry points over
+    logits share, checked; ``per_row``: (name, float32 [BT] tensor or None) pairs."""
+    BT, V, ld = _rows2d(student, "student")
+    dt, dev, f32 = _dtype_code(student), student.device, torch.float32
+    K = ids.shape[1] if ids.dim() == 2 else 0
+    _arg(target, "target", torch.int64, (BT,), dev)
+    _arg(ids, "ids", torch.int32, (BT, K), dev)
+    _arg(top, "top", f32, (BT, K), dev)
+    if lse_rest is not None:
+        _arg(lse_rest, "lse_rest", f32, (BT,), dev)
+    for name, t in per_row:
+        if t is not None:
+            _arg(t, name, f32, (BT,), dev)
+    _arg(state, "state", f32, (BT, LX_KD_STATE_FLOATS), dev)
+    ldg = V
+    if grad is not None:
+        if grad.shape != student.shape or grad.dtype != student.dtype or grad.device != dev:
+            raise ValueError("grad must match student in shape and dtype and lie on its device")
+        ldg = _rows2d(grad, "grad")[2]
+    return BT, V, K, dt, dev, ld, ldg
+
+
+def _scale_ptr(g_scale, dev):
+    if g_scale is None:
+        return None
+    if g_scale.dtype is not torch.float32 or g_scale.numel() != 1 or g_scale.device != dev:
+        raise ValueError(f"g_scale must be one float32 on {dev}")
+    return g_scale.data_ptr()
+
+
+def lx_ce_kd_workspace_bytes(BT: int, V: int, dt: int) -> int:
+    return lib.lx_ce_kd_workspace_bytes(BT, V, dt)
+
+
+def lx_ce_kd_forward_backward_workspace_bytes(BT: int, V: int, dt: int) -> int:
+    return lib.lx_ce_kd_forward_backward_workspace_bytes(BT, V, dt)
+
+
+def lx_ce_kd_forward(student, target, ignore_index, ids, top, lse_rest, temperature: float, ce, kd, lse, state,
+                     workspace=None, stream=None) -> None:
+    """Cross entropy and the divergence from a teacher's top logits: ``student`` (BT, V) with contiguous rows;
+    ``ids`` int32 and ``top`` float32 (BT, K), ``lse_rest`` float32 [BT] or None, as lx_top_logits writes them;
+    into ``ce``, ``kd``, ``lse`` float32 [BT] and ``state`` float32 [BT, 4].  The workspace (uint8 device
+    tensor) is allocated here with torch when not given."""
+    BT, V, K, dt, dev, ld, _ = _kd_set(student, target, ids, top, lse_rest, (("ce", ce), ("kd", kd), ("lse", lse)), state)
+    with _Launch(dev, stream) as at:
+        ws, wbytes, _held = at.workspace(workspace, lib.lx_ce_kd_workspace_bytes(BT, V, dt))
+        _check(lib.lx_ce_kd_forward(_ptr(student), ld, _ptr(target), _ptr(ids), _ptr(top), _ptr(lse_rest), BT, V, K,
+                                    int(ignore_index), float(temperature), _ptr(ce), _ptr(kd), _ptr(lse), _ptr(state), dt,
+                                    ws, wbytes, at.ptr), "lx_ce_kd_forward")
+
+
+def lx_ce_kd_backward(grad, student, target, ignore_index, ids, top, temperature: float, lse, state, g_ce: float,
+                      g_kd: float, grad_ce_rows=None, grad_kd_rows=None, g_scale=None, stream=None) -> None:
+    """The gradient of g_ce ce + g_kd kd into ``grad`` (may be ``student``), from lx_ce_kd_forward's ``lse`` and
+    ``state``; ``grad_ce_rows``, ``grad_kd_rows`` float32 [BT] factors or None, ``g_scale`` one float32 or None."""
+    BT, V, K, dt, dev, ld, ldg = _kd_set(student, target, ids, top, None, (
+        ("lse", lse), ("grad_ce_rows", grad_ce_rows), ("grad_kd_rows", grad_kd_rows)), state, grad)
+    with _Launch(dev, stream) as at:
+        _check(lib.lx_ce_kd_backward(_ptr(grad), ldg, _ptr(student), ld, _ptr(target), _ptr(ids), _ptr(top), BT, V, K,
+                                     int(ignore_index), float(temperature), _ptr(lse), _ptr(state), float(g_ce), float(g_kd),
+                                     _ptr(grad_ce_rows), _ptr(grad_kd_rows), _scale_ptr(g_scale, dev), dt, at.ptr),
+               "lx_ce_kd_backward")
+
+
+def lx_ce_kd_forward_backward(student, target, ignore_index, ids, top, lse_rest, temperature: float, ce, kd, lse, state,
+                              grad, g_ce: float, g_kd: float, grad_ce_rows=None, grad_kd_rows=None, g_scale=None,
+                              workspace=None, stream=None) -> None:
+    """lx_ce_kd_forward and lx_ce_kd_backward in one call (``grad`` may be ``student``)."""
+    BT, V, K, dt, dev, ld, ldg = _kd_set(student, target, ids, top, lse_rest, (
+        ("ce", ce), ("kd", kd), ("lse", lse), ("grad_ce_rows", grad_ce_rows), ("grad_kd_rows", grad_kd_rows)), state, grad)
+    with _Launch(dev, stream) as at:
+        ws, wbytes, _held = at.workspace(workspace, lib.lx_ce_kd_forward_backward_workspace_bytes(BT, V, dt))
+        _check(lib.lx_ce_kd_forward_backward(_ptr(student), ld, _ptr(target), _ptr(ids), _ptr(top), _ptr(lse_rest), BT, V, K,
+                                             int(ignore_index), float(temperature), _ptr(ce), _ptr(kd), _ptr(lse),
+                                             _ptr(state), _ptr(grad), ldg, float(g_ce), float(g_kd), _ptr(grad_ce_rows),
+                                             _ptr(grad_kd_rows), _scale_ptr(g_scale, dev), dt, ws, wbytes, at.ptr),
+               "lx_ce_kd_forward_backward")
+
+
 __all__ = [
     "LxError", "lib", "LIB_PATH", "LX_OK", "LX_ERR_INVALID_ARG", "LX_ERR_UNSUPPORTED_DTYPE", "LX_ERR_ALIAS",
     "LX_ERR_WORKSPACE", "LX_ERR_HIP", "LX_F32", "LX_BF16", "LX_F16", "lx_status_string", "lx_abi_version",
@@ -618,7 +712,9 @@ __all__ = [
     "lx_ce_tvd_backward_shard", "lx_ce_tvd_forward_ex", "lx_ce_tvd_backward_ex", "lx_ce_tvd_forward_backward_ex",
     "lx_gemm_bf16", "lx_ce_tvd_linear_workspace_bytes", "lx_ce_tvd_linear_forward_backward",
     "lx_draft_verify_workspace_bytes", "lx_draft_verify", "lx_lora_forward_workspace_bytes", "lx_lora_forward",
-    "lx_lora_backward_workspace_bytes", "lx_lora_backward",
+    "lx_lora_backward_workspace_bytes", "lx_lora_backward", "LX_KD_MAX_TOP", "LX_KD_STATE_FLOATS",
+    "lx_ce_kd_workspace_bytes", "lx_ce_kd_forward", "lx_ce_kd_backward", "lx_ce_kd_forward_backward_workspace_bytes",
+    "lx_ce_kd_forward_backward",
 ]
 
 

@@ -4,6 +4,7 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include "distill.hpp"
 #include "gemm.hpp"
 #include "launch.hpp"
 #include "linear.hpp"
@@ -317,6 +318,67 @@ bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld % 8 == 0 && ld <=
 bool lora_set_ok(const lx::LoraSet& s) {
   return s.A && s.B && s.adapter && s.start && s.scale && aligned(s.A, 16) && aligned(s.B, 16) && aligned(s.adapter, 8) &&
          aligned(s.start, 8) && aligned(s.scale, 4) && aligned(s.rank, 8);
+}
+
+// What the entry points of the distillation from top logits share: the loss's sizes, its pointers and
+// their spans.
+// 2^-10 to 2^10, by its bits (positive floats are ordered as integers are): these sources are compiled without
+// NaNs, and a comparison could let one through
+bool temperature_ok(float t) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, t);
+  return b >= 0x3a800000u && b <= 0x44800000u;
+}
+// workgroups of at least 4096 columns, counted within the rows of a cut grid
+bool kd_shape_ok(int64_t BT, int64_t V) { return BT <= ((int64_t)1 << 34) / ((V + 4095) / 4096); }
+
+lx_status kd_check(const lx::KdLoss& l, bool outputs) {
+  if (l.K < 1 || l.K > LX_KD_MAX_TOP || !temperature_ok(l.temperature) || !kd_shape_ok(l.BT, l.V)) return LX_ERR_INVALID_ARG;
+  if (!l.target || !l.ids || !l.top || !l.lse || !l.state || (outputs && (!l.ce || !l.kd))) return LX_ERR_INVALID_ARG;
+  if (!aligned(l.target, 8) || !aligned(l.ids, 4) || !aligned(l.top, 4) || !aligned(l.rest, 4) || !aligned(l.ce, 4) ||
+      !aligned(l.kd, 4) || !aligned(l.lse, 4) || !aligned(l.state, 16))
+    return LX_ERR_INVALID_ARG;
+  return LX_OK;
+}
+bool kd_grad_ok(const lx::KdGrad& g) { return aligned(g.ce_rows, 4) && aligned(g.kd_rows, 4) && aligned(g.g_scale, 4); }
+
+// outs overlap nothing; ins may overlap each other
+bool outputs_clear(const Span* outs, int n_out, const Span* ins, int n_in) {
+  if (any_overlap(outs, n_out)) return false;
+  for (int o = 0; o < n_out; ++o)
+    for (int i = 0; i < n_in; ++i)
+      if (overlaps(outs[o], ins[i])) return false;
+  return true;
+}
+
+// backward: l.lse and l.state are inputs, and ce, kd are absent
+lx_status kd_impl(lx::KdArgs& a, lx_dtype dt, bool forward, bool backward, size_t need, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  const int es = esize_of(dt);
+  if (!es) return LX_ERR_UNSUPPORTED_DTYPE;
+  if (lx_status s = check_shape(a.l.BT, a.l.V, es)) return s;
+  if (a.l.BT == 0) return LX_OK;
+  if (lx_status s = kd_check(a.l, forward)) return s;
+  const int64_t BT = a.l.BT, V = a.l.V, fb = BT * 4;
+  if (!stride_ok(BT, V, a.ldz, es) || (backward && !stride_ok(BT, V, a.ldg, es))) return LX_ERR_INVALID_ARG;
+  if (!a.z || !aligned(a.z, es) || (backward && (!a.grad || !aligned(a.grad, es))) || !kd_grad_ok(a.g))
+    return LX_ERR_INVALID_ARG;
+  const Span z = span(a.z, strided_bytes(BT, V, a.ldz, es));
+  const Span grad = span(backward ? a.grad : nullptr, backward ? strided_bytes(BT, V, a.ldg, es) : 0);
+  const bool in_place = backward && a.grad == a.z && a.ldg == a.ldz;
+  const Span lse = span(a.l.lse, fb), state = span(a.l.state, fb * lx::kKdState);
+  const Span none{0, 0};
+  const Span outs[6] = {grad, span(a.l.ce, fb), span(a.l.kd, fb), forward ? lse : none, forward ? state : none,
+                        span(need ? workspace : nullptr, (int64_t)need)};
+  const Span ins[10] = {in_place ? none : z, span(a.l.target, BT * 8), span(a.l.ids, BT * a.l.K * 4),
+                        span(a.l.top, BT * a.l.K * 4), span(a.l.rest, fb), span(a.g.ce_rows, fb), span(a.g.kd_rows, fb),
+                        span(a.g.g_scale, 4), forward ? none : lse, forward ? none : state};
+  if (!outputs_clear(outs, 6, ins, 10)) return LX_ERR_ALIAS;
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return LX_ERR_WORKSPACE;
+  a.workspace = workspace;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const lx::Dt t = dt_of(dt);
+  if (forward && backward) return from_hip(lx::launch_kd_step(a, t, st));
+  return from_hip(forward ? lx::launch_kd_forward(a, t, st) : lx::launch_kd_backward(a, t, st));
 }
 
 }  // namespace
@@ -790,6 +852,63 @@ lx_status lx_lora_backward(const void* grad_y, int64_t ld_grad_y, const void* x,
   const lx::LoraBackwardArgs a{s, static_cast<const uint16_t*>(grad_y), static_cast<const uint16_t*>(x), ld_grad_y, ldx,
                                base, ld_base, grad_x, ld_grad_x, grad_A, grad_B, workspace};
   return from_hip(lx::launch_lora_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t lx_ce_kd_workspace_bytes(int64_t BT, int64_t V, lx_dtype dt) {
+  const int es = esize_of(dt);
+  if (!es || check_shape(BT, V, es) || BT == 0 || !kd_shape_ok(BT, V)) return 0;
+  return lx::kd_forward_workspace_bytes(BT, V);
+}
+
+lx_status lx_ce_kd_forward(const void* student, int64_t ld_student, const int64_t* target, const int32_t* ids,
+                           const float* top, const float* lse_rest, int64_t BT, int64_t V, int64_t K,
+                           int64_t ignore_index, float temperature, float* ce, float* kd, float* lse, float* state,
+                           lx_dtype dt, void* workspace, size_t workspace_bytes, void* stream) {
+  lx::KdArgs a{};
+  a.l = lx::KdLoss{target, ignore_index, ids, top, lse_rest, BT, V, K, temperature, ce, kd, lse, state};
+  a.z = student;
+  a.ldz = ld_student;
+  return kd_impl(a, dt, true, false, lx_ce_kd_workspace_bytes(BT, V, dt), workspace, workspace_bytes, stream);
+}
+
+lx_status lx_ce_kd_backward(void* grad, int64_t ld_grad, const void* student, int64_t ld_student,
+                            const int64_t* target, const int32_t* ids, const float* top, int64_t BT, int64_t V,
+                            int64_t K, int64_t ignore_index, float temperature, const float* lse, const float* state,
+                            float g_ce, float g_kd, const float* grad_ce_rows, const float* grad_kd_rows,
+                            const float* g_scale, lx_dtype dt, void* stream) {
+  lx::KdArgs a{};
+  a.l = lx::KdLoss{target, ignore_index, ids, top, nullptr, BT, V, K, temperature, nullptr, nullptr,
+                   const_cast<float*>(lse), const_cast<float*>(state)};
+  a.z = student;
+  a.ldz = ld_student;
+  a.grad = grad;
+  a.ldg = ld_grad;
+  a.g = lx::KdGrad{g_ce, g_kd, grad_ce_rows, grad_kd_rows, g_scale};
+  return kd_impl(a, dt, false, true, 0, nullptr, 0, stream);
+}
+
+size_t lx_ce_kd_forward_backward_workspace_bytes(int64_t BT, int64_t V, lx_dtype dt) {
+  const int es = esize_of(dt);
+  if (!es || check_shape(BT, V, es) || BT == 0 || !kd_shape_ok(BT, V)) return 0;
+  return lx::kd_step_workspace_bytes(BT, V);
+}
+
+lx_status lx_ce_kd_forward_backward(const void* student, int64_t ld_student, const int64_t* target,
+                                    const int32_t* ids, const float* top, const float* lse_rest, int64_t BT,
+                                    int64_t V, int64_t K, int64_t ignore_index, float temperature, float* ce,
+                                    float* kd, float* lse, float* state, void* grad, int64_t ld_grad, float g_ce,
+                                    float g_kd, const float* grad_ce_rows, const float* grad_kd_rows,
+                                    const float* g_scale, lx_dtype dt, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  lx::KdArgs a{};
+  a.l = lx::KdLoss{target, ignore_index, ids, top, lse_rest, BT, V, K, temperature, ce, kd, lse, state};
+  a.z = student;
+  a.ldz = ld_student;
+  a.grad = grad;
+  a.ldg = ld_grad;
+  a.g = lx::KdGrad{g_ce, g_kd, grad_ce_rows, grad_kd_rows, g_scale};
+  return kd_impl(a, dt, true, true, lx_ce_kd_forward_backward_workspace_bytes(BT, V, dt), workspace, workspace_bytes,
+                 stream);
 }
 
 }  // extern "C"

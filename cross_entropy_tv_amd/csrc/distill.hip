@@ -1,0 +1,561 @@
+// Cross entropy and distillation from a teacher's top logits, over student logits: forward, backward
+// and both in one pass.
+//
+// With p = softmax(z / T) and the teacher's q (kd_row.hpp), for the columns named by the teacher's ids
+// and for all others
+//
+//   d kd / dz_v = (p_v - q_v) / T                               v among the ids
+//               = e_v (p_r - q_r) / T,  e_v = exp(z_v / T - lse_rest)   v outside
+//
+// (e_v is p_v / p_r: formed from the outside's own log-sum it never divides by a p_r that has
+// vanished), and ce's gradient p1_v - [v == t] is added, p1 = softmax(z).  At T = 1 p1_v = p_r e_v
+// outside, so one exponential an element serves both.
+//
+// What bounds them: reading the logits once (forward), reading and writing them once (backward, one
+// pass).  The ids are K of up to 10^5 columns; which groups of 8 hold one is a byte of a bit mask in LDS
+// that each workgroup sets for its columns, read beside the group, so that a group without one (all but
+// a few in a thousand) costs a compare.
+//
+// Sums of exponentials are taken against an integer exponent n per thread, sum 2^(c z - n): c z - n is
+// one fused multiply-add with no rounding of the reference.  n comes from the thread's first group; a sum
+// that reaches 2^100 is redone against the true maximum.
+#include "common.hpp"
+#include "distill.hpp"
+#include "kd_row.hpp"
+
+namespace lx {
+
+namespace {
+
+// ------------------------------------------------------------------ sums of 2^(c x - n)
+
+struct Sum2 {
+  float n, s;
+};
+
+// The smallest reference: a masked logit's c x lies below it, so its power of two is 0 against any.
+__device__ __forceinline__ float floor_of(float c) { return kMasked * c; }
+__device__ __forceinline__ float ref_for(float m, float c) { return fmaxf(__builtin_rintf(m * c), floor_of(c)); }
+
+__device__ __forceinline__ void sum8(const float (&x)[8], float c, float n, float& s0, float& s1) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    s0 += exp2_hw(__builtin_fmaf(x[e], c, -n));
+    s1 += exp2_hw(__builtin_fmaf(x[e + 1], c, -n));
+  }
+}
+
+__device__ __forceinline__ Sum2 wave_sum2(Sum2 a) {
+  const float n = wave_max(a.n);
+  return Sum2{n, wave_sum32(a.s * exp2_hw(a.n - n))};
+}
+__device__ __forceinline__ void add_sum2(Sum2& a, const Sum2& b) {
+  const float n = fmaxf(a.n, b.n);
+  a.s = a.s * exp2_hw(a.n - n) + b.s * exp2_hw(b.n - n);
+  a.n = n;
+}
+// log2 of the sum, -inf without any
+__device__ __forceinline__ double log2_of(const Sum2& a) {
+  return a.s > 0.0f ? (double)a.n + log2_64((double)a.s) : -kInf64;
+}
+
+// The logits of the columns whose bit is set count as masked.
+__device__ __forceinline__ void leave_out_bits(uint32_t byte, float (&x)[8]) {
+  if (byte) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (byte >> e) & 1u ? ninf() : x[e];
+  }
+}
+
+// ------------------------------------------------------------------ the teacher's entries in LDS
+
+struct Entries {
+  int id[kKdMaxTop];    // -1: left out
+  float u[kKdMaxTop];
+  float z[kKdMaxTop];   // the student's logit there, -inf where masked
+};
+
+// Entry j of row r as thread j < K takes it; id -1 where it is left out, bad where its id is past the
+// vocabulary.
+__device__ __forceinline__ int entry_id(const KdLoss& l, int64_t r, int j, float& u, bool& bad) {
+  const int v = l.ids[r * l.K + j];
+  u = l.top[r * l.K + j];
+  bad = v >= l.V;
+  return bad || v < 0 || u < kMasked ? -1 : v;
+}
+
+// ------------------------------------------------------------------ forward
+
+// Rows of up to 2^18 columns are one workgroup's (its mask is 32 KB); 512 threads, H groups at once.
+constexpr int kFwdThreads = 512;
+constexpr int kFwdHeld = 4;
+constexpr int64_t kMaxChunk = 1 << 18;
+constexpr int64_t kMinChunk = 4096;
+constexpr int64_t kWantedChunks = 1024;
+
+// Chunks of a row.  A workgroup a row while rows fill the GPU; few rows are cut so that about 1024
+// workgroups run.
+struct Split {
+  int64_t chunks, columns;
+};
+Split split_of(int64_t BT, int64_t V) {
+  int64_t s = (kWantedChunks + BT - 1) / BT;
+  if (BT >= kWantedChunks / 2) s = 1;
+  if (s > V / kMinChunk) s = V / kMinChunk;
+  const int64_t fit = (V + kMaxChunk - 1) / kMaxChunk;
+  if (s < fit) s = fit;
+  if (s < 1) s = 1;
+  constexpr int64_t unit = kFwdThreads * 8;
+  const int64_t columns = ((V + s - 1) / s + unit - 1) / unit * unit;
+  return Split{(V + columns - 1) / columns, columns};
+}
+
+// Outside-the-ids sums of the columns [lo, hi) of a row (and, TEMP, sums at temperature 1 of all of
+// them), this thread's share.
+template <typename T, bool TEMP, int NT, int H>
+__device__ __forceinline__ void chunk_sums(const T* row, int64_t lo, int64_t hi, int64_t V, const uint8_t* mask,
+                                           float c, Sum2& a, Sum2& a1) {
+  a = Sum2{floor_of(c), 0.0f};
+  a1 = Sum2{floor_of(kLog2e), 0.0f};
+  bool first = true;
+  for (int64_t b = lo; b < hi; b += (int64_t)NT * 8 * H) {
+    Group<T> g[H];
+    uint32_t byte[H];
+    if (V >= 8) {
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        const int64_t v = b + k * (NT * 8) + tid_x() * 8;
+        g[k].load(row + (v < V - 8 ? v : V - 8));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      const int64_t v = b + k * (NT * 8) + tid_x() * 8;
+      byte[k] = v < hi ? mask[(v - lo) >> 3] : 0u;
+    }
+    // the group's logits; -inf behind the chunk's end
+    auto get = [&](int k, float(&x)[8]) {
+      const int64_t v = b + k * (NT * 8) + tid_x() * 8;
+      launder(g[k]);
+      if (v + 8 <= hi) {
+        g[k].get(x);
+      } else {
+        load_edge(row, v, hi, x);
+      }
+    };
+    if (first) {
+      float x[8];
+      get(0, x);
+      a1.n = ref_for(max8(x), kLog2e);
+      leave_out_bits(byte[0], x);
+      a.n = ref_for(max8(x), c);
+      first = false;
+    }
+    float b0 = 0.0f, b1 = 0.0f, c0 = 0.0f, c1 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      float x[8];
+      get(k, x);
+      if (TEMP) sum8(x, kLog2e, a1.n, c0, c1);
+      leave_out_bits(byte[k], x);
+      sum8(x, c, a.n, b0, b1);
+    }
+    if (fmaxf(b0 + b1, c0 + c1) >= kRefSumLimit) {  // again, against the true maxima
+      float m = ninf(), m1 = ninf();
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        float x[8];
+        get(k, x);
+        m1 = fmaxf(m1, max8(x));
+        leave_out_bits(byte[k], x);
+        m = fmaxf(m, max8(x));
+      }
+      const float n = fmaxf(a.n, ref_for(m, c)), n1 = fmaxf(a1.n, ref_for(m1, kLog2e));
+      a = Sum2{n, a.s * exp2_hw(a.n - n)};
+      a1 = Sum2{n1, a1.s * exp2_hw(a1.n - n1)};
+      b0 = b1 = c0 = c1 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        float x[8];
+        get(k, x);
+        if (TEMP) sum8(x, kLog2e, a1.n, c0, c1);
+        leave_out_bits(byte[k], x);
+        sum8(x, c, a.n, b0, b1);
+      }
+    }
+    a.s += b0 + b1;
+    if (TEMP) a1.s += c0 + c1;
+  }
+}
+
+__device__ __forceinline__ void store_state(float* state, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(state) = make_float4(a, b, c, d);
+}
+
+// Wave 0, all lanes: the row's outputs from its sums and entries.  z_t: the target's logit.
+template <bool TEMP>
+__device__ __forceinline__ void finish_row(const KdLoss& l, int64_t r, const Entries& en, bool bad, int64_t t, float zt,
+                                           double c, const Sum2& a, const Sum2& a1) {
+  const int lane = tid_x() & 63, K = (int)l.K;
+  double ua[kLaneTop], q[kLaneTop];
+  const Teacher te = teacher_of(en.id, en.u, K, lane, c, l.rest ? l.rest[r] : ninf(), ua, q);
+  const double lr = log2_of(a);
+  double t2[kLaneTop], m = lr;
+#pragma unroll
+  for (int k = 0; k < kLaneTop; ++k) {
+    const int j = lane + 64 * k;
+    const bool here = j < K && en.id[j] >= 0;
+    t2[k] = here && !(en.z[j] < kMasked) ? (double)en.z[j] * c : -kInf64;
+    m = __builtin_fmax(m, t2[k]);
+  }
+  m = wave_max64(m);
+  const double ref = m > -kInf64 ? m : 0.0;
+  double s = 0.0, terms = 0.0;
+#pragma unroll
+  for (int k = 0; k < kLaneTop; ++k) {
+    const int j = lane + 64 * k;
+    if (j < K && en.id[j] >= 0) {
+      if (!named_before(en.id, j)) s += exp2_64(t2[k] - ref);
+      if (q[k] > 0.0) terms += q[k] * (ua[k] - t2[k]);
+    }
+  }
+  s = wave_sum64(s) + exp2_64(lr - ref);
+  terms = wave_sum64(terms);
+  if (lane != 0) return;
+  if (!(m > -kInf64)) {  // no unmasked logit
+    l.ce[r] = 0.0f;
+    l.kd[r] = 0.0f;
+    l.lse[r] = ninf();
+    store_state(l.state + kKdState * r, ninf(), 0.0f, 0.0f, 0.0f);
+    return;
+  }
+  const double lz = ref + log2_64(s);
+  const RowOut o = row_out(te, terms, lz, lr);
+  const double l1 = TEMP ? log2_of(a1) * kLn2 : lz * kLn2;
+  l.lse[r] = (float)l1;
+  if (t >= 0 && t < l.V) l.ce[r] = zt < kMasked ? -ninf() : (float)(l1 - (double)zt);
+  else store_nan(l.ce + r);
+  if (bad) store_nan(l.kd + r);
+  else l.kd[r] = o.kd;
+  store_state(l.state + kKdState * r, o.lse_t, o.lse_rest, o.off, o.norm);
+}
+
+__device__ __forceinline__ void ignored_row(const KdLoss& l, int64_t r) {
+  l.ce[r] = 0.0f;
+  l.kd[r] = 0.0f;
+  l.lse[r] = 0.0f;
+  store_state(l.state + kKdState * r, 0.0f, 0.0f, 0.0f, 0.0f);
+}
+
+// One workgroup per (row, chunk).  A whole row (chunks == 1) is finished here; chunks leave their sums
+// in parts [row][chunk][4].
+template <typename T, bool TEMP>
+__global__ __launch_bounds__(kFwdThreads) void kd_forward_kernel(KdLoss l, const T* __restrict__ z, int64_t ldz,
+                                                                 double c64, int chunks, int64_t columns, float* parts) {
+  extern __shared__ uint32_t bits[];
+  constexpr int W = kFwdThreads / 64;
+  __shared__ Entries en;
+  __shared__ Sum2 red[2][W];
+  __shared__ int bad_any;
+  const int64_t tile = large_bid();
+  const int64_t r = tile / chunks;
+  if (r >= l.BT) return;
+  const int ch = (int)(tile - r * chunks), tid = tid_x();
+  const int64_t t = l.target[r];
+  if (t == l.ignore_index) {
+    if (ch == 0 && tid == 0) ignored_row(l, r);
+    return;
+  }
+  const int K = (int)l.K;
+  const int64_t lo = ch * columns, hi = l.V < lo + columns ? l.V : lo + columns;
+  const T* row = z + r * ldz;
+  const float c = (float)c64;
+  if (tid == 0) bad_any = 0;
+  for (int w = tid; w < (int)(columns / 32); w += kFwdThreads) bits[w] = 0u;
+  __syncthreads();
+  float zj = ninf(), zt = 0.0f;
+  if (tid < K) {
+    float u;
+    bool bad;
+    const int v = entry_id(l, r, tid, u, bad);
+    en.id[tid] = v;
+    en.u[tid] = u;
+    if (bad) bad_any = 1;
+    if (v >= 0) {
+      mark(bits, v, lo, hi);
+      if (chunks == 1) zj = load1(row + v);
+    }
+  }
+  if (chunks == 1 && tid == 0 && t >= 0 && t < l.V) zt = load1(row + t);
+  __syncthreads();
+  Sum2 a, a1;
+  chunk_sums<T, TEMP, kFwdThreads, kFwdHeld>(row, lo, hi, l.V, reinterpret_cast<const uint8_t*>(bits), c, a, a1);
+  a = wave_sum2(a);
+  if (TEMP) a1 = wave_sum2(a1);
+  if ((tid & 63) == 0) {
+    red[0][tid >> 6] = a;
+    red[1][tid >> 6] = a1;
+  }
+  if (tid < K) en.z[tid] = zj;
+  __syncthreads();
+  if (tid >= 64) return;
+  a = red[0][0];
+  a1 = red[1][0];
+  for (int w = 1; w < W; ++w) {
+    add_sum2(a, red[0][w]);
+    if (TEMP) add_sum2(a1, red[1][w]);
+  }
+  if (chunks > 1) {
+    if (tid == 0) store_state(parts + 4 * tile, a.n, a.s, a1.n, a1.s);
+    return;
+  }
+  finish_row<TEMP>(l, r, en, bad_any != 0, t, zt, c64, a, a1);
+}
+
+// Rows cut into chunks: a wave a row joins its chunks' sums, lane by lane and then the lanes, in a fixed
+// order.
+template <typename T, bool TEMP>
+__global__ __launch_bounds__(64) void kd_finish_kernel(KdLoss l, const T* __restrict__ z, int64_t ldz, double c64,
+                                                       int chunks, const float* __restrict__ parts) {
+  __shared__ Entries en;
+  const int64_t r = large_bid();
+  if (r >= l.BT) return;
+  const int64_t t = l.target[r];
+  if (t == l.ignore_index) return;
+  const int lane = tid_x(), K = (int)l.K;
+  const T* row = z + r * ldz;
+  bool bad_any = false;
+  for (int j = lane; j < K; j += 64) {
+    float u;
+    bool bad;
+    const int v = entry_id(l, r, j, u, bad);
+    bad_any |= bad;
+    en.id[j] = v;
+    en.u[j] = u;
+    en.z[j] = v >= 0 ? load1(row + v) : ninf();
+  }
+  const float zt = t >= 0 && t < l.V ? load1(row + t) : 0.0f;
+  Sum2 a{floor_of((float)c64), 0.0f}, a1{floor_of(kLog2e), 0.0f};
+  for (int k = lane; k < chunks; k += 64) {
+    const float4 p = *reinterpret_cast<const float4*>(parts + 4 * (r * chunks + k));
+    add_sum2(a, Sum2{p.x, p.y});
+    if (TEMP) add_sum2(a1, Sum2{p.z, p.w});
+  }
+  a = wave_sum2(a);
+  if (TEMP) a1 = wave_sum2(a1);
+  __syncthreads();
+  finish_row<TEMP>(l, r, en, __any(bad_any), t, zt, c64, a, a1);
+}
+
+template <typename T, bool TEMP>
+hipError_t launch_kd_forward_t(const KdArgs& a, double c64, hipStream_t st) {
+  const Split s = split_of(a.l.BT, a.l.V);
+  const T* z = static_cast<const T*>(a.z);
+  float* parts = static_cast<float*>(a.workspace);
+  (void)hipGetLastError();
+  kd_forward_kernel<T, TEMP><<<large_grid(a.l.BT * s.chunks), dim3(kFwdThreads), (size_t)(s.columns / 8), st>>>(
+      a.l, z, a.ldz, c64, (int)s.chunks, s.columns, parts);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (s.chunks == 1) return hipSuccess;
+  kd_finish_kernel<T, TEMP><<<large_grid(a.l.BT), dim3(64), 0, st>>>(a.l, z, a.ldz, c64, (int)s.chunks, parts);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ the gradient of a row's columns
+
+// What the gradient of a row needs, in fp32 (uniform).
+struct RowGrad {
+  float kce, kkd;     // k g_ce, k g_kd / T, with the row's factors
+  float n1;           // lse log2 e
+  float nz, nr, nq;   // log-sums (base 2): student at T, its outside, the teacher's
+  float out;          // outside: factor of 2^(c z - nr); at T = 1 with ce's part
+};
+
+template <bool TEMP>
+__device__ __forceinline__ RowGrad row_grad(const KdGrad& g, const KdLoss& l, int64_t r, float lse, float lse_t,
+                                            float lse_rest, float off, float norm) {
+  const float k = g.g_scale ? *g.g_scale : 1.0f;
+  RowGrad o;
+  o.kce = k * g.g_ce * (g.ce_rows ? g.ce_rows[r] : 1.0f);
+  o.kkd = k * g.g_kd * (g.kd_rows ? g.kd_rows[r] : 1.0f) / l.temperature;
+  o.n1 = lse * kLog2e;
+  o.nz = lse_t * kLog2e;
+  o.nr = lse_rest * kLog2e;
+  o.nq = norm * kLog2e;
+  o.out = o.kkd * off;
+  // (without anything outside, lse_rest is 0 and every such logit masked: the factor only has to be finite)
+  if (!TEMP) o.out += o.kce * fminf(exp2_hw(o.nr - o.nz), 1.0f);
+  return o;
+}
+
+// The gradient at a column outside the ids.
+template <bool TEMP>
+__device__ __forceinline__ float grad_outside(const RowGrad& g, float x, float c) {
+  const float e = g.out * exp2_hw(__builtin_fmaf(x, c, -g.nr));
+  return TEMP ? __builtin_fmaf(g.kce, exp2_hw(__builtin_fmaf(x, kLog2e, -g.n1)), e) : e;
+}
+
+// At column v of the ids: the q of every entry that names it, in their order.
+__device__ __forceinline__ float grad_named(const RowGrad& g, float x, float c, int v, const int* id, const float* q,
+                                            int K) {
+  float sum = 0.0f;
+  for (int j = 0; j < K; ++j) sum += id[j] == v ? q[j] : 0.0f;
+  return g.kce * exp2_hw(__builtin_fmaf(x, kLog2e, -g.n1)) + g.kkd * (exp2_hw(__builtin_fmaf(x, c, -g.nz)) - sum);
+}
+
+// 16 bytes at any element (gfx950 stores them at any address).
+typedef u32x4_t __attribute__((aligned(2))) loose16_t;
+template <typename T>
+__device__ __forceinline__ void store8_any(T* p, const float (&o)[8]) {
+  unsigned w[sizeof(T) * 2];
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (__is_same(T, _Float16)) w[e] = pack_f16x2_rne(o[2 * e], o[2 * e + 1]);
+      else w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+    }
+  }
+  loose16_t* to = reinterpret_cast<loose16_t*>(p);
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+    __builtin_nontemporal_store((u32x4_t){w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]}, to + k);
+}
+template <typename T>
+__device__ __forceinline__ void fill8_any(T* p, uint32_t bits) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) store_bits1(p + e, bits);
+}
+
+// ------------------------------------------------------------------ backward
+
+constexpr int kBwdThreads = 256;
+constexpr int kBwdHeld = 2;
+constexpr int kBwdColumns = kBwdThreads * 8 * kBwdHeld;
+
+// One workgroup per (row, 4096 columns).  The logits are requested first; the mask of the ids is made
+// while they arrive.  Each thread reads a group before it writes it: the gradient may be the logits.
+template <typename T, bool TEMP>
+__global__ __launch_bounds__(kBwdThreads) void kd_backward_kernel(KdLoss l, KdGrad g, const T* z, int64_t ldz, T* grad,
+                                                                  int64_t ldg, float c, int chunks) {
+  __shared__ uint32_t bits[kBwdColumns / 32];
+  __shared__ int id[kKdMaxTop];
+  __shared__ float q[kKdMaxTop];
+  __shared__ int bad_any;
+  const int64_t tile = large_bid();
+  const int64_t r = tile / chunks;
+  if (r >= l.BT) return;
+  const int tid = tid_x(), K = (int)l.K;
+  const int64_t lo = (tile - r * chunks) * kBwdColumns;
+  const int64_t hi = l.V < lo + kBwdColumns ? l.V : lo + kBwdColumns;
+  const T* row = z + r * ldz;
+  T* out = grad + r * ldg;
+  const int64_t t = l.target[r];
+  const float lse = l.lse[r];
+  const bool t_ok = t >= 0 && t < l.V;
+  if (t == l.ignore_index || !t_ok || lse == ninf()) {
+    const uint32_t fill = t == l.ignore_index || t_ok ? 0u : kQNaN32;
+    for (int64_t v = lo + tid; v < hi; v += kBwdThreads) store_bits1(out + v, fill);
+    return;
+  }
+  Group<T> gr[kBwdHeld];
+  if (l.V >= 8) {
+#pragma unroll
+    for (int k = 0; k < kBwdHeld; ++k) {
+      const int64_t v = lo + k * (kBwdThreads * 8) + tid * 8;
+      gr[k].load(row + (v < l.V - 8 ? v : l.V - 8));
+    }
+  }
+  const float4 state = *reinterpret_cast<const float4*>(l.state + kKdState * r);
+  if (tid < kBwdColumns / 32) bits[tid] = 0u;
+  if (tid == 0) bad_any = 0;
+  __syncthreads();
+  if (tid < K) {
+    float u;
+    bool bad;
+    const int v = entry_id(l, r, tid, u, bad);
+    id[tid] = v;
+    if (bad) bad_any = 1;
+    if (v >= 0) {
+      mark(bits, v, lo, hi);
+      q[tid] = exp2_hw(__builtin_fmaf(u, c, -state.w * kLog2e));
+    }
+  }
+  const RowGrad rg = row_grad<TEMP>(g, l, r, lse, state.x, state.y, state.z, state.w);
+  __syncthreads();
+  const bool bad = bad_any != 0;
+#pragma unroll
+  for (int k = 0; k < kBwdHeld; ++k) {
+    const int at = k * (kBwdThreads * 8) + tid * 8;
+    const int64_t v = lo + at;
+    if (v >= hi) continue;
+    const uint32_t byte = reinterpret_cast<const uint8_t*>(bits)[at >> 3];
+    float x[8], o[8];
+    if (v + 8 <= l.V) gr[k].get(x);
+    else load_edge(row, v, l.V, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = grad_outside<TEMP>(rg, x[e], c);
+    if (byte) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if ((byte >> e) & 1u) o[e] = grad_named(rg, x[e], c, (int)v + e, id, q, K);
+    }
+    const int64_t rel = t - v;
+    if (rel >= 0 && rel < 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = e == (int)rel ? o[e] - rg.kce : o[e];
+    }
+    if (bad) {
+      for (int e = 0; e < 8 && v + e < l.V; ++e) store_bits1(out + v + e, kQNaN32);
+    } else if (v + 8 <= l.V) {
+      store8_any(out + v, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (v + e < l.V) store1(out + v + e, o[e]);
+    }
+  }
+}
+
+template <typename T, bool TEMP>
+hipError_t launch_kd_backward_t(const KdArgs& a, double c64, hipStream_t st) {
+  const int64_t chunks = (a.l.V + kBwdColumns - 1) / kBwdColumns;
+  (void)hipGetLastError();
+  kd_backward_kernel<T, TEMP><<<large_grid(a.l.BT * chunks), dim3(kBwdThreads), 0, st>>>(
+      a.l, a.g, static_cast<const T*>(a.z), a.ldz, static_cast<T*>(a.grad), a.ldg, (float)c64, (int)chunks);
+  return hipGetLastError();
+}
+
+// The scale of the exponents, log2(e) / T.
+double scale_of(float temperature) { return kLog2e64 / (double)temperature; }
+
+}  // namespace
+
+size_t kd_forward_workspace_bytes(int64_t BT, int64_t V) {
+  if (BT <= 0 || V <= 0) return 0;
+  const Split s = split_of(BT, V);
+  return s.chunks == 1 ? 0 : ((size_t)(BT * s.chunks) * 16 + 255) & ~(size_t)255;
+}
+
+size_t kd_step_workspace_bytes(int64_t BT, int64_t V) { return kd_forward_workspace_bytes(BT, V); }
+
+#define LX_BY_TYPE(F, ...)                                                                     \
+  const double c64 = scale_of(a.l.temperature);                                                \
+  const bool temp = a.l.temperature != 1.0f;                                                   \
+  switch (dt) {                                                                                \
+    case Dt::BF16: return temp ? F<uint16_t, true>(a, c64, st) : F<uint16_t, false>(a, c64, st); \
+    case Dt::F16: return temp ? F<_Float16, true>(a, c64, st) : F<_Float16, false>(a, c64, st);  \
+    default: return temp ? F<float, true>(a, c64, st) : F<float, false>(a, c64, st);             \
+  }
+
+hipError_t launch_kd_forward(const KdArgs& a, Dt dt, hipStream_t st) { LX_BY_TYPE(launch_kd_forward_t) }
+hipError_t launch_kd_backward(const KdArgs& a, Dt dt, hipStream_t st) { LX_BY_TYPE(launch_kd_backward_t) }
+
+hipError_t launch_kd_step(const KdArgs& a, Dt dt, hipStream_t st) {
+  if (hipError_t e = launch_kd_forward(a, dt, st)) return e;
+  return launch_kd_backward(a, dt, st);
+}
+
+}  // namespace lx

@@ -600,6 +600,77 @@ lx_status lx_lora_backward(const void* grad_y, int64_t ld_grad_y, const void* x,
 
 /*
  * ---------------------------------------------------------------------------
+ * Distillation from a teacher's top logits: a teacher that is not resident leaves K of its
+ * logits a token behind, and the student is trained on cross entropy and the
+ * Kullback-Leibler divergence from them.
+ *
+ * With T = temperature, p = softmax(z / T) of the student and, over the row's entries (ids[j],
+ * top[j] = u_j), R = lse_rest[r] (none: -inf), A = log(sum_j exp(u_j / T) + exp(R)):
+ *
+ *   q_j = exp(u_j / T - A),  q_r = exp(R - A)            (without R the top is the whole teacher)
+ *   p_r = sum of p over the tokens that no entry names
+ *   ce = log sum_v exp(z_v) - z_t
+ *   kd = sum_j q_j (log q_j - log p_{ids[j]}) + q_r (log q_r - log p_r)
+ *   d kd / dz_v = (p_v - q_v) / T at a named token (q_v the sum over its entries),
+ *                 (1 - q_r / p_r) p_v / T elsewhere
+ *   grad = k (g_ce d ce/dz + g_kd d kd/dz),  k = *g_scale or 1, g_ce and g_kd times the row's
+ *   grad_ce_rows and grad_kd_rows where these are given.  (The usual T^2 is the caller's, in g_kd.)
+ *
+ * - student (BT, V), row stride ld_student; grad (BT, V) of the same type, row stride ld_grad; it
+ *   may EQUAL student (same row stride).  Any element alignment and strides; fp32, bf16, binary16.
+ * - ids int32[BT][K], top float[BT][K], 1 <= K <= LX_KD_MAX_TOP; lse_rest float[BT] or NULL: as
+ *   lx_top_logits writes them for the same temperature (in any order; from anywhere).  A negative
+ *   id leaves the entry out.  An id of V or more is a caller error the device cannot report: the
+ *   row's kd and its gradient row are NaN.  An id given twice is two entries of one token.
+ * - target, ignore_index as lx_ce_tvd_forward (ignored rows: every output 0, logits not read; a
+ *   target outside [0, V): ce and the gradient row NaN).
+ * - Masked tokens: a logit below -1e30 (-inf, the lowest value of bf16 or fp32) has no mass,
+ *   the teacher's too.  A token that the teacher names and the student masks makes kd +inf, a
+ *   masked target ce +inf; the gradients are as above with p = 0.  A row whose teacher names nothing and has no
+ *   rest has kd 0 and no gradient of it.  A student row without any unmasked logit has ce = kd = 0,
+ *   lse = -inf and gradient 0.  Other logits are finite, at most 1e30 in size.
+ * - Outputs: ce, kd, lse float[BT] (lse at temperature 1); state float[BT][LX_KD_STATE_FLOATS],
+ *   16-byte aligned, which the backward takes: log sum exp(z / T), that over the tokens that no entry
+ *   names (0 where there are none), p_r - q_r, A.
+ * - temperature: 2^-10 to 2^10.
+ * Results are deterministic.  fp32 sums, the K terms of a row in fp64; gradients rounded to nearest
+ * even.
+ * Workspace: at least the bytes that the query says, 256-byte aligned, contents ignored and
+ *   clobbered; may be NULL where that is 0.
+ * Errors : LX_ERR_INVALID_ARG, LX_ERR_UNSUPPORTED_DTYPE, LX_ERR_ALIAS (an output or the
+ *   workspace overlapping anything else), LX_ERR_WORKSPACE, LX_ERR_HIP.
+ */
+#define LX_KD_MAX_TOP 256
+#define LX_KD_STATE_FLOATS 4
+
+size_t lx_ce_kd_workspace_bytes(int64_t BT, int64_t V, lx_dtype dt);
+
+lx_status lx_ce_kd_forward(const void* student, int64_t ld_student, const int64_t* target, const int32_t* ids,
+                           const float* top, const float* lse_rest, int64_t BT, int64_t V, int64_t K,
+                           int64_t ignore_index, float temperature, float* ce, float* kd, float* lse, float* state,
+                           lx_dtype dt, void* workspace, size_t workspace_bytes, void* stream);
+
+/* lse and state as lx_ce_kd_forward wrote them for the same inputs. */
+lx_status lx_ce_kd_backward(void* grad, int64_t ld_grad, const void* student, int64_t ld_student,
+                            const int64_t* target, const int32_t* ids, const float* top, int64_t BT, int64_t V,
+                            int64_t K, int64_t ignore_index, float temperature, const float* lse, const float* state,
+                            float g_ce, float g_kd, const float* grad_ce_rows, const float* grad_kd_rows,
+                            const float* g_scale, lx_dtype dt, void* stream);
+
+/* Both in one call, for a loss whose upstream gradients are known before it: where the rows allow it
+   each logit is read once. */
+size_t lx_ce_kd_forward_backward_workspace_bytes(int64_t BT, int64_t V, lx_dtype dt);
+
+lx_status lx_ce_kd_forward_backward(const void* student, int64_t ld_student, const int64_t* target,
+                                    const int32_t* ids, const float* top, const float* lse_rest, int64_t BT,
+                                    int64_t V, int64_t K, int64_t ignore_index, float temperature, float* ce,
+                                    float* kd, float* lse, float* state, void* grad, int64_t ld_grad, float g_ce,
+                                    float g_kd, const float* grad_ce_rows, const float* grad_kd_rows,
+                                    const float* g_scale, lx_dtype dt, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Reference streams: the practical HBM ceilings the loss kernels are measured
  * against (not part of the loss).  They move bytes the way the loss kernels
  * do: 16-byte buffer loads and stores with the streamed-once cache policy.
