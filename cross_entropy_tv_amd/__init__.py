@@ -112,6 +112,10 @@ def _load() -> ctypes.CDLL:
     L.lx_lora_backward.argtypes = [p, i64, p, i64, p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, p, i64, p, i64, p, p, p,
                                    sz, p]
     L.lx_lora_backward.restype = i32
+    L.lx_top_logits_workspace_bytes.argtypes = [i64, i64, i64]
+    L.lx_top_logits_workspace_bytes.restype = sz
+    L.lx_top_logits.argtypes = [p, i64, i64, i64, i64, f32, p, p, p, p, i32, p, sz, p]
+    L.lx_top_logits.restype = i32
     for name in ("lx_ce_kd_workspace_bytes", "lx_ce_kd_forward_backward_workspace_bytes"):
         getattr(L, name).argtypes = [i64, i64, i32]
         getattr(L, name).restype = sz
@@ -622,6 +626,29 @@ def lx_lora_backward(grad_y, x, A, B, adapter, req_start, scale, rank, base, gra
 LX_KD_MAX_TOP, LX_KD_STATE_FLOATS = 256, 4
 
 
+def lx_top_logits_workspace_bytes(BT: int, V: int, K: int) -> int:
+    return lib.lx_top_logits_workspace_bytes(BT, V, K)
+
+
+def lx_top_logits(logits, temperature: float, top, ids, lse=None, lse_rest=None, workspace=None, stream=None) -> None:
+    """The K largest logits of every row of ``logits`` (BT, V, contiguous rows) into ``top`` float32 and ``ids`` int32
+    (BT, K), and, each or None, the log-sum-exp of the row's logits / temperature and of those outside the K into
+    ``lse`` and ``lse_rest`` float32 [BT].  The workspace (uint8 device tensor) is allocated here with torch when not
+    given."""
+    BT, V, ld = _rows2d(logits, "logits")
+    dt, dev, f32 = _dtype_code(logits), logits.device, torch.float32
+    K = top.shape[1] if top.dim() == 2 else 0
+    _arg(top, "top", f32, (BT, K), dev)
+    _arg(ids, "ids", torch.int32, (BT, K), dev)
+    for t, name in ((lse, "lse"), (lse_rest, "lse_rest")):
+        if t is not None:
+            _arg(t, name, f32, (BT,), dev)
+    with _Launch(dev, stream) as at:
+        ws, wbytes, _held = at.workspace(workspace, lib.lx_top_logits_workspace_bytes(BT, V, K))
+        _check(lib.lx_top_logits(_ptr(logits), ld, BT, V, K, float(temperature), _ptr(top), _ptr(ids), _ptr(lse),
+                                 _ptr(lse_rest), dt, ws, wbytes, at.ptr), "lx_top_logits")
+
+
 def _kd_set(student, target, ids, top, lse_rest, per_row, state, grad=None):
     """(BT, V, K, dtype code, device, student's row stride, grad's) of the arguments that the entry points over
     logits share, checked; ``per_row``: (name, float32 [BT] tensor or None) pairs."""
@@ -713,6 +740,7 @@ __all__ = [
     "lx_gemm_bf16", "lx_ce_tvd_linear_workspace_bytes", "lx_ce_tvd_linear_forward_backward",
     "lx_draft_verify_workspace_bytes", "lx_draft_verify", "lx_lora_forward_workspace_bytes", "lx_lora_forward",
     "lx_lora_backward_workspace_bytes", "lx_lora_backward", "LX_KD_MAX_TOP", "LX_KD_STATE_FLOATS",
+    "lx_top_logits_workspace_bytes", "lx_top_logits",
     "lx_ce_kd_workspace_bytes", "lx_ce_kd_forward", "lx_ce_kd_backward", "lx_ce_kd_forward_backward_workspace_bytes",
     "lx_ce_kd_forward_backward",
 ]

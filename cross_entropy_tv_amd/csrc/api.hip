@@ -854,6 +854,33 @@ lx_status lx_lora_backward(const void* grad_y, int64_t ld_grad_y, const void* x,
   return from_hip(lx::launch_lora_backward(a, static_cast<hipStream_t>(stream)));
 }
 
+size_t lx_top_logits_workspace_bytes(int64_t BT, int64_t V, int64_t K) {
+  if (check_shape(BT, V, 4) || BT == 0 || K < 1 || K > LX_KD_MAX_TOP || !kd_shape_ok(BT, V)) return 0;
+  return lx::top_workspace_bytes(BT, V, K);
+}
+
+lx_status lx_top_logits(const void* logits, int64_t ld, int64_t BT, int64_t V, int64_t K, float temperature, float* top,
+                        int32_t* ids, float* lse, float* lse_rest, lx_dtype dt, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const int es = esize_of(dt);
+  if (!es) return LX_ERR_UNSUPPORTED_DTYPE;
+  if (lx_status s = check_shape(BT, V, es)) return s;
+  if (BT == 0) return LX_OK;
+  if (K < 1 || K > LX_KD_MAX_TOP || !temperature_ok(temperature) || !kd_shape_ok(BT, V) || !stride_ok(BT, V, ld, es))
+    return LX_ERR_INVALID_ARG;
+  if (!logits || !top || !ids || !aligned(logits, es) || !aligned(top, 4) || !aligned(ids, 4) || !aligned(lse, 4) ||
+      !aligned(lse_rest, 4))
+    return LX_ERR_INVALID_ARG;
+  const size_t need = lx_top_logits_workspace_bytes(BT, V, K);
+  const Span outs[5] = {span(top, BT * K * 4), span(ids, BT * K * 4), span(lse, BT * 4), span(lse_rest, BT * 4),
+                        span(need ? workspace : nullptr, (int64_t)need)};
+  const Span in = span(logits, strided_bytes(BT, V, ld, es));
+  if (!outputs_clear(outs, 5, &in, 1)) return LX_ERR_ALIAS;
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return LX_ERR_WORKSPACE;
+  const lx::TopArgs a{logits, ld, BT, V, K, temperature, top, ids, lse, lse_rest, workspace};
+  return from_hip(lx::launch_top(a, dt_of(dt), static_cast<hipStream_t>(stream)));
+}
+
 size_t lx_ce_kd_workspace_bytes(int64_t BT, int64_t V, lx_dtype dt) {
   const int es = esize_of(dt);
   if (!es || check_shape(BT, V, es) || BT == 0 || !kd_shape_ok(BT, V)) return 0;

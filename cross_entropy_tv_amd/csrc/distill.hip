@@ -22,42 +22,11 @@
 #include "common.hpp"
 #include "distill.hpp"
 #include "kd_row.hpp"
+#include "sum2.hpp"
 
 namespace lx {
 
 namespace {
-
-// ------------------------------------------------------------------ sums of 2^(c x - n)
-
-struct Sum2 {
-  float n, s;
-};
-
-// The smallest reference: a masked logit's c x lies below it, so its power of two is 0 against any.
-__device__ __forceinline__ float floor_of(float c) { return kMasked * c; }
-__device__ __forceinline__ float ref_for(float m, float c) { return fmaxf(__builtin_rintf(m * c), floor_of(c)); }
-
-__device__ __forceinline__ void sum8(const float (&x)[8], float c, float n, float& s0, float& s1) {
-#pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    s0 += exp2_hw(__builtin_fmaf(x[e], c, -n));
-    s1 += exp2_hw(__builtin_fmaf(x[e + 1], c, -n));
-  }
-}
-
-__device__ __forceinline__ Sum2 wave_sum2(Sum2 a) {
-  const float n = wave_max(a.n);
-  return Sum2{n, wave_sum32(a.s * exp2_hw(a.n - n))};
-}
-__device__ __forceinline__ void add_sum2(Sum2& a, const Sum2& b) {
-  const float n = fmaxf(a.n, b.n);
-  a.s = a.s * exp2_hw(a.n - n) + b.s * exp2_hw(b.n - n);
-  a.n = n;
-}
-// log2 of the sum, -inf without any
-__device__ __forceinline__ double log2_of(const Sum2& a) {
-  return a.s > 0.0f ? (double)a.n + log2_64((double)a.s) : -kInf64;
-}
 
 // The logits of the columns whose bit is set count as masked.
 __device__ __forceinline__ void leave_out_bits(uint32_t byte, float (&x)[8]) {
@@ -527,9 +496,6 @@ hipError_t launch_kd_backward_t(const KdArgs& a, double c64, hipStream_t st) {
       a.l, a.g, static_cast<const T*>(a.z), a.ldz, static_cast<T*>(a.grad), a.ldg, (float)c64, (int)chunks);
   return hipGetLastError();
 }
-
-// The scale of the exponents, log2(e) / T.
-double scale_of(float temperature) { return kLog2e64 / (double)temperature; }
 
 }  // namespace
 

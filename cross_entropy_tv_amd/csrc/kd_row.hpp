@@ -18,13 +18,10 @@
 
 #include "distill.hpp"
 #include "group.hpp"
+#include "sum2.hpp"
 
 namespace lx {
 
-constexpr float kMasked = -1.0e30f;
-constexpr double kInf64 = __builtin_inf();
-
-__device__ __forceinline__ double log2_64(double s) { return log_64(s) * kLog2e64; }
 __device__ __forceinline__ double wave_max64(double v) {
   return wave_all(v, [](double a, double b) { return __builtin_fmax(a, b); });
 }

@@ -600,6 +600,34 @@ lx_status lx_lora_backward(const void* grad_y, int64_t ld_grad_y, const void* x,
 
 /*
  * ---------------------------------------------------------------------------
+ * The K largest logits of every row: what a teacher that will not be resident leaves behind for
+ * each token (the loss below trains from it), and a server's likeliest tokens.
+ *
+ * - logits (BT, V), row stride ld; any element alignment.  1 <= K <= LX_KD_MAX_TOP; K may exceed V.
+ * Outputs: top float[BT][K]: the K largest logits (as they are: not divided by the temperature), largest
+ *   first, equal ones by id, and ids int32[BT][K]; places beyond a row's unmasked logits hold
+ *   -inf and -1.  lse, lse_rest float[BT], each or NULL: log of the sum of exp(u / temperature)
+ *   over the row, and over the tokens that are not in top (-inf where nothing is left).
+ * - A logit below -1e30 (-inf, the lowest value of bf16 or fp32) is masked: it has no mass and is never
+ *   in top.  Others are finite, at most 1e30 in size; NaN or +inf give unspecified values (ids in
+ *   [-1, V)) for their row.  -0 counts as 0 and is given as 0.
+ * - temperature: 2^-10 to 2^10.
+ * Results are deterministic.
+ * Workspace: at least lx_top_logits_workspace_bytes(BT, V, K) bytes, 256-byte aligned, contents
+ *   ignored and clobbered; may be NULL where that is 0.
+ * Errors : LX_ERR_INVALID_ARG, LX_ERR_UNSUPPORTED_DTYPE, LX_ERR_ALIAS (an output or the
+ *   workspace overlapping anything else), LX_ERR_WORKSPACE, LX_ERR_HIP.
+ */
+#define LX_KD_MAX_TOP 256
+
+size_t lx_top_logits_workspace_bytes(int64_t BT, int64_t V, int64_t K);
+
+lx_status lx_top_logits(const void* logits, int64_t ld, int64_t BT, int64_t V, int64_t K, float temperature, float* top,
+                        int32_t* ids, float* lse, float* lse_rest, lx_dtype dt, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Distillation from a teacher's top logits: a teacher that is not resident leaves K of its
  * logits a token behind, and the student is trained on cross entropy and the
  * Kullback-Leibler divergence from them.
@@ -640,7 +668,6 @@ lx_status lx_lora_backward(const void* grad_y, int64_t ld_grad_y, const void* x,
  * Errors : LX_ERR_INVALID_ARG, LX_ERR_UNSUPPORTED_DTYPE, LX_ERR_ALIAS (an output or the
  *   workspace overlapping anything else), LX_ERR_WORKSPACE, LX_ERR_HIP.
  */
-#define LX_KD_MAX_TOP 256
 #define LX_KD_STATE_FLOATS 4
 
 size_t lx_ce_kd_workspace_bytes(int64_t BT, int64_t V, lx_dtype dt);

@@ -85,3 +85,26 @@ def test_the_package_checks_what_it_passes():
 
     with pytest.raises(ValueError, match="device tensor"):
         call()
+
+
+NEED_TOP = lx.lx_top_logits_workspace_bytes(4, 100000, 8)
+
+
+def top(z=A, ld=100000, BT=4, V=100000, K=8, T=1.0, out=A * 2, ids=A * 3, lse=A * 4, rest=A * 5, dt=1, ws=A * 6, wsb=NEED_TOP):
+    return L.lx_top_logits(z, ld, BT, V, K, T, out, ids, lse, rest, dt, ws, wsb, None)
+
+
+def test_top_logits():
+    assert top(BT=0) == lx.LX_OK
+    assert top(dt=-1) == lx.LX_ERR_UNSUPPORTED_DTYPE
+    for kw in (dict(BT=-1), dict(V=0), dict(V=2 ** 31), dict(K=0), dict(K=257), dict(T=0.0), dict(T=float("nan")),
+               dict(T=2.0 ** -11), dict(ld=99999), dict(z=None), dict(z=A + 1), dict(out=None), dict(ids=None),
+               dict(out=A * 2 + 2), dict(ids=A * 3 + 1), dict(lse=A * 4 + 2), dict(rest=A * 5 + 1)):
+        assert top(**kw) == BAD, kw
+    for kw in (dict(out=A + 4), dict(ids=A * 2), dict(lse=A * 3), dict(rest=A * 4), dict(ws=A)):
+        assert top(**kw) == ALIAS, kw
+    assert NEED_TOP > 0
+    assert top(ws=None) == top(wsb=NEED_TOP - 1) == top(ws=A * 6 + 16) == WS
+    q = lx.lx_top_logits_workspace_bytes
+    assert q(0, 100, 8) == q(4, 0, 8) == q(4, 100, 0) == q(4, 100, 257) == 0
+    assert q(1, 2 ** 31 - 1, 256) < 1 << 20
