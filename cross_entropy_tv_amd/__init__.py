@@ -126,6 +126,11 @@ def _load() -> ctypes.CDLL:
     L.lx_ce_kd_forward_backward.argtypes = [p, i64, p, p, p, p, i64, i64, i64, i64, f32, p, p, p, p, p, i64, f32, f32, p, p,
                                             p, i32, p, sz, p]
     L.lx_ce_kd_forward_backward.restype = i32
+    L.lx_ce_kd_linear_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i32]
+    L.lx_ce_kd_linear_workspace_bytes.restype = sz
+    L.lx_ce_kd_linear_forward_backward.argtypes = [p, p, i64, p, p, p, p, i64, i64, i64, i64, f32, p, p, p, p, p, p, i32,
+                                                   f32, f32, p, p, p, i64, p, sz, p]
+    L.lx_ce_kd_linear_forward_backward.restype = i32
     return L
 
 
@@ -730,6 +735,63 @@ def lx_ce_kd_forward_backward(student, target, ignore_index, ids, top, lse_rest,
                "lx_ce_kd_forward_backward")
 
 
+def lx_ce_kd_linear_workspace_bytes(BT: int, V: int, H: int, K: int, piece: int, grads: bool) -> int:
+    return lib.lx_ce_kd_linear_workspace_bytes(BT, V, H, K, piece, int(bool(grads)))
+
+
+def lx_ce_kd_linear_piece(BT: int, V: int) -> int:
+    """The columns of a piece that lx_ce_kd_linear_forward_backward takes when none are given: at most 2^27 elements
+    of the gradient of the logits at once, and at least 2048 columns."""
+    return max(1, min(V, max(2048, (1 << 27) // max(1, BT) // 256 * 256), 1 << 22))
+
+
+def lx_ce_kd_linear_forward_backward(x, w, target, ignore_index, ids, top, lse_rest, temperature: float, ce, kd, lse, state,
+                                     grad_x, grad_w, g_ce: float, g_kd: float, grad_ce_rows=None, grad_kd_rows=None,
+                                     g_scale=None, piece: int | None = None, workspace=None, stream=None) -> None:
+    """The loss of lx_ce_kd_forward (``ids`` None: cross entropy alone, ``top``, ``lse_rest``, ``kd`` and ``state`` None
+    too) of the logits x w^T, and their gradients, in pieces of ``piece`` columns of the vocabulary: ``x`` (BT, H) and
+    ``w`` (V, H) contiguous bfloat16; ``grad_x`` and ``grad_w`` of the same shapes, both float32 or both bfloat16, or
+    None.  The workspace (uint8 device tensor) is allocated here with torch when not given."""
+    f32, bf16, dev = torch.float32, torch.bfloat16, x.device
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or not x.is_cuda:
+        raise ValueError("x must be (BT, H) and w (V, H), device tensors")
+    (BT, H), V = x.shape, w.shape[0]
+    _arg(x, "x", bf16, (BT, H), dev)
+    _arg(w, "w", bf16, (V, H), dev)
+    _arg(target, "target", torch.int64, (BT,), dev)
+    K = 0
+    if ids is not None:
+        K = ids.shape[1] if ids.dim() == 2 else 0
+        if K < 1:
+            raise ValueError("ids must be (BT, K), K at least 1")
+        _arg(ids, "ids", torch.int32, (BT, K), dev)
+        _arg(top, "top", f32, (BT, K), dev)
+        _arg(state, "state", f32, (BT, LX_KD_STATE_FLOATS), dev)
+        _arg(kd, "kd", f32, (BT,), dev)
+    elif top is not None or lse_rest is not None or kd is not None or state is not None:
+        raise ValueError("without ids there are no top, lse_rest, kd and state")
+    for name, t in (("lse_rest", lse_rest), ("ce", ce), ("lse", lse), ("grad_ce_rows", grad_ce_rows),
+                    ("grad_kd_rows", grad_kd_rows)):
+        if t is not None or name in ("ce", "lse"):
+            _arg(t, name, f32, (BT,), dev)
+    kinds = {t.dtype for t in (grad_x, grad_w) if t is not None}
+    if kinds - {f32, bf16} or len(kinds) > 1:
+        raise ValueError("grad_x and grad_w must both be float32 or both bfloat16")
+    grad_dt = kinds.pop() if kinds else f32
+    for name, t, like in (("grad_x", grad_x, x), ("grad_w", grad_w, w)):
+        if t is not None:
+            _arg(t, name, grad_dt, like.shape, dev)
+    piece = lx_ce_kd_linear_piece(BT, V) if piece is None else int(piece)
+    with _Launch(dev, stream) as at:
+        ws, wbytes, _held = at.workspace(workspace, lib.lx_ce_kd_linear_workspace_bytes(
+            BT, V, H, K, piece, int(grad_x is not None or grad_w is not None)))
+        _check(lib.lx_ce_kd_linear_forward_backward(
+            _ptr(x), _ptr(w), H, _ptr(target), _ptr(ids), _ptr(top), _ptr(lse_rest), BT, V, K, int(ignore_index),
+            float(temperature), _ptr(ce), _ptr(kd), _ptr(lse), _ptr(state), _ptr(grad_x), _ptr(grad_w),
+            _DTYPE_CODES[grad_dt], float(g_ce), float(g_kd), _ptr(grad_ce_rows), _ptr(grad_kd_rows),
+            _scale_ptr(g_scale, dev), piece, ws, wbytes, at.ptr), "lx_ce_kd_linear_forward_backward")
+
+
 __all__ = [
     "LxError", "lib", "LIB_PATH", "LX_OK", "LX_ERR_INVALID_ARG", "LX_ERR_UNSUPPORTED_DTYPE", "LX_ERR_ALIAS",
     "LX_ERR_WORKSPACE", "LX_ERR_HIP", "LX_F32", "LX_BF16", "LX_F16", "lx_status_string", "lx_abi_version",
@@ -742,7 +804,8 @@ __all__ = [
     "lx_lora_backward_workspace_bytes", "lx_lora_backward", "LX_KD_MAX_TOP", "LX_KD_STATE_FLOATS",
     "lx_top_logits_workspace_bytes", "lx_top_logits",
     "lx_ce_kd_workspace_bytes", "lx_ce_kd_forward", "lx_ce_kd_backward", "lx_ce_kd_forward_backward_workspace_bytes",
-    "lx_ce_kd_forward_backward",
+    "lx_ce_kd_forward_backward", "lx_ce_kd_linear_workspace_bytes", "lx_ce_kd_linear_piece",
+    "lx_ce_kd_linear_forward_backward",
 ]
 
 

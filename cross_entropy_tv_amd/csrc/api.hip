@@ -332,7 +332,7 @@ bool temperature_ok(float t) {
 bool kd_shape_ok(int64_t BT, int64_t V) { return BT <= ((int64_t)1 << 34) / ((V + 4095) / 4096); }
 
 lx_status kd_check(const lx::KdLoss& l, bool outputs) {
-  if (l.K < 1 || l.K > LX_KD_MAX_TOP || !temperature_ok(l.temperature) || !kd_shape_ok(l.BT, l.V)) return LX_ERR_INVALID_ARG;
+  if (l.K < 1 || l.K > LX_KD_MAX_TOP || !temperature_ok(l.temperature)) return LX_ERR_INVALID_ARG;
   if (!l.target || !l.ids || !l.top || !l.lse || !l.state || (outputs && (!l.ce || !l.kd))) return LX_ERR_INVALID_ARG;
   if (!aligned(l.target, 8) || !aligned(l.ids, 4) || !aligned(l.top, 4) || !aligned(l.rest, 4) || !aligned(l.ce, 4) ||
       !aligned(l.kd, 4) || !aligned(l.lse, 4) || !aligned(l.state, 16))
@@ -350,6 +350,14 @@ bool outputs_clear(const Span* outs, int n_out, const Span* ins, int n_in) {
   return true;
 }
 
+// Sizes that lx_ce_kd_linear_forward_backward takes: operand rows of whole 16 bytes, rows, columns and tiles counted
+// within int32.
+bool kd_linear_shape_ok(int64_t BT, int64_t V, int64_t H, int64_t K, int64_t piece) {
+  if (BT < 0 || BT > (1 << 30) || V < 1 || V > (int64_t)INT_MAX - 4096 || H < 8 || H % 8 || H > lx::kGemmMaxLd) return false;
+  if (K < 0 || K > LX_KD_MAX_TOP || piece < 1 || piece > lx::kGemmMaxLd) return false;
+  return (BT + 255) / 256 <= (int64_t)INT_MAX / ((V + 255) / 256 + 8);
+}
+
 // backward: l.lse and l.state are inputs, and ce, kd are absent
 lx_status kd_impl(lx::KdArgs& a, lx_dtype dt, bool forward, bool backward, size_t need, void* workspace,
                   size_t workspace_bytes, void* stream) {
@@ -357,6 +365,7 @@ lx_status kd_impl(lx::KdArgs& a, lx_dtype dt, bool forward, bool backward, size_
   if (!es) return LX_ERR_UNSUPPORTED_DTYPE;
   if (lx_status s = check_shape(a.l.BT, a.l.V, es)) return s;
   if (a.l.BT == 0) return LX_OK;
+  if (!kd_shape_ok(a.l.BT, a.l.V)) return LX_ERR_INVALID_ARG;
   if (lx_status s = kd_check(a.l, forward)) return s;
   const int64_t BT = a.l.BT, V = a.l.V, fb = BT * 4;
   if (!stride_ok(BT, V, a.ldz, es) || (backward && !stride_ok(BT, V, a.ldg, es))) return LX_ERR_INVALID_ARG;
@@ -936,6 +945,62 @@ lx_status lx_ce_kd_forward_backward(const void* student, int64_t ld_student, con
   a.g = lx::KdGrad{g_ce, g_kd, grad_ce_rows, grad_kd_rows, g_scale};
   return kd_impl(a, dt, true, true, lx_ce_kd_forward_backward_workspace_bytes(BT, V, dt), workspace, workspace_bytes,
                  stream);
+}
+
+size_t lx_ce_kd_linear_workspace_bytes(int64_t BT, int64_t V, int64_t H, int64_t K, int64_t piece, int grads) {
+  if (!kd_linear_shape_ok(BT, V, H, K, piece)) return 0;
+  return lx::kd_linear_workspace_bytes(BT, V, H, K, piece, grads != 0);
+}
+
+lx_status lx_ce_kd_linear_forward_backward(const void* x, const void* w, int64_t H, const int64_t* target,
+                                           const int32_t* ids, const float* top, const float* lse_rest, int64_t BT,
+                                           int64_t V, int64_t K, int64_t ignore_index, float temperature, float* ce,
+                                           float* kd, float* lse, float* state, void* grad_x, void* grad_w,
+                                           lx_dtype grad_dt, float g_ce, float g_kd, const float* grad_ce_rows,
+                                           const float* grad_kd_rows, const float* g_scale, int64_t piece,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+  const bool grads = grad_x || grad_w;
+  if (grads && grad_dt != LX_F32 && grad_dt != LX_BF16) return LX_ERR_UNSUPPORTED_DTYPE;
+  if (!kd_linear_shape_ok(BT, V, H, K, piece)) return LX_ERR_INVALID_ARG;
+  if (BT == 0) {  // (no row: a gradient of w that is 0)
+    if (!grad_w) return LX_OK;
+    if (!aligned(grad_w, 16)) return LX_ERR_INVALID_ARG;
+    return from_hip(lx::launch_kd_linear_zero(grad_w, V * H / 8 * (grad_dt == LX_BF16 ? 1 : 2),
+                                              static_cast<hipStream_t>(stream)));
+  }
+  lx::KdLinearArgs a{};
+  a.l = lx::KdLoss{target, ignore_index, ids, top, lse_rest, BT, V, K, temperature, ce, kd, lse, state};
+  a.g = lx::KdGrad{g_ce, g_kd, grad_ce_rows, grad_kd_rows, g_scale};
+  if (K == 0) {
+    a.l.ids = nullptr;
+    a.l.top = a.l.rest = nullptr;
+    a.l.kd = a.l.state = nullptr;
+    a.l.temperature = 1.0f;
+    a.g.kd_rows = nullptr;
+    if (!target || !ce || !lse || !aligned(target, 8) || !aligned(ce, 4) || !aligned(lse, 4)) return LX_ERR_INVALID_ARG;
+  } else if (lx_status s = kd_check(a.l, true)) {
+    return s;
+  }
+  if (!x || !w || !aligned(x, 16) || !aligned(w, 16) || !aligned(grad_x, 16) || !aligned(grad_w, 16) || !kd_grad_ok(a.g))
+    return LX_ERR_INVALID_ARG;
+  const size_t need = lx_ce_kd_linear_workspace_bytes(BT, V, H, K, piece, grads);
+  const int64_t fb = BT * 4, ge = grad_dt == LX_BF16 ? 2 : 4;
+  const Span outs[7] = {span(ce, fb), span(a.l.kd, fb), span(lse, fb), span(a.l.state, fb * lx::kKdState),
+                        span(grad_x, BT * H * ge), span(grad_w, V * H * ge), span(workspace, (int64_t)need)};
+  const Span ins[9] = {span(x, BT * H * 2), span(w, V * H * 2), span(target, BT * 8), span(a.l.ids, BT * K * 4),
+                       span(a.l.top, BT * K * 4), span(a.l.rest, fb), span(grad_ce_rows, fb), span(a.g.kd_rows, fb),
+                       span(g_scale, 4)};
+  if (!outputs_clear(outs, 7, ins, 9)) return LX_ERR_ALIAS;
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LX_ERR_WORKSPACE;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = static_cast<const uint16_t*>(w);
+  a.H = H;
+  a.grad_x = grad_x;
+  a.grad_w = grad_w;
+  a.grad_dt = dt_of(grad_dt);
+  a.piece = piece;
+  a.workspace = workspace;
+  return from_hip(lx::launch_kd_linear(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

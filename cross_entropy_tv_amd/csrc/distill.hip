@@ -36,23 +36,6 @@ __device__ __forceinline__ void leave_out_bits(uint32_t byte, float (&x)[8]) {
   }
 }
 
-// ------------------------------------------------------------------ the teacher's entries in LDS
-
-struct Entries {
-  int id[kKdMaxTop];    // -1: left out
-  float u[kKdMaxTop];
-  float z[kKdMaxTop];   // the student's logit there, -inf where masked
-};
-
-// Entry j of row r as thread j < K takes it; id -1 where it is left out, bad where its id is past the
-// vocabulary.
-__device__ __forceinline__ int entry_id(const KdLoss& l, int64_t r, int j, float& u, bool& bad) {
-  const int v = l.ids[r * l.K + j];
-  u = l.top[r * l.K + j];
-  bad = v >= l.V;
-  return bad || v < 0 || u < kMasked ? -1 : v;
-}
-
 // ------------------------------------------------------------------ forward
 
 // Rows of up to 2^18 columns are one workgroup's (its mask is 32 KB); 512 threads, H groups at once.
@@ -157,65 +140,6 @@ __device__ __forceinline__ void chunk_sums(const T* row, int64_t lo, int64_t hi,
   }
 }
 
-__device__ __forceinline__ void store_state(float* state, float a, float b, float c, float d) {
-  *reinterpret_cast<float4*>(state) = make_float4(a, b, c, d);
-}
-
-// Wave 0, all lanes: the row's outputs from its sums and entries.  z_t: the target's logit.
-template <bool TEMP>
-__device__ __forceinline__ void finish_row(const KdLoss& l, int64_t r, const Entries& en, bool bad, int64_t t, float zt,
-                                           double c, const Sum2& a, const Sum2& a1) {
-  const int lane = tid_x() & 63, K = (int)l.K;
-  double ua[kLaneTop], q[kLaneTop];
-  const Teacher te = teacher_of(en.id, en.u, K, lane, c, l.rest ? l.rest[r] : ninf(), ua, q);
-  const double lr = log2_of(a);
-  double t2[kLaneTop], m = lr;
-#pragma unroll
-  for (int k = 0; k < kLaneTop; ++k) {
-    const int j = lane + 64 * k;
-    const bool here = j < K && en.id[j] >= 0;
-    t2[k] = here && !(en.z[j] < kMasked) ? (double)en.z[j] * c : -kInf64;
-    m = __builtin_fmax(m, t2[k]);
-  }
-  m = wave_max64(m);
-  const double ref = m > -kInf64 ? m : 0.0;
-  double s = 0.0, terms = 0.0;
-#pragma unroll
-  for (int k = 0; k < kLaneTop; ++k) {
-    const int j = lane + 64 * k;
-    if (j < K && en.id[j] >= 0) {
-      if (!named_before(en.id, j)) s += exp2_64(t2[k] - ref);
-      if (q[k] > 0.0) terms += q[k] * (ua[k] - t2[k]);
-    }
-  }
-  s = wave_sum64(s) + exp2_64(lr - ref);
-  terms = wave_sum64(terms);
-  if (lane != 0) return;
-  if (!(m > -kInf64)) {  // no unmasked logit
-    l.ce[r] = 0.0f;
-    l.kd[r] = 0.0f;
-    l.lse[r] = ninf();
-    store_state(l.state + kKdState * r, ninf(), 0.0f, 0.0f, 0.0f);
-    return;
-  }
-  const double lz = ref + log2_64(s);
-  const RowOut o = row_out(te, terms, lz, lr);
-  const double l1 = TEMP ? log2_of(a1) * kLn2 : lz * kLn2;
-  l.lse[r] = (float)l1;
-  if (t >= 0 && t < l.V) l.ce[r] = zt < kMasked ? -ninf() : (float)(l1 - (double)zt);
-  else store_nan(l.ce + r);
-  if (bad) store_nan(l.kd + r);
-  else l.kd[r] = o.kd;
-  store_state(l.state + kKdState * r, o.lse_t, o.lse_rest, o.off, o.norm);
-}
-
-__device__ __forceinline__ void ignored_row(const KdLoss& l, int64_t r) {
-  l.ce[r] = 0.0f;
-  l.kd[r] = 0.0f;
-  l.lse[r] = 0.0f;
-  store_state(l.state + kKdState * r, 0.0f, 0.0f, 0.0f, 0.0f);
-}
-
 // One workgroup per (row, chunk).  A whole row (chunks == 1) is finished here; chunks leave their sums
 // in parts [row][chunk][4].
 template <typename T, bool TEMP>
@@ -232,7 +156,7 @@ __global__ __launch_bounds__(kFwdThreads) void kd_forward_kernel(KdLoss l, const
   const int ch = (int)(tile - r * chunks), tid = tid_x();
   const int64_t t = l.target[r];
   if (t == l.ignore_index) {
-    if (ch == 0 && tid == 0) ignored_row(l, r);
+    if (ch == 0 && tid == 0) store_row(l, r, RowResult{});
     return;
   }
   const int K = (int)l.K;
@@ -275,10 +199,12 @@ __global__ __launch_bounds__(kFwdThreads) void kd_forward_kernel(KdLoss l, const
     if (TEMP) add_sum2(a1, red[1][w]);
   }
   if (chunks > 1) {
-    if (tid == 0) store_state(parts + 4 * tile, a.n, a.s, a1.n, a1.s);
+    if (tid == 0) *reinterpret_cast<float4*>(parts + 4 * tile) = make_float4(a.n, a.s, a1.n, a1.s);
     return;
   }
-  finish_row<TEMP>(l, r, en, bad_any != 0, t, zt, c64, a, a1);
+  double q[kLaneTop];
+  const RowResult o = finish_row<TEMP>(l, r, en, bad_any != 0, t, zt, c64, a, a1, q);
+  if (tid == 0) store_row(l, r, o);
 }
 
 // Rows cut into chunks: a wave a row joins its chunks' sums, lane by lane and then the lanes, in a fixed
@@ -313,7 +239,9 @@ __global__ __launch_bounds__(64) void kd_finish_kernel(KdLoss l, const T* __rest
   a = wave_sum2(a);
   if (TEMP) a1 = wave_sum2(a1);
   __syncthreads();
-  finish_row<TEMP>(l, r, en, __any(bad_any), t, zt, c64, a, a1);
+  double q[kLaneTop];
+  const RowResult o = finish_row<TEMP>(l, r, en, __any(bad_any), t, zt, c64, a, a1, q);
+  if (lane == 0) store_row(l, r, o);
 }
 
 template <typename T, bool TEMP>
@@ -332,44 +260,12 @@ hipError_t launch_kd_forward_t(const KdArgs& a, double c64, hipStream_t st) {
 
 // ------------------------------------------------------------------ the gradient of a row's columns
 
-// What the gradient of a row needs, in fp32 (uniform).
-struct RowGrad {
-  float kce, kkd;     // k g_ce, k g_kd / T, with the row's factors
-  float n1;           // lse log2 e
-  float nz, nr, nq;   // log-sums (base 2): student at T, its outside, the teacher's
-  float out;          // outside: factor of 2^(c z - nr); at T = 1 with ce's part
-};
-
-template <bool TEMP>
-__device__ __forceinline__ RowGrad row_grad(const KdGrad& g, const KdLoss& l, int64_t r, float lse, float lse_t,
-                                            float lse_rest, float off, float norm) {
-  const float k = g.g_scale ? *g.g_scale : 1.0f;
-  RowGrad o;
-  o.kce = k * g.g_ce * (g.ce_rows ? g.ce_rows[r] : 1.0f);
-  o.kkd = k * g.g_kd * (g.kd_rows ? g.kd_rows[r] : 1.0f) / l.temperature;
-  o.n1 = lse * kLog2e;
-  o.nz = lse_t * kLog2e;
-  o.nr = lse_rest * kLog2e;
-  o.nq = norm * kLog2e;
-  o.out = o.kkd * off;
-  // (without anything outside, lse_rest is 0 and every such logit masked: the factor only has to be finite)
-  if (!TEMP) o.out += o.kce * fminf(exp2_hw(o.nr - o.nz), 1.0f);
-  return o;
-}
-
-// The gradient at a column outside the ids.
-template <bool TEMP>
-__device__ __forceinline__ float grad_outside(const RowGrad& g, float x, float c) {
-  const float e = g.out * exp2_hw(__builtin_fmaf(x, c, -g.nr));
-  return TEMP ? __builtin_fmaf(g.kce, exp2_hw(__builtin_fmaf(x, kLog2e, -g.n1)), e) : e;
-}
-
 // At column v of the ids: the q of every entry that names it, in their order.
 __device__ __forceinline__ float grad_named(const RowGrad& g, float x, float c, int v, const int* id, const float* q,
                                             int K) {
   float sum = 0.0f;
   for (int j = 0; j < K; ++j) sum += id[j] == v ? q[j] : 0.0f;
-  return g.kce * exp2_hw(__builtin_fmaf(x, kLog2e, -g.n1)) + g.kkd * (exp2_hw(__builtin_fmaf(x, c, -g.nz)) - sum);
+  return grad_named(g, x, c, sum);
 }
 
 // 16 bytes at any element (gfx950 stores them at any address).
@@ -452,7 +348,7 @@ __global__ __launch_bounds__(kBwdThreads) void kd_backward_kernel(KdLoss l, KdGr
       q[tid] = exp2_hw(__builtin_fmaf(u, c, -state.w * kLog2e));
     }
   }
-  const RowGrad rg = row_grad<TEMP>(g, l, r, lse, state.x, state.y, state.z, state.w);
+  const RowGrad rg = row_grad<TEMP>(g, l, r, lse, state.x, state.y, state.z);
   __syncthreads();
   const bool bad = bad_any != 0;
 #pragma unroll

@@ -75,5 +75,7 @@ struct KdLinearArgs {
 
 size_t kd_linear_workspace_bytes(int64_t BT, int64_t V, int64_t H, int64_t K, int64_t piece, bool grads);
 hipError_t launch_kd_linear(const KdLinearArgs& a, hipStream_t stream);
+// 16-byte units of zeros
+hipError_t launch_kd_linear_zero(void* p, int64_t units, hipStream_t stream);
 
 }  // namespace lx

@@ -29,6 +29,12 @@ struct GemmArgs {
   // floats of scratch.
   int splits = 1;
   float* partials = nullptr;
+  // C holds bf16 (not accumulated; B along N).
+  bool c_bf16 = false;
+  // Bytes of A and B that may be read, 0: to the end of the last row that M, N and K make.  An operand whose last
+  // 16 bytes reach past M, N or K has to be stored that far (what lies there meets zeros or is not written); rows of K
+  // past the end read as zeros.
+  int64_t a_end = 0, b_end = 0;
 };
 
 hipError_t launch_gemm_bf16(const GemmArgs& g, hipStream_t stream);

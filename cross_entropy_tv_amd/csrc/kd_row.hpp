@@ -72,22 +72,129 @@ __device__ __forceinline__ bool named_before(const int* id, int j) {
   return seen;
 }
 
-struct RowOut {
-  float kd, lse_t, lse_rest, off, norm;
+// ------------------------------------------------------------------ the teacher's entries in LDS
+
+struct Entries {
+  int id[kKdMaxTop];    // -1: left out
+  float u[kKdMaxTop];
+  float z[kKdMaxTop];   // the student's logit there, -inf where masked
 };
 
-// kd and the row's state from its log-sums (base 2; lr -inf: nothing outside the ids) and
-// terms = sum_j q_j (c u_j - c z_j).
-__device__ __forceinline__ RowOut row_out(const Teacher& t, double terms, double lz, double lr) {
-  RowOut o;
-  terms += (lz - t.lq) * (1.0 - t.q_rest);
-  if (t.q_rest > 0.0) terms += t.q_rest * ((t.lr - t.lq) - (lr - lz));
-  o.kd = t.any ? (float)(terms * kLn2) : 0.0f;
+// Entry j of row r as thread j < K takes it; id -1 where it is left out, bad where its id is past the
+// vocabulary.
+__device__ __forceinline__ int entry_id(const KdLoss& l, int64_t r, int j, float& u, bool& bad) {
+  const int v = l.ids[r * l.K + j];
+  u = l.top[r * l.K + j];
+  bad = v >= l.V;
+  return bad || v < 0 || u < kMasked ? -1 : v;
+}
+
+// ------------------------------------------------------------------ a row's results
+
+struct RowResult {
+  float ce, kd, lse, lse_t, lse_rest, off, norm;  // all 0: an ignored row
+  uint32_t bad;                                   // bit 0: ce is NaN, bit 1: kd is NaN
+};
+
+// One thread writes them.  kd and state may be absent (cross entropy alone).
+__device__ __forceinline__ void store_row(const KdLoss& l, int64_t r, const RowResult& o) {
+  l.lse[r] = o.lse;
+  if (o.bad & 1u) store_nan(l.ce + r);
+  else l.ce[r] = o.ce;
+  if (!l.kd) return;
+  if (o.bad & 2u) store_nan(l.kd + r);
+  else l.kd[r] = o.kd;
+  *reinterpret_cast<float4*>(l.state + kKdState * r) = make_float4(o.lse_t, o.lse_rest, o.off, o.norm);
+}
+
+// One wave: the row's results from its sums (a: outside the ids at the temperature; TEMP, a1: all columns at
+// temperature 1) and entries, valid in every lane; q: the masses of the lane's entries.  t, zt: the target and its
+// logit.
+template <bool TEMP>
+__device__ __forceinline__ RowResult finish_row(const KdLoss& l, int64_t r, const Entries& en, bool bad, int64_t t,
+                                                float zt, double c, const Sum2& a, const Sum2& a1,
+                                                double (&q)[kLaneTop]) {
+  const int lane = tid_x() & 63, K = (int)l.K;
+  double ua[kLaneTop];
+  const Teacher te = teacher_of(en.id, en.u, K, lane, c, l.rest ? l.rest[r] : ninf(), ua, q);
+  const double lr = log2_of(a);
+  double t2[kLaneTop], m = lr;
+#pragma unroll
+  for (int k = 0; k < kLaneTop; ++k) {
+    const int j = lane + 64 * k;
+    const bool here = j < K && en.id[j] >= 0;
+    t2[k] = here && !(en.z[j] < kMasked) ? (double)en.z[j] * c : -kInf64;
+    m = __builtin_fmax(m, t2[k]);
+  }
+  m = wave_max64(m);
+  RowResult o{};
+  if (!(m > -kInf64)) {  // no unmasked logit
+    o.lse = o.lse_t = ninf();
+    return o;
+  }
+  double s = 0.0, terms = 0.0;
+#pragma unroll
+  for (int k = 0; k < kLaneTop; ++k) {
+    const int j = lane + 64 * k;
+    if (j < K && en.id[j] >= 0) {
+      if (!named_before(en.id, j)) s += exp2_64(t2[k] - m);
+      if (q[k] > 0.0) terms += q[k] * (ua[k] - t2[k]);
+    }
+  }
+  s = wave_sum64(s) + exp2_64(lr - m);
+  terms = wave_sum64(terms);
+  const double lz = m + log2_64(s);
+  const double l1 = TEMP ? log2_of(a1) * kLn2 : lz * kLn2;
+  // kd: terms holds sum_j q_j (c u_j - c z_j)
+  terms += (lz - te.lq) * (1.0 - te.q_rest);
+  if (te.q_rest > 0.0) terms += te.q_rest * ((te.lr - te.lq) - (lr - lz));
+  o.kd = te.any ? (float)(terms * kLn2) : 0.0f;
+  o.lse = (float)l1;
+  o.ce = zt < kMasked ? -ninf() : (float)(l1 - (double)zt);
   o.lse_t = (float)(lz * kLn2);
   o.lse_rest = lr > -kInf64 ? (float)(lr * kLn2) : 0.0f;
-  o.off = t.any ? (float)(exp2_64(lr - lz) - t.q_rest) : 0.0f;
-  o.norm = (float)(t.lq * kLn2);
+  o.off = te.any ? (float)(exp2_64(lr - lz) - te.q_rest) : 0.0f;
+  o.norm = (float)(te.lq * kLn2);
+  o.bad = (t >= 0 && t < l.V ? 0u : 1u) | (bad ? 2u : 0u);
   return o;
+}
+
+// ------------------------------------------------------------------ a row's gradient
+
+// What the gradient of a row needs, in fp32 (uniform).
+struct RowGrad {
+  float kce, kkd;     // k g_ce, k g_kd / T, with the row's factors
+  float n1;           // lse log2 e
+  float nz, nr;       // log-sums (base 2) at T: the row's, and that of its outside
+  float out;          // outside: factor of 2^(c z - nr); at T = 1 with ce's part
+};
+
+template <bool TEMP>
+__device__ __forceinline__ RowGrad row_grad(const KdGrad& g, const KdLoss& l, int64_t r, float lse, float lse_t,
+                                            float lse_rest, float off) {
+  const float k = g.g_scale ? *g.g_scale : 1.0f;
+  RowGrad o;
+  o.kce = k * g.g_ce * (g.ce_rows ? g.ce_rows[r] : 1.0f);
+  o.kkd = k * g.g_kd * (g.kd_rows ? g.kd_rows[r] : 1.0f) / l.temperature;
+  o.n1 = lse * kLog2e;
+  o.nz = lse_t * kLog2e;
+  o.nr = lse_rest * kLog2e;
+  o.out = o.kkd * off;
+  // (without anything outside, lse_rest is 0 and every such logit masked: the factor only has to be finite)
+  if (!TEMP) o.out += o.kce * fminf(exp2_hw(o.nr - o.nz), 1.0f);
+  return o;
+}
+
+// The gradient at a column outside the ids.
+template <bool TEMP>
+__device__ __forceinline__ float grad_outside(const RowGrad& g, float x, float c) {
+  const float e = g.out * exp2_hw(__builtin_fmaf(x, c, -g.nr));
+  return TEMP ? __builtin_fmaf(g.kce, exp2_hw(__builtin_fmaf(x, kLog2e, -g.n1)), e) : e;
+}
+
+// At a column of the ids with the teacher's mass q.
+__device__ __forceinline__ float grad_named(const RowGrad& g, float x, float c, float q) {
+  return g.kce * exp2_hw(__builtin_fmaf(x, kLog2e, -g.n1)) + g.kkd * (exp2_hw(__builtin_fmaf(x, c, -g.nz)) - q);
 }
 
 // The mask of a row's ids over the columns [lo, hi) in LDS: bit v - lo of `bits`.

@@ -39,6 +39,7 @@
 #include "linear.hpp"
 #include "gemm.hpp"
 #include "mm.hpp"
+#include "mm_wide.hpp"
 #include "common.hpp"
 
 namespace lx {
@@ -47,17 +48,8 @@ namespace {
 
 using mm::f32x16_t;
 
-// LDS of the main loop: 2 stages of a 64-k slice, 64 KB each for 256 x 256
-// tiles and 48 KB for the dual 256 x 128 tiles.
-constexpr int kLds = 2 * 65536;
+// LDS of the dual 256 x 128 tiles' main loop: 2 stages of a 64-k slice, 48 KB each.
 constexpr int kLdsDual = 2 * (32768 + 16384);
-// The 256 x 256 kernels (the gradient products and pass 1) run 8 waves, two per
-// SIMD, each 128 x 64 of the tile (4 x 2 accumulators, 128 registers): while one
-// wave of a SIMD waits for its slice data the other issues its MFMAs (6-7%
-// faster than 4 waves of 128 x 128 on the same main loop); each MFMA is then
-// followed by up to three of the slice's memory instructions.
-constexpr int kWideThreads = 512;
-constexpr int kWideMem = 3;
 // pass 2's epilogue in the same LDS: row bases, (S, Q) partials, the tile's
 // binary16 p (rows padded to 272 bytes: the two half-waves' rows, 4 apart, fall
 // on different banks) and its tie words
@@ -76,10 +68,11 @@ static_assert(kTileT + 256 * 4 * 4 <= kLdsDual, "pass 2 epilogue exceeds the mai
 // min(K, (s + 1) kslice)) (kslice a multiple of the 64-k slice) by moving the
 // operands' bases to its first k, and writes its product (ACC = false) to
 // C + s * split_stride.
-template <bool AK, bool BK, bool ACC>
+// TC: float, or uint16_t for a bf16 C (rounded to nearest even once, from the whole sum).
+template <bool AK, bool BK, bool ACC, typename TC = float>
 __global__ __attribute__((amdgpu_flat_work_group_size(kWideThreads, kWideThreads), amdgpu_waves_per_eu(2, 2)))
 void gemm_bf16_kernel(const uint16_t* __restrict__ A, int64_t lda, int64_t a_end, const uint16_t* __restrict__ B,
-                      int64_t ldb, int64_t b_end, float* __restrict__ C, int64_t ldc, int M, int N, int K,
+                      int64_t ldb, int64_t b_end, TC* __restrict__ C, int64_t ldc, int M, int N, int K,
                       int tiles_m, int tiles_n, int splits, int kslice, int64_t split_stride) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   int tm, tn;
@@ -123,28 +116,35 @@ void gemm_bf16_kernel(const uint16_t* __restrict__ A, int64_t lda, int64_t a_end
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int m = m0 + wm + 32 * i + mm::acc_row(r, lane);
-          old[r] = (m < M && n < N) ? C[(int64_t)m * ldc + n] : 0.0f;
+          old[r] = (m < M && n < N) ? load1(C + (int64_t)m * ldc + n) : 0.0f;
         }
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int m = m0 + wm + 32 * i + mm::acc_row(r, lane);
-        if (m < M && n < N) C[(int64_t)m * ldc + n] = ACC ? old[r] + acc[i][j][r] : acc[i][j][r];
+        if (m < M && n < N) store1(C + (int64_t)m * ldc + n, ACC ? old[r] + acc[i][j][r] : acc[i][j][r]);
       }
     }
   }
 }
 
-template <bool AK, bool BK, bool ACC>
+// bytes from each operand's start to the end of its last stored row
+template <bool AK>
+int64_t a_end_of(const GemmArgs& g) {
+  return g.a_end ? g.a_end : 2 * (AK ? (g.M - 1) * g.lda + g.K : (g.K - 1) * g.lda + g.M);
+}
+template <bool BK>
+int64_t b_end_of(const GemmArgs& g) {
+  return g.b_end ? g.b_end : 2 * (BK ? (g.N - 1) * g.ldb + g.K : (g.K - 1) * g.ldb + g.N);
+}
+
+template <bool AK, bool BK, bool ACC, typename TC = float>
 hipError_t launch_gemm_t(const GemmArgs& g, hipStream_t st) {
   const int tiles_m = (int)((g.M + mm::kBM - 1) / mm::kBM);
   const int tiles_n = (int)((g.N + 255) / 256);
-  // bytes from each operand's start to the end of its last stored row
-  const int64_t a_end = 2 * (AK ? (g.M - 1) * g.lda + g.K : (g.K - 1) * g.lda + g.M);
-  const int64_t b_end = 2 * (BK ? (g.N - 1) * g.ldb + g.K : (g.K - 1) * g.ldb + g.N);
-  hipLaunchKernelGGL((gemm_bf16_kernel<AK, BK, ACC>), dim3(mm::grid_for(tiles_m, tiles_n)), dim3(kWideThreads), 0, st,
-                     g.A, g.lda, a_end, g.B, g.ldb, b_end, g.C, g.ldc, (int)g.M, (int)g.N, (int)g.K, tiles_m,
-                     tiles_n, 1, (int)g.K, (int64_t)0);
+  hipLaunchKernelGGL((gemm_bf16_kernel<AK, BK, ACC, TC>), dim3(mm::grid_for(tiles_m, tiles_n)), dim3(kWideThreads), 0,
+                     st, g.A, g.lda, a_end_of<AK>(g), g.B, g.ldb, b_end_of<BK>(g), reinterpret_cast<TC*>(g.C), g.ldc,
+                     (int)g.M, (int)g.N, (int)g.K, tiles_m, tiles_n, 1, (int)g.K, (int64_t)0);
   return hipGetLastError();
 }
 
@@ -166,13 +166,11 @@ template <bool AK, bool BK>
 hipError_t launch_gemm_split(const GemmArgs& g, hipStream_t st) {
   const int tiles_m = (int)((g.M + mm::kBM - 1) / mm::kBM);
   const int tiles_n = (int)((g.N + 255) / 256);
-  const int64_t a_end = 2 * (AK ? (g.M - 1) * g.lda + g.K : (g.K - 1) * g.lda + g.M);
-  const int64_t b_end = 2 * (BK ? (g.N - 1) * g.ldb + g.K : (g.K - 1) * g.ldb + g.N);
   const int64_t per = (g.K + g.splits - 1) / g.splits;
   const int kslice = (int)((per + mm::kBK - 1) / mm::kBK * mm::kBK);
   const int splits = (int)((g.K + kslice - 1) / kslice);  // no empty split
   hipLaunchKernelGGL((gemm_bf16_kernel<AK, BK, false>), dim3(mm::grid_for(tiles_m, tiles_n * splits)),
-                     dim3(kWideThreads), 0, st, g.A, g.lda, a_end, g.B, g.ldb, b_end, g.partials, g.N, (int)g.M,
+                     dim3(kWideThreads), 0, st, g.A, g.lda, a_end_of<AK>(g), g.B, g.ldb, b_end_of<BK>(g), g.partials, g.N, (int)g.M,
                      (int)g.N, (int)g.K, tiles_m, tiles_n, splits, kslice, g.M * g.N);
   if (hipError_t e = hipGetLastError()) return e;
   const int64_t total = g.M * g.N;
@@ -204,84 +202,6 @@ struct DualArgs {
   uint32_t* ties;                     // TV with gradients and a teacher: (rows, tie_words(V)) tie bits
   int tiles_m, tiles_n;
 };
-
-// Reductions over the 32 lanes of each half-wave (the 32 columns of one
-// accumulator row), on the vector ALU: two quad permutations and two rotations
-// inside each row of 16 lanes (DPP), then the gfx950 swap of rows 0 <-> 1 and
-// 2 <-> 3.  Every lane ends with the reduction of its half; the sum's
-// association order is fixed, so the half's first lane always sees the same
-// value for the same data.
-template <int CTRL>
-__device__ __forceinline__ float dpp_mov(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
-}
-__device__ __forceinline__ float swap16(float v, float* other) {
-  const unsigned u = __float_as_uint(v);
-  const auto pr = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  // the elements go through scalars: this compiler's __builtin_bit_cast of an
-  // element of the returned pair reads element 0 whatever the index
-  const unsigned lo = pr[0], hi = pr[1];
-  *other = __uint_as_float(hi);
-  return __uint_as_float(lo);
-}
-__device__ __forceinline__ float half_max(float v) {
-  v = fmaxf(v, dpp_mov<0xB1>(v));   // quad_perm [1, 0, 3, 2]
-  v = fmaxf(v, dpp_mov<0x4E>(v));   // quad_perm [2, 3, 0, 1]
-  v = fmaxf(v, dpp_mov<0x124>(v));  // row_ror 4
-  v = fmaxf(v, dpp_mov<0x128>(v));  // row_ror 8
-  float hi;
-  const float lo = swap16(v, &hi);
-  return fmaxf(lo, hi);
-}
-__device__ __forceinline__ float half_sum(float v) {
-  v += dpp_mov<0xB1>(v);
-  v += dpp_mov<0x4E>(v);
-  v += dpp_mov<0x124>(v);
-  v += dpp_mov<0x128>(v);
-  float hi;
-  const float lo = swap16(v, &hi);
-  return lo + hi;
-}
-
-// Row sums of a 32 x 32 accumulator block (one column per lane of each
-// half-wave, v[r] the lane's value in row r of its half, r = 0..15), all rows at
-// once: at the level of lane bit b every lane keeps half of its rows (those
-// its bit b selects), sends the other half to its partner (the lane differing
-// only in bit b) and adds what it receives.  Bit 4: the row-pair swap, two rows
-// an instruction; bit 3: row_ror 8; bits 0 and 1: quad permutations; then one
-// row per lane is left, and bit 2 (a swizzle) completes its sum.  Lane L of a
-// half ends with the total of row xsum_row(L) = b1 + 2 b0 + 4 b3 + 8 b4 (lanes
-// L and L ^ 4 the same row).  The association order is fixed.
-__device__ __forceinline__ int xsum_row(int lane) {
-  return ((lane >> 1) & 1) | ((lane & 1) << 1) | (((lane >> 3) & 1) << 2) | (((lane >> 4) & 1) << 3);
-}
-template <int CTRL>
-__device__ __forceinline__ float xsum_level(float lo, float hi, bool bit) {
-  const float keep = bit ? hi : lo, send = bit ? lo : hi;
-  return keep + dpp_mov<CTRL>(send);
-}
-__device__ __forceinline__ float xsum16(const float (&v)[16], int lane) {
-  float w[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    // rows 0 and 2 of v[k] stay, rows 1 and 3 receive v[k + 8] of rows 0 and 2,
-    // and the reverse in the second result: a lane of row 0 gets v[k] of both
-    // partners, a lane of row 1 v[k + 8] of both
-    const auto pr = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 8]), false, false);
-    const unsigned a = pr[0], b = pr[1];  // copied out: see swap16
-    w[k] = __uint_as_float(a) + __uint_as_float(b);
-  }
-  const bool b3 = (lane >> 3) & 1, b0 = lane & 1, b1 = (lane >> 1) & 1;
-  float u[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) u[k] = xsum_level<0x128>(w[k], w[k + 4], b3);  // row_ror 8
-  float t[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) t[k] = xsum_level<0xB1>(u[k], u[k + 2], b0);    // quad_perm [1, 0, 3, 2]
-  const float x = xsum_level<0x4E>(t[0], t[1], b1);                           // quad_perm [2, 3, 0, 1]
-  // lane ^ 4 within each 32 lanes: and-mask 31, or-mask 0, xor-mask 4
-  return x + __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, x), 0x101F));
-}
 
 // Per-row (max, sum-exp) of one tensor's tile values for the wave's 128 rows x
 // 32 NJ columns (the maxima reduced row by row, the sums 16 rows at a time),
@@ -809,6 +729,10 @@ hipError_t launch_gemm_bf16(const GemmArgs& g, hipStream_t st) {
   if (g.splits > 1) {
     if (!g.partials || !g.a_kc) return hipErrorInvalidValue;  // the lm_head path's layouts only
     return g.b_kc ? launch_gemm_split<true, true>(g, st) : launch_gemm_split<true, false>(g, st);
+  }
+  if (g.c_bf16) {  // the gradients' layouts only
+    if (g.b_kc || g.accumulate) return hipErrorInvalidValue;
+    return g.a_kc ? launch_gemm_t<true, false, false, uint16_t>(g, st) : launch_gemm_t<false, false, false, uint16_t>(g, st);
   }
   if (g.a_kc) {
     if (g.b_kc) return g.accumulate ? launch_gemm_t<true, true, true>(g, st) : launch_gemm_t<true, true, false>(g, st);

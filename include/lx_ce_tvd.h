@@ -697,6 +697,35 @@ lx_status lx_ce_kd_forward_backward(const void* student, int64_t ld_student, con
                                     void* stream);
 
 /*
+ * The same loss, or cross entropy alone, from hidden states and the lm_head's weight, in pieces of the vocabulary: z =
+ * x w^T is never stored, and of the gradient of the logits there is one piece of `piece` columns (bf16) at a time.
+ *
+ * - x bf16 (BT, H), w bf16 (V, H), row-major, 16-byte aligned; H a multiple of 8, at most 2^22.  Any V and BT.
+ * - K == 0: cross entropy alone (ids, top, lse_rest, kd, state may be NULL; g_kd, grad_kd_rows are not used, and
+ *   temperature is 1).  Otherwise target, ids .. state as above.
+ * - grad_x (BT, H) and grad_w (V, H), fp32 or bf16 (grad_dt), 16-byte aligned, each optional (NULL: not computed;
+ *   both NULL: the loss alone); both OVERWRITTEN.  Sums are fp32; a bf16 gradient is rounded once, from the
+ *   whole sum.  The gradient of the logits enters both products rounded to bf16.
+ * - A row whose gradient is NaN (as above) makes its row of grad_x NaN, and since grad_w sums over rows, every
+ *   element of grad_w.
+ * - piece: 1 to 2^22 columns, rounded up to a multiple of 256.
+ * - BT == 0 sets grad_w to 0.
+ * Workspace: at least lx_ce_kd_linear_workspace_bytes(...) bytes, 256-byte aligned: per row 16 bytes for 256 logits
+ *   and 12 K, and with grads 2 bytes for each column of a piece and 4 H (16 times as much where a product has
+ *   few tiles).
+ * Errors : as above; LX_ERR_UNSUPPORTED_DTYPE for a grad_dt that is neither.
+ */
+size_t lx_ce_kd_linear_workspace_bytes(int64_t BT, int64_t V, int64_t H, int64_t K, int64_t piece, int grads);
+
+lx_status lx_ce_kd_linear_forward_backward(const void* x, const void* w, int64_t H, const int64_t* target,
+                                           const int32_t* ids, const float* top, const float* lse_rest, int64_t BT,
+                                           int64_t V, int64_t K, int64_t ignore_index, float temperature, float* ce,
+                                           float* kd, float* lse, float* state, void* grad_x, void* grad_w,
+                                           lx_dtype grad_dt, float g_ce, float g_kd, const float* grad_ce_rows,
+                                           const float* grad_kd_rows, const float* g_scale, int64_t piece,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * ---------------------------------------------------------------------------
  * Reference streams: the practical HBM ceilings the loss kernels are measured
  * against (not part of the loss).  They move bytes the way the loss kernels

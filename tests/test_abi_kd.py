@@ -108,3 +108,36 @@ def test_top_logits():
     q = lx.lx_top_logits_workspace_bytes
     assert q(0, 100, 8) == q(4, 0, 8) == q(4, 100, 0) == q(4, 100, 257) == 0
     assert q(1, 2 ** 31 - 1, 256) < 1 << 20
+
+
+NEED_LIN = lx.lx_ce_kd_linear_workspace_bytes(4, 1000, 64, 8, 512, True)
+
+
+def linear(x=A, w=A * 2, H=64, t=A * 3, ids=A * 4, top=A * 5, rest=A * 6, BT=4, V=1000, K=8, T=1.0, ce=A * 7, kd=A * 8,
+           lse=A * 9, state=A * 10, gx=A * 11, gw=A * 12, gdt=1, cr=None, kr=None, gs=None, piece=512, ws=A * 13, wsb=NEED_LIN):
+    return L.lx_ce_kd_linear_forward_backward(x, w, H, t, ids, top, rest, BT, V, K, -100, T, ce, kd, lse, state, gx, gw, gdt,
+                                              1.0, 1.0, cr, kr, gs, piece, ws, wsb, None)
+
+
+def test_linear():
+    assert linear(BT=0, gw=None) == lx.LX_OK
+    assert linear(gdt=2) == lx.LX_ERR_UNSUPPORTED_DTYPE
+    for kw in (dict(BT=-1), dict(BT=2 ** 31), dict(V=0), dict(V=2 ** 31), dict(H=0), dict(H=60), dict(H=2 ** 22 + 8), dict(K=-1),
+               dict(K=257), dict(T=0.0), dict(piece=0), dict(piece=2 ** 22 + 1), dict(x=None), dict(w=None), dict(x=A + 8),
+               dict(w=A * 2 + 2), dict(t=None), dict(ids=None), dict(top=None), dict(ce=None), dict(kd=None), dict(lse=None),
+               dict(state=None), dict(state=A * 10 + 8), dict(gx=A * 11 + 8), dict(gw=A * 12 + 4), dict(cr=A * 14 + 2),
+               dict(kr=A * 14 + 2), dict(gs=A * 14 + 2), dict(BT=2 ** 30, V=2 ** 30), dict(BT=0, gw=A * 12 + 4),
+               dict(K=0, ce=None), dict(K=0, lse=None), dict(K=0, t=None)):
+        assert linear(**kw) == BAD, kw
+    for kw in (dict(ce=A), dict(kd=A * 2), dict(lse=A * 3), dict(state=A * 4), dict(gx=A * 5), dict(gw=A * 6), dict(ce=A * 8),
+               dict(gx=A * 12), dict(ws=A * 2), dict(cr=A * 11), dict(kr=A * 12), dict(gs=A * 12)):
+        assert linear(**kw) == ALIAS, kw
+    assert linear(ws=None) == linear(wsb=NEED_LIN - 1) == linear(ws=A * 13 + 128) == WS
+    q = lx.lx_ce_kd_linear_workspace_bytes
+    assert q(0, 1000, 64, 8, 512, True) == q(4, 0, 64, 8, 512, True) == q(4, 1000, 60, 8, 512, True) == 0
+    assert q(4, 1000, 64, 8, 512, False) < q(4, 1000, 64, 8, 512, True)
+    # one piece of the gradient of the logits, sums and grad_x: far below the logits
+    assert q(8192, 151936, 4096, 64, 8192, True) < 8192 * 151936 * 2 // 4
+    assert lx.lx_ce_kd_linear_piece(8192, 151936) * 8192 <= 1 << 27
+    assert lx.lx_ce_kd_linear_piece(1, 100) == 100
+    assert lx.lx_ce_kd_linear_piece(0, 2 ** 31 - 1) <= 1 << 22
