@@ -28,14 +28,6 @@ namespace lx {
 
 namespace {
 
-// The logits of the columns whose bit is set count as masked.
-__device__ __forceinline__ void leave_out_bits(uint32_t byte, float (&x)[8]) {
-  if (byte) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (byte >> e) & 1u ? ninf() : x[e];
-  }
-}
-
 // ------------------------------------------------------------------ forward
 
 // Rows of up to 2^18 columns are one workgroup's (its mask is 32 KB); 512 threads, H groups at once.
@@ -260,40 +252,6 @@ hipError_t launch_kd_forward_t(const KdArgs& a, double c64, hipStream_t st) {
 
 // ------------------------------------------------------------------ the gradient of a row's columns
 
-// At column v of the ids: the q of every entry that names it, in their order.
-__device__ __forceinline__ float grad_named(const RowGrad& g, float x, float c, int v, const int* id, const float* q,
-                                            int K) {
-  float sum = 0.0f;
-  for (int j = 0; j < K; ++j) sum += id[j] == v ? q[j] : 0.0f;
-  return grad_named(g, x, c, sum);
-}
-
-// 16 bytes at any element (gfx950 stores them at any address).
-typedef u32x4_t __attribute__((aligned(2))) loose16_t;
-template <typename T>
-__device__ __forceinline__ void store8_any(T* p, const float (&o)[8]) {
-  unsigned w[sizeof(T) * 2];
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (__is_same(T, _Float16)) w[e] = pack_f16x2_rne(o[2 * e], o[2 * e + 1]);
-      else w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
-    }
-  }
-  loose16_t* to = reinterpret_cast<loose16_t*>(p);
-#pragma unroll
-  for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-    __builtin_nontemporal_store((u32x4_t){w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]}, to + k);
-}
-template <typename T>
-__device__ __forceinline__ void fill8_any(T* p, uint32_t bits) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) store_bits1(p + e, bits);
-}
-
 // ------------------------------------------------------------------ backward
 
 constexpr int kBwdThreads = 256;
@@ -308,7 +266,7 @@ __global__ __launch_bounds__(kBwdThreads) void kd_backward_kernel(KdLoss l, KdGr
   __shared__ uint32_t bits[kBwdColumns / 32];
   __shared__ int id[kKdMaxTop];
   __shared__ float q[kKdMaxTop];
-  __shared__ int bad_any;
+  __shared__ int bad_any, twice;
   const int64_t tile = large_bid();
   const int64_t r = tile / chunks;
   if (r >= l.BT) return;
@@ -335,7 +293,7 @@ __global__ __launch_bounds__(kBwdThreads) void kd_backward_kernel(KdLoss l, KdGr
   }
   const float4 state = *reinterpret_cast<const float4*>(l.state + kKdState * r);
   if (tid < kBwdColumns / 32) bits[tid] = 0u;
-  if (tid == 0) bad_any = 0;
+  if (tid == 0) bad_any = twice = 0;
   __syncthreads();
   if (tid < K) {
     float u;
@@ -343,30 +301,36 @@ __global__ __launch_bounds__(kBwdThreads) void kd_backward_kernel(KdLoss l, KdGr
     const int v = entry_id(l, r, tid, u, bad);
     id[tid] = v;
     if (bad) bad_any = 1;
-    if (v >= 0) {
-      mark(bits, v, lo, hi);
-      q[tid] = exp2_hw(__builtin_fmaf(u, c, -state.w * kLog2e));
-    }
+    if (mark(bits, v, lo, hi)) twice = 1;
+    q[tid] = exp2_hw(__builtin_fmaf(u, c, -state.w * kLog2e));
   }
   const RowGrad rg = row_grad<TEMP>(g, l, r, lse, state.x, state.y, state.z);
   __syncthreads();
   const bool bad = bad_any != 0;
+  if (twice) {  // a token's masses, in the order of its entries, at each of them
+    float sum = 0.0f;
+    if (tid < K)
+      for (int i = 0; i < K; ++i) sum += id[i] == id[tid] ? q[i] : 0.0f;
+    __syncthreads();
+    if (tid < K) q[tid] = sum;
+    __syncthreads();
+  }
 #pragma unroll
   for (int k = 0; k < kBwdHeld; ++k) {
     const int at = k * (kBwdThreads * 8) + tid * 8;
     const int64_t v = lo + at;
-    if (v >= hi) continue;
-    const uint32_t byte = reinterpret_cast<const uint8_t*>(bits)[at >> 3];
+    const uint32_t byte = v < hi ? reinterpret_cast<const uint8_t*>(bits)[at >> 3] : 0u;
     float x[8], o[8];
     if (v + 8 <= l.V) gr[k].get(x);
     else load_edge(row, v, l.V, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = grad_outside<TEMP>(rg, x[e], c);
-    if (byte) {
+    for_named(byte, (int)v, id, K, [&](int lane, int place, int j) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if ((byte >> e) & 1u) o[e] = grad_named(rg, x[e], c, (int)v + e, id, q, K);
-    }
+        if ((tid & 63) == lane && e == place) o[e] = grad_named(rg, x[e], c, q[j]);
+    });
+    if (v >= hi) continue;
     const int64_t rel = t - v;
     if (rel >= 0 && rel < 8) {
 #pragma unroll
@@ -401,8 +365,6 @@ size_t kd_forward_workspace_bytes(int64_t BT, int64_t V) {
   return s.chunks == 1 ? 0 : ((size_t)(BT * s.chunks) * 16 + 255) & ~(size_t)255;
 }
 
-size_t kd_step_workspace_bytes(int64_t BT, int64_t V) { return kd_forward_workspace_bytes(BT, V); }
-
 #define LX_BY_TYPE(F, ...)                                                                     \
   const double c64 = scale_of(a.l.temperature);                                                \
   const bool temp = a.l.temperature != 1.0f;                                                   \
@@ -414,10 +376,5 @@ size_t kd_step_workspace_bytes(int64_t BT, int64_t V) { return kd_forward_worksp
 
 hipError_t launch_kd_forward(const KdArgs& a, Dt dt, hipStream_t st) { LX_BY_TYPE(launch_kd_forward_t) }
 hipError_t launch_kd_backward(const KdArgs& a, Dt dt, hipStream_t st) { LX_BY_TYPE(launch_kd_backward_t) }
-
-hipError_t launch_kd_step(const KdArgs& a, Dt dt, hipStream_t st) {
-  if (hipError_t e = launch_kd_forward(a, dt, st)) return e;
-  return launch_kd_backward(a, dt, st);
-}
 
 }  // namespace lx

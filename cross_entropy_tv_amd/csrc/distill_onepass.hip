@@ -1,0 +1,463 @@
+// Cross entropy and distillation from a teacher's top logits: the loss and the gradient of the logits in one pass.
+//
+// A row is cut into up to 16 members' chunks, each held in the registers of one workgroup between the row's sums and
+// the gradient, so every logit is read once.  Tiles are taken by ticket: a workgroup waits only for members
+// of its own row, whose tickets lie within 16 of its own, so with 16 workgroups running the exchange cannot
+// deadlock; every wait is bounded, and one that gives up leaves NaN in the row.
+//
+//   1. the chunk is requested, and while it arrives the ids that fall into it are marked in LDS and wave 0 forms
+//      the teacher's masses;
+//   2. each thread's sum of 2^(c z - n) outside the ids, n from its exact maximum (no sum can overflow).  At
+//      temperature 1 the exponentials stay in the registers; else the logits stay, packed, and a second sum is taken
+//      at temperature 1;
+//   3. a member publishes its sums, those of its ids' logits, and its parts of kd and of the target's logit, and waits
+//      for the row's;
+//   4. the gradient of its chunk.
+//
+// Every member has read its chunk and its ids' logits before it publishes, and stores after all have published: the
+// gradient may overwrite the logits.  What is published is one 64-bit word a slot, preset to a pattern that no
+// result has, so that a slot is its own flag.
+//
+// What bounds it: reading and writing the logits once.
+#include "common.hpp"
+#include "distill.hpp"
+#include "kd_row.hpp"
+#include "sum2.hpp"
+
+namespace lx {
+
+namespace {
+
+constexpr int kStepThreads = 256;
+constexpr int kStepWaves = kStepThreads / 64;
+constexpr int kStepGroups = 15;    // groups of 8 a thread holds (five members of 151936 columns)
+constexpr int kStepShort = 2;      // of a short row
+constexpr int kMaxMembers = 16;
+constexpr int kSlots = 4;          // words a member publishes
+constexpr uint64_t kEmpty = ~0ull;
+constexpr unsigned kSpinLimit = 1u << 18;
+constexpr int64_t kStepTiles = 512;  // workgroups that few rows are cut into
+
+struct StepArgs {
+  KdLoss l;
+  KdGrad g;
+  const void* z;
+  void* grad;
+  int64_t ldz, ldg;
+  double c64;
+  int members, gpm;  // workgroups a row, groups a member
+  uint64_t* slots;   // [BT][members][kSlots]
+  unsigned* ticket;
+};
+
+struct Plan {
+  int members, gpm;
+};
+// members 0: rows too long
+Plan plan_of(int64_t BT, int64_t V) {
+  const int64_t groups = (V + 7) / 8, most = (int64_t)kStepThreads * kStepGroups;
+  const int64_t fit = (groups + most - 1) / most;
+  int64_t fill = (kStepTiles + BT - 1) / BT;
+  if (fill > groups / (2 * kStepThreads)) fill = groups / (2 * kStepThreads);
+  int64_t k = fit > fill ? fit : fill;
+  if (fit > kMaxMembers || BT > ((int64_t)1 << 26)) return Plan{0, 0};
+  if (k > kMaxMembers) k = kMaxMembers;
+  const int64_t gpm = (groups + k - 1) / k;
+  return Plan{(int)((groups + gpm - 1) / gpm), (int)gpm};
+}
+
+// Lanes [0, n) of wave 0 wait for slots sl[0 .. n) and keep what they read in got.  Whether the wait gave up.
+__device__ __forceinline__ bool wait_slots(const uint64_t* sl, int n, uint64_t* got) {
+  const int lane = tid_x();
+  const bool mine = lane < n;
+  uint64_t v = kEmpty;
+  bool gave_up = false;
+  __builtin_amdgcn_s_setprio(2);
+  for (unsigned spins = 0;; ++spins) {
+    if (mine && v == kEmpty) v = fetch(sl + lane);
+    if (__all(!mine || v != kEmpty)) break;
+    if (spins > kSpinLimit) {
+      gave_up = true;
+      break;
+    }
+    __builtin_amdgcn_s_sleep(1);
+  }
+  __builtin_amdgcn_s_setprio(0);
+  if (mine) got[lane] = v;
+  return gave_up;
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ Sum2 sum_of(uint64_t v) { return Sum2{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))}; }
+
+struct StepLds {
+  uint32_t bits[kStepThreads * kStepGroups / 4];
+  int id[kKdMaxTop];    // in the chunk, else -1
+  float u[kKdMaxTop], z[kKdMaxTop], q[kKdMaxTop];
+  int all[kKdMaxTop];   // ids wherever they are, -1: left out
+  Sum2 red[2][kStepWaves];
+  uint64_t got[kMaxMembers * kSlots];
+  unsigned tile;
+  int bad, twice;       // an id past the vocabulary; one given twice
+  // the row's sums as the gradient takes them, from wave 0
+  float out, rest_n;    // outside the ids: factor of 2^(c z - rest_n)
+  float ce1, n1;        // ce's part: factor of 2^(z log2 e - n1)
+  float kd, n;          // at the ids: factor of 2^(c z - n) / kkd
+  int state;            // 0, 1: no unmasked logit, 2: NaN
+};
+
+// G groups of 8 a thread.
+template <typename T, bool TEMP, int G>
+__global__ __attribute__((amdgpu_flat_work_group_size(kStepThreads, kStepThreads), amdgpu_waves_per_eu(G > 4 ? 3 : 4)))
+void kd_step_kernel(StepArgs a) {
+  // (fp32 logits fill the registers: their exponentials are formed twice)
+  constexpr bool kKeepLogits = TEMP || sizeof(T) == 4;
+  __shared__ StepLds s;
+  const int tid = tid_x();
+  const KdLoss& l = a.l;
+  const int K = (int)l.K, members = a.members;
+  __builtin_amdgcn_s_setprio(3);  // until the chunk is requested: ahead of the arithmetic of other workgroups
+  unsigned tile = large_bid();
+#pragma unroll
+  for (int k = 0; k < (G + 3) / 4; ++k)
+    if (tid + k * kStepThreads < kStepThreads * G / 4) s.bits[tid + k * kStepThreads] = 0u;
+  if (tid == 0) {
+    s.bad = s.twice = 0;
+    if (members > 1) s.tile = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (members > 1) tile = s.tile;
+  const int64_t r = tile / (unsigned)members;
+  if (r >= l.BT) return;
+  const int member = (int)(tile - (unsigned)r * (unsigned)members);
+  const int V = (int)l.V;
+  // the chunk's columns [first, end) and groups (the last may reach past the row's end)
+  const int first = member * a.gpm * 8;
+  const int count = min(a.gpm, (V + 7) / 8 - member * a.gpm);
+  const int end = V - first < 8 * count ? V : first + 8 * count;
+  const T* row = static_cast<const T*>(a.z) + r * a.ldz;
+  T* out = static_cast<T*>(a.grad) + r * a.ldg;
+  // the ids before the chunk: loads return in order
+  const int64_t t = l.target[r];
+  int my_id = -1;
+  float my_u = 0.0f;
+  bool my_bad = false;
+  if (tid < K) my_id = entry_id(l, r, tid, my_u, my_bad);
+  if (t == l.ignore_index) {
+    if (member == 0 && tid == 0) store_row(l, r, RowResult{});
+    for (int v = first + 8 * tid; v < end; v += 8 * kStepThreads) {
+      const float zero[8] = {};
+      if (v + 8 <= V) store8_any(out + v, zero);
+      else
+        for (int e = v; e < V; ++e) store_bits1(out + e, 0u);
+    }
+    return;
+  }
+
+  // ---- the chunk, and meanwhile the ids
+  // The thread's k-th group: columns v .. v + 7, read from base = v or, at the row's end, V - 8, where its first d
+  // places are other groups' columns (d = 8: nothing).  A row of fewer than 8 columns is its group's last V places.
+  auto place = [&](int k, int& base) {
+    const int at = tid + k * kStepThreads;
+    const int v = first + 8 * at;
+    base = min(v, V - 8);
+    return at < count ? v - base : 8;
+  };
+  Group<T> h[G];
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    if (k * kStepThreads < count) {
+      if (V >= 8) {
+        int base;
+        place(k, base);
+        h[k].load(row + base);
+      } else {
+        T few[8] = {};
+        for (int e = 0; e < V; ++e) few[8 - V + e] = row[e];
+        h[k].load(few);
+      }
+    }
+  }
+  __builtin_amdgcn_s_setprio(0);
+  const bool t_here = t >= first && t < end;
+  float my_z = ninf(), my_zt = 0.0f;  // (wanted after the sums)
+  if (tid < K) {
+    const bool here = my_id >= first && my_id < end;
+    if (mark(s.bits, my_id, first, end)) s.twice = 1;
+    s.id[tid] = here ? my_id : -1;
+    s.all[tid] = my_id;
+    s.u[tid] = my_u;
+    if (my_bad) s.bad = 1;
+    if (here) my_z = load1(row + my_id);
+  }
+  if (tid == 0 && t_here) my_zt = load1(row + t);
+  __syncthreads();
+  Teacher te{};
+  double ua[kLaneTop], q[kLaneTop];
+  if (tid < 64) te = teacher_of(s.all, s.u, K, tid, a.c64, l.rest ? l.rest[r] : ninf(), ua, q);
+
+  // ---- sums
+  const float c = (float)a.c64;
+  const uint8_t* mask = reinterpret_cast<const uint8_t*>(s.bits);
+  // logits that are not the thread's count as masked
+  auto get = [&](int k, float(&x)[8]) {
+    launder(h[k]);
+    h[k].get(x);
+    int base;
+    const int d = place(k, base);
+    if (d > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = e < d ? ninf() : x[e];
+    }
+  };
+  // the mask's byte of a group, in its places
+  auto named = [&](int k) {
+    int base;
+    const int d = place(k, base);
+    return d < 8 ? (uint32_t)mask[tid + k * kStepThreads] << d : 0u;
+  };
+  float ez[kKeepLogits ? 1 : G][8];
+  float m = ninf(), m1 = ninf();
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    if (k * kStepThreads < count) {
+      float x[8];
+      get(k, x);
+      if (TEMP) m1 = fmaxf(m1, max8(x));
+      leave_out_bits(named(k), x);
+      m = fmaxf(m, max8(x));
+      if (!kKeepLogits) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ez[k][e] = x[e];
+      }
+    }
+  }
+  Sum2 sum{ref_for(m, c), 0.0f}, sum1{ref_for(m1, kLog2e), 0.0f};
+  float b0 = 0.0f, b1 = 0.0f, c0 = 0.0f, c1 = 0.0f;
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    if (k * kStepThreads < count) {
+      if (kKeepLogits) {
+        float x[8];
+        get(k, x);
+        if (TEMP) sum8(x, kLog2e, sum1.n, c0, c1);
+        leave_out_bits(named(k), x);
+        sum8(x, c, sum.n, b0, b1);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          b0 += ez[k][e] = exp2_hw(__builtin_fmaf(ez[k][e], c, -sum.n));
+          b1 += ez[k][e + 1] = exp2_hw(__builtin_fmaf(ez[k][e + 1], c, -sum.n));
+        }
+      }
+    }
+  }
+  const float mine_n = sum.n;
+  sum = wave_sum2(Sum2{sum.n, b0 + b1});
+  if (TEMP) sum1 = wave_sum2(Sum2{sum1.n, c0 + c1});
+  if ((tid & 63) == 0) {
+    s.red[0][tid >> 6] = sum;
+    s.red[1][tid >> 6] = sum1;
+  }
+  if (tid < K) s.z[tid] = my_z;
+  __syncthreads();
+
+  // ---- wave 0: the member's part, the exchange, the row
+  Sum2 rest{}, whole{}, all{};
+  double terms = 0.0;
+  float zt = my_zt;
+  bool gave_up = false;
+  if (tid < 64) {
+    Sum2 top{floor_of(c), 0.0f};
+    const bool twice = s.twice != 0;
+#pragma unroll
+    for (int k = 0; k < kLaneTop; ++k) {
+      const int j = tid + 64 * k;
+      if (j < K) {
+        s.q[j] = (float)q[k];  // (a token's whole mass, see below)
+        if (s.id[j] >= 0) {
+          const float z = s.z[j];
+          if (q[k] > 0.0) terms += z < kMasked ? kInf64 : q[k] * (ua[k] - (double)z * a.c64);
+          if (!(z < kMasked) && !(twice && named_before(s.id, j))) {
+            const double t2 = (double)z * a.c64, n = __builtin_rint(t2);
+            add_sum2(top, Sum2{(float)n, exp2_hw((float)(t2 - n))});
+          }
+        }
+      }
+    }
+    if (twice) {  // the masses of a token's entries, in their order, at each of them
+      float whole_q[kLaneTop] = {};
+#pragma unroll
+      for (int k = 0; k < kLaneTop; ++k) {
+        const int j = tid + 64 * k;
+        if (j < K)
+          for (int i = 0; i < K; ++i) whole_q[k] += s.id[i] == s.id[j] ? s.q[i] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < kLaneTop; ++k)
+        if (tid + 64 * k < K) s.q[tid + 64 * k] = whole_q[k];
+    }
+    top = wave_sum2(top);
+    terms = wave_sum64(terms);
+    rest = s.red[0][0];
+    whole = s.red[1][0];
+    for (int w = 1; w < kStepWaves; ++w) {
+      add_sum2(rest, s.red[0][w]);
+      if (TEMP) add_sum2(whole, s.red[1][w]);
+    }
+    zt = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(zt)));
+    if (members > 1) {
+      uint64_t* slots = a.slots + r * (int64_t)(members * kSlots);
+      const uint64_t w = tid == 0   ? pack2(rest.n, rest.s)
+                         : tid == 1 ? pack2(top.n, top.s)
+                         : tid == 2 ? pack2((float)terms, zt)
+                                    : pack2(whole.n, whole.s);
+      if (tid < kSlots) publish(slots + member * kSlots + tid, w);
+      gave_up = wait_slots(slots, members * kSlots, s.got);
+      const bool mine = tid < members;  // lane k has member k's
+      const Sum2 nothing{floor_of(c), 0.0f};
+      const Sum2 part = mine ? sum_of(s.got[tid * kSlots + 2]) : Sum2{0.0f, 0.0f};
+      rest = wave_sum2(mine ? sum_of(s.got[tid * kSlots]) : nothing);
+      top = wave_sum2(mine ? sum_of(s.got[tid * kSlots + 1]) : nothing);
+      if (TEMP) whole = wave_sum2(mine ? sum_of(s.got[tid * kSlots + 3]) : Sum2{floor_of(kLog2e), 0.0f});
+      terms = wave_sum64((double)part.n);
+      zt = wave_sum32(part.s);
+    }
+    all = top;
+    add_sum2(all, rest);
+    if (!TEMP) whole = all;
+    if (tid == 0) {
+      const RowFactors f = row_factors(a.g, l, r);
+      const bool any = all.s > 0.0f;
+      const float p_rest = any ? rest.s * exp2_hw(rest.n - all.n) / all.s : 0.0f;
+      const float off = te.any ? p_rest - (float)te.q_rest : 0.0f;
+      const float part = f.kkd * off + (TEMP ? 0.0f : f.kce * p_rest);
+      s.out = rest.s > 0.0f ? part / rest.s : 0.0f;
+      s.rest_n = rest.n;
+      s.ce1 = any ? f.kce / whole.s : 0.0f;
+      s.n1 = whole.n;
+      s.kd = any ? 1.0f / all.s : 0.0f;
+      s.n = all.n;
+      s.state = gave_up || s.bad || t < 0 || t >= V ? 2 : any ? 0 : 1;
+    }
+  }
+  __syncthreads();
+  if (tid < 64 && member == 0) {  // the row's results
+    const double lr = log2_of(rest), lz = log2_of(all);
+    RowResult o = row_result(l, te, s.bad != 0, t, zt, terms, lz, lr, TEMP ? log2_of(whole) * kLn2 : lz * kLn2);
+    if (gave_up) o.bad = 3u;
+    if (tid == 0) store_row(l, r, o);
+  }
+
+  // ---- the gradient
+  const RowFactors f = row_factors(a.g, l, r);
+  const float g_out = s.out, rest_n = s.rest_n, ce1 = s.ce1, n1 = s.n1;
+  const float alpha = g_out * exp2_hw(mine_n - rest_n);
+  const int state = s.state;
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    if (k * kStepThreads < count) {
+      int base;
+      const int d = place(k, base);
+      float w[8];
+      if (kKeepLogits) {
+        float x[8];
+        launder(h[k]);
+        h[k].get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          w[e] = g_out * exp2_hw(__builtin_fmaf(x[e], c, -rest_n));
+          if (TEMP) w[e] = __builtin_fmaf(ce1, exp2_hw(__builtin_fmaf(x[e], kLog2e, -n1)), w[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = ez[k][e] * alpha;
+      }
+      for_named(named(k), base, s.id, K, [&](int lane, int at, int j) {
+        const float x = s.z[j];
+        const float v = ce1 * exp2_hw(__builtin_fmaf(x, kLog2e, -n1)) +
+                        f.kkd * (s.kd * exp2_hw(__builtin_fmaf(x, c, -s.n)) - s.q[j]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = (tid & 63) == lane && e == at ? v : w[e];
+      });
+      if (d == 8) continue;
+      if (t_here && (unsigned)((int)t - base) < 8u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = e == (int)t - base ? w[e] - f.kce : w[e];
+      }
+      if (state == 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 0.0f;
+      }
+      if (d == 0 && state != 2) {
+        store8_any(out + base, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (e >= d) {
+            if (state == 2) store_bits1(out + base + e, kQNaN32);
+            else store1(out + base + e, w[e]);
+          }
+        }
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void kd_step_init_kernel(uint64_t* slots, int64_t n, unsigned* ticket) {
+  const int64_t i0 = (int64_t)bid_x() * 256 + tid_x();
+  if (i0 == 0) *ticket = 0u;
+  for (int64_t i = i0; i < n; i += (int64_t)nblocks_x() * 256) slots[i] = kEmpty;
+}
+
+template <typename T, bool TEMP>
+hipError_t launch_t(const KdArgs& a, const Plan& p, hipStream_t st) {
+  StepArgs s{};
+  s.l = a.l; s.g = a.g; s.z = a.z; s.grad = a.grad; s.ldz = a.ldz; s.ldg = a.ldg;
+  s.c64 = scale_of(a.l.temperature);
+  s.members = p.members; s.gpm = p.gpm;
+  (void)hipGetLastError();
+  if (p.members > 1) {
+    const int64_t n = a.l.BT * p.members * kSlots, blocks = (n + 255) / 256;
+    s.slots = static_cast<uint64_t*>(a.workspace);
+    s.ticket = reinterpret_cast<unsigned*>(s.slots + n);
+    kd_step_init_kernel<<<dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st>>>(s.slots, n, s.ticket);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  const dim3 grid = large_grid(a.l.BT * p.members);
+  if (p.gpm <= kStepShort * kStepThreads) kd_step_kernel<T, TEMP, kStepShort><<<grid, dim3(kStepThreads), 0, st>>>(s);
+  else kd_step_kernel<T, TEMP, kStepGroups><<<grid, dim3(kStepThreads), 0, st>>>(s);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_dt(const KdArgs& a, const Plan& p, hipStream_t st) {
+  return a.l.temperature != 1.0f ? launch_t<T, true>(a, p, st) : launch_t<T, false>(a, p, st);
+}
+
+}  // namespace
+
+size_t kd_step_workspace_bytes(int64_t BT, int64_t V) {
+  if (BT <= 0 || V <= 0) return 0;
+  const Plan p = plan_of(BT, V);
+  if (p.members == 0) return kd_forward_workspace_bytes(BT, V);
+  if (p.members == 1) return 0;
+  return ((size_t)(BT * p.members) * kSlots * 8 + 4 + 255) & ~(size_t)255;
+}
+
+hipError_t launch_kd_step(const KdArgs& a, Dt dt, hipStream_t st) {
+  const Plan p = plan_of(a.l.BT, a.l.V);
+  if (p.members == 0) {  // rows too long to be held: the forward, then the backward
+    if (hipError_t e = launch_kd_forward(a, dt, st)) return e;
+    return launch_kd_backward(a, dt, st);
+  }
+  switch (dt) {
+    case Dt::BF16: return launch_dt<uint16_t>(a, p, st);
+    case Dt::F16: return launch_dt<_Float16>(a, p, st);
+    default: return launch_dt<float>(a, p, st);
+  }
+}
+
+}  // namespace lx

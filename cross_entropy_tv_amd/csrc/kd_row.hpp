@@ -52,7 +52,8 @@ __device__ __forceinline__ Teacher teacher_of(const int* id, const float* u, int
   double s = 0.0;
 #pragma unroll
   for (int k = 0; k < kLaneTop; ++k) {
-    q[k] = exp2_64(a[k] - ref);
+    q[k] = 0.0;
+    if (64 * k < K) q[k] = exp2_64(a[k] - ref);  // (uniform: the lanes' k-th entries may all be missing)
     s += q[k];
   }
   t.q_rest = exp2_64(t.lr - ref);
@@ -107,6 +108,28 @@ __device__ __forceinline__ void store_row(const KdLoss& l, int64_t r, const RowR
   *reinterpret_cast<float4*>(l.state + kKdState * r) = make_float4(o.lse_t, o.lse_rest, o.off, o.norm);
 }
 
+// The row's results from its log-sums in base 2 (lz: the whole row at the temperature, -inf: no unmasked logit; lr:
+// outside the ids), l1 = log sum exp(z), terms = sum_j q_j (c u_j - c z_j).
+__device__ __forceinline__ RowResult row_result(const KdLoss& l, const Teacher& te, bool bad, int64_t t, float zt,
+                                                double terms, double lz, double lr, double l1) {
+  RowResult o{};
+  if (!(lz > -kInf64)) {
+    o.lse = o.lse_t = ninf();
+    return o;
+  }
+  terms += (lz - te.lq) * (1.0 - te.q_rest);
+  if (te.q_rest > 0.0) terms += te.q_rest * ((te.lr - te.lq) - (lr - lz));
+  o.kd = te.any ? (float)(terms * kLn2) : 0.0f;
+  o.lse = (float)l1;
+  o.ce = zt < kMasked ? -ninf() : (float)(l1 - (double)zt);
+  o.lse_t = (float)(lz * kLn2);
+  o.lse_rest = lr > -kInf64 ? (float)(lr * kLn2) : 0.0f;
+  o.off = te.any ? (float)(exp2_64(lr - lz) - te.q_rest) : 0.0f;
+  o.norm = (float)(te.lq * kLn2);
+  o.bad = (t >= 0 && t < l.V ? 0u : 1u) | (bad ? 2u : 0u);
+  return o;
+}
+
 // One wave: the row's results from its sums (a: outside the ids at the temperature; TEMP, a1: all columns at
 // temperature 1) and entries, valid in every lane; q: the masses of the lane's entries.  t, zt: the target and its
 // logit.
@@ -127,11 +150,7 @@ __device__ __forceinline__ RowResult finish_row(const KdLoss& l, int64_t r, cons
     m = __builtin_fmax(m, t2[k]);
   }
   m = wave_max64(m);
-  RowResult o{};
-  if (!(m > -kInf64)) {  // no unmasked logit
-    o.lse = o.lse_t = ninf();
-    return o;
-  }
+  if (!(m > -kInf64)) return row_result(l, te, bad, t, zt, 0.0, m, lr, 0.0);
   double s = 0.0, terms = 0.0;
 #pragma unroll
   for (int k = 0; k < kLaneTop; ++k) {
@@ -142,21 +161,8 @@ __device__ __forceinline__ RowResult finish_row(const KdLoss& l, int64_t r, cons
     }
   }
   s = wave_sum64(s) + exp2_64(lr - m);
-  terms = wave_sum64(terms);
   const double lz = m + log2_64(s);
-  const double l1 = TEMP ? log2_of(a1) * kLn2 : lz * kLn2;
-  // kd: terms holds sum_j q_j (c u_j - c z_j)
-  terms += (lz - te.lq) * (1.0 - te.q_rest);
-  if (te.q_rest > 0.0) terms += te.q_rest * ((te.lr - te.lq) - (lr - lz));
-  o.kd = te.any ? (float)(terms * kLn2) : 0.0f;
-  o.lse = (float)l1;
-  o.ce = zt < kMasked ? -ninf() : (float)(l1 - (double)zt);
-  o.lse_t = (float)(lz * kLn2);
-  o.lse_rest = lr > -kInf64 ? (float)(lr * kLn2) : 0.0f;
-  o.off = te.any ? (float)(exp2_64(lr - lz) - te.q_rest) : 0.0f;
-  o.norm = (float)(te.lq * kLn2);
-  o.bad = (t >= 0 && t < l.V ? 0u : 1u) | (bad ? 2u : 0u);
-  return o;
+  return row_result(l, te, bad, t, zt, wave_sum64(terms), lz, lr, TEMP ? log2_of(a1) * kLn2 : lz * kLn2);
 }
 
 // ------------------------------------------------------------------ a row's gradient
@@ -169,13 +175,23 @@ struct RowGrad {
   float out;          // outside: factor of 2^(c z - nr); at T = 1 with ce's part
 };
 
+// k g_ce and k g_kd / T with the row's factors.
+struct RowFactors {
+  float kce, kkd;
+};
+__device__ __forceinline__ RowFactors row_factors(const KdGrad& g, const KdLoss& l, int64_t r) {
+  const float k = g.g_scale ? *g.g_scale : 1.0f;
+  return RowFactors{k * g.g_ce * (g.ce_rows ? g.ce_rows[r] : 1.0f),
+                    k * g.g_kd * (g.kd_rows ? g.kd_rows[r] : 1.0f) / l.temperature};
+}
+
 template <bool TEMP>
 __device__ __forceinline__ RowGrad row_grad(const KdGrad& g, const KdLoss& l, int64_t r, float lse, float lse_t,
                                             float lse_rest, float off) {
-  const float k = g.g_scale ? *g.g_scale : 1.0f;
+  const RowFactors f = row_factors(g, l, r);
   RowGrad o;
-  o.kce = k * g.g_ce * (g.ce_rows ? g.ce_rows[r] : 1.0f);
-  o.kkd = k * g.g_kd * (g.kd_rows ? g.kd_rows[r] : 1.0f) / l.temperature;
+  o.kce = f.kce;
+  o.kkd = f.kkd;
   o.n1 = lse * kLog2e;
   o.nz = lse_t * kLog2e;
   o.nr = lse_rest * kLog2e;
@@ -197,9 +213,65 @@ __device__ __forceinline__ float grad_named(const RowGrad& g, float x, float c, 
   return g.kce * exp2_hw(__builtin_fmaf(x, kLog2e, -g.n1)) + g.kkd * (exp2_hw(__builtin_fmaf(x, c, -g.nz)) - q);
 }
 
-// The mask of a row's ids over the columns [lo, hi) in LDS: bit v - lo of `bits`.
-__device__ __forceinline__ void mark(uint32_t* bits, int64_t v, int64_t lo, int64_t hi) {
-  if (v >= lo && v < hi) atomicOr(bits + ((v - lo) >> 5), 1u << ((v - lo) & 31));
+// The mask of a row's ids over the columns [lo, hi) in LDS: bit v - lo of `bits`.  Whether it was set before.
+__device__ __forceinline__ bool mark(uint32_t* bits, int64_t v, int64_t lo, int64_t hi) {
+  if (v < lo || v >= hi) return false;
+  const uint32_t bit = 1u << ((v - lo) & 31);
+  return (atomicOr(bits + ((v - lo) >> 5), bit) & bit) != 0u;
+}
+
+// The logits of the columns whose bit is set count as masked.
+__device__ __forceinline__ void leave_out_bits(uint32_t byte, float (&x)[8]) {
+  if (byte) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (byte >> e) & 1u ? ninf() : x[e];
+  }
+}
+
+// 16 bytes at any element (gfx950 stores them at any address).
+typedef u32x4_t __attribute__((aligned(2))) loose16_t;
+template <typename T>
+__device__ __forceinline__ void store8_any(T* p, const float (&o)[8]) {
+  unsigned w[sizeof(T) * 2];
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (__is_same(T, _Float16)) w[e] = pack_f16x2_rne(o[2 * e], o[2 * e + 1]);
+      else w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+    }
+  }
+  loose16_t* to = reinterpret_cast<loose16_t*>(p);
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+    __builtin_nontemporal_store((u32x4_t){w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]}, to + k);
+}
+// For every column of the lanes' groups that an entry names, one after the other: f(lane, e, j), with column base + e of
+// that lane's group the one that entry j names (the first of them).  byte: the mask of the lane's group.  All lanes of
+// the wave call it, and f, together: an entry is found by all comparing theirs, and not by a walk over K of them.
+template <typename F>
+__device__ __forceinline__ void for_named(uint32_t byte, int base, const int* id, int K, F f) {
+  const int lane = tid_x() & 63;
+  uint64_t some = __ballot(byte != 0u);
+  while (some) {
+    const int at = __builtin_ctzll(some);
+    some &= some - 1;
+    uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)byte, at);
+    const int v = __builtin_amdgcn_readlane(base, at);
+    while (b) {
+      const int e = __builtin_ctz(b);
+      b &= b - 1;
+      for (int k = 0; k < K; k += 64) {
+        const uint64_t match = __ballot(k + lane < K && id[k + lane] == v + e);
+        if (match) {
+          f(at, e, k + __builtin_ctzll(match));
+          break;
+        }
+      }
+    }
+  }
 }
 
 }  // namespace lx
