@@ -53,9 +53,9 @@ struct StepArgs {
 struct Plan {
   int members, gpm;
 };
-// members 0: rows too long
+// members 0: rows too long.  The last member also has the V % 8 columns behind the row's whole groups.
 Plan plan_of(int64_t BT, int64_t V) {
-  const int64_t groups = (V + 7) / 8, most = (int64_t)kStepThreads * kStepGroups;
+  const int64_t groups = V < 8 ? 1 : V / 8, most = (int64_t)kStepThreads * kStepGroups;
   const int64_t fit = (groups + most - 1) / most;
   int64_t fill = (kStepTiles + BT - 1) / BT;
   if (fill > groups / (2 * kStepThreads)) fill = groups / (2 * kStepThreads);
@@ -93,7 +93,12 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 __device__ __forceinline__ Sum2 sum_of(uint64_t v) { return Sum2{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))}; }
 
 struct StepLds {
-  uint32_t bits[kStepThreads * kStepGroups / 4];
+  uint32_t bits[kStepThreads * kStepGroups / 4 + 1];  // of the chunk's columns, those behind its groups last
+  // Groups that hold an id: their numbers in the order in which they were found, and by number what becomes of their
+  // columns.
+  uint16_t number[kStepThreads * kStepGroups + 1];
+  float value[kKdMaxTop][8];
+  int groups;
   int id[kKdMaxTop];    // in the chunk, else -1
   float u[kKdMaxTop], z[kKdMaxTop], q[kKdMaxTop];
   int all[kKdMaxTop];   // ids wherever they are, -1: left out
@@ -120,11 +125,9 @@ void kd_step_kernel(StepArgs a) {
   const int K = (int)l.K, members = a.members;
   __builtin_amdgcn_s_setprio(3);  // until the chunk is requested: ahead of the arithmetic of other workgroups
   unsigned tile = large_bid();
-#pragma unroll
-  for (int k = 0; k < (G + 3) / 4; ++k)
-    if (tid + k * kStepThreads < kStepThreads * G / 4) s.bits[tid + k * kStepThreads] = 0u;
+  for (int w = tid; w < kStepThreads * G / 4 + 1; w += kStepThreads) s.bits[w] = 0u;
   if (tid == 0) {
-    s.bad = s.twice = 0;
+    s.bad = s.twice = s.groups = 0;
     if (members > 1) s.tile = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
@@ -133,10 +136,11 @@ void kd_step_kernel(StepArgs a) {
   if (r >= l.BT) return;
   const int member = (int)(tile - (unsigned)r * (unsigned)members);
   const int V = (int)l.V;
-  // the chunk's columns [first, end) and groups (the last may reach past the row's end)
+  // the chunk's whole groups and columns [first, end)
   const int first = member * a.gpm * 8;
-  const int count = min(a.gpm, (V + 7) / 8 - member * a.gpm);
-  const int end = V - first < 8 * count ? V : first + 8 * count;
+  const int count = min(a.gpm, V / 8 - member * a.gpm);
+  const int behind = member == members - 1 ? V - first - 8 * count : 0;  // columns behind its groups
+  const int end = first + 8 * count + behind;
   const T* row = static_cast<const T*>(a.z) + r * a.ldz;
   T* out = static_cast<T*>(a.grad) + r * a.ldg;
   // the ids before the chunk: loads return in order
@@ -147,45 +151,35 @@ void kd_step_kernel(StepArgs a) {
   if (tid < K) my_id = entry_id(l, r, tid, my_u, my_bad);
   if (t == l.ignore_index) {
     if (member == 0 && tid == 0) store_row(l, r, RowResult{});
-    for (int v = first + 8 * tid; v < end; v += 8 * kStepThreads) {
-      const float zero[8] = {};
-      if (v + 8 <= V) store8_any(out + v, zero);
-      else
-        for (int e = v; e < V; ++e) store_bits1(out + e, 0u);
-    }
+    const float zero[8] = {};
+    for (int g = tid; g < count; g += kStepThreads) store8_any(out + first + 8 * g, zero);
+    if (tid < behind) store_bits1(out + first + 8 * count + tid, 0u);
     return;
   }
 
   // ---- the chunk, and meanwhile the ids
-  // The thread's k-th group: columns v .. v + 7, read from base = v or, at the row's end, V - 8, where its first d
-  // places are other groups' columns (d = 8: nothing).  A row of fewer than 8 columns is its group's last V places.
-  auto place = [&](int k, int& base) {
-    const int at = tid + k * kStepThreads;
-    const int v = first + 8 * at;
-    base = min(v, V - 8);
-    return at < count ? v - base : 8;
-  };
+  // (groups tid + k 256; past the chunk's end a group of it again, which counts for nothing)
   Group<T> h[G];
+  const T* mine = row + first;
+  const int last = max(count - 1, 0) * 8;
+  float extra = ninf();  // the thread's column behind the groups
+  if (count > 0) {
 #pragma unroll
-  for (int k = 0; k < G; ++k) {
-    if (k * kStepThreads < count) {
-      if (V >= 8) {
-        int base;
-        place(k, base);
-        h[k].load(row + base);
-      } else {
-        T few[8] = {};
-        for (int e = 0; e < V; ++e) few[8 - V + e] = row[e];
-        h[k].load(few);
-      }
-    }
+    for (int k = 0; k < G; ++k)
+      if (k * kStepThreads < count) h[k].load(mine + min(8 * (tid + k * kStepThreads), last));
   }
+  if (tid < behind) extra = load1(mine + 8 * count + tid);
   __builtin_amdgcn_s_setprio(0);
   const bool t_here = t >= first && t < end;
   float my_z = ninf(), my_zt = 0.0f;  // (wanted after the sums)
   if (tid < K) {
     const bool here = my_id >= first && my_id < end;
-    if (mark(s.bits, my_id, first, end)) s.twice = 1;
+    if (here) {
+      const int at = my_id - first;
+      const uint32_t old = atomicOr(&s.bits[at >> 5], 1u << (at & 31));
+      if (old >> (at & 31) & 1u) s.twice = 1;
+      if ((old >> (at & 24) & 0xffu) == 0u) s.number[at >> 3] = (uint16_t)atomicAdd(&s.groups, 1);
+    }
     s.id[tid] = here ? my_id : -1;
     s.all[tid] = my_id;
     s.u[tid] = my_u;
@@ -201,32 +195,21 @@ void kd_step_kernel(StepArgs a) {
   // ---- sums
   const float c = (float)a.c64;
   const uint8_t* mask = reinterpret_cast<const uint8_t*>(s.bits);
-  // logits that are not the thread's count as masked
   auto get = [&](int k, float(&x)[8]) {
     launder(h[k]);
     h[k].get(x);
-    int base;
-    const int d = place(k, base);
-    if (d > 0) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = e < d ? ninf() : x[e];
-    }
   };
-  // the mask's byte of a group, in its places
-  auto named = [&](int k) {
-    int base;
-    const int d = place(k, base);
-    return d < 8 ? (uint32_t)mask[tid + k * kStepThreads] << d : 0u;
-  };
+  auto is_mine = [&](int k) { return tid + k * kStepThreads < count; };
+  const bool extra_named = tid < behind && (mask[count] >> tid & 1u);
   float ez[kKeepLogits ? 1 : G][8];
-  float m = ninf(), m1 = ninf();
+  float m = extra_named ? ninf() : extra, m1 = extra;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
-    if (k * kStepThreads < count) {
+    if (is_mine(k)) {
       float x[8];
       get(k, x);
       if (TEMP) m1 = fmaxf(m1, max8(x));
-      leave_out_bits(named(k), x);
+      leave_out_bits(mask[tid + k * kStepThreads], x);
       m = fmaxf(m, max8(x));
       if (!kKeepLogits) {
 #pragma unroll
@@ -235,15 +218,16 @@ void kd_step_kernel(StepArgs a) {
     }
   }
   Sum2 sum{ref_for(m, c), 0.0f}, sum1{ref_for(m1, kLog2e), 0.0f};
-  float b0 = 0.0f, b1 = 0.0f, c0 = 0.0f, c1 = 0.0f;
+  float b0 = extra_named ? 0.0f : exp2_hw(__builtin_fmaf(extra, c, -sum.n)), b1 = 0.0f;
+  float c0 = TEMP ? exp2_hw(__builtin_fmaf(extra, kLog2e, -sum1.n)) : 0.0f, c1 = 0.0f;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
-    if (k * kStepThreads < count) {
+    if (is_mine(k)) {
       if (kKeepLogits) {
         float x[8];
         get(k, x);
         if (TEMP) sum8(x, kLog2e, sum1.n, c0, c1);
-        leave_out_bits(named(k), x);
+        leave_out_bits(mask[tid + k * kStepThreads], x);
         sum8(x, c, sum.n, b0, b1);
       } else {
 #pragma unroll
@@ -354,55 +338,59 @@ void kd_step_kernel(StepArgs a) {
   // ---- the gradient
   const RowFactors f = row_factors(a.g, l, r);
   const float g_out = s.out, rest_n = s.rest_n, ce1 = s.ce1, n1 = s.n1;
-  const float alpha = g_out * exp2_hw(mine_n - rest_n);
+  if (tid < K && s.id[tid] >= 0) {  // at the ids
+    const int at = s.id[tid] - first;
+    const float v = ce1 * exp2_hw(__builtin_fmaf(my_z, kLog2e, -n1)) +
+                    f.kkd * (s.kd * exp2_hw(__builtin_fmaf(my_z, c, -s.n)) - s.q[tid]);
+    s.value[s.number[at >> 3]][at & 7] = v;
+  }
+  __syncthreads();
   const int state = s.state;
+  if (state != 0) {  // (nothing or NaN)
+    const uint32_t fill = state == 2 ? kQNaN32 : 0u;
+    for (int v = first + tid; v < end; v += kStepThreads) store_bits1(out + v, fill);
+    return;
+  }
+  const int t_at = t_here ? (int)t - first : -8;
+  auto outside = [&](float x) {
+    const float w = g_out * exp2_hw(__builtin_fmaf(x, c, -rest_n));
+    return TEMP ? __builtin_fmaf(ce1, exp2_hw(__builtin_fmaf(x, kLog2e, -n1)), w) : w;
+  };
+  const float alpha = g_out * exp2_hw(mine_n - rest_n);
+  T* to = out + first;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
-    if (k * kStepThreads < count) {
-      int base;
-      const int d = place(k, base);
+    if (is_mine(k)) {
+      const int at = tid + k * kStepThreads;
+      const uint32_t byte = mask[at];
       float w[8];
       if (kKeepLogits) {
         float x[8];
-        launder(h[k]);
-        h[k].get(x);
+        get(k, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          w[e] = g_out * exp2_hw(__builtin_fmaf(x[e], c, -rest_n));
-          if (TEMP) w[e] = __builtin_fmaf(ce1, exp2_hw(__builtin_fmaf(x[e], kLog2e, -n1)), w[e]);
-        }
+        for (int e = 0; e < 8; ++e) w[e] = outside(x[e]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = ez[k][e] * alpha;
       }
-      for_named(named(k), base, s.id, K, [&](int lane, int at, int j) {
-        const float x = s.z[j];
-        const float v = ce1 * exp2_hw(__builtin_fmaf(x, kLog2e, -n1)) +
-                        f.kkd * (s.kd * exp2_hw(__builtin_fmaf(x, c, -s.n)) - s.q[j]);
+      if (byte) {
+        const float4* v = reinterpret_cast<const float4*>(s.value[s.number[at]]);
+        const float4 lo = v[0], hi = v[1];
+        const float n[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = (tid & 63) == lane && e == at ? v : w[e];
-      });
-      if (d == 8) continue;
-      if (t_here && (unsigned)((int)t - base) < 8u) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = e == (int)t - base ? w[e] - f.kce : w[e];
+        for (int e = 0; e < 8; ++e) w[e] = byte >> e & 1u ? n[e] : w[e];
       }
-      if (state == 1) {
+      if (at == t_at >> 3) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 0.0f;
+        for (int e = 0; e < 8; ++e) w[e] = e == (t_at & 7) ? w[e] - f.kce : w[e];
       }
-      if (d == 0 && state != 2) {
-        store8_any(out + base, w);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (e >= d) {
-            if (state == 2) store_bits1(out + base + e, kQNaN32);
-            else store1(out + base + e, w[e]);
-          }
-        }
-      }
+      store8_any(to + 8 * at, w);
     }
+  }
+  if (tid < behind) {
+    float w = extra_named ? s.value[s.number[count]][tid] : outside(extra);
+    if (8 * count + tid == t_at) w -= f.kce;
+    store1(to + 8 * count + tid, w);
   }
 }
 
