@@ -7,9 +7,8 @@
 //
 //   1. the chunk is requested, and while it arrives the ids that fall into it are marked in LDS and wave 0 forms
 //      the teacher's masses;
-//   2. each thread's sum of 2^(c z - n) outside the ids, n from its exact maximum (no sum can overflow).  At
-//      temperature 1 the exponentials stay in the registers; else the logits stay, packed, and a second sum is taken
-//      at temperature 1;
+//   2. each thread's sum of 2^(c z - n) outside the ids, n from its exact maximum (no sum can overflow), and, at another
+//      temperature than 1, that of 2^(z log2 e - n1);
 //   3. a member publishes its sums, those of its ids' logits, and its parts of kd and of the target's logit, and waits
 //      for the row's;
 //   4. the gradient of its chunk.
@@ -18,10 +17,18 @@
 // gradient may overwrite the logits.  What is published is one 64-bit word a slot, preset to a pattern that no
 // result has, so that a slot is its own flag.
 //
-// What bounds it: reading and writing the logits once.
+// The logits stay in the registers as they lie in memory, and their exponentials are formed twice: kept in fp32 they
+// would take twice the registers, three workgroups a compute unit instead of four, which cost more (8192 x 151936 bf16:
+// 965 against 860 us) than 1.2 G exponentials.
+//
+// What bounds it: reading and writing the logits once, by workgroups whose life is a chain (ids, chunk, sums, exchange,
+// stores: 17 us) that four of them a compute unit cover: 860 us, 5.8 TB/s (the same pass of cross entropy alone takes
+// 832).  Loads and stores are non-temporal (with plain loads 1400).  Code size matters as well: what happens at the ids
+// once stood in every group's code.
 #include "common.hpp"
 #include "distill.hpp"
 #include "kd_row.hpp"
+#include "mm.hpp"
 #include "sum2.hpp"
 
 namespace lx {
@@ -31,7 +38,8 @@ namespace {
 constexpr int kStepThreads = 256;
 constexpr int kStepWaves = kStepThreads / 64;
 constexpr int kStepGroups = 15;    // groups of 8 a thread holds (five members of 151936 columns)
-constexpr int kStepShort = 2;      // of a short row
+constexpr int kStepShort = 2;      // of a short row,
+constexpr int kStepMiddle = 6;     // and of a middling one
 constexpr int kMaxMembers = 16;
 constexpr int kSlots = 4;          // words a member publishes
 constexpr uint64_t kEmpty = ~0ull;
@@ -113,25 +121,26 @@ struct StepLds {
   int state;            // 0, 1: no unmasked logit, 2: NaN
 };
 
-// G groups of 8 a thread.
+// G groups of 8 a thread (0: rows of fewer than 8 columns).
 template <typename T, bool TEMP, int G>
-__global__ __attribute__((amdgpu_flat_work_group_size(kStepThreads, kStepThreads), amdgpu_waves_per_eu(G > 4 ? 3 : 4)))
+__global__ __attribute__((amdgpu_flat_work_group_size(kStepThreads, kStepThreads), amdgpu_waves_per_eu(sizeof(T) == 4 && G > 6 ? 3 : 4)))
 void kd_step_kernel(StepArgs a) {
-  // (fp32 logits fill the registers: their exponentials are formed twice)
-  constexpr bool kKeepLogits = TEMP || sizeof(T) == 4;
   __shared__ StepLds s;
   const int tid = tid_x();
   const KdLoss& l = a.l;
   const int K = (int)l.K, members = a.members;
   __builtin_amdgcn_s_setprio(3);  // until the chunk is requested: ahead of the arithmetic of other workgroups
   unsigned tile = large_bid();
-  for (int w = tid; w < kStepThreads * G / 4 + 1; w += kStepThreads) s.bits[w] = 0u;
+#pragma unroll
+  for (int w = 0; w <= kStepThreads * G / 4; w += kStepThreads)
+    if (w + tid <= kStepThreads * G / 4) s.bits[w + tid] = 0u;
   if (tid == 0) {
     s.bad = s.twice = s.groups = 0;
     if (members > 1) s.tile = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
-  if (members > 1) tile = s.tile;
+  // (uniform: what is read by row goes through scalar loads, which the wait for the chunk does not hold back)
+  if (members > 1) tile = (unsigned)__builtin_amdgcn_readfirstlane((int)s.tile);
   const int64_t r = tile / (unsigned)members;
   if (r >= l.BT) return;
   const int member = (int)(tile - (unsigned)r * (unsigned)members);
@@ -143,12 +152,7 @@ void kd_step_kernel(StepArgs a) {
   const int end = first + 8 * count + behind;
   const T* row = static_cast<const T*>(a.z) + r * a.ldz;
   T* out = static_cast<T*>(a.grad) + r * a.ldg;
-  // the ids before the chunk: loads return in order
   const int64_t t = l.target[r];
-  int my_id = -1;
-  float my_u = 0.0f;
-  bool my_bad = false;
-  if (tid < K) my_id = entry_id(l, r, tid, my_u, my_bad);
   if (t == l.ignore_index) {
     if (member == 0 && tid == 0) store_row(l, r, RowResult{});
     const float zero[8] = {};
@@ -157,23 +161,28 @@ void kd_step_kernel(StepArgs a) {
     return;
   }
 
-  // ---- the chunk, and meanwhile the ids
-  // (groups tid + k 256; past the chunk's end a group of it again, which counts for nothing)
-  Group<T> h[G];
+  // ---- the ids, then the chunk (loads return in order); no load is conditional, so that the compiler knows how
+  // many are in flight behind the one that it waits for
+  const int entry = min(tid, K - 1);
+  const int raw_id = l.ids[r * K + entry];
+  const float my_u = l.top[r * K + entry];
+  // groups tid + k 256; past the chunk's end its last one again, which counts for nothing
+  Group<T> h[G > 0 ? G : 1];
   const T* mine = row + first;
-  const int last = max(count - 1, 0) * 8;
-  float extra = ninf();  // the thread's column behind the groups
-  if (count > 0) {
+  if constexpr (G > 0) {
+    const int last = 8 * (count - 1);
 #pragma unroll
-    for (int k = 0; k < G; ++k)
-      if (k * kStepThreads < count) h[k].load(mine + min(8 * (tid + k * kStepThreads), last));
+    for (int k = 0; k < G; ++k) h[k].load_once(mine + min(8 * (tid + k * kStepThreads), last));
   }
-  if (tid < behind) extra = load1(mine + 8 * count + tid);
   __builtin_amdgcn_s_setprio(0);
   const bool t_here = t >= first && t < end;
-  float my_z = ninf(), my_zt = 0.0f;  // (wanted after the sums)
+  const bool my_bad = tid < K && raw_id >= V;
+  const int my_id = tid >= K || my_bad || raw_id < 0 || my_u < kMasked ? -1 : raw_id;
+  const bool here = my_id >= first && my_id < end;
+  // (wanted after the sums)
+  const T raw_z = row[here ? my_id : 0], raw_zt = row[t_here ? (int)t : 0];
+  const T raw_extra = row[tid < behind ? first + 8 * count + tid : 0];
   if (tid < K) {
-    const bool here = my_id >= first && my_id < end;
     if (here) {
       const int at = my_id - first;
       const uint32_t old = atomicOr(&s.bits[at >> 5], 1u << (at & 31));
@@ -184,10 +193,9 @@ void kd_step_kernel(StepArgs a) {
     s.all[tid] = my_id;
     s.u[tid] = my_u;
     if (my_bad) s.bad = 1;
-    if (here) my_z = load1(row + my_id);
   }
-  if (tid == 0 && t_here) my_zt = load1(row + t);
-  __syncthreads();
+  const RowFactors f = row_factors(a.g, l, r);
+  mm::lds_barrier();  // (the chunk stays in flight)
   Teacher te{};
   double ua[kLaneTop], q[kLaneTop];
   if (tid < 64) te = teacher_of(s.all, s.u, K, tid, a.c64, l.rest ? l.rest[r] : ninf(), ua, q);
@@ -201,7 +209,7 @@ void kd_step_kernel(StepArgs a) {
   };
   auto is_mine = [&](int k) { return tid + k * kStepThreads < count; };
   const bool extra_named = tid < behind && (mask[count] >> tid & 1u);
-  float ez[kKeepLogits ? 1 : G][8];
+  const float extra = tid < behind ? load1(&raw_extra) : ninf();  // the thread's column behind the groups
   float m = extra_named ? ninf() : extra, m1 = extra;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
@@ -211,10 +219,6 @@ void kd_step_kernel(StepArgs a) {
       if (TEMP) m1 = fmaxf(m1, max8(x));
       leave_out_bits(mask[tid + k * kStepThreads], x);
       m = fmaxf(m, max8(x));
-      if (!kKeepLogits) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ez[k][e] = x[e];
-      }
     }
   }
   Sum2 sum{ref_for(m, c), 0.0f}, sum1{ref_for(m1, kLog2e), 0.0f};
@@ -223,35 +227,27 @@ void kd_step_kernel(StepArgs a) {
 #pragma unroll
   for (int k = 0; k < G; ++k) {
     if (is_mine(k)) {
-      if (kKeepLogits) {
-        float x[8];
-        get(k, x);
-        if (TEMP) sum8(x, kLog2e, sum1.n, c0, c1);
-        leave_out_bits(mask[tid + k * kStepThreads], x);
-        sum8(x, c, sum.n, b0, b1);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          b0 += ez[k][e] = exp2_hw(__builtin_fmaf(ez[k][e], c, -sum.n));
-          b1 += ez[k][e + 1] = exp2_hw(__builtin_fmaf(ez[k][e + 1], c, -sum.n));
-        }
-      }
+      float x[8];
+      get(k, x);
+      if (TEMP) sum8(x, kLog2e, sum1.n, c0, c1);
+      leave_out_bits(mask[tid + k * kStepThreads], x);
+      sum8(x, c, sum.n, b0, b1);
     }
   }
-  const float mine_n = sum.n;
   sum = wave_sum2(Sum2{sum.n, b0 + b1});
   if (TEMP) sum1 = wave_sum2(Sum2{sum1.n, c0 + c1});
   if ((tid & 63) == 0) {
     s.red[0][tid >> 6] = sum;
     s.red[1][tid >> 6] = sum1;
   }
+  const float my_z = here ? load1(&raw_z) : ninf();
   if (tid < K) s.z[tid] = my_z;
   __syncthreads();
 
   // ---- wave 0: the member's part, the exchange, the row
   Sum2 rest{}, whole{}, all{};
   double terms = 0.0;
-  float zt = my_zt;
+  float zt = t_here ? load1(&raw_zt) : 0.0f;
   bool gave_up = false;
   if (tid < 64) {
     Sum2 top{floor_of(c), 0.0f};
@@ -291,7 +287,6 @@ void kd_step_kernel(StepArgs a) {
       add_sum2(rest, s.red[0][w]);
       if (TEMP) add_sum2(whole, s.red[1][w]);
     }
-    zt = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(zt)));
     if (members > 1) {
       uint64_t* slots = a.slots + r * (int64_t)(members * kSlots);
       const uint64_t w = tid == 0   ? pack2(rest.n, rest.s)
@@ -300,12 +295,12 @@ void kd_step_kernel(StepArgs a) {
                                     : pack2(whole.n, whole.s);
       if (tid < kSlots) publish(slots + member * kSlots + tid, w);
       gave_up = wait_slots(slots, members * kSlots, s.got);
-      const bool mine = tid < members;  // lane k has member k's
+      const bool lane_member = tid < members;  // lane k has member k's
       const Sum2 nothing{floor_of(c), 0.0f};
-      const Sum2 part = mine ? sum_of(s.got[tid * kSlots + 2]) : Sum2{0.0f, 0.0f};
-      rest = wave_sum2(mine ? sum_of(s.got[tid * kSlots]) : nothing);
-      top = wave_sum2(mine ? sum_of(s.got[tid * kSlots + 1]) : nothing);
-      if (TEMP) whole = wave_sum2(mine ? sum_of(s.got[tid * kSlots + 3]) : Sum2{floor_of(kLog2e), 0.0f});
+      const Sum2 part = lane_member ? sum_of(s.got[tid * kSlots + 2]) : Sum2{0.0f, 0.0f};
+      rest = wave_sum2(lane_member ? sum_of(s.got[tid * kSlots]) : nothing);
+      top = wave_sum2(lane_member ? sum_of(s.got[tid * kSlots + 1]) : nothing);
+      if (TEMP) whole = wave_sum2(lane_member ? sum_of(s.got[tid * kSlots + 3]) : Sum2{floor_of(kLog2e), 0.0f});
       terms = wave_sum64((double)part.n);
       zt = wave_sum32(part.s);
     }
@@ -313,7 +308,6 @@ void kd_step_kernel(StepArgs a) {
     add_sum2(all, rest);
     if (!TEMP) whole = all;
     if (tid == 0) {
-      const RowFactors f = row_factors(a.g, l, r);
       const bool any = all.s > 0.0f;
       const float p_rest = any ? rest.s * exp2_hw(rest.n - all.n) / all.s : 0.0f;
       const float off = te.any ? p_rest - (float)te.q_rest : 0.0f;
@@ -336,7 +330,6 @@ void kd_step_kernel(StepArgs a) {
   }
 
   // ---- the gradient
-  const RowFactors f = row_factors(a.g, l, r);
   const float g_out = s.out, rest_n = s.rest_n, ce1 = s.ce1, n1 = s.n1;
   if (tid < K && s.id[tid] >= 0) {  // at the ids
     const int at = s.id[tid] - first;
@@ -356,7 +349,6 @@ void kd_step_kernel(StepArgs a) {
     const float w = g_out * exp2_hw(__builtin_fmaf(x, c, -rest_n));
     return TEMP ? __builtin_fmaf(ce1, exp2_hw(__builtin_fmaf(x, kLog2e, -n1)), w) : w;
   };
-  const float alpha = g_out * exp2_hw(mine_n - rest_n);
   T* to = out + first;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
@@ -364,15 +356,10 @@ void kd_step_kernel(StepArgs a) {
       const int at = tid + k * kStepThreads;
       const uint32_t byte = mask[at];
       float w[8];
-      if (kKeepLogits) {
-        float x[8];
-        get(k, x);
+      float x[8];
+      get(k, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = outside(x[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = ez[k][e] * alpha;
-      }
+      for (int e = 0; e < 8; ++e) w[e] = outside(x[e]);
       if (byte) {
         const float4* v = reinterpret_cast<const float4*>(s.value[s.number[at]]);
         const float4 lo = v[0], hi = v[1];
@@ -415,7 +402,9 @@ hipError_t launch_t(const KdArgs& a, const Plan& p, hipStream_t st) {
     if (hipError_t e = hipGetLastError()) return e;
   }
   const dim3 grid = large_grid(a.l.BT * p.members);
-  if (p.gpm <= kStepShort * kStepThreads) kd_step_kernel<T, TEMP, kStepShort><<<grid, dim3(kStepThreads), 0, st>>>(s);
+  if (a.l.V < 8) kd_step_kernel<T, TEMP, 0><<<grid, dim3(kStepThreads), 0, st>>>(s);
+  else if (p.gpm <= kStepShort * kStepThreads) kd_step_kernel<T, TEMP, kStepShort><<<grid, dim3(kStepThreads), 0, st>>>(s);
+  else if (p.gpm <= kStepMiddle * kStepThreads) kd_step_kernel<T, TEMP, kStepMiddle><<<grid, dim3(kStepThreads), 0, st>>>(s);
   else kd_step_kernel<T, TEMP, kStepGroups><<<grid, dim3(kStepThreads), 0, st>>>(s);
   return hipGetLastError();
 }

@@ -12,6 +12,8 @@ constexpr double kLn2 = 0.69314718055994530942;
 
 
 typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+// 16 bytes at any element (gfx950 loads and stores them at any address).
+typedef u32x4_t __attribute__((aligned(2))) loose16_t;
 
 // ------------------------------------------------------------------ rows
 
@@ -24,6 +26,10 @@ template <>
 struct Group<uint16_t> {
   u32x4_t w;
   __device__ __forceinline__ void load(const uint16_t* p) { __builtin_memcpy(&w, p, 16); }
+  // read once: non-temporal
+  __device__ __forceinline__ void load_once(const uint16_t* p) {
+    w = __builtin_nontemporal_load(reinterpret_cast<const loose16_t*>(p));
+  }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const unsigned w0 = w.x, w1 = w.y, w2 = w.z, w3 = w.w;
     x[0] = __uint_as_float(w0 << 16); x[1] = __uint_as_float(w0 & 0xffff0000u);
@@ -36,6 +42,9 @@ template <>
 struct Group<_Float16> {
   u32x4_t w;
   __device__ __forceinline__ void load(const _Float16* p) { __builtin_memcpy(&w, p, 16); }
+  __device__ __forceinline__ void load_once(const _Float16* p) {
+    w = __builtin_nontemporal_load(reinterpret_cast<const loose16_t*>(p));
+  }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const unsigned w0 = w.x, w1 = w.y, w2 = w.z, w3 = w.w;
     unpack_f16x2(w0, x[0], x[1]); unpack_f16x2(w1, x[2], x[3]);
@@ -48,6 +57,10 @@ struct Group<float> {
   __device__ __forceinline__ void load(const float* p) {
     __builtin_memcpy(&w, p, 16);
     __builtin_memcpy(&v, p + 4, 16);
+  }
+  __device__ __forceinline__ void load_once(const float* p) {
+    w = __builtin_nontemporal_load(reinterpret_cast<const loose16_t*>(p));
+    v = __builtin_nontemporal_load(reinterpret_cast<const loose16_t*>(p + 4));
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const unsigned a[8] = {w.x, w.y, w.z, w.w, v.x, v.y, v.z, v.w};

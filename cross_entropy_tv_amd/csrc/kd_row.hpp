@@ -228,8 +228,6 @@ __device__ __forceinline__ void leave_out_bits(uint32_t byte, float (&x)[8]) {
   }
 }
 
-// 16 bytes at any element (gfx950 stores them at any address).
-typedef u32x4_t __attribute__((aligned(2))) loose16_t;
 template <typename T>
 __device__ __forceinline__ void store8_any(T* p, const float (&o)[8]) {
   unsigned w[sizeof(T) * 2];
