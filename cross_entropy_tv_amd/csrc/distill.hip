@@ -17,8 +17,7 @@
 // a few in a thousand) costs a compare.
 //
 // Sums of exponentials are taken against an integer exponent n per thread, sum 2^(c z - n): c z - n is
-// one fused multiply-add with no rounding of the reference.  n comes from the thread's first group; a sum
-// that reaches 2^100 is redone against the true maximum.
+// one fused multiply-add with no rounding of the reference.
 #include "common.hpp"
 #include "distill.hpp"
 #include "kd_row.hpp"
@@ -61,81 +60,35 @@ __device__ __forceinline__ void chunk_sums(const T* row, int64_t lo, int64_t hi,
                                            float c, Sum2& a, Sum2& a1) {
   a = Sum2{floor_of(c), 0.0f};
   a1 = Sum2{floor_of(kLog2e), 0.0f};
-  bool first = true;
-  for (int64_t b = lo; b < hi; b += (int64_t)NT * 8 * H) {
+  const int count = (int)(hi - lo);
+  row += lo;
+  const int last = (int)(V - lo) - 8;  // the last whole group that may be read
+  for (int b = tid_x() * 8; b < count; b += NT * 8 * H) {
     Group<T> g[H];
-    uint32_t byte[H];
-    if (V >= 8) {
+    if (last >= 0) {
 #pragma unroll
-      for (int k = 0; k < H; ++k) {
-        const int64_t v = b + k * (NT * 8) + tid_x() * 8;
-        g[k].load(row + (v < V - 8 ? v : V - 8));
-      }
+      for (int k = 0; k < H; ++k) g[k].load_once(row + min(b + k * (NT * 8), last));
     }
 #pragma unroll
     for (int k = 0; k < H; ++k) {
-      const int64_t v = b + k * (NT * 8) + tid_x() * 8;
-      byte[k] = v < hi ? mask[(v - lo) >> 3] : 0u;
-    }
-    // the group's logits; -inf behind the chunk's end
-    auto get = [&](int k, float(&x)[8]) {
-      const int64_t v = b + k * (NT * 8) + tid_x() * 8;
-      launder(g[k]);
-      if (v + 8 <= hi) {
-        g[k].get(x);
-      } else {
-        load_edge(row, v, hi, x);
-      }
-    };
-    if (first) {
-      float x[8];
-      get(0, x);
-      a1.n = ref_for(max8(x), kLog2e);
-      leave_out_bits(byte[0], x);
-      a.n = ref_for(max8(x), c);
-      first = false;
-    }
-    float b0 = 0.0f, b1 = 0.0f, c0 = 0.0f, c1 = 0.0f;
-#pragma unroll
-    for (int k = 0; k < H; ++k) {
-      float x[8];
-      get(k, x);
-      if (TEMP) sum8(x, kLog2e, a1.n, c0, c1);
-      leave_out_bits(byte[k], x);
-      sum8(x, c, a.n, b0, b1);
-    }
-    if (fmaxf(b0 + b1, c0 + c1) >= kRefSumLimit) {  // again, against the true maxima
-      float m = ninf(), m1 = ninf();
-#pragma unroll
-      for (int k = 0; k < H; ++k) {
+      const int v = b + k * (NT * 8);
+      if (v < count) {
         float x[8];
-        get(k, x);
-        m1 = fmaxf(m1, max8(x));
-        leave_out_bits(byte[k], x);
-        m = fmaxf(m, max8(x));
-      }
-      const float n = fmaxf(a.n, ref_for(m, c)), n1 = fmaxf(a1.n, ref_for(m1, kLog2e));
-      a = Sum2{n, a.s * exp2_hw(a.n - n)};
-      a1 = Sum2{n1, a1.s * exp2_hw(a1.n - n1)};
-      b0 = b1 = c0 = c1 = 0.0f;
-#pragma unroll
-      for (int k = 0; k < H; ++k) {
-        float x[8];
-        get(k, x);
-        if (TEMP) sum8(x, kLog2e, a1.n, c0, c1);
-        leave_out_bits(byte[k], x);
-        sum8(x, c, a.n, b0, b1);
+        if (v + 8 <= count) g[k].get(x);
+        else load_edge(row, v, count, x);  // -inf behind the end
+        if (TEMP) add_group(x, kLog2e, a1);
+        leave_out_bits(mask[v >> 3], x);
+        add_group(x, c, a);
       }
     }
-    a.s += b0 + b1;
-    if (TEMP) a1.s += c0 + c1;
   }
 }
 
 // One workgroup per (row, chunk).  A whole row (chunks == 1) is finished here; chunks leave their sums
 // in parts [row][chunk][4].
 template <typename T, bool TEMP>
-__global__ __launch_bounds__(kFwdThreads) void kd_forward_kernel(KdLoss l, const T* __restrict__ z, int64_t ldz,
+__global__ __attribute__((amdgpu_flat_work_group_size(kFwdThreads, kFwdThreads), amdgpu_waves_per_eu(sizeof(T) == 4 ? 6 : 8)))
+void kd_forward_kernel(KdLoss l, const T* __restrict__ z, int64_t ldz,
                                                                  double c64, int chunks, int64_t columns, float* parts) {
   extern __shared__ uint32_t bits[];
   constexpr int W = kFwdThreads / 64;
@@ -288,7 +241,7 @@ __global__ __launch_bounds__(kBwdThreads) void kd_backward_kernel(KdLoss l, KdGr
 #pragma unroll
     for (int k = 0; k < kBwdHeld; ++k) {
       const int64_t v = lo + k * (kBwdThreads * 8) + tid * 8;
-      gr[k].load(row + (v < l.V - 8 ? v : l.V - 8));
+      gr[k].load_once(row + (v < l.V - 8 ? v : l.V - 8));
     }
   }
   const float4 state = *reinterpret_cast<const float4*>(l.state + kKdState * r);

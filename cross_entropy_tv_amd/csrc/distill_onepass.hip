@@ -7,8 +7,8 @@
 //
 //   1. the chunk is requested, and while it arrives the ids that fall into it are marked in LDS and wave 0 forms
 //      the teacher's masses;
-//   2. each thread's sum of 2^(c z - n) outside the ids, n from its exact maximum (no sum can overflow), and, at another
-//      temperature than 1, that of 2^(z log2 e - n1);
+//   2. each thread's sum of 2^(c z - n) outside the ids and, at another temperature than 1, of 2^(z log2 e - n1) of
+//      all columns, as the chunk arrives;
 //   3. a member publishes its sums, those of its ids' logits, and its parts of kd and of the target's logit, and waits
 //      for the row's;
 //   4. the gradient of its chunk.
@@ -210,32 +210,21 @@ void kd_step_kernel(StepArgs a) {
   auto is_mine = [&](int k) { return tid + k * kStepThreads < count; };
   const bool extra_named = tid < behind && (mask[count] >> tid & 1u);
   const float extra = tid < behind ? load1(&raw_extra) : ninf();  // the thread's column behind the groups
-  float m = extra_named ? ninf() : extra, m1 = extra;
+  Sum2 sum{floor_of(c), 0.0f}, sum1{floor_of(kLog2e), 0.0f};
+  if (!extra_named) add_one(sum, extra, c);
+  if (TEMP) add_one(sum1, extra, kLog2e);
 #pragma unroll
   for (int k = 0; k < G; ++k) {
     if (is_mine(k)) {
       float x[8];
       get(k, x);
-      if (TEMP) m1 = fmaxf(m1, max8(x));
+      if (TEMP) add_group(x, kLog2e, sum1);
       leave_out_bits(mask[tid + k * kStepThreads], x);
-      m = fmaxf(m, max8(x));
+      add_group(x, c, sum);
     }
   }
-  Sum2 sum{ref_for(m, c), 0.0f}, sum1{ref_for(m1, kLog2e), 0.0f};
-  float b0 = extra_named ? 0.0f : exp2_hw(__builtin_fmaf(extra, c, -sum.n)), b1 = 0.0f;
-  float c0 = TEMP ? exp2_hw(__builtin_fmaf(extra, kLog2e, -sum1.n)) : 0.0f, c1 = 0.0f;
-#pragma unroll
-  for (int k = 0; k < G; ++k) {
-    if (is_mine(k)) {
-      float x[8];
-      get(k, x);
-      if (TEMP) sum8(x, kLog2e, sum1.n, c0, c1);
-      leave_out_bits(mask[tid + k * kStepThreads], x);
-      sum8(x, c, sum.n, b0, b1);
-    }
-  }
-  sum = wave_sum2(Sum2{sum.n, b0 + b1});
-  if (TEMP) sum1 = wave_sum2(Sum2{sum1.n, c0 + c1});
+  sum = wave_sum2(sum);
+  if (TEMP) sum1 = wave_sum2(sum1);
   if ((tid & 63) == 0) {
     s.red[0][tid >> 6] = sum;
     s.red[1][tid >> 6] = sum1;

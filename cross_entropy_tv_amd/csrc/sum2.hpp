@@ -45,4 +45,24 @@ __device__ __forceinline__ double log2_of(const Sum2& a) {
   return a.s > 0.0f ? (double)a.n + log2_64((double)a.s) : -kInf64;
 }
 
+// Adds a group's powers of two to s 2^n.  n is a group's maximum before it: a group that goes 2^100 beyond it is taken
+// again against its own (as the first one is: n starts below every logit).
+__device__ __forceinline__ void add_group(const float (&x)[8], float c, Sum2& a) {
+  float p0 = 0.0f, p1 = 0.0f;
+  sum8(x, c, a.n, p0, p1);
+  if (p0 + p1 >= kRefSumLimit) {
+    const float n = fmaxf(a.n, ref_for(max8(x), c));
+    a = Sum2{n, a.s * exp2_hw(a.n - n)};
+    p0 = p1 = 0.0f;
+    sum8(x, c, n, p0, p1);
+  }
+  a.s += p0 + p1;
+}
+
+// One logit.
+__device__ __forceinline__ void add_one(Sum2& a, float x, float c) {
+  const float n = ref_for(x, c);
+  add_sum2(a, Sum2{n, exp2_hw(__builtin_fmaf(x, c, -n))});
+}
+
 }  // namespace lx

@@ -102,12 +102,6 @@ __device__ __forceinline__ void rank_keys(List& s, int n) {
   __syncthreads();
 }
 
-// A logit joins a thread's sum.
-__device__ __forceinline__ void add_one(Sum2& a, float x, float c) {
-  const float n = ref_for(x, c);
-  add_sum2(a, Sum2{n, exp2_hw(__builtin_fmaf(x, c, -n))});
-}
-
 // Cuts the list to its K largest; those that leave join the sums.  Every thread, behind a barrier; ends behind one.
 __device__ __forceinline__ int cut_list(List& s, int n, int K, float c, Sum2& a) {
   rank_keys(s, n);
