@@ -220,14 +220,6 @@ __device__ __forceinline__ bool mark(uint32_t* bits, int64_t v, int64_t lo, int6
   return (atomicOr(bits + ((v - lo) >> 5), bit) & bit) != 0u;
 }
 
-// The logits of the columns whose bit is set count as masked.
-__device__ __forceinline__ void leave_out_bits(uint32_t byte, float (&x)[8]) {
-  if (byte) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (byte >> e) & 1u ? ninf() : x[e];
-  }
-}
-
 template <typename T>
 __device__ __forceinline__ void store8_any(T* p, const float (&o)[8]) {
   unsigned w[sizeof(T) * 2];

@@ -65,4 +65,12 @@ __device__ __forceinline__ void add_one(Sum2& a, float x, float c) {
   add_sum2(a, Sum2{n, exp2_hw(__builtin_fmaf(x, c, -n))});
 }
 
+// The logits of the columns whose bit is set count as masked.
+__device__ __forceinline__ void leave_out_bits(uint32_t byte, float (&x)[8]) {
+  if (byte) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (byte >> e) & 1u ? ninf() : x[e];
+  }
+}
+
 }  // namespace lx
