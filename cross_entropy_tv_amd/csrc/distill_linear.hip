@@ -86,15 +86,22 @@ __device__ __forceinline__ void scan_ids(TileLds& s, const TileArgs& a, int m0, 
   if (tid == 0) s.listed = 0;
   __syncthreads();
   if (a.K) {
-    const int rows = min(256, a.rows - m0), total = rows * a.K;
+    const int total = min(256, a.rows - m0) * a.K;
     const int32_t* ids = a.ids + (int64_t)m0 * a.K;
-    for (int i = tid; i < total; i += kWideThreads) {
-      const int col = ids[i] - n0;
-      if ((unsigned)col < 256u) {
-        const int r = i / a.K, j = i - r * a.K;
-        if (MASK) atomicOr(&s.mask[r][col >> 5], 1u << (col & 31));
-        const int at = atomicAdd(&s.listed, 1);
-        if (at < kTileEntries) s.list[at] = (uint32_t)(r << 16 | col << 8 | j);
+    // eight requested at once: one by one they would cost a memory latency each
+    for (int i0 = tid; i0 < total; i0 += 8 * kWideThreads) {
+      int col[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) col[k] = ids[min(i0 + k * kWideThreads, total - 1)] - n0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * kWideThreads;
+        if (i < total && (unsigned)col[k] < 256u) {
+          const int r = i / a.K, j = i - r * a.K;
+          if (MASK) atomicOr(&s.mask[r][col[k] >> 5], 1u << (col[k] & 31));
+          const int at = atomicAdd(&s.listed, 1);
+          if (at < kTileEntries) s.list[at] = (uint32_t)(r << 16 | col[k] << 8 | j);
+        }
       }
     }
   }
@@ -169,20 +176,18 @@ void kd_tile_kernel(TileArgs a) {
   if constexpr (!GRAD) {
     float* table = reinterpret_cast<float*>(lds);  // [256][128]
     const int half = wn >> 7;
-    // the logits at the ids and at the target
-    for (int h = 0; h < 2; ++h) {
+    // the logits at the ids
+    for (int h = 0; h < 2 && s.listed; ++h) {
       if (half == h) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int lr = wm + 32 * i + mm::acc_row(r, lane);
-            const int tcol = s.target[lr];
             const uint2 mask = *reinterpret_cast<const uint2*>(&s.mask[lr][wn >> 5]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int lc = wn + 32 * j + (lane & 31);
-              if (lc == tcol) a.z_target[m0 + lr] = acc[i][j][r];
               if (((j ? mask.y : mask.x) >> (lane & 31)) & 1u) table[lr * 128 + (lc & 127)] = acc[i][j][r];
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -205,10 +210,12 @@ void kd_tile_kernel(TileArgs a) {
       for (int r = 0; r < 16; ++r) {
         const int lr = wm + 32 * i + mm::acc_row(r, lane);
         const uint2 mask = *reinterpret_cast<const uint2*>(&s.mask[lr][wn >> 5]);
+        const int tcol = s.target[lr];
         float v[2], y[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int lc = wn + 32 * j + (lane & 31);
+          if (lc == tcol) a.z_target[m0 + lr] = acc[i][j][r];
           y[j] = n0 + lc < end ? acc[i][j][r] : ninf();
           v[j] = ((j ? mask.y : mask.x) >> (lane & 31)) & 1u ? ninf() : y[j];
         }
