@@ -53,6 +53,11 @@ Split split_of(int64_t BT, int64_t V) {
   return Split{(V + columns - 1) / columns, columns};
 }
 
+// What a chunk leaves behind: the sums outside the ids, and of all its columns at temperature 1.
+struct ChunkSums {
+  Sum2d outside, whole;
+};
+
 // Outside-the-ids sums of the columns [lo, hi) of a row (and, TEMP, sums at temperature 1 of all of
 // them), this thread's share.
 template <typename T, bool TEMP, int NT, int H>
@@ -85,15 +90,15 @@ __device__ __forceinline__ void chunk_sums(const T* row, int64_t lo, int64_t hi,
 }
 
 // One workgroup per (row, chunk).  A whole row (chunks == 1) is finished here; chunks leave their sums
-// in parts [row][chunk][4].
+// in parts [row][chunk].
 template <typename T, bool TEMP>
 __global__ __attribute__((amdgpu_flat_work_group_size(kFwdThreads, kFwdThreads), amdgpu_waves_per_eu(sizeof(T) == 4 ? 6 : 8)))
 void kd_forward_kernel(KdLoss l, const T* __restrict__ z, int64_t ldz,
-                                                                 double c64, int chunks, int64_t columns, float* parts) {
+                                                                 double c64, int chunks, int64_t columns, ChunkSums* parts) {
   extern __shared__ uint32_t bits[];
   constexpr int W = kFwdThreads / 64;
   __shared__ Entries en;
-  __shared__ Sum2 red[2][W];
+  __shared__ Sum2d red[2][W];
   __shared__ int bad_any;
   const int64_t tile = large_bid();
   const int64_t r = tile / chunks;
@@ -128,27 +133,27 @@ void kd_forward_kernel(KdLoss l, const T* __restrict__ z, int64_t ldz,
   __syncthreads();
   Sum2 a, a1;
   chunk_sums<T, TEMP, kFwdThreads, kFwdHeld>(row, lo, hi, l.V, reinterpret_cast<const uint8_t*>(bits), c, a, a1);
-  a = wave_sum2(a);
-  if (TEMP) a1 = wave_sum2(a1);
+  Sum2d all = wave_sum2d(a), all1 = {};
+  if (TEMP) all1 = wave_sum2d(a1);
   if ((tid & 63) == 0) {
-    red[0][tid >> 6] = a;
-    red[1][tid >> 6] = a1;
+    red[0][tid >> 6] = all;
+    red[1][tid >> 6] = all1;
   }
   if (tid < K) en.z[tid] = zj;
   __syncthreads();
   if (tid >= 64) return;
-  a = red[0][0];
-  a1 = red[1][0];
+  all = red[0][0];
+  all1 = red[1][0];
   for (int w = 1; w < W; ++w) {
-    add_sum2(a, red[0][w]);
-    if (TEMP) add_sum2(a1, red[1][w]);
+    add_sum2d(all, red[0][w]);
+    if (TEMP) add_sum2d(all1, red[1][w]);
   }
   if (chunks > 1) {
-    if (tid == 0) *reinterpret_cast<float4*>(parts + 4 * tile) = make_float4(a.n, a.s, a1.n, a1.s);
+    if (tid == 0) parts[tile] = ChunkSums{all, all1};
     return;
   }
   double q[kLaneTop];
-  const RowResult o = finish_row<TEMP>(l, r, en, bad_any != 0, t, zt, c64, a, a1, q);
+  const RowResult o = finish_row<TEMP>(l, r, en, bad_any != 0, t, zt, c64, all, all1, q);
   if (tid == 0) store_row(l, r, o);
 }
 
@@ -156,7 +161,7 @@ void kd_forward_kernel(KdLoss l, const T* __restrict__ z, int64_t ldz,
 // order.
 template <typename T, bool TEMP>
 __global__ __launch_bounds__(64) void kd_finish_kernel(KdLoss l, const T* __restrict__ z, int64_t ldz, double c64,
-                                                       int chunks, const float* __restrict__ parts) {
+                                                       int chunks, const ChunkSums* __restrict__ parts) {
   __shared__ Entries en;
   const int64_t r = large_bid();
   if (r >= l.BT) return;
@@ -175,14 +180,14 @@ __global__ __launch_bounds__(64) void kd_finish_kernel(KdLoss l, const T* __rest
     en.z[j] = v >= 0 ? load1(row + v) : ninf();
   }
   const float zt = t >= 0 && t < l.V ? load1(row + t) : 0.0f;
-  Sum2 a{floor_of((float)c64), 0.0f}, a1{floor_of(kLog2e), 0.0f};
+  Sum2d a{floor_of((float)c64), 0.0}, a1{floor_of(kLog2e), 0.0};
   for (int k = lane; k < chunks; k += 64) {
-    const float4 p = *reinterpret_cast<const float4*>(parts + 4 * (r * chunks + k));
-    add_sum2(a, Sum2{p.x, p.y});
-    if (TEMP) add_sum2(a1, Sum2{p.z, p.w});
+    const ChunkSums p = parts[r * chunks + k];
+    add_sum2d(a, p.outside);
+    if (TEMP) add_sum2d(a1, p.whole);
   }
-  a = wave_sum2(a);
-  if (TEMP) a1 = wave_sum2(a1);
+  a = wave_sum2d(a);
+  if (TEMP) a1 = wave_sum2d(a1);
   __syncthreads();
   double q[kLaneTop];
   const RowResult o = finish_row<TEMP>(l, r, en, __any(bad_any), t, zt, c64, a, a1, q);
@@ -193,7 +198,7 @@ template <typename T, bool TEMP>
 hipError_t launch_kd_forward_t(const KdArgs& a, double c64, hipStream_t st) {
   const Split s = split_of(a.l.BT, a.l.V);
   const T* z = static_cast<const T*>(a.z);
-  float* parts = static_cast<float*>(a.workspace);
+  ChunkSums* parts = static_cast<ChunkSums*>(a.workspace);
   (void)hipGetLastError();
   kd_forward_kernel<T, TEMP><<<large_grid(a.l.BT * s.chunks), dim3(kFwdThreads), (size_t)(s.columns / 8), st>>>(
       a.l, z, a.ldz, c64, (int)s.chunks, s.columns, parts);
@@ -315,7 +320,7 @@ hipError_t launch_kd_backward_t(const KdArgs& a, double c64, hipStream_t st) {
 size_t kd_forward_workspace_bytes(int64_t BT, int64_t V) {
   if (BT <= 0 || V <= 0) return 0;
   const Split s = split_of(BT, V);
-  return s.chunks == 1 ? 0 : ((size_t)(BT * s.chunks) * 16 + 255) & ~(size_t)255;
+  return s.chunks == 1 ? 0 : ((size_t)(BT * s.chunks) * sizeof(ChunkSums) + 255) & ~(size_t)255;
 }
 
 #define LX_BY_TYPE(F, ...)                                                                     \

@@ -362,18 +362,18 @@ __global__ __launch_bounds__(64) void kd_rows_kernel(RowsArgs a) {
     en.z[j] = v >= 0 ? a.z_top[r * K + j] : ninf();
   }
   const float zt = t >= 0 && t < l.V ? a.z_target[r] : 0.0f;
-  Sum2 s{floor_of((float)a.c), 0.0f}, s1{floor_of(kLog2e), 0.0f};
+  Sum2d s{floor_of((float)a.c), 0.0}, s1{floor_of(kLog2e), 0.0};
   const float* parts = a.parts + r * a.tiles_n * (TEMP ? 4 : 2);
   for (int k = lane; k < a.tiles_n; k += 64) {
     const float2 w = *reinterpret_cast<const float2*>(parts + k * (TEMP ? 4 : 2));
-    add_sum2(s, Sum2{w.x, w.y});
+    add_sum2d(s, Sum2d{w.x, w.y});
     if (TEMP) {
       const float2 w1 = *reinterpret_cast<const float2*>(parts + k * 4 + 2);
-      add_sum2(s1, Sum2{w1.x, w1.y});
+      add_sum2d(s1, Sum2d{w1.x, w1.y});
     }
   }
-  s = wave_sum2(s);
-  if (TEMP) s1 = wave_sum2(s1);
+  s = wave_sum2d(s);
+  if (TEMP) s1 = wave_sum2d(s1);
   __syncthreads();
   double q[kLaneTop];
   const RowResult o = finish_row<TEMP>(l, r, en, __any(bad_any), t, zt, a.c, s, s1, q);

@@ -1,21 +1,21 @@
 // Cross entropy and distillation from a teacher's top logits: the loss and the gradient of the logits in one pass.
 //
-// A row is cut into up to 16 members' chunks, each held in the registers of one workgroup between the row's sums and
+// A row is cut into up to 12 members' chunks, each held in the registers of one workgroup between the row's sums and
 // the gradient, so every logit is read once.  Tiles are taken by ticket: a workgroup waits only for members
-// of its own row, whose tickets lie within 16 of its own, so with 16 workgroups running the exchange cannot
+// of its own row, whose tickets lie within 12 of its own, so with 12 workgroups running the exchange cannot
 // deadlock; every wait is bounded, and one that gives up leaves NaN in the row.
 //
 //   1. the chunk is requested, and while it arrives the ids that fall into it are marked in LDS and wave 0 forms
 //      the teacher's masses;
 //   2. each thread's sum of 2^(c z - n) outside the ids and, at another temperature than 1, of 2^(z log2 e - n1) of
 //      all columns, as the chunk arrives;
-//   3. a member publishes its sums, those of its ids' logits, and its parts of kd and of the target's logit, and waits
+//   3. a member publishes its sums, those of its ids' logits, and its part of kd, and waits
 //      for the row's;
 //   4. the gradient of its chunk.
 //
-// Every member has read its chunk and its ids' logits before it publishes, and stores after all have published: the
-// gradient may overwrite the logits.  What is published is one 64-bit word a slot, preset to a pattern that no
-// result has, so that a slot is its own flag.
+// Every member has read its chunk, its ids' logits and the target's before it publishes, and stores after all have
+// published: the gradient may overwrite the logits.  What is published is one 64-bit word a slot, preset to a
+// pattern that no result has, so that a slot is its own flag.
 //
 // The logits stay in the registers as they lie in memory, and their exponentials are formed twice: kept in fp32 they
 // would take twice the registers, three workgroups a compute unit instead of four, which cost more (8192 x 151936 bf16:
@@ -40,8 +40,8 @@ constexpr int kStepWaves = kStepThreads / 64;
 constexpr int kStepGroups = 15;    // groups of 8 a thread holds (five members of 151936 columns)
 constexpr int kStepShort = 2;      // of a short row,
 constexpr int kStepMiddle = 6;     // and of a middling one
-constexpr int kMaxMembers = 16;
-constexpr int kSlots = 4;          // words a member publishes
+constexpr int kMaxMembers = 12;
+constexpr int kSlots = 5;          // words a member publishes (a wave reads a row's)
 constexpr uint64_t kEmpty = ~0ull;
 constexpr unsigned kSpinLimit = 1u << 18;
 constexpr int64_t kStepTiles = 512;  // workgroups that few rows are cut into
@@ -98,7 +98,9 @@ __device__ __forceinline__ bool wait_slots(const uint64_t* sl, int n, uint64_t* 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
 }
-__device__ __forceinline__ Sum2 sum_of(uint64_t v) { return Sum2{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))}; }
+__device__ __forceinline__ float lo_of32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ double double_of(uint64_t v) { return __builtin_bit_cast(double, v); }
 
 struct StepLds {
   uint32_t bits[kStepThreads * kStepGroups / 4 + 1];  // of the chunk's columns, those behind its groups last
@@ -110,7 +112,7 @@ struct StepLds {
   int id[kKdMaxTop];    // in the chunk, else -1
   float u[kKdMaxTop], z[kKdMaxTop], q[kKdMaxTop];
   int all[kKdMaxTop];   // ids wherever they are, -1: left out
-  Sum2 red[2][kStepWaves];
+  Sum2d red[2][kStepWaves];
   uint64_t got[kMaxMembers * kSlots];
   unsigned tile;
   int bad, twice;       // an id past the vocabulary; one given twice
@@ -180,7 +182,7 @@ void kd_step_kernel(StepArgs a) {
   const int my_id = tid >= K || my_bad || raw_id < 0 || my_u < kMasked ? -1 : raw_id;
   const bool here = my_id >= first && my_id < end;
   // (wanted after the sums)
-  const T raw_z = row[here ? my_id : 0], raw_zt = row[t_here ? (int)t : 0];
+  const T raw_z = row[here ? my_id : 0], raw_zt = row[t >= 0 && t < V ? (int)t : 0];
   const T raw_extra = row[tid < behind ? first + 8 * count + tid : 0];
   if (tid < K) {
     if (here) {
@@ -223,23 +225,27 @@ void kd_step_kernel(StepArgs a) {
       add_group(x, c, sum);
     }
   }
-  sum = wave_sum2(sum);
-  if (TEMP) sum1 = wave_sum2(sum1);
-  if ((tid & 63) == 0) {
-    s.red[0][tid >> 6] = sum;
-    s.red[1][tid >> 6] = sum1;
+  {
+    const Sum2d w = wave_sum2d(sum);
+    Sum2d w1{};
+    if (TEMP) w1 = wave_sum2d(sum1);
+    if ((tid & 63) == 0) {
+      s.red[0][tid >> 6] = w;
+      s.red[1][tid >> 6] = w1;
+    }
   }
   const float my_z = here ? load1(&raw_z) : ninf();
   if (tid < K) s.z[tid] = my_z;
   __syncthreads();
 
   // ---- wave 0: the member's part, the exchange, the row
-  Sum2 rest{}, whole{}, all{};
+  Sum2d rest{}, whole{}, all{};
   double terms = 0.0;
-  float zt = t_here ? load1(&raw_zt) : 0.0f;
+  float zt = load1(&raw_zt);
+  asm volatile("" : "+v"(zt)::"memory");  // read before anything is published: its owner may overwrite it then
   bool gave_up = false;
   if (tid < 64) {
-    Sum2 top{floor_of(c), 0.0f};
+    Sum2d top{floor_of(c), 0.0};
     const bool twice = s.twice != 0;
 #pragma unroll
     for (int k = 0; k < kLaneTop; ++k) {
@@ -251,7 +257,7 @@ void kd_step_kernel(StepArgs a) {
           if (q[k] > 0.0) terms += z < kMasked ? kInf64 : q[k] * (ua[k] - (double)z * a.c64);
           if (!(z < kMasked) && !(twice && named_before(s.id, j))) {
             const double t2 = (double)z * a.c64, n = __builtin_rint(t2);
-            add_sum2(top, Sum2{(float)n, exp2_hw((float)(t2 - n))});
+            add_sum2d(top, Sum2d{(float)n, exp2_64(t2 - n)});
           }
         }
       }
@@ -268,44 +274,45 @@ void kd_step_kernel(StepArgs a) {
       for (int k = 0; k < kLaneTop; ++k)
         if (tid + 64 * k < K) s.q[tid + 64 * k] = whole_q[k];
     }
-    top = wave_sum2(top);
+    top = wave_sum2d(top);
     terms = wave_sum64(terms);
     rest = s.red[0][0];
     whole = s.red[1][0];
     for (int w = 1; w < kStepWaves; ++w) {
-      add_sum2(rest, s.red[0][w]);
-      if (TEMP) add_sum2(whole, s.red[1][w]);
+      add_sum2d(rest, s.red[0][w]);
+      if (TEMP) add_sum2d(whole, s.red[1][w]);
     }
     if (members > 1) {
       uint64_t* slots = a.slots + r * (int64_t)(members * kSlots);
-      const uint64_t w = tid == 0   ? pack2(rest.n, rest.s)
-                         : tid == 1 ? pack2(top.n, top.s)
-                         : tid == 2 ? pack2((float)terms, zt)
-                                    : pack2(whole.n, whole.s);
+      const uint64_t w = tid == 0   ? pack2(rest.n, top.n)
+                         : tid == 1 ? __builtin_bit_cast(uint64_t, rest.s)
+                         : tid == 2 ? __builtin_bit_cast(uint64_t, top.s)
+                         : tid == 3 ? __builtin_bit_cast(uint64_t, terms)
+                                    : pack2(whole.n, (float)whole.s);
       if (tid < kSlots) publish(slots + member * kSlots + tid, w);
       gave_up = wait_slots(slots, members * kSlots, s.got);
-      const bool lane_member = tid < members;  // lane k has member k's
-      const Sum2 nothing{floor_of(c), 0.0f};
-      const Sum2 part = lane_member ? sum_of(s.got[tid * kSlots + 2]) : Sum2{0.0f, 0.0f};
-      rest = wave_sum2(lane_member ? sum_of(s.got[tid * kSlots]) : nothing);
-      top = wave_sum2(lane_member ? sum_of(s.got[tid * kSlots + 1]) : nothing);
-      if (TEMP) whole = wave_sum2(lane_member ? sum_of(s.got[tid * kSlots + 3]) : Sum2{floor_of(kLog2e), 0.0f});
-      terms = wave_sum64((double)part.n);
-      zt = wave_sum32(part.s);
+      const bool theirs = tid < members;  // lane k has member k's
+      const uint64_t* got = s.got + (theirs ? tid : 0) * kSlots;
+      const Sum2d nothing{floor_of(c), 0.0};
+      rest = wave_sum2d(theirs ? Sum2d{lo_of32(got[0]), double_of(got[1])} : nothing);
+      top = wave_sum2d(theirs ? Sum2d{hi_of32(got[0]), double_of(got[2])} : nothing);
+      if (TEMP) whole = wave_sum2d(theirs ? Sum2d{lo_of32(got[4]), (double)hi_of32(got[4])} : Sum2d{floor_of(kLog2e), 0.0});
+      terms = wave_sum64(theirs ? double_of(got[3]) : 0.0);
     }
     all = top;
-    add_sum2(all, rest);
+    add_sum2d(all, rest);
     if (!TEMP) whole = all;
     if (tid == 0) {
-      const bool any = all.s > 0.0f;
-      const float p_rest = any ? rest.s * exp2_hw(rest.n - all.n) / all.s : 0.0f;
+      const float rest_s = (float)rest.s, all_s = (float)all.s;
+      const bool any = all_s > 0.0f;
+      const float p_rest = any ? rest_s * exp2_hw(rest.n - all.n) / all_s : 0.0f;
       const float off = te.any ? p_rest - (float)te.q_rest : 0.0f;
       const float part = f.kkd * off + (TEMP ? 0.0f : f.kce * p_rest);
-      s.out = rest.s > 0.0f ? part / rest.s : 0.0f;
+      s.out = rest_s > 0.0f ? part / rest_s : 0.0f;
       s.rest_n = rest.n;
-      s.ce1 = any ? f.kce / whole.s : 0.0f;
+      s.ce1 = any ? f.kce / (float)whole.s : 0.0f;
       s.n1 = whole.n;
-      s.kd = any ? 1.0f / all.s : 0.0f;
+      s.kd = any ? 1.0f / all_s : 0.0f;
       s.n = all.n;
       s.state = gave_up || s.bad || t < 0 || t >= V ? 2 : any ? 0 : 1;
     }

@@ -135,7 +135,7 @@ __device__ __forceinline__ RowResult row_result(const KdLoss& l, const Teacher& 
 // logit.
 template <bool TEMP>
 __device__ __forceinline__ RowResult finish_row(const KdLoss& l, int64_t r, const Entries& en, bool bad, int64_t t,
-                                                float zt, double c, const Sum2& a, const Sum2& a1,
+                                                float zt, double c, const Sum2d& a, const Sum2d& a1,
                                                 double (&q)[kLaneTop]) {
   const int lane = tid_x() & 63, K = (int)l.K;
   double ua[kLaneTop];
