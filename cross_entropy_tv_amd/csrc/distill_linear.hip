@@ -13,7 +13,8 @@
 // what this path is there to avoid; a piece of the vocabulary makes grad_w's rows complete at once (no
 // accumulation over pieces), and only grad_x, BT H values, is added up in fp32 from piece to piece.
 //
-// What bounds it: the matrix cores, four products of 2 BT V H.  An epilogue takes its ids from a scan of its 256
+// What bounds it: the matrix cores, four products of 2 BT V H.  At 8192 x 151936 x 4096, K 64: first pass 9.1 ms (1124
+// TFLOP/s; a large library product reaches 1077 to 1216), second 8.4, grad_x 8.5, grad_w 8.1, all else 0.1.  An epilogue takes its ids from a scan of its 256
 // rows' K ids (64 KB at K = 64, from L2, against 125 us of products a tile at H = 4096), which sets the mask of the
 // tile in LDS and lists the entries that fall into it.
 //
@@ -429,7 +430,8 @@ struct Ws {
   size_t bytes;
 };
 
-// Splits of grad_x's product over a piece: few tiles would leave compute units idle through it.
+// Splits of grad_x's product over a piece: few tiles would leave compute units idle through it (64 x 32000 x 4096 whole
+// call 833 us without, 353 with; 300 x 2000 x 576 112 and 90; 512 x 151936 x 4096 5.0 and 2.6 ms).
 int splits_of(int64_t BT, int64_t H, int64_t piece) {
   const int64_t tiles = ((BT + 255) / 256) * ((H + 255) / 256);
   int64_t s = (256 + tiles - 1) / tiles;

@@ -10,7 +10,7 @@
 //              upper 16 bits of their ordered values (one wave, a bit a step).  Later ones: the same over the list.
 //              Truncated to 16 bits it is still one that K logits reach; a later logit has to
 //              exceed it (an equal one would have the higher id).
-//   the list   2048 keys (value, id), cut to those that reach the K-th behind each tile.  A thread marks its groups of
+//   the list   1024 keys (value, id), cut to those that reach the K-th behind each tile.  A thread marks its groups of
 //              8 that reach the threshold and goes on; they are loaded again behind the tile, shared out among all
 //              threads (a wave meets one at two groups of three, and would spend as much on them where it meets them as
 //              on the sums).  Where a tile has more logits above the threshold than there is room it is gone
@@ -487,15 +487,20 @@ __global__ __launch_bounds__(kJoinThreads) void top_join_kernel(TopArgs g, doubl
   write_row(g, r, s.sorted, n < K ? n : K, c64, rest);
 }
 
-// Chunks of a row: about 256 workgroups, chunks of at least 2048 columns, their keys within one list.  (From 128 rows on
-// a second launch costs what it gains: 259 x 50001, K 100, as whole rows 30 us, four chunks each 22 + 7.)
+// Chunks of a row: a workgroup for every compute unit, of at least 2048 columns, and of long rows (16384 columns a chunk
+// and more) about as many as run at once; their keys within one list.  A second launch joins them (7 us).  Whole rows, one
+// a compute unit, and this: 1 x 151936 bf16, K 64, 35 and 17 us, 128 of them 52 and 28, 256 52 and 37 (K 256: 109 and 60),
+// 511 75 and 58; 300 x 128256 fp32 84 and 61, 600 of them 116 and 98; 256 x 262144 fp32 83 and 91.
+constexpr int64_t kTopWanted = 1280;
 struct TopSplit {
   int64_t chunks, columns;
 };
 TopSplit top_split(int64_t BT, int64_t V, int64_t K) {
-  int64_t s = BT >= 128 ? 1 : (256 + BT - 1) / BT;
-  if (s > kJoinList / K) s = kJoinList / K;
+  int64_t s = BT >= 128 ? 1 : (256 + BT - 1) / BT, more = kTopWanted / BT;
   if (s > V / 2048) s = V / 2048;
+  if (more > V / 16384) more = V / 16384;
+  if (s < more) s = more;
+  if (s > kJoinList / K) s = kJoinList / K;
   if (s < 1) s = 1;
   const int64_t columns = ((V + s - 1) / s + 7) / 8 * 8;
   return TopSplit{(V + columns - 1) / columns, columns};

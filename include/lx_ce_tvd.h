@@ -684,8 +684,9 @@ lx_status lx_ce_kd_backward(void* grad, int64_t ld_grad, const void* student, in
                             float g_ce, float g_kd, const float* grad_ce_rows, const float* grad_kd_rows,
                             const float* g_scale, lx_dtype dt, void* stream);
 
-/* Both in one call, for a loss whose upstream gradients are known before it: where the rows allow it
-   each logit is read once. */
+/* Both in one call, for a loss whose upstream gradients are known before it: rows of up to 368640
+   tokens are read once, longer ones twice.  A workspace serves one call at a time (calls that may run at
+   once, two captured graphs on two streams, take one each). */
 size_t lx_ce_kd_forward_backward_workspace_bytes(int64_t BT, int64_t V, lx_dtype dt);
 
 lx_status lx_ce_kd_forward_backward(const void* student, int64_t ld_student, const int64_t* target,
