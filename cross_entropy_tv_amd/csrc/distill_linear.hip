@@ -44,15 +44,16 @@ constexpr int kTileEntries = 2048;  // entries of a tile that are listed; with m
 
 struct RowParam {  // a row of the second pass
   RowGrad g;
-  int target;  // -1: no column; kNanRow
+  int target;  // kNanRow, kZeroRow
 };
 constexpr int kNanRow = -2;
+constexpr int kZeroRow = -3;  // ignored, or without any unmasked logit: 0 whatever its logits are
 
 struct TileLds {
   uint32_t mask[256][8];        // bit c of row r: column n0 + c is one of the row's ids
   uint32_t list[kTileEntries];  // row << 16 | column << 8 | entry
   int listed;
-  int target[256];              // the target's column in the tile, or -1; second pass: kNanRow
+  int target[256];              // the target's column in the tile, or -1; second pass: kNanRow, kZeroRow
   float4 p[256];                // second pass: what every column takes, {out, nr, n1, kce}
   float2 p_named[256];          // {kkd, nz}
 };
@@ -163,7 +164,7 @@ void kd_tile_kernel(TileArgs a) {
     if (m < a.rows) {
       if (GRAD) {
         const RowParam p = a.param[m];
-        col = p.target == kNanRow ? kNanRow : p.target >= n0 && p.target < n0 + 256 ? p.target - n0 : -1;
+        col = p.target < -1 ? p.target : p.target >= n0 && p.target < n0 + 256 ? p.target - n0 : -1;
         s.p[tid] = make_float4(p.g.out, p.g.nr, p.g.n1, p.g.kce);
         s.p_named[tid] = make_float2(p.g.kkd, p.g.nz);
       } else {
@@ -298,6 +299,7 @@ void kd_tile_kernel(TileArgs a) {
       if (m >= a.rows) continue;
       uint4 v = *reinterpret_cast<const uint4*>(stage + row * kStagePitch + c);
       if (s.target[row] == kNanRow) v.x = v.y = v.z = v.w = (uint32_t)kQNaN16 * 0x10001u;
+      if (s.target[row] == kZeroRow) v = make_uint4(0u, 0u, 0u, 0u);
       if (n0 + 256 > end) {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -342,7 +344,7 @@ __global__ __launch_bounds__(64) void kd_rows_kernel(RowsArgs a) {
   const int lane = tid_x(), K = (int)l.K;
   const int64_t t = l.target[r];
   const float none = 1.0e30f;  // 2^(c z - none) is 0
-  RowParam p{RowGrad{0.0f, 0.0f, none, none, none, 0.0f}, -1};
+  RowParam p{RowGrad{0.0f, 0.0f, none, none, none, 0.0f}, kZeroRow};
   if (t == l.ignore_index) {
     if (lane == 0) {
       store_row(l, r, RowResult{});
@@ -395,8 +397,8 @@ __global__ __launch_bounds__(64) void kd_rows_kernel(RowsArgs a) {
     }
   }
   if (lane == 0) {
-    p.g = row_grad<TEMP>(a.g, l, r, o.lse, o.lse_t, o.lse_rest, o.off);
-    p.target = o.bad ? kNanRow : (int)t;
+    if (o.lse != ninf()) p.g = row_grad<TEMP>(a.g, l, r, o.lse, o.lse_t, o.lse_rest, o.off);
+    p.target = o.bad || t < 0 || t >= l.V ? kNanRow : o.lse == ninf() ? kZeroRow : (int)t;
     a.param[r] = p;
   }
 }

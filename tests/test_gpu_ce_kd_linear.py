@@ -252,3 +252,34 @@ def test_no_rows():
                                         None, e(0), None, e(0, 64), gw, 1.0, 0.0)
     torch.cuda.synchronize()
     assert (gw == 0).all()
+
+
+@pytest.mark.parametrize("T", [1.0, 2.0])
+@pytest.mark.parametrize("K", [0, 12])
+def test_rows_whose_logits_are_not_used(T, K):
+    """An ignored row of large finite values, whose logits overflow, and a row whose logits are all masked: they leave the
+    gradients as they are without them."""
+    if K == 0:
+        T = 1.0
+
+    def edit(c):
+        c.target[3] = IGN
+        c.x[:, 0] = 0.0
+        c.w[:, 0] = 2.0 ** 50
+        c.x[5] = 0.0
+        c.x[5, 0] = -2.0 ** 60
+        c.z = c.x.astype(np.float64) @ c.w.astype(np.float64).T
+
+    c = Linear(15, 9, 700, 64, K, T=T, edit=edit)
+    c.run(piece=256)
+    rows = [r for r in range(9) if r not in (3, 5)]
+    if K:
+        c.check_loss(rows=rows)
+    assert c.out[0][5] == 0 and c.out[1][5] == 0 and c.out[2][5] == NINF
+    assert not c.gx[[3, 5]].any()
+    first = [c.gx.clone(), c.gw.clone()]
+    assert torch.isfinite(first[0]).all() and torch.isfinite(first[1]).all()
+    c.xd[3] = 3e38
+    c.xd[3, ::2] = -3e38
+    c.run(piece=256)
+    assert torch.equal(c.gx, first[0]) and torch.equal(c.gw, first[1])
