@@ -318,7 +318,7 @@ void kd_step_kernel(StepArgs a) {
       s.n1 = whole.n;
       s.kd = any ? 1.0f / all_s : 0.0f;
       s.n = all.n;
-      s.state = gave_up || s.bad || t < 0 || t >= V ? 2 : any ? 0 : 1;
+      s.state = gave_up || t < 0 || t >= V ? 2 : !any ? 1 : s.bad ? 2 : 0;
     }
   }
   __syncthreads();

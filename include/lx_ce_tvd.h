@@ -656,7 +656,7 @@ lx_status lx_top_logits(const void* logits, int64_t ld, int64_t BT, int64_t V, i
  *   the teacher's too.  A token that the teacher names and the student masks makes kd +inf, a
  *   masked target ce +inf; the gradients are as above with p = 0.  A row whose teacher names nothing and has no
  *   rest has kd 0 and no gradient of it.  A student row without any unmasked logit has ce = kd = 0,
- *   lse = -inf and gradient 0.  Other logits are finite, at most 1e30 in size.
+ *   lse = -inf and gradient 0 (its ids are not looked at).  Other logits are finite, at most 1e30 in size.
  * - Outputs: ce, kd, lse float[BT] (lse at temperature 1); state float[BT][LX_KD_STATE_FLOATS],
  *   16-byte aligned, which the backward takes: log sum exp(z / T), that over the tokens that no entry
  *   names (0 where there are none), p_r - q_r, A.
@@ -711,6 +711,7 @@ lx_status lx_ce_kd_forward_backward(const void* student, int64_t ld_student, con
  *   element of grad_w.
  * - piece: 1 to 2^22 columns, rounded up to a multiple of 256.
  * - BT == 0 sets grad_w to 0.
+ * - x and w are finite.  An ignored row of x may hold any finite values: its row of G is 0.
  * Workspace: at least lx_ce_kd_linear_workspace_bytes(...) bytes, 256-byte aligned: per row 16 bytes for 256 logits
  *   and 12 K, and with grads 2 bytes for each column of a piece and 4 H (16 times as much where a product has
  *   few tiles).

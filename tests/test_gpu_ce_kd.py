@@ -252,3 +252,20 @@ def test_no_rows():
                                  *(e(o) for o in c.out), e(c.gd), 1.0, 1.0)
     torch.cuda.synchronize()
     assert (c.out[0] == 99).all() and (c.gd == 55).all()
+
+
+@pytest.mark.parametrize("V", [300, 50000])
+def test_a_bad_id_in_a_masked_row(V):
+    """A row without any unmasked logit has no gradient, whatever its ids: in one pass as in two."""
+    def edit(c):
+        c.z[1] = NINF
+        c.ids[1, 2] = V + 5
+    c = Case(21, 3, V, 5, "bf16", edit=edit).place()
+    c.step(lx, c.gd)
+    other = torch.empty_like(c.gd)
+    assert not c.gd[1].any() and not torch.isnan(c.gd).any()
+    assert c.out[0][1] == 0 and c.out[1][1] == 0 and c.out[2][1] == NINF
+    c.forward(lx)
+    c.backward(lx, other)
+    assert not other[1].any() and not torch.isnan(other).any()
+    assert c.out[0][1] == 0 and c.out[1][1] == 0 and c.out[2][1] == NINF
