@@ -10,11 +10,14 @@ import numpy as np
 import pytest
 import torch
 
-import cross_entropy_tv_amd as lx
-from _kd import DEV, IGN, TOL_LOG, TOL_LOSS, Case, near
-from oracle import kd as oracle
-
 pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import cross_entropy_tv_amd as lx  # noqa: E402
+from _kd import DEV, IGN, TOL_LOG, TOL_LOSS, Case, near  # noqa: E402
+from oracle import kd as oracle  # noqa: E402
 
 
 class Run:
